@@ -26,8 +26,10 @@ EXPORTS = ("moe_last_error", "moe_version", "moe_device_status", "moe_route_deep
            "moe_forward_workspace_bytes", "moe_set_phase_events", "moe_forward_noalloc",
            "moe_route_softmax", "moe_shared_gate", "moe_combine_gated", "moe_forward_ex",
            "moe_forward_ex_workspace_bytes", "moe_watchdog_selftest", "moe_indexer_topk",
-           "moe_set_fault", "moe_get_fault")
-MOE_ROUTE_DEEPSEEK, MOE_ROUTE_SOFTMAX = 0, 1
+           "moe_set_fault", "moe_get_fault", "moe_route_softmax_grouped", "moe_quantize_blocks",
+           "moe_matmul_blocks")
+MOE_ROUTE_DEEPSEEK, MOE_ROUTE_SOFTMAX, MOE_ROUTE_SOFTMAX_GROUPED = 0, 1, 2
+MOE_BITS_E4M3 = 0x108  # expert weights: e4m3 codes with an fp32 scale per 128 x 128 block
 
 
 class MoeError(RuntimeError):
@@ -107,13 +109,18 @@ def lib(path: str | None = None):
             L.moe_watchdog_selftest.argtypes = [i64, P]
             L.moe_indexer_topk.argtypes = [P, ctypes.c_int, i64, i32, i64, P, i32, P, P, i64, P]
             L.moe_set_fault.argtypes = [i32, i32]
+            L.moe_route_softmax_grouped.argtypes = [P, ctypes.c_int, i64, i32, P,
+                                                    ctypes.POINTER(RouteParams), P, P, P]
+            L.moe_quantize_blocks.argtypes = [P, ctypes.c_int, i64, i32, i64, i32, P, P, P]
+            L.moe_matmul_blocks.argtypes = [P, P, i64, i64, P, P, i32, i32, ctypes.c_int, P, P]
             L.moe_get_fault.argtypes = [ctypes.POINTER(i32), ctypes.POINTER(i32)]
             for name in ("moe_device_status", "moe_route_deepseek", "moe_permute",
                          "moe_router_logits", "moe_grouped_swiglu", "moe_combine",
                          "moe_forward", "moe_set_phase_events", "moe_forward_noalloc",
                          "moe_route_softmax", "moe_shared_gate", "moe_combine_gated",
                          "moe_forward_ex", "moe_watchdog_selftest", "moe_indexer_topk",
-                         "moe_set_fault", "moe_get_fault"):
+                         "moe_set_fault", "moe_get_fault", "moe_route_softmax_grouped",
+                         "moe_quantize_blocks", "moe_matmul_blocks"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -152,7 +159,8 @@ def route_params(top_k, n_group, topk_group, norm_topk_prob, routed_scaling_fact
 def expert_weights(w: dict | None):
     """ExpertWeights from a dict: bits 16 -> gate/up/down bf16; bits 8 or 4 -> gate/up/down
     int32 (packed uint32 words) plus gate_s/gate_b/up_s/up_b/down_s/down_b fp16 and an
-    optional 'group' (inputs per scale: 32, 64 or 128; default 64)."""
+    optional 'group' (inputs per scale: 32, 64 or 128; default 64); bits MOE_BITS_E4M3 ->
+    gate/up/down float8_e4m3fn plus gate_s/up_s/down_s fp32 [.., rows/128, inputs/128]."""
     if w is None:
         return None
     bits = int(w.get("bits", 16))
@@ -161,12 +169,24 @@ def expert_weights(w: dict | None):
             _need(w[k], torch.bfloat16, k)
         return ExpertWeights(16, 0, w["gate"].data_ptr(), w["up"].data_ptr(), w["down"].data_ptr(),
                              None, None, None, None, None, None)
+    if bits == MOE_BITS_E4M3:
+        for k in ("gate", "up", "down"):
+            q, sc = w[k], w[k + "_s"]
+            _need(q, torch.float8_e4m3fn, k)
+            _need(sc, torch.float32, k + "_s", q.device)
+            want = tuple(q.shape[:-2]) + (-(-q.shape[-2] // 128), -(-q.shape[-1] // 128))
+            if tuple(sc.shape) != want:
+                raise ValueError(f"{k}_s: shape {tuple(sc.shape)}, expected {want}")
+        return ExpertWeights(MOE_BITS_E4M3, 128, w["gate"].data_ptr(), w["up"].data_ptr(),
+                             w["down"].data_ptr(), w["gate_s"].data_ptr(), None,
+                             w["up_s"].data_ptr(), None, w["down_s"].data_ptr(), None)
     for k in ("gate", "up", "down"):
         _need(w[k], torch.int32, k)
     for k in ("gate_s", "gate_b", "up_s", "up_b", "down_s", "down_b"):
         _need(w[k], torch.float16, k)
     if bits not in (4, 8):
-        raise ValueError(f"bits = {bits}: expert weights are bf16 (16) or affine 8 / 4-bit")
+        raise ValueError(f"bits = {bits}: expert weights are bf16 (16), affine 8 / 4-bit or "
+                         "MOE_BITS_E4M3")
     return ExpertWeights(bits, int(w.get("group", 64)), w["gate"].data_ptr(), w["up"].data_ptr(),
                          w["down"].data_ptr(), w["gate_s"].data_ptr(), w["gate_b"].data_ptr(),
                          w["up_s"].data_ptr(), w["up_b"].data_ptr(), w["down_s"].data_ptr(),
@@ -220,6 +240,88 @@ def route_softmax(logits, top_k, inds=None, scores=None, stream=None):
     _check(lib().moe_route_softmax(_ptr(logits), dt, rows, E, int(top_k), _ptr(inds),
                                    _ptr(scores), _stream(stream)))
     return inds, scores
+
+
+def route_softmax_grouped(logits, top_k, n_group, topk_group, norm_topk_prob,
+                          routed_scaling_factor, bias=None, inds=None, scores=None, stream=None):
+    """Group-limited softmax gate: probabilities over all experts, groups ranked by their best
+    expert, weights renormalised only with norm_topk_prob; logits [..., E] fp32/bf16, bias [E]
+    fp32 or None -> (inds int32, scores fp32) [..., K]."""
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be fp32 or bf16")
+    _need(logits, logits.dtype, "logits")
+    E = logits.shape[-1]
+    if bias is not None:
+        if bias.dim() != 1 or bias.shape[0] != E:
+            raise ValueError("bias must have rank 1 and length E (the last dim of logits)")
+        _need(bias, torch.float32, "bias", logits.device)
+    rows = logits.numel() // E if E else 0
+    shape = tuple(logits.shape[:-1]) + (int(top_k),)
+    if inds is None:
+        inds = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    if scores is None:
+        scores = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    p = route_params(top_k, n_group, topk_group, norm_topk_prob, routed_scaling_factor)
+    dt = MOE_DTYPE_F32 if logits.dtype == torch.float32 else MOE_DTYPE_BF16
+    _check(lib().moe_route_softmax_grouped(_ptr(logits), dt, rows, E, _ptr(bias),
+                                           ctypes.byref(p), _ptr(inds), _ptr(scores),
+                                           _stream(stream)))
+    return inds, scores
+
+
+def quantize_blocks(x, block_rows=1, codes=None, scales=None, stream=None):
+    """x [rows, n] fp32/bf16 (rows may be strided) -> (codes float8_e4m3fn [rows, n], scales
+    fp32 [ceil(rows/block_rows), ceil(n/128)]); block_rows 1 (activations) or 128 (weights)."""
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("x must be fp32 or bf16")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [rows, n] with unit stride along n")
+    rows, n = x.shape
+    ld = x.stride(0) if rows > 1 else max(n, 1)
+    R = -(-rows // int(block_rows)) if int(block_rows) > 0 else 0
+    if codes is None:
+        codes = torch.empty(rows, n, dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty(R, -(-n // 128), dtype=torch.float32, device=x.device)
+    _need(codes, torch.float8_e4m3fn, "codes", x.device)
+    _need(scales, torch.float32, "scales", x.device)
+    if codes.shape != x.shape or tuple(scales.shape) != (R, -(-n // 128)):
+        raise ValueError(f"codes must be {tuple(x.shape)} and scales {(R, -(-n // 128))}")
+    dt = MOE_DTYPE_F32 if x.dtype == torch.float32 else MOE_DTYPE_BF16
+    _check(lib().moe_quantize_blocks(_ptr(x), dt, rows, n, ld, int(block_rows), _ptr(codes),
+                                     _ptr(scales), _stream(stream)))
+    return codes, scales
+
+
+def matmul_blocks(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stream=None):
+    """Block-scaled e4m3 product a w^T: a float8_e4m3fn [M, K] (rows may be strided), a_scale
+    fp32 [M, ceil(K/128)], w float8_e4m3fn [N, K], w_scale fp32 [ceil(N/128), ceil(K/128)] ->
+    bf16 or fp32 [M, N]."""
+    if a.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"a: dtype {a.dtype}, expected {torch.float8_e4m3fn}")
+    if a.dim() != 2 or (a.shape[1] > 1 and a.stride(1) != 1):
+        raise ValueError("a must be [M, K] with unit stride along K")
+    _need(w, torch.float8_e4m3fn, "w", a.device)
+    _need(a_scale, torch.float32, "a_scale", a.device)
+    _need(w_scale, torch.float32, "w_scale", a.device)
+    if w.dim() != 2 or w.shape[1] != a.shape[1]:
+        raise ValueError(f"w must be [N, {a.shape[1]}]")
+    (M, K), N = a.shape, w.shape[0]
+    kb = -(-K // 128)
+    if tuple(a_scale.shape) != (M, kb) or tuple(w_scale.shape) != (-(-N // 128), kb):
+        raise ValueError(f"a_scale must be {(M, kb)} and w_scale {(-(-N // 128), kb)}")
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=a.device)
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out must be fp32 or bf16")
+    _need(out, out.dtype, "out", a.device)
+    if tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be {(M, N)}")
+    dt = MOE_DTYPE_F32 if out.dtype == torch.float32 else MOE_DTYPE_BF16
+    lda = a.stride(0) if M > 1 else max(K, 1)
+    _check(lib().moe_matmul_blocks(_ptr(a), _ptr(a_scale), M, lda, _ptr(w), _ptr(w_scale), N, K,
+                                   dt, _ptr(out), _stream(stream)))
+    return out
 
 
 def shared_gate(x, w_gate, stream=None):

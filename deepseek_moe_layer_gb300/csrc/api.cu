@@ -153,8 +153,37 @@ int check_route_params(int32_t E, const moe_route_params_t* p) {
     return MOE_OK;
 }
 
-int check_weights(const moe_expert_weights_t* w, const char* what, int shared) {
+// The grouped softmax gate: groups of any size (their score is one expert's), and no more
+// experts than the kept groups hold (the others are never selected).
+int check_grouped_params(int32_t E, const moe_route_params_t* p) {
+    MOE_CHECK(p, "params is NULL");
+    MOE_CHECK(E >= 1 && E <= kMaxExperts, "E = %d outside [1, %d]", E, kMaxExperts);
+    MOE_CHECK(p->n_group >= 1 && p->n_group <= kMaxGroups, "n_group = %d outside [1, %d]",
+              p->n_group, kMaxGroups);
+    MOE_CHECK(E % p->n_group == 0, "E = %d not divisible by n_group = %d", E, p->n_group);
+    MOE_CHECK(p->topk_group >= 1 && p->topk_group <= p->n_group,
+              "topk_group = %d outside [1, n_group = %d]", p->topk_group, p->n_group);
+    const int32_t left = p->topk_group * (E / p->n_group);
+    MOE_CHECK(p->top_k >= 1 && p->top_k <= left && p->top_k <= kMaxTopK,
+              "top_k = %d outside [1, min(%d, the %d experts of topk_group groups)]", p->top_k,
+              kMaxTopK, left);
+    return MOE_OK;
+}
+
+int check_weights(const moe_expert_weights_t* w, const char* what, int shared, bool scaled) {
     MOE_CHECK(w, "%s weights are NULL", what);
+    if (scaled) {
+        MOE_CHECK(w->bits == MOE_BITS_E4M3,
+                  "%s weights: bits = %d, but the routed experts are MOE_BITS_E4M3", what, w->bits);
+        MOE_CHECK(w->gate && w->up && w->down, "%s weights: gate/up/down pointer is NULL", what);
+        MOE_CHECK(aligned(w->gate, 16) && aligned(w->up, 16) && aligned(w->down, 16),
+                  "%s weights: pointers must be 16-byte aligned", what);
+        MOE_CHECK(w->gate_scale && w->up_scale && w->down_scale,
+                  "%s weights: e4m3 scale pointer is NULL", what);
+        MOE_CHECK(aligned(w->gate_scale, 4) && aligned(w->up_scale, 4) && aligned(w->down_scale, 4),
+                  "%s weights: fp32 scale pointers must be 4-byte aligned", what);
+        return MOE_OK;
+    }
     MOE_CHECK(w->bits == 16 || w->bits == 8 || w->bits == 4, "%s weights: bits = %d (16, 8 or 4)",
               what, w->bits);
     MOE_CHECK(!shared || w->bits == 16, "%s weights must be bf16 (bits 16)", what);
@@ -174,6 +203,18 @@ int check_weights(const moe_expert_weights_t* w, const char* what, int shared) {
     }
     return MOE_OK;
 }
+
+// A weight row's index is a 32-bit copy coordinate, and so is a tile's.
+int check_scaled_dims(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K) {
+    const int64_t wide = d > I ? d : I;
+    MOE_CHECK(E * wide < ((int64_t)1 << 31) &&
+                  (T * (K + 1) / 128 + E + 1) * (wide / 128) < ((int64_t)1 << 31) &&
+                  T * (K + 1) * (d / 128) < ((int64_t)1 << 36),
+              "T = %lld, E = %d, d = %d, I = %d: too large for e4m3 experts", (long long)T, E, d, I);
+    return MOE_OK;
+}
+
+bool is_scaled(const moe_expert_weights_t* w) { return w && w->bits == MOE_BITS_E4M3; }
 
 int check_dims(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K) {
     MOE_CHECK(T >= 0, "T = %lld < 0", (long long)T);
@@ -241,6 +282,22 @@ RouterPlan router_plan(int64_t T, int32_t d, int32_t E) {
 struct SwigluWs {
     size_t x_perm, h, total;
 };
+// With e4m3 experts the same space holds the codes and scales of the rows [P + T, d] and of h
+// [P + T, I].  They fit wherever top_k >= 2; the sizes reported cover both.
+struct ScaledWs {
+    size_t x, sx, h, sh, total;
+};
+ScaledWs scaled_ws(int64_t T, int32_t d, int32_t I, int32_t K, int has_shared) {
+    ScaledWs w;
+    const int64_t R = T * K + (has_shared ? T : 0);
+    size_t off = 0;
+    w.x = off;  off += align256((size_t)R * d);
+    w.sx = off; off += align256((size_t)R * (d / 128) * 4);
+    w.h = off;  off += align256((size_t)R * I);
+    w.sh = off; off += align256((size_t)R * (I / 128) * 4);
+    w.total = off;
+    return w;
+}
 SwigluWs swiglu_ws(int64_t T, int32_t d, int32_t I, int32_t K, int has_shared) {
     SwigluWs w;
     const int64_t P = T * K;
@@ -251,6 +308,11 @@ SwigluWs swiglu_ws(int64_t T, int32_t d, int32_t I, int32_t K, int has_shared) {
     off += align256((size_t)(P + (has_shared ? T : 0)) * I * 2);
     w.total = off;
     return w;
+}
+size_t swiglu_ws_bytes(int64_t T, int32_t d, int32_t I, int32_t K, int has_shared) {
+    const size_t a = swiglu_ws(T, d, I, K, has_shared).total;
+    const size_t b = scaled_ws(T, d, I, K, has_shared).total;
+    return a > b ? a : b;
 }
 
 // Whole-layer workspace.
@@ -270,7 +332,7 @@ ForwardWs forward_ws(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K, int 
     w.perm = off;        off += align256((size_t)P * 4);
     w.inv = off;         off += align256((size_t)P * 4);
     w.expert_out = off;  off += align256((size_t)(P + (has_shared ? T : 0)) * d * 2);
-    w.swiglu = off;      off += swiglu_ws(T, d, I, K, has_shared).total;
+    w.swiglu = off;      off += swiglu_ws_bytes(T, d, I, K, has_shared);
     w.total = off;
     return w;
 }
@@ -280,9 +342,62 @@ ForwardWs forward_ws(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K, int 
 // so no plan splits more than d/512 ways.
 int router_ksplit_bound(int32_t d) { return d / 512 > 1 ? d / 512 : 1; }
 
+// e4m3 experts: quantised rows of the dispatch, gate/up product with SwiGLU and quantisation in
+// its epilogue, down product.
+int run_swiglu_scaled(const void* x, int64_t T, int32_t d, int32_t I, int32_t E, int32_t K,
+                      const int32_t* offsets, const int32_t* perm, const moe_expert_weights_t* ex,
+                      const moe_expert_weights_t* sh, void* out, uint8_t* ws, cudaStream_t s) {
+    const int64_t P = T * K;
+    const ScaledWs lw = scaled_ws(T, d, I, K, sh != nullptr);
+    uint8_t* xq = ws + lw.x;
+    float* sx = reinterpret_cast<float*>(ws + lw.sx);
+    uint8_t* hq = ws + lw.h;
+    float* shq = reinterpret_cast<float*>(ws + lw.sh);
+    const int64_t shared_rows = sh ? T : 0;
+    MOE_LAUNCH(moe::launch_quantize_dispatched(x, perm, offsets, E, K, P, shared_rows, d, xq, sx, s),
+             "quantise rows");
+    MOE_CUDA(phase(4, s), "phase event");
+    const auto fp = [](const void* q) { return static_cast<const float*>(q); };
+    moe::ScaledGemmArgs g = {};
+    g.swiglu = 1;
+    g.x = xq;
+    g.sx = sx;
+    g.rows = P + shared_rows;
+    g.ldx = d;
+    g.offsets = offsets;
+    g.E = E;
+    g.has_shared = sh != nullptr;
+    g.shared_rows = shared_rows;
+    g.shared_row0 = P;
+    g.K = d;
+    g.F = I;
+    g.w = {ex->gate, ex->up, fp(ex->gate_scale), fp(ex->up_scale)};
+    if (sh) g.ws = {sh->gate, sh->up, fp(sh->gate_scale), fp(sh->up_scale)};
+    g.out = hq;
+    g.out_scale = shq;
+    MOE_LAUNCH(moe::launch_scaled_gemm(g, s), "gate/up GEMM");
+    MOE_CUDA(phase(5, s), "phase event");
+    moe::ScaledGemmArgs dn = g;
+    dn.swiglu = 0;
+    dn.x = hq;
+    dn.sx = shq;
+    dn.ldx = I;
+    dn.K = I;
+    dn.F = d;
+    dn.w = {ex->down, nullptr, fp(ex->down_scale), nullptr};
+    if (sh) dn.ws = {sh->down, nullptr, fp(sh->down_scale), nullptr};
+    dn.out = out;
+    dn.out_scale = nullptr;
+    MOE_LAUNCH(moe::launch_scaled_gemm(dn, s), "down GEMM");
+    MOE_CUDA(phase(6, s), "phase event");
+    return MOE_OK;
+}
+
 int run_swiglu(const void* x, int64_t T, int32_t d, int32_t I, int32_t E, int32_t K,
                const int32_t* offsets, const int32_t* perm, const moe_expert_weights_t* ex,
                const moe_expert_weights_t* sh, void* out, uint8_t* ws, cudaStream_t s) {
+    if (is_scaled(ex))
+        return run_swiglu_scaled(x, T, d, I, E, K, offsets, perm, ex, sh, out, ws, s);
     const int64_t P = T * K;
     const SwigluWs lw = swiglu_ws(T, d, I, K, sh != nullptr);
     void* x_perm = ws + lw.x_perm;
@@ -368,9 +483,10 @@ int forward_impl(const moe_layer_args_t& A, void* ws, size_t ws_bytes, cudaStrea
     const int32_t d = A.d, I = A.I, E = A.E;
     const moe_route_params_t* params = &A.params;
     const bool softmax = A.route_kind == MOE_ROUTE_SOFTMAX;
-    MOE_CHECK(A.route_kind == MOE_ROUTE_DEEPSEEK || softmax, "route_kind %d unknown",
+    const bool grouped = A.route_kind == MOE_ROUTE_SOFTMAX_GROUPED;
+    MOE_CHECK(A.route_kind == MOE_ROUTE_DEEPSEEK || softmax || grouped, "route_kind %d unknown",
               (int)A.route_kind);
-    MOE_CHECK(A.w_router && (softmax || A.bias) && ws && (T == 0 || (A.x && A.y)),
+    MOE_CHECK(A.w_router && (softmax || grouped || A.bias) && ws && (T == 0 || (A.x && A.y)),
               "NULL pointer argument");
     int rc;
     if (softmax) {
@@ -378,18 +494,20 @@ int forward_impl(const moe_layer_args_t& A, void* ws, size_t ws_bytes, cudaStrea
         MOE_CHECK(params->top_k >= 1 && params->top_k <= E, "top_k = %d outside [1, E = %d]",
                   params->top_k, E);
     } else {
-        rc = check_route_params(E, params);
+        rc = grouped ? check_grouped_params(E, params) : check_route_params(E, params);
         if (rc) return rc;
     }
     const int32_t K = params->top_k;
     rc = check_dims(T, d, I, E, K);
     if (rc) return rc;
-    rc = check_weights(A.experts, "expert", 0);
+    const bool scaled = is_scaled(A.experts);
+    rc = check_weights(A.experts, "expert", 0, scaled);
     if (rc) return rc;
     if (A.shared) {
-        rc = check_weights(A.shared, "shared expert", 1);
+        rc = check_weights(A.shared, "shared expert", 1, scaled);
         if (rc) return rc;
     }
+    if (scaled && (rc = check_scaled_dims(T, d, I, E, K))) return rc;
     MOE_CHECK(!A.w_shared_gate || A.shared, "w_shared_gate given without a shared expert");
     MOE_CHECK(aligned(A.x, 16) && aligned(A.w_router, 16) && aligned(A.y, 16) &&
                   aligned(A.w_shared_gate, 16),
@@ -463,7 +581,8 @@ int forward_impl(const moe_layer_args_t& A, void* ws, size_t ws_bytes, cudaStrea
     ra.scores = scores;
     ra.logits_out = A.logits_out;
     ra.softmax = softmax ? 1 : 0;
-    MOE_LAUNCH(moe::launch_route(ra, s), "route kernel");
+    MOE_LAUNCH(grouped ? moe::launch_route_grouped(ra, s) : moe::launch_route(ra, s),
+             "route kernel");
     MOE_CUDA(phase(2, s), "phase event");
 
     // a3: dispatch
@@ -509,6 +628,9 @@ int moe_device_status(int32_t clear, moe_stream_t stream) {
     if (rc) return rc;
     unsigned int st = 0;
     MOE_CUDA(moe::read_device_status(&st, clear, (cudaStream_t)stream), "status read");
+    unsigned int st8 = 0;
+    MOE_CUDA(moe::read_scaled_status(&st8, clear, (cudaStream_t)stream), "status read");
+    if (st == 0) st = st8;
     if (st == 5)
         return fail(MOE_ERR_CUDA, "a CTA pair of an expert GEMM held different TMEM columns "
                                   "(status %u); the GEMM did no work", st);
@@ -648,7 +770,7 @@ size_t moe_grouped_swiglu_workspace_bytes(int64_t T, int32_t d, int32_t I, int32
                                           int32_t has_shared) {
     (void)E;
     if (T < 0 || d < 0 || I < 0 || K < 0) return 0;
-    return swiglu_ws(T, d, I, K, has_shared != 0).total;
+    return swiglu_ws_bytes(T, d, I, K, has_shared != 0);
 }
 
 int moe_grouped_swiglu(const void* x, int64_t T, int32_t d, int32_t I, int32_t E, int32_t K,
@@ -659,15 +781,18 @@ int moe_grouped_swiglu(const void* x, int64_t T, int32_t d, int32_t I, int32_t E
     MOE_CHECK(offsets && ws && (T == 0 || (x && perm && out)), "NULL pointer argument");
     int rc = check_dims(T, d, I, E, K);
     if (rc) return rc;
-    rc = check_weights(experts, "expert", 0);
+    const bool scaled = is_scaled(experts);
+    rc = check_weights(experts, "expert", 0, scaled);
     if (rc) return rc;
     if (shared) {
-        rc = check_weights(shared, "shared expert", 1);
+        rc = check_weights(shared, "shared expert", 1, scaled);
         if (rc) return rc;
     }
+    if (scaled && (rc = check_scaled_dims(T, d, I, E, K))) return rc;
     MOE_CHECK(aligned(x, 16) && aligned(out, 16), "x and out must be 16-byte aligned");
     MOE_CHECK(aligned(ws, 256), "ws must be 256-byte aligned");
-    const size_t need = swiglu_ws(T, d, I, K, shared != nullptr).total;
+    const size_t need = scaled ? scaled_ws(T, d, I, K, shared != nullptr).total
+                               : swiglu_ws(T, d, I, K, shared != nullptr).total;
     MOE_CHECK(ws_bytes >= need, "ws_bytes = %zu < %zu required", ws_bytes, need);
     if (T == 0) return MOE_OK;
     rc = check_device();
@@ -767,6 +892,102 @@ int moe_route_softmax(const void* logits, moe_dtype_t dtype, int64_t rows, int32
     a.scores = scores;
     a.softmax = 1;
     MOE_LAUNCH(moe::launch_route(a, (cudaStream_t)stream), "route kernel");
+    return MOE_OK;
+}
+
+int moe_route_softmax_grouped(const void* logits, moe_dtype_t dtype, int64_t rows, int32_t E,
+                              const float* bias, const moe_route_params_t* params, int32_t* inds,
+                              float* scores, moe_stream_t stream) {
+    begin_call();
+    MOE_CHECK(rows == 0 || (logits && inds && scores), "NULL pointer argument");
+    MOE_CHECK(dtype == MOE_DTYPE_F32 || dtype == MOE_DTYPE_BF16, "dtype %d unknown", (int)dtype);
+    MOE_CHECK(rows >= 0, "rows = %lld < 0", (long long)rows);
+    int rc = check_grouped_params(E, params);
+    if (rc) return rc;
+    if (rows == 0) return MOE_OK;
+    rc = check_device();
+    if (rc) return rc;
+    moe::RouteArgs a = {};
+    a.logits = logits;
+    a.bf16 = dtype == MOE_DTYPE_BF16;
+    a.nsplit = 1;
+    a.bias = bias;
+    a.rows = rows;
+    a.E = E;
+    a.top_k = params->top_k;
+    a.n_group = params->n_group;
+    a.topk_group = params->topk_group;
+    a.norm = params->norm_topk_prob != 0;
+    a.scale = params->routed_scaling_factor;
+    a.inds = inds;
+    a.scores = scores;
+    MOE_LAUNCH(moe::launch_route_grouped(a, (cudaStream_t)stream), "route kernel");
+    return MOE_OK;
+}
+
+int moe_quantize_blocks(const void* x, moe_dtype_t dtype, int64_t rows, int32_t n, int64_t ld,
+                        int32_t block_rows, void* codes, float* scales, moe_stream_t stream) {
+    begin_call();
+    MOE_CHECK(dtype == MOE_DTYPE_F32 || dtype == MOE_DTYPE_BF16, "dtype %d unknown", (int)dtype);
+    MOE_CHECK(rows >= 0 && rows < ((int64_t)1 << 31), "rows = %lld outside [0, 2^31)",
+              (long long)rows);
+    MOE_CHECK(n >= 16 && n % 16 == 0, "n = %d must be a positive multiple of 16", n);
+    MOE_CHECK(block_rows == 1 || block_rows == 128, "block_rows = %d (1 or 128)", block_rows);
+    const int per16 = dtype == MOE_DTYPE_BF16 ? 8 : 4;
+    MOE_CHECK(ld >= n && ld % per16 == 0, "ld = %lld must be at least n = %d and a multiple of %d",
+              (long long)ld, n, per16);
+    const int64_t nb = ((int64_t)n + 127) / 128;
+    MOE_CHECK((rows + block_rows - 1) / block_rows * nb < ((int64_t)1 << 31),
+              "rows * n = %lld * %d has too many blocks", (long long)rows, n);
+    MOE_CHECK(rows == 0 || (x && codes && scales), "NULL pointer argument");
+    MOE_CHECK(aligned(x, 16) && aligned(codes, 16) && aligned(scales, 4),
+              "x and codes must be 16-byte aligned, scales 4-byte");
+    if (rows == 0) return MOE_OK;
+    int rc = check_device();
+    if (rc) return rc;
+    const int bf16 = dtype == MOE_DTYPE_BF16;
+    uint8_t* q = static_cast<uint8_t*>(codes);
+    MOE_LAUNCH(block_rows == 1
+                   ? moe::launch_quantize_rows(x, bf16, rows, n, ld, q, scales, (cudaStream_t)stream)
+                   : moe::launch_quantize_square(x, bf16, rows, n, ld, q, scales,
+                                                 (cudaStream_t)stream),
+             "quantise kernel");
+    return MOE_OK;
+}
+
+int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t lda, const void* w,
+                      const float* w_scale, int32_t N, int32_t K, moe_dtype_t out_dtype, void* out,
+                      moe_stream_t stream) {
+    begin_call();
+    MOE_CHECK(out_dtype == MOE_DTYPE_F32 || out_dtype == MOE_DTYPE_BF16, "dtype %d unknown",
+              (int)out_dtype);
+    MOE_CHECK(M >= 0 && M < ((int64_t)1 << 31), "M = %lld outside [0, 2^31)", (long long)M);
+    MOE_CHECK(N >= 1, "N = %d < 1", N);
+    MOE_CHECK(K >= 16 && K % 16 == 0, "K = %d must be a positive multiple of 16", K);
+    MOE_CHECK(lda >= K && lda % 16 == 0, "lda = %lld must be at least K = %d and a multiple of 16",
+              (long long)lda, K);
+    MOE_CHECK((M + 127) / 128 * (((int64_t)N + 127) / 128) < ((int64_t)1 << 31),
+              "M x N = %lld x %d has too many tiles", (long long)M, N);
+    MOE_CHECK(w && w_scale && (M == 0 || (a && a_scale && out)), "NULL pointer argument");
+    MOE_CHECK(aligned(a, 16) && aligned(w, 16), "a and w must be 16-byte aligned");
+    MOE_CHECK(aligned(a_scale, 4) && aligned(w_scale, 4) &&
+                  aligned(out, out_dtype == MOE_DTYPE_F32 ? 4 : 2),
+              "scales and out must be aligned to their type");
+    if (M == 0) return MOE_OK;
+    int rc = check_device();
+    if (rc) return rc;
+    moe::ScaledGemmArgs g = {};
+    g.x = a;
+    g.sx = a_scale;
+    g.rows = M;
+    g.ldx = lda;
+    g.E = 1;
+    g.K = K;
+    g.F = N;
+    g.w = {w, nullptr, w_scale, nullptr};
+    g.out = out;
+    g.f32 = out_dtype == MOE_DTYPE_F32;
+    MOE_LAUNCH(moe::launch_scaled_gemm(g, (cudaStream_t)stream), "block-scaled product");
     return MOE_OK;
 }
 

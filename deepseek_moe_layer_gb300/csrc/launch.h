@@ -55,6 +55,8 @@ struct RouteArgs {
     int softmax;                 // 1: softmax route (bias, groups, norm, scale unused)
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
+// The group-limited softmax gate (route_softmax.cu); bias may be nullptr.
+cudaError_t launch_route_grouped(const RouteArgs& a, cudaStream_t s);
 // logits[t, e] += offset[e] for a [T, E] fp32 matrix.
 cudaError_t launch_add_offset(float* logits, long long T, int E, const float* offset,
                               cudaStream_t s);
@@ -142,8 +144,44 @@ struct GemmArgs {
 };
 cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t s);
 
+// ---- block-scaled e4m3 -------------------------------------------------------------
+// codes [rows, n], scales [rows, ceil(n/128)]; x rows `ld` elements apart; n % 16 == 0.
+cudaError_t launch_quantize_rows(const void* x, int bf16, long long rows, int n, long long ld,
+                                 uint8_t* codes, float* scales, cudaStream_t s);
+// The same with a scale for each 128 x 128 block: scales [ceil(rows/128), ceil(n/128)].
+cudaError_t launch_quantize_square(const void* x, int bf16, long long rows, int n, long long ld,
+                                   uint8_t* codes, float* scales, cudaStream_t s);
+// Rows of the dispatch: row j < offsets[E] from token perm[j] / K, row P + t from token t
+// (shared_rows of them), of bf16 x [T, d].
+cudaError_t launch_quantize_dispatched(const void* x, const int32_t* perm, const int32_t* offsets,
+                                       int E, int K, long long P, long long shared_rows, int d,
+                                       uint8_t* codes, float* scales, cudaStream_t s);
+
+struct ScaledWeights {           // e4m3 codes [groups, F, K] and scales, one or two (gate, up)
+    const void *w0, *w1;
+    const float *s0, *s1;        // [groups, ceil(F/128), ceil(K/128)]
+};
+struct ScaledGemmArgs {
+    int swiglu;                  // 1: codes and scales of silu(x w0^T) * (x w1^T); 0: x w0^T
+    const void* x;               // e4m3 codes [rows, K], rows ldx bytes apart
+    const float* sx;             // [rows, ceil(K/128)]
+    long long rows, ldx;
+    const int32_t* offsets;      // [E + 1] routed row offsets (device), or nullptr: one group
+    int E, has_shared;
+    long long shared_rows;       // T
+    long long shared_row0;       // first row of the shared group (= the routed rows at most)
+    int K, F;                    // inputs; outputs per group
+    ScaledWeights w, ws;         // routed (or the only) weights; the shared expert's
+    void* out;                   // swiglu: codes [rows, F]; else bf16 (or fp32: f32) [rows, F]
+    float* out_scale;            // swiglu: [rows, F / 128]
+    int f32;
+};
+cudaError_t launch_scaled_gemm(const ScaledGemmArgs& a, cudaStream_t s);
+
 // Per-device status word of the kernels with bounded waits.
 cudaError_t read_device_status(unsigned int* out, int clear, cudaStream_t s);
+// The block-scaled products' own.
+cudaError_t read_scaled_status(unsigned int* out, int clear, cudaStream_t s);
 // One CTA waits `limit_ns` on an mbarrier nothing completes and records the timeout.
 cudaError_t launch_watchdog_selftest(unsigned long long limit_ns, cudaStream_t s);
 

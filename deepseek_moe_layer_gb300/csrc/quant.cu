@@ -1,0 +1,222 @@
+// quant.cu -- rows (or 128 x 128 blocks) of bf16 / fp32 numbers to e4m3 codes with one scale for
+// each block of 128.
+//
+// For a block with largest finite magnitude A the scale is the smallest power of two s >= 2^-126
+// with A / s <= 448 (the largest e4m3 number), 1 for a block of zeros, and the codes are x / s
+// rounded to nearest, ties to even.  A power of two makes x / s exact, so a code is the one
+// rounding of its input; NaN and +-inf become the e4m3 NaN and leave the scale to the rest of
+// their block.
+//
+// Rows: half a warp per block of 128 (8 elements per lane, 16 B of bf16 or 32 B of fp32), so the
+// maximum is four shuffles; each half warp takes kPer blocks with all their loads in flight.
+#include "launch.h"
+#include "scaled.cuh"
+
+namespace moe {
+namespace {
+
+constexpr float kInf = __builtin_huge_valf();
+
+template <bool BF16>
+MOE_DEV void load8(const void* p, long long at, float (&v)[8]) {
+    if constexpr (BF16) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16_lo(u[i]);
+            v[2 * i + 1] = bf16_hi(u[i]);
+        }
+    } else {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+        const float4 a = __ldg(q), b = __ldg(q + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
+
+// Largest magnitude of eight numbers; NaN is skipped (fmaxf), infinities are not.
+MOE_DEV float amax8(const float (&v)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
+}
+MOE_DEV float amax8_finite(const float (&v)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]) < kInf ? fabsf(v[i]) : 0.0f);
+    return m;
+}
+
+MOE_DEV uint2 codes8(const float (&v)[8], float inv) {
+    return make_uint2(cvt_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                      cvt_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+MOE_DEV void inf_to_nan(float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (fabsf(v[i]) == kInf) v[i] = __int_as_float(0x7FFFFFFF);
+}
+
+// Rows.  GATHER: output row j < P is row perm[j] / K of x when j < *dispatched (else it is left
+// alone), and row P + t (shared rows) is row t.
+struct QuantRows {
+    const void* x;
+    long long rows;      // output rows
+    long long ld;        // elements between rows of x
+    int n, nb;           // columns (a multiple of 16), blocks of 128 per row
+    uint8_t* codes;      // [rows, n]
+    float* scales;       // [rows, nb]
+    const int32_t* perm; // GATHER
+    const int32_t* dispatched;
+    long long P;
+    int K;
+};
+
+constexpr int kPer = 4;
+
+template <bool BF16, bool GATHER>
+__global__ void __launch_bounds__(256) quant_rows_kernel(const QuantRows a) {
+    const int lane = threadIdx.x & 15;
+    const long long total = a.rows * a.nb;
+    const long long b0 = ((long long)blockIdx.x * 16 + (threadIdx.x >> 4)) * kPer;
+    pdl_launch_dependents();
+    pdl_wait();  // the dispatch (GATHER) or x come from the kernels before
+    float v[kPer][8];
+    long long row[kPer];
+    int col[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const long long b = b0 + u;
+        row[u] = b / a.nb;
+        col[u] = (int)(b - row[u] * a.nb) * 128 + lane * 8;
+        long long src = row[u];
+        bool on = b < total;
+        if (GATHER && on) {
+            if (src >= a.P) src -= a.P;
+            else if (src < *a.dispatched) src = a.perm[src] / a.K;
+            else on = false;
+        }
+        if (!on) row[u] = -1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+        if (on && col[u] < a.n) load8<BF16>(a.x, src * a.ld + col[u], v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        float m = amax8(v[u]);
+#pragma unroll
+        for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+        if (__any_sync(0xFFFFFFFFu, m == kInf)) {  // an infinity in one of the warp's two blocks
+            m = amax8_finite(v[u]);
+#pragma unroll
+            for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+            inf_to_nan(v[u]);
+        }
+        float s, inv;
+        block_scale(m, s, inv);
+        if (row[u] < 0) continue;
+        if (col[u] < a.n)
+            *reinterpret_cast<uint2*>(a.codes + row[u] * a.n + col[u]) = codes8(v[u], inv);
+        if (lane == 0) a.scales[row[u] * a.nb + (col[u] >> 7)] = s;
+    }
+}
+
+// 128 x 128 blocks (weights): one CTA per block, its 16 half warps take eight rows each and
+// keep them in registers between the maximum and the codes.
+template <bool BF16>
+__global__ void __launch_bounds__(256) quant_square_kernel(const void* x, long long rows,
+                                                           long long ld, int n, int nb,
+                                                           uint8_t* codes, float* scales) {
+    __shared__ float part[8];
+    const int lane = threadIdx.x & 15, hw = threadIdx.x >> 4;
+    const long long br = blockIdx.x / nb;
+    const int bc = (int)(blockIdx.x - br * nb);
+    const int col = bc * 128 + lane * 8;
+    pdl_launch_dependents();
+    pdl_wait();
+    float v[8][8];
+    float m = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const long long r = br * 128 + u * 16 + hw;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+        if (r < rows && col < n) load8<BF16>(x, r * ld + col, v[u]);
+        m = fmaxf(m, amax8(v[u]));
+    }
+    if (__syncthreads_or(m == kInf)) {
+        m = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            m = fmaxf(m, amax8_finite(v[u]));
+            inf_to_nan(v[u]);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, part[w]);
+    float s, inv;
+    block_scale(m, s, inv);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const long long r = br * 128 + u * 16 + hw;
+        if (r < rows && col < n)
+            *reinterpret_cast<uint2*>(codes + r * n + col) = codes8(v[u], inv);
+    }
+    if (threadIdx.x == 0) scales[br * nb + bc] = s;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const void* x, int bf16, long long rows, int n, long long ld,
+                                 uint8_t* codes, float* scales, cudaStream_t s) {
+    QuantRows a = {};
+    a.x = x;
+    a.rows = rows;
+    a.ld = ld;
+    a.n = n;
+    a.nb = (n + 127) / 128;
+    a.codes = codes;
+    a.scales = scales;
+    const long long per = 16 * kPer;
+    const unsigned grid = (unsigned)((rows * a.nb + per - 1) / per);
+    return bf16 ? launch_kernel(quant_rows_kernel<true, false>, dim3(grid), dim3(256), 0, s, a)
+                : launch_kernel(quant_rows_kernel<false, false>, dim3(grid), dim3(256), 0, s, a);
+}
+
+cudaError_t launch_quantize_square(const void* x, int bf16, long long rows, int n, long long ld,
+                                   uint8_t* codes, float* scales, cudaStream_t s) {
+    const int nb = (n + 127) / 128;
+    const unsigned grid = (unsigned)((rows + 127) / 128 * nb);
+    return bf16 ? launch_kernel(quant_square_kernel<true>, dim3(grid), dim3(256), 0, s, x, rows, ld,
+                                n, nb, codes, scales)
+                : launch_kernel(quant_square_kernel<false>, dim3(grid), dim3(256), 0, s, x, rows,
+                                ld, n, nb, codes, scales);
+}
+
+cudaError_t launch_quantize_dispatched(const void* x, const int32_t* perm, const int32_t* offsets,
+                                       int E, int K, long long P, long long shared_rows, int d,
+                                       uint8_t* codes, float* scales, cudaStream_t s) {
+    QuantRows a = {};
+    a.x = x;
+    a.rows = P + shared_rows;
+    a.ld = d;
+    a.n = d;
+    a.nb = (d + 127) / 128;
+    a.codes = codes;
+    a.scales = scales;
+    a.perm = perm;
+    a.dispatched = offsets + E;
+    a.P = P;
+    a.K = K;
+    const long long per = 16 * kPer;
+    const unsigned grid = (unsigned)((a.rows * a.nb + per - 1) / per);
+    return launch_kernel(quant_rows_kernel<true, true>, dim3(grid), dim3(256), 0, s, a);
+}
+
+}  // namespace moe

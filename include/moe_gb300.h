@@ -75,8 +75,16 @@ typedef struct {
  *               first) of word j/4.
  *   Quantised weights are dequantised to bf16 inside the expert GEMMs (4-bit: one bf16
  *   fused multiply-add; 8-bit: fp32 fused multiply-add, then one rounding to bf16).
- *   All pointers 16-byte aligned (the scales and biases: 2-byte).
+ *   bits == MOE_BITS_E4M3: block-scaled 8-bit floating point.  gate, up: e4m3 (fn: no
+ *               infinities) [NE, I, d]; down: e4m3 [NE, d, I]; *_scale: fp32 [NE, I/128, d/128]
+ *               (gate, up) and [NE, d/128, I/128] (down), one for each 128 x 128 block;
+ *               w = scale * code; group_size and the biases are ignored.  The rows that meet
+ *               them are quantised too (moe_quantize_blocks with block_rows 1) and the products
+ *               run in 8 bits, as in moe_matmul_blocks.  A shared expert beside them is
+ *               MOE_BITS_E4M3 as well.
+ *   All pointers 16-byte aligned (fp16 scales and biases: 2-byte; fp32 scales: 4-byte).
  */
+#define MOE_BITS_E4M3 0x108
 typedef struct {
     int32_t bits;
     int32_t group_size;
@@ -161,6 +169,61 @@ int moe_route_softmax(const void* logits, moe_dtype_t dtype, int64_t rows, int32
                       int32_t top_k, int32_t* inds, float* scores, moe_stream_t stream);
 
 /*
+ * moe_route_softmax_grouped -- the group-limited softmax gate, without a counterpart in the
+ * pages: softmax over ALL E experts, selection inside the best groups, weights that need not
+ * be renormalised.  logits [rows, E] fp32 or bf16; bias [E] fp32 or NULL.
+ * Per row, with a NaN logit counted as -inf and m the largest logit:
+ *   p_j = exp(l_j - m) / sum_i exp(l_i - m)   (all 0 when m = -inf; shared by the +inf logits
+ *   when m = +inf);  v_j = p_j + bias_j (a NaN sum counts as -inf);  a group's score is its
+ *   largest v; the topk_group best groups stay (lower group index first among equals), experts
+ *   of the others are never selected; the K largest v are selected, in descending order, lower
+ *   expert index first among equals; the weights are p (without the bias), divided by their sum
+ *   only when K > 1 and norm_topk_prob (0 when that sum is 0), times routed_scaling_factor.
+ * The selection is that of exact arithmetic to 64 bits: without a bias it compares the logits,
+ * with one it falls back on fp64 where fp32 cannot tell two neighbours apart.
+ * Out: inds [rows, K] int32, scores [rows, K] fp32.
+ * Errors: MOE_ERR_INVALID for NULL pointers (bias may be NULL), rows < 0, an unknown dtype, E
+ * outside [1, 1024], n_group outside [1, 32] or not dividing E, topk_group outside
+ * [1, n_group], top_k outside [1, min(32, topk_group * E / n_group)].  rows == 0 is a no-op.
+ */
+int moe_route_softmax_grouped(const void* logits, moe_dtype_t dtype, int64_t rows, int32_t E,
+                              const float* bias, const moe_route_params_t* params, int32_t* inds,
+                              float* scores, moe_stream_t stream);
+
+/*
+ * moe_quantize_blocks -- numbers to e4m3 codes with one scale for each block of 128, without a
+ * counterpart in the pages: what the block-scaled products read.
+ *   x [rows, ld] fp32 or bf16, n columns per row (ld >= n, in elements; rows 16-byte aligned).
+ *   block_rows 1: a block is 128 columns of a row (the last one shorter when n % 128 != 0);
+ *   block_rows 128: 128 rows x 128 columns (weights).
+ *   Out: codes e4m3 [rows, n], scales fp32 [ceil(rows / block_rows), ceil(n / 128)].
+ * With A the block's largest finite magnitude, its scale s is the smallest power of two
+ * >= 2^-126 with A / s <= 448 (1 when A = 0), and a code is x / s rounded to nearest, ties to
+ * even.  NaN and infinities become the e4m3 NaN.
+ * Errors: MOE_ERR_INVALID for NULL pointers, an unknown dtype, rows < 0, n not a positive
+ * multiple of 16, ld < n or not a multiple of 16 bytes, block_rows not 1 or 128, x or codes not
+ * 16-byte aligned, 2^31 blocks or more.  rows == 0 is a no-op.
+ */
+int moe_quantize_blocks(const void* x, moe_dtype_t dtype, int64_t rows, int32_t n, int64_t ld,
+                        int32_t block_rows, void* codes, float* scales, moe_stream_t stream);
+
+/*
+ * moe_matmul_blocks -- the product of block-scaled e4m3 matrices, without a counterpart in the
+ * pages:
+ *     out[r, n] = sum_b a_scale[r, b] * w_scale[n / 128, b] * (sum over block b of a[r, k] w[n, k])
+ *   a e4m3 [M, K], rows lda bytes apart; a_scale fp32 [M, ceil(K / 128)]; w e4m3 [N, K];
+ *   w_scale fp32 [ceil(N / 128), ceil(K / 128)]; the scales are any fp32 numbers.  A block's
+ *   sum runs in the tensor cores' fp32, the sum over the blocks in fp32, and out [M, N] is that
+ *   (MOE_DTYPE_F32) or rounded once (MOE_DTYPE_BF16).
+ * Errors: MOE_ERR_INVALID for NULL pointers, an unknown dtype, M < 0, N < 1, K not a positive
+ * multiple of 16, lda < K or not a multiple of 16, a or w not 16-byte aligned, 2^31 tiles of
+ * 128 x 128 or more.  M == 0 is a no-op.
+ */
+int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t lda, const void* w,
+                      const float* w_scale, int32_t N, int32_t K, moe_dtype_t out_dtype, void* out,
+                      moe_stream_t stream);
+
+/*
  * moe_permute -- token-to-expert dispatch ([epic] first paragraph: the grouping that
  * gather_mm / gather_qmm consume).  inds [T, K] int32 expert ids of the P = T*K pairs
  * p = t*K + k.
@@ -190,15 +253,17 @@ int moe_router_logits(const void* x, int64_t T, int32_t d, const void* w_router,
  * For each slot j of expert e (token t = perm[j] / K):
  *     out[j] = W_down[e] (silu(W_gate[e] x[t]) * (W_up[e] x[t])),  silu(a) = a/(1+e^-a),
  * with fp32 accumulation, h rounded to bf16 between the two GEMMs, out stored as bf16.
+ * MOE_BITS_E4M3 experts: x[t] and h are quantised as by moe_quantize_blocks (h from fp32) and
+ * the three products are those of moe_matmul_blocks.
  * If shared != NULL the shared expert runs on every token in the same launches and its
  * rows follow: out[P + t] = FFN_shared(x[t]).
  *   x bf16 [T, d]; offsets [E+1] and perm [P] as produced by moe_permute; experts with
- *   NE = E; shared (NE = 1, bits 16) or NULL.  Out: out bf16 [P (+T), d].
+ *   NE = E; shared (NE = 1, bits 16, or MOE_BITS_E4M3 as the experts) or NULL.  Out: out bf16 [P (+T), d].
  *   ws: device workspace of at least moe_grouped_swiglu_workspace_bytes() bytes,
  *   256-byte aligned; its contents need no initialisation and are clobbered.
  * Errors: MOE_ERR_INVALID for NULL pointers, T < 0, K < 1, E < 1 or > 1024, d or I not a
- * multiple of 128, T*K >= 2^31, bits not 16, 8 or 4, group_size not 32, 64 or 128 for
- * quantised weights, shared bits != 16, misaligned pointers, or a workspace that is too
+ * multiple of 128, T*K >= 2^31, bits not 16, 8, 4 or MOE_BITS_E4M3, group_size not 32, 64 or 128 for
+ * quantised weights, shared bits != 16 (MOE_BITS_E4M3 beside such experts), misaligned pointers, or a workspace that is too
  * small.
  */
 int moe_grouped_swiglu(const void* x, int64_t T, int32_t d, int32_t I, int32_t E, int32_t K,
@@ -261,14 +326,19 @@ size_t moe_forward_workspace_bytes(int64_t T, int32_t d, int32_t I, int32_t E, i
 /*
  * moe_forward_ex -- the layer with a choice of gate and an optional shared-expert gate:
  * route_kind MOE_ROUTE_DEEPSEEK (moe_route_deepseek; bias required) or MOE_ROUTE_SOFTMAX
- * (moe_route_softmax; bias, groups, norm and scale unused), and w_shared_gate bf16 [d]
+ * (moe_route_softmax; bias, groups, norm and scale unused) or MOE_ROUTE_SOFTMAX_GROUPED
+ * (moe_route_softmax_grouped; bias may be NULL), and w_shared_gate bf16 [d]
  * (non-NULL: the shared expert's output is weighted by sigmoid(x . w_shared_gate), as in
  * moe_combine_gated; NULL: weight 1).  Every other field as in moe_forward.
  * ws: at least moe_forward_ex_workspace_bytes(args) bytes, 256-byte aligned.
  * Errors: those of moe_forward, an unknown route_kind, w_shared_gate without a shared
  * expert.
  */
-typedef enum { MOE_ROUTE_DEEPSEEK = 0, MOE_ROUTE_SOFTMAX = 1 } moe_route_kind_t;
+typedef enum {
+    MOE_ROUTE_DEEPSEEK = 0,
+    MOE_ROUTE_SOFTMAX = 1,
+    MOE_ROUTE_SOFTMAX_GROUPED = 2
+} moe_route_kind_t;
 
 typedef struct {
     int32_t route_kind;

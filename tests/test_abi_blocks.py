@@ -1,0 +1,179 @@
+"""Refusals of the block-scaled e4m3 calls and of the grouped softmax gate, on a machine without
+a GPU: every check runs on the host before any CUDA call."""
+import ctypes
+
+import pytest
+import torch
+
+from deepseek_moe_layer_gb300 import binding
+
+FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: every call below fails its host checks
+BAD = binding.MOE_ERR_INVALID
+F8 = torch.float8_e4m3fn
+
+
+def _err():
+    return binding.lib().moe_last_error().decode()
+
+
+def _quant(x=FAKE, dtype=1, rows=4, n=256, ld=256, block_rows=1, codes=FAKE, scales=FAKE):
+    return binding.lib().moe_quantize_blocks(x, dtype, rows, n, ld, block_rows, codes, scales, None)
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(x=None), "NULL"), (dict(codes=None), "NULL"), (dict(scales=None), "NULL"),
+    (dict(dtype=2), "dtype"), (dict(rows=-1), "rows"), (dict(rows=1 << 31), "rows"),
+    (dict(n=0), "n = 0"), (dict(n=24), "n = 24"), (dict(n=-16), "n = -16"),
+    (dict(ld=248), "ld = 248"), (dict(ld=260), "ld = 260"), (dict(dtype=0, ld=258), "ld = 258"),
+    (dict(block_rows=0), "block_rows"), (dict(block_rows=64), "block_rows"),
+    (dict(x=ctypes.c_void_p(0x1008)), "aligned"), (dict(codes=ctypes.c_void_p(0x1008)), "aligned"),
+    (dict(scales=ctypes.c_void_p(0x1002)), "aligned"),
+    (dict(rows=(1 << 31) - 1, n=1 << 20, ld=1 << 20), "too many blocks"),
+])
+def test_quantize_refusals(kw, msg):
+    assert _quant(**kw) == BAD
+    assert msg in _err()
+
+
+def _matmul(a=FAKE, sa=FAKE, M=4, lda=256, w=FAKE, sw=FAKE, N=8, K=256, dt=1, out=FAKE):
+    return binding.lib().moe_matmul_blocks(a, sa, M, lda, w, sw, N, K, dt, out, None)
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(a=None), "NULL"), (dict(sa=None), "NULL"), (dict(w=None), "NULL"),
+    (dict(sw=None), "NULL"), (dict(out=None), "NULL"), (dict(M=0, w=None), "NULL"),
+    (dict(M=-1), "M = -1"), (dict(M=1 << 31), "M = "), (dict(N=0), "N = 0"), (dict(K=0), "K = 0"),
+    (dict(K=8, lda=16), "K = 8"), (dict(K=200, lda=256), "K = 200"), (dict(lda=240), "lda = 240"),
+    (dict(lda=264), "lda = 264"), (dict(dt=3), "dtype"),
+    (dict(a=ctypes.c_void_p(0x1004)), "aligned"), (dict(w=ctypes.c_void_p(0x1001)), "aligned"),
+    (dict(out=ctypes.c_void_p(0x1001)), "aligned"),
+    (dict(dt=0, out=ctypes.c_void_p(0x1002)), "aligned"),
+    (dict(sa=ctypes.c_void_p(0x1002)), "aligned"),
+    (dict(M=(1 << 31) - 1, N=(1 << 31) - 1), "too many tiles"),
+])
+def test_matmul_refusals(kw, msg):
+    assert _matmul(**kw) == BAD
+    assert msg in _err()
+
+
+def test_empty_calls_do_nothing():
+    assert _quant(rows=0, x=None, codes=None, scales=None) == binding.MOE_OK
+    assert _matmul(M=0, a=None, sa=None, out=None) == binding.MOE_OK
+
+
+def _grouped(E=16, K=2, G=4, tg=2, rows=3, logits=FAKE, inds=FAKE, scores=FAKE, dtype=0):
+    p = binding.route_params(K, G, tg, True, 1.0)
+    return binding.lib().moe_route_softmax_grouped(logits, dtype, rows, E, None, ctypes.byref(p),
+                                                   inds, scores, None)
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(logits=None), "NULL"), (dict(inds=None), "NULL"), (dict(scores=None), "NULL"),
+    (dict(dtype=9), "dtype"), (dict(rows=-2), "rows"), (dict(E=0), "E = 0"),
+    (dict(E=1025, G=1, tg=1), "E = 1025"), (dict(G=0), "n_group"), (dict(G=3), "not divisible"),
+    (dict(E=66, G=33, tg=1), "n_group = 33"), (dict(tg=0), "topk_group"), (dict(tg=5), "topk_group"),
+    (dict(K=0), "top_k"), (dict(K=9), "top_k = 9"), (dict(E=64, G=1, tg=1, K=33), "top_k = 33"),
+])
+def test_grouped_gate_refusals(kw, msg):
+    assert _grouped(**kw) == BAD
+    assert msg in _err()
+
+
+def test_grouped_gate_empty_and_without_params():
+    assert _grouped(rows=0, logits=None, inds=None, scores=None) == binding.MOE_OK
+    assert binding.lib().moe_route_softmax_grouped(FAKE, 0, 3, 16, None, None, FAKE, FAKE,
+                                                   None) == BAD
+
+
+def _ew(bits=binding.MOE_BITS_E4M3, **kw):
+    f = dict(gate=0x1000, up=0x1000, down=0x1000, gate_scale=0x1000, up_scale=0x1000,
+             down_scale=0x1000)
+    f.update(kw)
+    return binding.ExpertWeights(bits, 0, f["gate"], f["up"], f["down"], f["gate_scale"], None,
+                                 f["up_scale"], None, f["down_scale"], None)
+
+
+def _swiglu(experts, shared=None, T=4, d=256, I=128, E=16, K=2, ws_bytes=1 << 30):
+    return binding.lib().moe_grouped_swiglu(
+        FAKE, T, d, I, E, K, FAKE, FAKE, ctypes.byref(experts),
+        None if shared is None else ctypes.byref(shared), FAKE, ctypes.c_void_p(0x10000), ws_bytes,
+        None)
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(gate=None), "NULL"), (dict(down_scale=None), "scale pointer is NULL"),
+    (dict(up=0x1008), "16-byte aligned"), (dict(gate_scale=0x1002), "4-byte aligned"),
+])
+def test_scaled_expert_weight_refusals(kw, msg):
+    assert _swiglu(_ew(**kw)) == BAD
+    assert msg in _err()
+    assert _swiglu(_ew(), shared=_ew(**kw)) == BAD
+    assert "shared expert" in _err() and msg in _err()
+
+
+def test_scaled_experts_need_a_scaled_shared_expert():
+    bf16 = binding.ExpertWeights(16, 0, 0x1000, 0x1000, 0x1000, *([None] * 6))
+    assert _swiglu(_ew(), shared=bf16) == BAD and "MOE_BITS_E4M3" in _err()
+    assert _swiglu(bf16, shared=_ew()) == BAD and "bits = 264" in _err()
+
+
+def test_scaled_experts_workspace_and_sizes():
+    L = binding.lib()
+    need = L.moe_grouped_swiglu_workspace_bytes(4, 256, 128, 16, 1, 1)
+    R = 4 * 1 + 4  # slots: the codes and fp32 scales of the rows and of h, 256-byte aligned
+    al = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    scaled = al(R * 256) + al(R * 2 * 4) + al(R * 128) + al(R * 4)
+    assert need >= scaled
+    assert _swiglu(_ew(), shared=_ew(), K=1, ws_bytes=scaled - 1) == BAD and "ws_bytes" in _err()
+    assert _swiglu(_ew(), E=1024, d=1 << 22, I=128, T=1, K=1) == BAD and "too large" in _err()
+    assert _swiglu(_ew(), d=200) == BAD and "d = 200" in _err()
+
+
+def test_forward_takes_the_grouped_gate_without_a_bias():
+    L = binding.lib()
+    a = binding.LayerArgs()
+    a.route_kind, a.x, a.T, a.d, a.I, a.E = binding.MOE_ROUTE_SOFTMAX_GROUPED, 0x1000, 4, 256, 128, 16
+    a.w_router, a.y = 0x1000, 0x1000
+    ew = _ew()
+    a.experts = ctypes.pointer(ew)
+    for K, G, tg, msg in ((9, 4, 2, "top_k = 9"), (2, 3, 1, "not divisible"), (2, 4, 0, "topk_group")):
+        a.params = binding.route_params(K, G, tg, True, 1.0)
+        assert L.moe_forward_ex(ctypes.byref(a), ctypes.c_void_p(0x10000), 1 << 30, None) == BAD
+        assert msg in _err()
+    a.params = binding.route_params(8, 4, 2, True, 1.0)
+    rc = L.moe_forward_ex(ctypes.byref(a), ctypes.c_void_p(0x10000), 64, None)
+    assert rc == BAD and "ws_bytes" in _err()
+
+
+def test_binding_checks_types_and_shapes():
+    x = torch.zeros(4, 256)
+    with pytest.raises(TypeError):
+        binding.quantize_blocks(x.half())
+    with pytest.raises(ValueError):
+        binding.quantize_blocks(x.t())
+    with pytest.raises(ValueError):
+        binding.quantize_blocks(x, codes=torch.zeros(4, 128).to(F8))
+    with pytest.raises(TypeError):
+        binding.quantize_blocks(x, scales=torch.zeros(4, 2, dtype=torch.bfloat16))
+    a, w = torch.zeros(4, 256).to(F8), torch.zeros(130, 256).to(F8)
+    sa, sw = torch.ones(4, 2), torch.ones(2, 2)
+    with pytest.raises(TypeError):
+        binding.matmul_blocks(x, sa, w, sw)
+    with pytest.raises(ValueError):
+        binding.matmul_blocks(a, sa[:, :1].contiguous(), w, sw)
+    with pytest.raises(ValueError):
+        binding.matmul_blocks(a, sa, w, sw[:1])
+    with pytest.raises(ValueError):
+        binding.matmul_blocks(a, sa, w[:, :128].contiguous(), sw)
+    with pytest.raises(TypeError):
+        binding.matmul_blocks(a, sa, w, sw, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        binding.route_softmax_grouped(x, 2, 4, 2, True, 1.0, bias=torch.zeros(4))
+    e = {"bits": binding.MOE_BITS_E4M3, "gate": torch.zeros(2, 128, 256).to(F8),
+         "up": torch.zeros(2, 128, 256).to(F8), "down": torch.zeros(2, 256, 128).to(F8),
+         "gate_s": torch.ones(2, 1, 2), "up_s": torch.ones(2, 1, 2), "down_s": torch.ones(2, 2, 1)}
+    assert binding.expert_weights(e).bits == binding.MOE_BITS_E4M3
+    with pytest.raises(ValueError):
+        binding.expert_weights({**e, "down_s": torch.ones(2, 1, 2)})
+    with pytest.raises(TypeError):
+        binding.expert_weights({**e, "up": torch.zeros(2, 128, 256)})
