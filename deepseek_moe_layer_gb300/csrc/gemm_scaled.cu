@@ -17,9 +17,9 @@
 // (two per instruction) while the tensor core fills the other.  A row is one thread's, so the
 // row scale is a register and the weight scale is uniform over a warp's 128 columns.
 //
-// Warp roles (320 threads, one CTA per SM, persistent over tiles): warp 0 TMA producer,
-// warp 1 TMEM owner and UMMA issuer, warps 2..9 scaling and epilogue (warp % 4 = TMEM lane
-// quarter, (warp - 2) / 4 = column half).  Every wait is bounded, as in the expert GEMMs.
+// Warp roles (384 threads, one CTA per SM, persistent over tiles): warp 0 TMA producer,
+// warp 1 TMEM owner and UMMA issuer, warps 4..11 scaling and epilogue (warp % 4 = TMEM lane
+// quarter, (warp - 4) / 4 = column half; warps 2 and 3 only lend their registers).  Every wait is bounded, as in the expert GEMMs.
 #include <mutex>
 
 #include "launch.h"
@@ -33,8 +33,9 @@ namespace {
 
 enum { kLinear = 0, kSwiglu = 1 };
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
+constexpr int kEpiWarp0 = 4;  // first of them: two whole warpgroups
 constexpr int kBK = 128;                        // codes per 128-byte swizzled row = one k-block
 constexpr int kABytes = 128 * kBK;
 constexpr int kBBytes = 256 * kBK;
@@ -110,6 +111,15 @@ MOE_DEV unsigned long long both(float f) {
     unsigned long long r;
     asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(f));
     return r;
+}
+MOE_DEV unsigned long long pair_of(float lo, float hi) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+// An infinity has no e4m3 code: it becomes NaN, and leaves the block's scale to the others.
+MOE_DEV float nan_for_inf(float v) {
+    return fabsf(v) == __int_as_float(0x7F800000) ? __int_as_float(0x7FFFFFFF) : v;
 }
 MOE_DEV float lo_of(unsigned long long v) { return __uint_as_float((uint32_t)v); }
 MOE_DEV float hi_of(unsigned long long v) { return __uint_as_float((uint32_t)(v >> 32)); }
@@ -230,6 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const int total = prefix[ngroups];
 
+    // 384 threads at 168 registers: the scaling warps' 128 sums take from the other four warps
+    // (56 * 128 + 224 * 256 = 168 * 384)
+    if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
         // =============================== TMA producer ===============================
         if (lane == 0) {
@@ -303,9 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(done, 0u, nullptr, 100000000ull);
             }
         }
+    }
     } else {
         // ============================ scaling and epilogue ==========================
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
         const int r = q * 32 + lane;  // the thread's row of the tile
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
         // the warp's four chunks of 32 columns
@@ -367,17 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (MODE == kSwiglu) {
                 // h over the gate and up sums in place, the row's maximum with the other half
                 float m = 0.0f;
-                float h[64];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    h[2 * i] = silu(lo_of(acc[i])) * lo_of(acc[32 + i]);
-                    h[2 * i + 1] = silu(hi_of(acc[i])) * hi_of(acc[32 + i]);
-                }
-                const float inf = __int_as_float(0x7F800000);
-#pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    if (fabsf(h[i]) == inf) h[i] = __int_as_float(0x7FFFFFFF);
-                    m = fmaxf(m, fabsf(h[i]));
+                    const float h0 = nan_for_inf(silu(lo_of(acc[i])) * lo_of(acc[32 + i]));
+                    const float h1 = nan_for_inf(silu(hi_of(acc[i])) * hi_of(acc[32 + i]));
+                    m = fmaxf(m, fmaxf(fabsf(h0), fabsf(h1)));
+                    acc[i] = pair_of(h0, h1);
                 }
                 float* am = amax + (lt & 1) * 256;
                 am[half * 128 + r] = m;
@@ -398,8 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float* x = h + 16 * i + 4 * j;
-                            w[j] = cvt_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                            const unsigned long long a = acc[8 * i + 2 * j], b = acc[8 * i + 2 * j + 1];
+                            w[j] = cvt_e4m3x4(lo_of(a) * inv, hi_of(a) * inv, lo_of(b) * inv,
+                                              hi_of(b) * inv);
                         }
                         *reinterpret_cast<uint4*>(o + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
