@@ -209,7 +209,7 @@ int check_scaled_dims(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K) {
     const int64_t wide = d > I ? d : I;
     MOE_CHECK(E * wide < ((int64_t)1 << 31) &&
                   (T * (K + 1) / 128 + E + 1) * (wide / 128) < ((int64_t)1 << 31) &&
-                  T * (K + 1) * (d / 128) < ((int64_t)1 << 36),
+                  T * (K + 1) * (d / 128) < ((int64_t)1 << 31),
               "T = %lld, E = %d, d = %d, I = %d: too large for e4m3 experts", (long long)T, E, d, I);
     return MOE_OK;
 }

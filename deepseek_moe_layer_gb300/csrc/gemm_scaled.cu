@@ -12,14 +12,16 @@
 // from the offsets on the device.
 //
 // The scales vary along K, so the sum cannot stay in TMEM: every 128-wide k-block is one
-// UMMA group (128 x 256 x 128, four K = 32 steps) into one of two TMEM buffers, and eight
+// UMMA group (128 x 256 x 128, four K = 32 steps) into one of two TMEM buffers, and sixteen
 // warps fold the finished buffer into fp32 sums in registers with one multiply-add per element
 // (two per instruction) while the tensor core fills the other.  A row is one thread's, so the
-// row scale is a register and the weight scale is uniform over a warp's 128 columns.
+// row scale is a register and the weight scale is uniform over a warp's columns.
 //
 // Warp roles (384 threads, one CTA per SM, persistent over tiles): warp 0 TMA producer,
-// warp 1 TMEM owner and UMMA issuer, warps 4..11 scaling and epilogue (warp % 4 = TMEM lane
-// quarter, (warp - 4) / 4 = column half; warps 2 and 3 only lend their registers).  Every wait is bounded, as in the expert GEMMs.
+// warp 1 TMEM owner and UMMA issuer, warps 4..19 scaling and epilogue (warp % 4 = TMEM lane
+// quarter, (warp - 4) / 4 = quarter of the columns; warps 2 and 3 only lend their registers).
+// Sixteen warps of 64 sums rather than eight of 128: four per scheduler hide each other's TMEM
+// and barrier latency, and the sums stay in registers.  Every wait is bounded, as in the expert GEMMs.
 #include <mutex>
 
 #include "launch.h"
@@ -33,9 +35,10 @@ namespace {
 
 enum { kLinear = 0, kSwiglu = 1 };
 
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
-constexpr int kEpiWarp0 = 4;  // first of them: two whole warpgroups
+constexpr int kThreads = 640;
+constexpr int kEpiWarps = 16;
+constexpr int kEpiWarp0 = 4;  // first of them: four whole warpgroups
+constexpr int kParts = 4;     // warps per TMEM lane quarter, each a quarter of the columns
 constexpr int kBK = 128;                        // codes per 128-byte swizzled row = one k-block
 constexpr int kABytes = 128 * kBK;
 constexpr int kBBytes = 256 * kBK;
@@ -48,7 +51,9 @@ constexpr int kMiscOff = kBarOff + 8 * kNumBars;
 constexpr int kPrefixOff = (kMiscOff + 16 + 15) / 16 * 16;
 constexpr int kRowOffOff = kPrefixOff + 4 * (kMaxGroups + 1);
 constexpr int kAmaxOff = (kRowOffOff + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
-constexpr int kSmemBytes = kAmaxOff + 4 * 2 * 2 * 128 + 1024;  // + alignment of the stages
+constexpr int kRagOff = kAmaxOff + 4 * 2 * kParts * 128;
+constexpr int kRagLd = 9;  // floats per row of a warp's 32 x 8 piece: no bank conflicts by row
+constexpr int kSmemBytes = kRagOff + 4 * kEpiWarps * 32 * kRagLd + 1024;  // + stage alignment
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
 // kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), e4m3 A and B (formats 0), both K-major,
@@ -71,7 +76,7 @@ struct Params {
     void* out;               // kLinear: bf16 or fp32 [rows, ld]; kSwiglu: codes [rows, F]
     long long ld;
     int f32;                 // kLinear: fp32 out
-    int vec;                 // kLinear: 16-byte stores allowed
+    int vec;                 // kLinear: rows of `out` are 32-byte aligned
     float* out_scale;        // kSwiglu: [rows, F / 128]
 };
 
@@ -86,17 +91,14 @@ MOE_DEV void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32
 
 // Waits for this thread's TMEM loads; the registers pass through it so that no use of them
 // moves ahead of the wait.
-MOE_DEV void tmem_wait32(uint32_t (&r)[32]) {
+MOE_DEV void tmem_wait16(uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.wait::ld.sync.aligned;"
         : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
           "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-          "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
-          "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-          "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+          "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
         :
         : "memory");
-    asm volatile("" : "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
 // acc (two fp32) += (lo, hi) * f, both lanes of f the same factor.
@@ -124,9 +126,18 @@ MOE_DEV float nan_for_inf(float v) {
 MOE_DEV float lo_of(unsigned long long v) { return __uint_as_float((uint32_t)v); }
 MOE_DEV float hi_of(unsigned long long v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
-MOE_DEV void fold32(unsigned long long* acc, const uint32_t (&r)[32], unsigned long long f) {
+// acc (16 sums) += 16 TMEM columns of the thread's lane * f.
+MOE_DEV void fold16(unsigned long long* acc, const uint32_t (&r)[16], float f) {
+    const unsigned long long ff = both(f);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) fma_pair(acc[i], r[2 * i], r[2 * i + 1], f);
+    for (int i = 0; i < 8; ++i) fma_pair(acc[i], r[2 * i], r[2 * i + 1], ff);
+}
+
+// One 32-byte store (a whole sector).
+MOE_DEV void st_global_32B(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 MOE_DEV void record_timeout(volatile int* abort) {
@@ -182,12 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* done = tempty + 2;
-    uint64_t* pair = done + 1;  // kSwiglu: the two warps of a lane quarter exchange row maxima
+    uint64_t* pair = done + 1;  // kSwiglu: the warps of a lane quarter exchange row maxima
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
     int32_t* prefix = reinterpret_cast<int32_t*>(smem + kPrefixOff);
     int32_t* rowoff = reinterpret_cast<int32_t*>(smem + kRowOffOff);
-    float* amax = reinterpret_cast<float*>(smem + kAmaxOff);  // [tile parity][half][row]
+    float* rag = reinterpret_cast<float*>(smem + kRagOff);
+    float* amax = reinterpret_cast<float*>(smem + kAmaxOff);  // [tile parity][part][row]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ngroups = p.offsets ? p.E + p.has_shared : 1;
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&tempty[b], kEpiWarps);
         }
         mbar_init(done, 1);
-        for (int q = 0; q < 4; ++q) mbar_init(&pair[q], 2);
+        for (int q = 0; q < 4; ++q) mbar_init(&pair[q], kParts);
         *abort = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_x);
@@ -240,10 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const int total = prefix[ngroups];
 
-    // 384 threads at 168 registers: the scaling warps' 128 sums take from the other four warps
-    // (56 * 128 + 224 * 256 = 168 * 384)
+    // 640 threads at 96 registers: the scaling warps take from the other four
+    // (64 * 128 + 104 * 512 = 96 * 640)
     if (warp < kEpiWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
         // =============================== TMA producer ===============================
         if (lane == 0) {
@@ -320,13 +332,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     } else {
         // ============================ scaling and epilogue ==========================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int q = warp & 3, part = (warp - kEpiWarp0) >> 2;
         const int r = q * 32 + lane;  // the thread's row of the tile
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
-        // the warp's four chunks of 32 columns
-        const int c0 = MODE == kSwiglu ? 64 * half : 128 * half;
-        const int c2 = MODE == kSwiglu ? 128 + 64 * half : 128 * half + 64;
+        // the warp's two chunks of 32 columns: 32 gate and 32 up, or 64 in a row
+        const int c0 = MODE == kSwiglu ? 32 * part : 64 * part;
+        const int c1 = MODE == kSwiglu ? 128 + 32 * part : 64 * part + 32;
         const int wblocks = (p.F + 127) / 128;
         int it = 0, lt = 0;
         bool ok = true;
@@ -336,19 +348,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool idle = q * 32 >= ti.rows;  // no row of this warp is in the tile
             const float* sx = p.sx + (ti.row + (mine ? r : 0)) * p.nkb;
             const long long wb = (long long)(ti.shared || !p.offsets ? 0 : ti.g) * wblocks +
-                                 (MODE == kSwiglu ? ti.f : min(2 * ti.f + half, wblocks - 1));
+                                 (MODE == kSwiglu ? ti.f : min(2 * ti.f + part / 2, wblocks - 1));
             const float* sw0 = (ti.shared ? p.ssw0 : p.sw0) + wb * p.nkb;
             const float* sw1 = MODE == kSwiglu ? (ti.shared ? p.ssw1 : p.sw1) + wb * p.nkb : sw0;
-            unsigned long long acc[64];
+            unsigned long long acc[32];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-            float x_next = sx[0], w0_next = sw0[0], w1_next = sw1[0];
+            for (int i = 0; i < 32; ++i) acc[i] = 0ull;
+            float x_next = sx[0], w0_next = sw0[0], w1_next = MODE == kSwiglu ? sw1[0] : 0.0f;
             for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                const unsigned long long f0 = both(x_next * w0_next), f1 = both(x_next * w1_next);
+                const float f0 = x_next * w0_next, f1 = MODE == kSwiglu ? x_next * w1_next : f0;
                 if (kb + 1 < p.nkb) {
                     x_next = sx[kb + 1];
                     w0_next = sw0[kb + 1];
-                    w1_next = sw1[kb + 1];
+                    if (MODE == kSwiglu) w1_next = sw1[kb + 1];
                 }
                 const int b = it & 1;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[b], ((uint32_t)it >> 1) & 1u, abort))) {
@@ -359,95 +371,111 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!idle) {
                     tc_fence_after();
                     const uint32_t col = taddr + (uint32_t)(b * 256);
-                    uint32_t u[32], v[32];
-                    tmem_ld32(col + (uint32_t)c0, u);
-                    tmem_wait32(u);
-                    tmem_ld32(col + (uint32_t)(c0 + 32), v);
-                    fold32(acc, u, f0);
-                    tmem_wait32(v);
-                    tmem_ld32(col + (uint32_t)c2, u);
-                    fold32(acc + 16, v, f0);
-                    tmem_wait32(u);
-                    tmem_ld32(col + (uint32_t)(c2 + 32), v);
-                    fold32(acc + 32, u, MODE == kSwiglu ? f1 : f0);
-                    tmem_wait32(v);
+                    uint32_t u[16], v[16];
+                    tmem_ld16(col + (uint32_t)c0, u);
+                    tmem_wait16(u);
+                    tmem_ld16(col + (uint32_t)c0 + 16u, v);
+                    fold16(acc, u, f0);
+                    tmem_wait16(v);
+                    tmem_ld16(col + (uint32_t)c1, u);
+                    fold16(acc + 8, v, f0);
+                    tmem_wait16(u);
+                    tmem_ld16(col + (uint32_t)c1 + 16u, v);
+                    fold16(acc + 16, u, f1);
+                    tmem_wait16(v);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&tempty[b]);
-                    fold32(acc + 48, v, MODE == kSwiglu ? f1 : f0);
+                    fold16(acc + 24, v, f1);
                 } else if (lane == 0) {
                     mbar_arrive(&tempty[b]);
                 }
             }
             if (!ok) break;
             if constexpr (MODE == kSwiglu) {
-                // h over the gate and up sums in place, the row's maximum with the other half
+                // h over the gate sums' registers, the row's maximum with the other parts
                 float m = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float h0 = nan_for_inf(silu(lo_of(acc[i])) * lo_of(acc[32 + i]));
-                    const float h1 = nan_for_inf(silu(hi_of(acc[i])) * hi_of(acc[32 + i]));
+                for (int i = 0; i < 16; ++i) {
+                    const float h0 = nan_for_inf(silu(lo_of(acc[i])) * lo_of(acc[16 + i]));
+                    const float h1 = nan_for_inf(silu(hi_of(acc[i])) * hi_of(acc[16 + i]));
                     m = fmaxf(m, fmaxf(fabsf(h0), fabsf(h1)));
                     acc[i] = pair_of(h0, h1);
                 }
-                float* am = amax + (lt & 1) * 256;
-                am[half * 128 + r] = m;
+                float* am = amax + (lt & 1) * (kParts * 128) + r;
+                am[part * 128] = m;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pair[q]);
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&pair[q], (uint32_t)lt & 1u, abort))) {
                     record_timeout(abort);
                     break;
                 }
-                m = fmaxf(m, am[(half ^ 1) * 128 + r]);
+#pragma unroll
+                for (int o = 0; o < kParts; ++o) m = fmaxf(m, am[o * 128]);
                 float s, inv;
                 block_scale(m, s, inv);
                 if (mine) {
-                    uint8_t* o = static_cast<uint8_t*>(p.out) + (ti.row + r) * p.F + ti.f * 128 +
-                                 64 * half;
+                    uint32_t w[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const unsigned long long a = acc[8 * i + 2 * j], b = acc[8 * i + 2 * j + 1];
-                            w[j] = cvt_e4m3x4(lo_of(a) * inv, hi_of(a) * inv, lo_of(b) * inv,
-                                              hi_of(b) * inv);
-                        }
-                        *reinterpret_cast<uint4*>(o + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                    if (half == 0) p.out_scale[(ti.row + r) * (p.F / 128) + ti.f] = s;
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = cvt_e4m3x4(lo_of(acc[2 * j]) * inv, hi_of(acc[2 * j]) * inv,
+                                          lo_of(acc[2 * j + 1]) * inv, hi_of(acc[2 * j + 1]) * inv);
+                    st_global_32B(static_cast<uint8_t*>(p.out) + (ti.row + r) * p.F + ti.f * 128 +
+                                      32 * part,
+                                  w);
+                    if (part == 0) p.out_scale[(ti.row + r) * (p.F / 128) + ti.f] = s;
                 }
-            } else if (mine) {
-                const int n0 = ti.f * 256 + 128 * half;
-                if (p.f32) {
-                    float* o = static_cast<float*>(p.out) + (ti.row + r) * p.ld + n0;
+            } else {
+                const int n0 = ti.f * 256 + 64 * part;
+                if (p.vec && n0 + 64 <= p.F) {
+                    if (mine && p.f32) {
+                        float* o = static_cast<float*>(p.out) + (ti.row + r) * p.ld + n0;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float x[4] = {lo_of(acc[2 * i]), hi_of(acc[2 * i]),
-                                            lo_of(acc[2 * i + 1]), hi_of(acc[2 * i + 1])};
-                        if (p.vec && n0 + 4 * i + 4 <= p.F) {
-                            *reinterpret_cast<float4*>(o + 4 * i) = make_float4(x[0], x[1], x[2], x[3]);
-                        } else {
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t w[8];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (n0 + 4 * i + j < p.F) o[4 * i + j] = x[j];
+                            for (int j = 0; j < 4; ++j) {
+                                w[2 * j] = __float_as_uint(lo_of(acc[4 * i + j]));
+                                w[2 * j + 1] = __float_as_uint(hi_of(acc[4 * i + j]));
+                            }
+                            st_global_32B(o + 8 * i, w);
                         }
-                    }
-                } else {
-                    uint16_t* o = static_cast<uint16_t*>(p.out) + (ti.row + r) * p.ld + n0;
+                    } else if (mine) {
+                        uint16_t* o = static_cast<uint16_t*>(p.out) + (ti.row + r) * p.ld + n0;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = pack_bf16x2(lo_of(acc[4 * i + j]), hi_of(acc[4 * i + j]));
-                        if (p.vec && n0 + 8 * i + 8 <= p.F) {
-                            *reinterpret_cast<uint4*>(o + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-                        } else {
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                if (n0 + 8 * i + j < p.F)
-                                    o[8 * i + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+                                w[j] = pack_bf16x2(lo_of(acc[8 * i + j]), hi_of(acc[8 * i + j]));
+                            st_global_32B(o + 16 * i, w);
+                        }
+                    }
+                } else if (!idle) {
+                    // rows without 32-byte alignment, or the last columns: eight columns at a
+                    // time through shared memory, so that a store covers eight columns of four
+                    // rows instead of one of 32
+                    float* piece = rag + (warp - kEpiWarp0) * (32 * kRagLd);
+                    const int pr = lane >> 3, pc = lane & 7;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            piece[lane * kRagLd + 2 * j] = lo_of(acc[4 * i + j]);
+                            piece[lane * kRagLd + 2 * j + 1] = hi_of(acc[4 * i + j]);
+                        }
+                        __syncwarp();
+                        const int n = n0 + 8 * i + pc;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int rr = 4 * k + pr;
+                            if (q * 32 + rr < ti.rows && n < p.F) {
+                                const long long at = (ti.row + q * 32 + rr) * p.ld + n;
+                                const float v = piece[rr * kRagLd + pc];
+                                if (p.f32) static_cast<float*>(p.out)[at] = v;
+                                else static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
+                            }
                         }
                     }
                 }
@@ -539,7 +567,7 @@ cudaError_t run(const ScaledGemmArgs& a, cudaStream_t s) {
     p.out = a.out;
     p.ld = a.F;
     p.f32 = a.f32;
-    p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.F % (a.f32 ? 4 : 8) == 0;
+    p.vec = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.F % (a.f32 ? 8 : 16) == 0;
     p.out_scale = a.out_scale;
 
     // at most this many tiles (the offsets are on the device): a group adds one ragged tile

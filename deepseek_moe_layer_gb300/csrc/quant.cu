@@ -63,7 +63,8 @@ MOE_DEV void inf_to_nan(float (&v)[8]) {
 // alone), and row P + t (shared rows) is row t.
 struct QuantRows {
     const void* x;
-    long long rows;      // output rows
+    unsigned units;      // half warps with work: rows * ceil(nb / kPer)
+    unsigned upr;        // of them per row
     long long ld;        // elements between rows of x
     int n, nb;           // columns (a multiple of 16), blocks of 128 per row
     uint8_t* codes;      // [rows, n]
@@ -79,32 +80,30 @@ constexpr int kPer = 4;
 template <bool BF16, bool GATHER>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantRows a) {
     const int lane = threadIdx.x & 15;
-    const long long total = a.rows * a.nb;
-    const long long b0 = ((long long)blockIdx.x * 16 + (threadIdx.x >> 4)) * kPer;
+    const unsigned unit = blockIdx.x * 16u + (threadIdx.x >> 4);
+    const unsigned r = unit / a.upr;
+    const int b0 = (int)(unit - r * a.upr) * kPer;
+    const long long row = r;
+    bool on = unit < a.units;
     pdl_launch_dependents();
     pdl_wait();  // the dispatch (GATHER) or x come from the kernels before
+    long long src = row;
+    if (GATHER && on) {
+        if (src >= a.P) src -= a.P;
+        else if (src < *a.dispatched) src = a.perm[src] / a.K;
+        else on = false;
+    }
     float v[kPer][8];
-    long long row[kPer];
-    int col[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-        const long long b = b0 + u;
-        row[u] = b / a.nb;
-        col[u] = (int)(b - row[u] * a.nb) * 128 + lane * 8;
-        long long src = row[u];
-        bool on = b < total;
-        if (GATHER && on) {
-            if (src >= a.P) src -= a.P;
-            else if (src < *a.dispatched) src = a.perm[src] / a.K;
-            else on = false;
-        }
-        if (!on) row[u] = -1;
+        const int col = (b0 + u) * 128 + lane * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
-        if (on && col[u] < a.n) load8<BF16>(a.x, src * a.ld + col[u], v[u]);
+        if (on && col < a.n) load8<BF16>(a.x, src * a.ld + col, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
+        const int col = (b0 + u) * 128 + lane * 8;
         float m = amax8(v[u]);
 #pragma unroll
         for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
@@ -116,10 +115,9 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantRows a) {
         }
         float s, inv;
         block_scale(m, s, inv);
-        if (row[u] < 0) continue;
-        if (col[u] < a.n)
-            *reinterpret_cast<uint2*>(a.codes + row[u] * a.n + col[u]) = codes8(v[u], inv);
-        if (lane == 0) a.scales[row[u] * a.nb + (col[u] >> 7)] = s;
+        if (on && col < a.n)
+            *reinterpret_cast<uint2*>(a.codes + row * a.n + col) = codes8(v[u], inv);
+        if (on && lane == 0 && b0 + u < a.nb) a.scales[row * a.nb + b0 + u] = s;
     }
 }
 
@@ -171,20 +169,26 @@ __global__ void __launch_bounds__(256) quant_square_kernel(const void* x, long l
     if (threadIdx.x == 0) scales[br * nb + bc] = s;
 }
 
+QuantRows quant_rows(const void* x, long long rows, long long ld, int n, uint8_t* codes,
+                     float* scales) {
+    QuantRows a = {};
+    a.x = x;
+    a.nb = (n + 127) / 128;
+    a.upr = (unsigned)((a.nb + kPer - 1) / kPer);
+    a.units = (unsigned)(rows * a.upr);  // fewer than 2^31 blocks: checked by the caller
+    a.ld = ld;
+    a.n = n;
+    a.codes = codes;
+    a.scales = scales;
+    return a;
+}
+
 }  // namespace
 
 cudaError_t launch_quantize_rows(const void* x, int bf16, long long rows, int n, long long ld,
                                  uint8_t* codes, float* scales, cudaStream_t s) {
-    QuantRows a = {};
-    a.x = x;
-    a.rows = rows;
-    a.ld = ld;
-    a.n = n;
-    a.nb = (n + 127) / 128;
-    a.codes = codes;
-    a.scales = scales;
-    const long long per = 16 * kPer;
-    const unsigned grid = (unsigned)((rows * a.nb + per - 1) / per);
+    const QuantRows a = quant_rows(x, rows, ld, n, codes, scales);
+    const unsigned grid = (a.units + 15) / 16;
     return bf16 ? launch_kernel(quant_rows_kernel<true, false>, dim3(grid), dim3(256), 0, s, a)
                 : launch_kernel(quant_rows_kernel<false, false>, dim3(grid), dim3(256), 0, s, a);
 }
@@ -202,20 +206,12 @@ cudaError_t launch_quantize_square(const void* x, int bf16, long long rows, int 
 cudaError_t launch_quantize_dispatched(const void* x, const int32_t* perm, const int32_t* offsets,
                                        int E, int K, long long P, long long shared_rows, int d,
                                        uint8_t* codes, float* scales, cudaStream_t s) {
-    QuantRows a = {};
-    a.x = x;
-    a.rows = P + shared_rows;
-    a.ld = d;
-    a.n = d;
-    a.nb = (d + 127) / 128;
-    a.codes = codes;
-    a.scales = scales;
+    QuantRows a = quant_rows(x, P + shared_rows, d, d, codes, scales);
     a.perm = perm;
     a.dispatched = offsets + E;
     a.P = P;
     a.K = K;
-    const long long per = 16 * kPer;
-    const unsigned grid = (unsigned)((a.rows * a.nb + per - 1) / per);
+    const unsigned grid = (a.units + 15) / 16;
     return launch_kernel(quant_rows_kernel<true, true>, dim3(grid), dim3(256), 0, s, a);
 }
 
