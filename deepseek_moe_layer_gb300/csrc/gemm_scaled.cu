@@ -8,20 +8,28 @@
 //
 // Groups and tiles follow the expert GEMMs: E routed groups (rows offsets[g] .. offsets[g+1])
 // and optionally the shared expert as group E, or a single group; a tile is 128 token rows x
-// 256 weight rows (kSwiglu: 128 gate rows and the same 128 up rows), tokens fastest, derived
-// from the offsets on the device.
+// two halves of 128 weight rows (kSwiglu: 128 gate rows and the same up rows), tokens fastest,
+// derived from the offsets on the device.
 //
-// The scales vary along K, so the sum cannot stay in TMEM: every 128-wide k-block is one
-// UMMA group (128 x 256 x 128, four K = 32 steps) into one of two TMEM buffers, and sixteen
-// warps fold the finished buffer into fp32 sums in registers with one multiply-add per element
-// (two per instruction) while the tensor core fills the other.  A row is one thread's, so the
-// row scale is a register and the weight scale is uniform over a warp's columns.
+// The scales vary along K, so the sum cannot stay in TMEM: a k-block of 128 is one group of
+// UMMAs (128 x 256 x 128, four K = 32 steps) into one of two TMEM buffers, and eight warps fold
+// the finished buffer into fp32 sums in registers, one multiply-add per element (two per
+// instruction), while the tensor core fills the other.  A row is one thread's, so the row scale
+// times the weight scale is one factor per thread, half and k-block.
 //
-// Warp roles (384 threads, one CTA per SM, persistent over tiles): warp 0 TMA producer,
-// warp 1 TMEM owner and UMMA issuer, warps 4..19 scaling and epilogue (warp % 4 = TMEM lane
-// quarter, (warp - 4) / 4 = quarter of the columns; warps 2 and 3 only lend their registers).
-// Sixteen warps of 64 sums rather than eight of 128: four per scheduler hide each other's TMEM
-// and barrier latency, and the sums stay in registers.  Every wait is bounded, as in the expert GEMMs.
+// What bounds a long product is the way round a buffer: UMMA issue, completion, TMEM loads and
+// multiply-adds, the buffer's release (470, 500, 450 and 190 cycles by the clock, against the
+// UMMAs' own 512): 8192 x 4096 x 7168 takes 210 us, 170 with the scaling left out, 107 for the
+// UMMAs alone.  Tried and slower there: sixteen warps of 64 columns (242 us), halves of 128
+// columns with barriers, issuers or warps of their own (261 .. 277), an issuer per buffer (225),
+// looking at the next k-block's barriers between UMMAs (223), CTA pairs with cta_group::2 (513:
+// the way round crosses the cluster twice).
+//
+// Warp roles (384 threads, one CTA per SM, persistent over tiles): warp 0 TMA producer, warp 1
+// TMEM owner and UMMA issuer, warps 2 and 3 multiply the scales ahead of the others, warps 4..11
+// scaling and epilogue: warp % 4 = TMEM lane quarter, (warp - 4) / 4 = part, the first or last 64
+// columns of each half (kSwiglu: of the gate and of the up rows, so silu(g) * u stays in the
+// thread).  Every wait is bounded, as in the expert GEMMs.
 #include <mutex>
 
 #include "launch.h"
@@ -35,29 +43,37 @@ namespace {
 
 enum { kLinear = 0, kSwiglu = 1 };
 
-constexpr int kThreads = 640;
-constexpr int kEpiWarps = 16;
-constexpr int kEpiWarp0 = 4;  // first of them: four whole warpgroups
-constexpr int kParts = 4;     // warps per TMEM lane quarter, each a quarter of the columns
-constexpr int kBK = 128;                        // codes per 128-byte swizzled row = one k-block
-constexpr int kABytes = 128 * kBK;
-constexpr int kBBytes = 256 * kBK;
-constexpr int kStageBytes = kABytes + kBBytes;  // 48 KB
-constexpr int kStages = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kEpiWarp0 = 4;                   // first of them: whole warpgroups
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kCols = 128;                     // columns (sums) of a warp, 64 of each half
+constexpr int kLowRegs = 56, kHighRegs = 224;  // 56 * 128 + 224 * 256 = 168 * 384
+constexpr int kBK = 128;                       // codes per 128-byte swizzled row = one k-block
 constexpr int kMaxGroups = 1025;
+constexpr int kFKb = 4;                        // k-blocks of factors per slot
+constexpr int kFSlots = 2;                     // a power of two
+constexpr int kFacFloats = kFKb * 2 * 128;     // [k-block][half][row]
+constexpr int kRagLd = 5;  // floats per row of a warp's 32 x 4 piece: no bank conflicts by row
+
+constexpr int kABytes = 128 * kBK;
+constexpr int kBBytes = 128 * kBK;             // per half
+constexpr int kStageBytes = kABytes + 2 * kBBytes;
+constexpr int kStages = 4;
 constexpr int kBarOff = kStages * kStageBytes;
-constexpr int kNumBars = 2 * kStages + 2 + 2 + 1 + 4;  // full, empty, tfull, tempty, done, pair
+// full, empty, tfull, tempty, done, row maxima, ffull, fempty
+constexpr int kNumBars = 2 * kStages + 2 + 2 + 1 + 4 + 2 * kFSlots;
 constexpr int kMiscOff = kBarOff + 8 * kNumBars;
 constexpr int kPrefixOff = (kMiscOff + 16 + 15) / 16 * 16;
 constexpr int kRowOffOff = kPrefixOff + 4 * (kMaxGroups + 1);
-constexpr int kAmaxOff = (kRowOffOff + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
-constexpr int kRagOff = kAmaxOff + 4 * 2 * kParts * 128;
-constexpr int kRagLd = 9;  // floats per row of a warp's 32 x 8 piece: no bank conflicts by row
-constexpr int kSmemBytes = kRagOff + 4 * kEpiWarps * 32 * kRagLd + 1024;  // + stage alignment
+constexpr int kFacOff = (kRowOffOff + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
+constexpr int kEpiOff = kFacOff + 4 * kFSlots * kFacFloats;
+constexpr int kEpiBytes = 4 * kEpiWarps * 32 * kRagLd;  // kLinear: pieces; kSwiglu: row maxima
+constexpr int kSmemBytes = kEpiOff + kEpiBytes + 1024;  // + alignment of the stages
+static_assert(kEpiBytes >= 4 * 2 * 2 * 128, "room for the row maxima");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
 // kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), e4m3 A and B (formats 0), both K-major,
-// N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+// N >> 3 at bits 17-22 (256), M >> 4 at bits 24-28 (128).
 constexpr uint32_t kIdesc = (1u << 4) | ((256u >> 3) << 17) | ((128u >> 4) << 24);
 
 struct Params {
@@ -89,48 +105,20 @@ MOE_DEV void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32
         : "memory");
 }
 
-// Waits for this thread's TMEM loads; the registers pass through it so that no use of them
-// moves ahead of the wait.
-MOE_DEV void tmem_wait16(uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.wait::ld.sync.aligned;"
-        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-          "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-          "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-        :
-        : "memory");
-}
-
-// acc (two fp32) += (lo, hi) * f, both lanes of f the same factor.
-MOE_DEV void fma_pair(unsigned long long& acc, uint32_t lo, uint32_t hi, unsigned long long f) {
-    asm("{\n\t.reg .b64 t;\n\t"
-        "mov.b64 t, {%1, %2};\n\t"
-        "fma.rn.f32x2 %0, t, %3, %0;\n\t}"
-        : "+l"(acc)
-        : "r"(lo), "r"(hi), "l"(f));
-}
-MOE_DEV unsigned long long both(float f) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(f));
-    return r;
-}
-MOE_DEV unsigned long long pair_of(float lo, float hi) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
 // An infinity has no e4m3 code: it becomes NaN, and leaves the block's scale to the others.
 MOE_DEV float nan_for_inf(float v) {
     return fabsf(v) == __int_as_float(0x7F800000) ? __int_as_float(0x7FFFFFFF) : v;
 }
-MOE_DEV float lo_of(unsigned long long v) { return __uint_as_float((uint32_t)v); }
-MOE_DEV float hi_of(unsigned long long v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // acc (16 sums) += 16 TMEM columns of the thread's lane * f.
-MOE_DEV void fold16(unsigned long long* acc, const uint32_t (&r)[16], float f) {
-    const unsigned long long ff = both(f);
+MOE_DEV void fold16(float* acc, const uint32_t (&r)[16], float f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) fma_pair(acc[i], r[2 * i], r[2 * i + 1], ff);
+    for (int i = 0; i < 16; i += 2) {
+        const float2 v = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                    make_float2(f, f), make_float2(acc[i], acc[i + 1]));
+        acc[i] = v.x;
+        acc[i + 1] = v.y;
+    }
 }
 
 // One 32-byte store (a whole sector).
@@ -138,6 +126,56 @@ MOE_DEV void st_global_32B(void* p, const uint32_t (&w)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
+}
+
+// What the scaling warps wait on and free: the two buffers in TMEM and the factor slots, with the
+// k-blocks and the slots taken so far.
+struct Rings {
+    uint64_t *tfull, *tempty, *ffull, *fempty;
+    uint32_t it, fn;
+};
+
+// One tile's sums of a warp: for every k-block its 64 columns of each half times the factor of
+// the thread's row (f: the first half's in slot 0) are added to acc.  LIVE false (no row of the
+// warp is in the tile): only the waiting.  False when a wait gave up (then in every lane).
+template <bool LIVE>
+MOE_DEV bool sums(float (&acc)[kCols], int nkb, Rings& rg, const float* f, uint32_t taddr,
+                  volatile int* abort) {
+    const int lane = threadIdx.x & 31;
+    int fi = 0;
+#pragma unroll 1
+    for (int kb = 0; kb < nkb; ++kb, ++rg.it) {
+        const uint32_t b = rg.it & 1u, s = rg.fn & (kFSlots - 1);
+        if (fi == 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&rg.ffull[s], (rg.fn / kFSlots) & 1u, abort)))
+            return false;
+        const float* g = f + s * kFacFloats + fi * 256;
+        const float f0 = g[0], f1 = g[128];
+        if (++fi == kFKb || kb == nkb - 1) {
+            fi = 0;
+            ++rg.fn;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rg.fempty[s]);
+        }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&rg.tfull[b], (rg.it >> 1) & 1u, abort))) return false;
+        if (LIVE) {
+            tc_fence_after();
+            uint32_t u[16];
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) {
+                tmem_ld16(taddr + b * 256u + (uint32_t)(c < 64 ? c : c + 64), u);
+                tmem_ld_wait();
+                if (c == kCols - 16) {  // the last load: the buffer is free before the last sums
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&rg.tempty[b]);
+                }
+                fold16(acc + c, u, c < 64 ? f0 : f1);
+            }
+        } else if (lane == 0) {
+            mbar_arrive(&rg.tempty[b]);
+        }
+    }
+    return true;
 }
 
 MOE_DEV void record_timeout(volatile int* abort) {
@@ -198,8 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
     int32_t* prefix = reinterpret_cast<int32_t*>(smem + kPrefixOff);
     int32_t* rowoff = reinterpret_cast<int32_t*>(smem + kRowOffOff);
-    float* rag = reinterpret_cast<float*>(smem + kRagOff);
-    float* amax = reinterpret_cast<float*>(smem + kAmaxOff);  // [tile parity][part][row]
+    uint64_t* ffull = pair + 4;
+    uint64_t* fempty = ffull + kFSlots;
+    float* fac = reinterpret_cast<float*>(smem + kFacOff);
+    float* rag = reinterpret_cast<float*>(smem + kEpiOff);
+    float* amax = rag;          // kSwiglu: [tile parity][part][row]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ngroups = p.offsets ? p.E + p.has_shared : 1;
@@ -215,7 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&tempty[b], kEpiWarps);
         }
         mbar_init(done, 1);
-        for (int q = 0; q < 4; ++q) mbar_init(&pair[q], kParts);
+        for (int q = 0; q < 4; ++q) mbar_init(&pair[q], 2);
+        for (int f = 0; f < kFSlots; ++f) {
+            mbar_init(&ffull[f], 64);
+            mbar_init(&fempty[f], kEpiWarps);
+        }
         *abort = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_x);
@@ -255,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 640 threads at 96 registers: the scaling warps take from the other four
     // (64 * 128 + 104 * 512 = 96 * 640)
     if (warp < kEpiWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == 0) {
         // =============================== TMA producer ===============================
         if (lane == 0) {
@@ -278,18 +323,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     uint8_t* st = smem + s * kStageBytes;
-                    mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * 32 * kBK + kBBytes));
-                    if (MODE == kSwiglu) {
-                        tma_load_2d(st + kABytes, w0, &full[s], kb * kBK, wrow, pol_w);
-                        tma_load_2d(st + kABytes + kBBytes / 2, w1, &full[s], kb * kBK, wrow, pol_w);
-                    } else {
-                        tma_load_2d(st + kABytes, w0, &full[s], kb * kBK, wrow, pol_w);
-                    }
+                    const int kx = kb * kBK;
+                    mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * 32 * kBK + 2 * kBBytes));
+                    tma_load_2d(st + kABytes, w0, &full[s], kx, wrow, pol_w);
+                    tma_load_2d(st + kABytes + kBBytes, MODE == kSwiglu ? w1 : w0, &full[s], kx,
+                                MODE == kSwiglu ? wrow : wrow + 128, pol_w);
                     if (boxes == 4)
-                        tma_load_2d(st, &tm_x, &full[s], kb * kBK, (int)ti.row, pol_x);
+                        tma_load_2d(st, &tm_x, &full[s], kx, (int)ti.row, pol_x);
                     else
                         for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(st + b * 32 * kBK, &tm_x32, &full[s], kb * kBK,
+                            tma_load_2d(st + b * 32 * kBK, &tm_x32, &full[s], kx,
                                         (int)ti.row + 32 * b, pol_x);
                 }
             }
@@ -307,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kb = 0; kb < p.nkb; ++kb, ++it) {
                     if (it > 0 && ++s == kStages) { s = 0; ph ^= 1u; }
                     const int b = it & 1;
-                    if (!mbar_wait(&tempty[b], (((uint32_t)it >> 1) & 1u) ^ 1u, abort) ||
-                        !mbar_wait(&full[s], ph, abort)) {
+                    if (!mbar_wait(&full[s], ph, abort) ||
+                        !mbar_wait(&tempty[b], (((uint32_t)it >> 1) & 1u) ^ 1u, abort)) {
                         record_timeout(abort);
                         ok = false;
                         break;
@@ -320,89 +363,95 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 4; ++kk)  // 32 codes = 32 bytes further each
                         umma_e4m3(tmem + (uint32_t)(b * 256), dx + (uint64_t)(2 * kk),
                                   dw + (uint64_t)(2 * kk), kk > 0 ? 1u : 0u);
-                    umma_commit(&empty[s]);
                     umma_commit(&tfull[b]);
+                    umma_commit(&empty[s]);
                 }
             }
-            if (it > 0) {  // every UMMA issued has finished before TMEM is given back
-                umma_commit(done);
-                mbar_wait(done, 0u, nullptr, 100000000ull);
+            // every UMMA issued has finished before TMEM is given back
+            umma_commit(done);
+            mbar_wait(done, 0u, nullptr, 100000000ull);
+        }
+    } else {
+        // ============================== scale factors ===============================
+        // fac[k-block][half][row] = sx[row] * sw[half], kFKb k-blocks per slot, ahead of the
+        // scaling warps: a row's scales are read once and in 16 bytes, not by every warp of
+        // the row in every k-block (32 lines per load)
+        const int w = threadIdx.x - 64;
+        const int wblocks = (p.F + 127) / 128;
+        const bool vec = (p.nkb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 15) == 0;
+        int n = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            const Tile ti = tile_at(p, prefix, rowoff, ngroups, t);
+            const long long wb = (long long)(ti.shared || !p.offsets ? 0 : ti.g) * wblocks;
+            const float* sw0 = ti.shared ? p.ssw0 : p.sw0;
+            const float* sw1 = MODE == kSwiglu ? (ti.shared ? p.ssw1 : p.sw1) : sw0;
+            sw0 += (wb + (MODE == kSwiglu ? ti.f : 2 * ti.f)) * p.nkb;
+            sw1 += (wb + (MODE == kSwiglu ? ti.f : min(2 * ti.f + 1, wblocks - 1))) * p.nkb;
+            const float* sx = p.sx + ti.row * p.nkb;
+            const int last = ti.rows - 1;
+            for (int kb = 0; kb < p.nkb; kb += kFKb, ++n) {
+                const int s = n % kFSlots;
+                float a[2][kFKb];  // rows w and w + 64
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float* x = sx + (long long)min(w + 64 * j, last) * p.nkb + kb;
+                    if (vec) {
+                        *reinterpret_cast<float4*>(a[j]) = *reinterpret_cast<const float4*>(x);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kFKb; ++i) a[j][i] = kb + i < p.nkb ? x[i] : 0.0f;
+                    }
+                }
+                if (!mbar_wait(&fempty[s], (((uint32_t)n / kFSlots) & 1u) ^ 1u, abort)) {
+                    record_timeout(abort);
+                    ok = false;
+                    break;
+                }
+                float* f = fac + s * kFacFloats + w;
+#pragma unroll
+                for (int i = 0; i < kFKb; ++i) {
+                    if (kb + i >= p.nkb) break;
+                    const float g0 = sw0[kb + i], g1 = sw1[kb + i];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        f[i * 256 + 64 * j] = a[j][i] * g0;
+                        f[i * 256 + 128 + 64 * j] = a[j][i] * g1;
+                    }
+                }
+                mbar_arrive(&ffull[s]);
             }
         }
     }
     } else {
         // ============================ scaling and epilogue ==========================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
         const int q = warp & 3, part = (warp - kEpiWarp0) >> 2;
         const int r = q * 32 + lane;  // the thread's row of the tile
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
-        // the warp's two chunks of 32 columns: 32 gate and 32 up, or 64 in a row
-        const int c0 = MODE == kSwiglu ? 32 * part : 64 * part;
-        const int c1 = MODE == kSwiglu ? 128 + 32 * part : 64 * part + 32;
-        const int wblocks = (p.F + 127) / 128;
-        int it = 0, lt = 0;
-        bool ok = true;
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(64 * part);
+        Rings rg = {tfull, tempty, ffull, fempty, 0u, 0u};
+        int lt = 0;  // tiles so far
         for (int t = blockIdx.x; t < total; t += gridDim.x, ++lt) {
             const Tile ti = tile_at(p, prefix, rowoff, ngroups, t);
             const bool mine = r < ti.rows;
             const bool idle = q * 32 >= ti.rows;  // no row of this warp is in the tile
-            const float* sx = p.sx + (ti.row + (mine ? r : 0)) * p.nkb;
-            const long long wb = (long long)(ti.shared || !p.offsets ? 0 : ti.g) * wblocks +
-                                 (MODE == kSwiglu ? ti.f : min(2 * ti.f + part / 2, wblocks - 1));
-            const float* sw0 = (ti.shared ? p.ssw0 : p.sw0) + wb * p.nkb;
-            const float* sw1 = MODE == kSwiglu ? (ti.shared ? p.ssw1 : p.sw1) + wb * p.nkb : sw0;
-            unsigned long long acc[32];
+            float acc[kCols];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = 0ull;
-            float x_next = sx[0], w0_next = sw0[0], w1_next = MODE == kSwiglu ? sw1[0] : 0.0f;
-            for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                const float f0 = x_next * w0_next, f1 = MODE == kSwiglu ? x_next * w1_next : f0;
-                if (kb + 1 < p.nkb) {
-                    x_next = sx[kb + 1];
-                    w0_next = sw0[kb + 1];
-                    if (MODE == kSwiglu) w1_next = sw1[kb + 1];
-                }
-                const int b = it & 1;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[b], ((uint32_t)it >> 1) & 1u, abort))) {
-                    record_timeout(abort);
-                    ok = false;
-                    break;
-                }
-                if (!idle) {
-                    tc_fence_after();
-                    const uint32_t col = taddr + (uint32_t)(b * 256);
-                    uint32_t u[16], v[16];
-                    tmem_ld16(col + (uint32_t)c0, u);
-                    tmem_wait16(u);
-                    tmem_ld16(col + (uint32_t)c0 + 16u, v);
-                    fold16(acc, u, f0);
-                    tmem_wait16(v);
-                    tmem_ld16(col + (uint32_t)c1, u);
-                    fold16(acc + 8, v, f0);
-                    tmem_wait16(u);
-                    tmem_ld16(col + (uint32_t)c1 + 16u, v);
-                    fold16(acc + 16, u, f1);
-                    tmem_wait16(v);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tempty[b]);
-                    fold16(acc + 24, v, f1);
-                } else if (lane == 0) {
-                    mbar_arrive(&tempty[b]);
-                }
+            for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+            if (!(idle ? sums<false>(acc, p.nkb, rg, fac + r, taddr, abort)
+                       : sums<true>(acc, p.nkb, rg, fac + r, taddr, abort))) {
+                record_timeout(abort);
+                break;
             }
-            if (!ok) break;
             if constexpr (MODE == kSwiglu) {
                 // h over the gate sums' registers, the row's maximum with the other parts
                 float m = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float h0 = nan_for_inf(silu(lo_of(acc[i])) * lo_of(acc[16 + i]));
-                    const float h1 = nan_for_inf(silu(hi_of(acc[i])) * hi_of(acc[16 + i]));
-                    m = fmaxf(m, fmaxf(fabsf(h0), fabsf(h1)));
-                    acc[i] = pair_of(h0, h1);
+                for (int i = 0; i < 64; ++i) {
+                    acc[i] = nan_for_inf(silu(acc[i]) * acc[64 + i]);
+                    m = fmaxf(m, fabsf(acc[i]));
                 }
-                float* am = amax + (lt & 1) * (kParts * 128) + r;
+                float* am = amax + (lt & 1) * 256 + r;
                 am[part * 128] = m;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pair[q]);
@@ -410,71 +459,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                     record_timeout(abort);
                     break;
                 }
-#pragma unroll
-                for (int o = 0; o < kParts; ++o) m = fmaxf(m, am[o * 128]);
+                m = fmaxf(m, am[(part ^ 1) * 128]);
                 float s, inv;
                 block_scale(m, s, inv);
                 if (mine) {
-                    uint32_t w[8];
+                    uint8_t* o = static_cast<uint8_t*>(p.out) + (ti.row + r) * p.F + ti.f * 128 +
+                                 64 * part;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w[j] = cvt_e4m3x4(lo_of(acc[2 * j]) * inv, hi_of(acc[2 * j]) * inv,
-                                          lo_of(acc[2 * j + 1]) * inv, hi_of(acc[2 * j + 1]) * inv);
-                    st_global_32B(static_cast<uint8_t*>(p.out) + (ti.row + r) * p.F + ti.f * 128 +
-                                      32 * part,
-                                  w);
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float* x = acc + 32 * i + 4 * j;
+                            w[j] = cvt_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                        }
+                        st_global_32B(o + 32 * i, w);
+                    }
                     if (part == 0) p.out_scale[(ti.row + r) * (p.F / 128) + ti.f] = s;
                 }
             } else {
-                const int n0 = ti.f * 256 + 64 * part;
-                if (p.vec && n0 + 64 <= p.F) {
-                    if (mine && p.f32) {
-                        float* o = static_cast<float*>(p.out) + (ti.row + r) * p.ld + n0;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            uint32_t w[8];
+                for (int h = 0; h < 2; ++h) {
+                    const int n0 = ti.f * 256 + 128 * h + 64 * part;
+                    const float* sum = acc + 64 * h;
+                    if (p.vec && n0 + 64 <= p.F) {
+                        if (mine && p.f32) {
+                            float* o = static_cast<float*>(p.out) + (ti.row + r) * p.ld + n0;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                w[2 * j] = __float_as_uint(lo_of(acc[4 * i + j]));
-                                w[2 * j + 1] = __float_as_uint(hi_of(acc[4 * i + j]));
+                            for (int i = 0; i < 8; ++i) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(sum[8 * i + j]);
+                                st_global_32B(o + 8 * i, w);
                             }
-                            st_global_32B(o + 8 * i, w);
+                        } else if (mine) {
+                            uint16_t* o = static_cast<uint16_t*>(p.out) + (ti.row + r) * p.ld + n0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    w[j] = pack_bf16x2(sum[16 * i + 2 * j], sum[16 * i + 2 * j + 1]);
+                                st_global_32B(o + 16 * i, w);
+                            }
                         }
-                    } else if (mine) {
-                        uint16_t* o = static_cast<uint16_t*>(p.out) + (ti.row + r) * p.ld + n0;
+                    } else if (!idle && n0 < p.F) {
+                        // rows without 32-byte alignment, or the last columns: four columns at
+                        // a time through shared memory, so that a store covers four columns of
+                        // eight rows instead of one of 32
+                        float* piece = rag + (warp - kEpiWarp0) * (32 * kRagLd);
+                        const int pr = lane >> 2, pc = lane & 3;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[8];
+                        for (int i = 0; i < 16; ++i) {
+                            __syncwarp();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                w[j] = pack_bf16x2(lo_of(acc[8 * i + j]), hi_of(acc[8 * i + j]));
-                            st_global_32B(o + 16 * i, w);
-                        }
-                    }
-                } else if (!idle) {
-                    // rows without 32-byte alignment, or the last columns: eight columns at a
-                    // time through shared memory, so that a store covers eight columns of four
-                    // rows instead of one of 32
-                    float* piece = rag + (warp - kEpiWarp0) * (32 * kRagLd);
-                    const int pr = lane >> 3, pc = lane & 7;
+                            for (int j = 0; j < 4; ++j) piece[lane * kRagLd + j] = sum[4 * i + j];
+                            __syncwarp();
+                            const int n = n0 + 4 * i + pc;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            piece[lane * kRagLd + 2 * j] = lo_of(acc[4 * i + j]);
-                            piece[lane * kRagLd + 2 * j + 1] = hi_of(acc[4 * i + j]);
-                        }
-                        __syncwarp();
-                        const int n = n0 + 8 * i + pc;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int rr = 4 * k + pr;
-                            if (q * 32 + rr < ti.rows && n < p.F) {
-                                const long long at = (ti.row + q * 32 + rr) * p.ld + n;
-                                const float v = piece[rr * kRagLd + pc];
-                                if (p.f32) static_cast<float*>(p.out)[at] = v;
-                                else static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
+                            for (int k = 0; k < 4; ++k) {
+                                const int rr = 8 * k + pr;
+                                if (q * 32 + rr < ti.rows && n < p.F) {
+                                    const long long at = (ti.row + q * 32 + rr) * p.ld + n;
+                                    const float v = piece[rr * kRagLd + pc];
+                                    if (p.f32) static_cast<float*>(p.out)[at] = v;
+                                    else static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
+                                }
                             }
                         }
                     }
@@ -538,7 +588,7 @@ cudaError_t run(const ScaledGemmArgs& a, cudaStream_t s) {
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     });
     if (err != cudaSuccess) return err;
-    const int wbox = MODE == kSwiglu ? 128 : 256;
+    const int wbox = 128;
     const long long wrows = (long long)(a.offsets ? a.E : 1) * a.F;
     CUtensorMap x, x32, w0, w1, s0, s1;
     bool ok = code_map(&x, a.x, a.rows, a.K, a.ldx, 128) &&
