@@ -46,7 +46,10 @@ enum { kLinear = 0, kSwiglu = 1 };
 constexpr int kEpiWarps = 8;
 constexpr int kEpiWarp0 = 4;                   // first of them: whole warpgroups
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr int kCols = 128;                     // columns (sums) of a warp, 64 of each half
+// Columns of each half that a warp sums: 64, or with FEW (tiles of 32 rows) 16.
+template <int FEW>
+constexpr int kRun = FEW ? 16 : 64;
+constexpr int kPartLd = 260;                   // SPLIT: floats per row of a CTA's partial sums
 constexpr int kLowRegs = 56, kHighRegs = 224;  // 56 * 128 + 224 * 256 = 168 * 384
 constexpr int kBK = 128;                       // codes per 128-byte swizzled row = one k-block
 constexpr int kMaxGroups = 1025;
@@ -94,6 +97,7 @@ struct Params {
     int f32;                 // kLinear: fp32 out
     int vec;                 // kLinear: rows of `out` are 32-byte aligned
     float* out_scale;        // kSwiglu: [rows, F / 128]
+    int split;               // SPLIT: CTAs per tile (the cluster's size), k-blocks shared out
 };
 
 MOE_DEV void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t accumulate) {
@@ -135,22 +139,22 @@ struct Rings {
     uint32_t it, fn;
 };
 
-// One tile's sums of a warp: for every k-block its 64 columns of each half times the factor of
+// One tile's sums of a warp over n k-blocks: its RUN columns of each half times the factor of
 // the thread's row (f: the first half's in slot 0) are added to acc.  LIVE false (no row of the
 // warp is in the tile): only the waiting.  False when a wait gave up (then in every lane).
-template <bool LIVE>
-MOE_DEV bool sums(float (&acc)[kCols], int nkb, Rings& rg, const float* f, uint32_t taddr,
+template <int RUN, bool LIVE>
+MOE_DEV bool sums(float (&acc)[2 * RUN], int n, Rings& rg, const float* f, uint32_t taddr,
                   volatile int* abort) {
     const int lane = threadIdx.x & 31;
     int fi = 0;
 #pragma unroll 1
-    for (int kb = 0; kb < nkb; ++kb, ++rg.it) {
+    for (int kb = 0; kb < n; ++kb, ++rg.it) {
         const uint32_t b = rg.it & 1u, s = rg.fn & (kFSlots - 1);
         if (fi == 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&rg.ffull[s], (rg.fn / kFSlots) & 1u, abort)))
             return false;
         const float* g = f + s * kFacFloats + fi * 256;
         const float f0 = g[0], f1 = g[128];
-        if (++fi == kFKb || kb == nkb - 1) {
+        if (++fi == kFKb || kb == n - 1) {
             fi = 0;
             ++rg.fn;
             __syncwarp();
@@ -161,21 +165,30 @@ MOE_DEV bool sums(float (&acc)[kCols], int nkb, Rings& rg, const float* f, uint3
             tc_fence_after();
             uint32_t u[16];
 #pragma unroll
-            for (int c = 0; c < kCols; c += 16) {
-                tmem_ld16(taddr + b * 256u + (uint32_t)(c < 64 ? c : c + 64), u);
+            for (int c = 0; c < 2 * RUN; c += 16) {
+                tmem_ld16(taddr + b * 256u + (uint32_t)(c < RUN ? c : c - RUN + 128), u);
                 tmem_ld_wait();
-                if (c == kCols - 16) {  // the last load: the buffer is free before the last sums
+                if (c == 2 * RUN - 16) {  // the last load: the buffer is free before the last sums
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&rg.tempty[b]);
                 }
-                fold16(acc + c, u, c < 64 ? f0 : f1);
+                fold16(acc + c, u, c < RUN ? f0 : f1);
             }
         } else if (lane == 0) {
             mbar_arrive(&rg.tempty[b]);
         }
     }
     return true;
+}
+
+MOE_DEV float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
 
 MOE_DEV void record_timeout(volatile int* abort) {
@@ -194,6 +207,7 @@ MOE_DEV long long rows_of(const Params& p, const int32_t* rowoff, int g) {
     return g == p.E ? p.shared_rows : (long long)(rowoff[g + 1] - rowoff[g]);
 }
 
+template <int TR>
 MOE_DEV Tile tile_at(const Params& p, const int32_t* prefix, const int32_t* rowoff, int ngroups,
                      int t) {
     int lo = 0, hi = ngroups - 1;  // largest g with prefix[g] <= t
@@ -205,16 +219,85 @@ MOE_DEV Tile tile_at(const Params& p, const int32_t* prefix, const int32_t* rowo
     ti.g = lo;
     ti.shared = p.offsets && lo == p.E;
     const long long rows = rows_of(p, rowoff, lo);
-    const int mt = (int)((rows + 127) / 128);
+    const int mt = (int)((rows + TR - 1) / TR);
     const int local = t - prefix[lo];
-    const long long r0 = (long long)(local % mt) * 128;
+    const long long r0 = (long long)(local % mt) * TR;
     ti.f = local / mt;
-    ti.rows = (int)(rows - r0 < 128 ? rows - r0 : 128);
+    ti.rows = (int)(rows - r0 < TR ? rows - r0 : TR);
     ti.row = (ti.shared ? p.shared_row0 : p.offsets ? (long long)rowoff[lo] : 0) + r0;
     return ti;
 }
 
+// SPLIT: adds the partial sums of a tile's CTAs (their shared memory at `part`, in rank order)
+// and writes the rows rank, rank + split, ..: a warp per row, a lane four columns of each half.
 template <int MODE>
+MOE_DEV void join_rows(const Params& p, const Tile& ti, const float* part, int rank) {
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kEpiWarp0;
+    for (int r = rank + p.split * w; r < ti.rows; r += p.split * kEpiWarps) {
+        const float* at = part + r * kPartLd + 4 * lane;
+        float4 x[8], y[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < p.split) {
+                const uint32_t from = mapa_shared(at, (uint32_t)c);
+                x[c] = ld_cluster_f4(from);
+                y[c] = ld_cluster_f4(from + 512u);
+            }
+        float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < p.split) {
+                g[0] += x[c].x; g[1] += x[c].y; g[2] += x[c].z; g[3] += x[c].w;
+                u[0] += y[c].x; u[1] += y[c].y; u[2] += y[c].z; u[3] += y[c].w;
+            }
+        const long long row = ti.row + r;
+        if constexpr (MODE == kSwiglu) {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                g[i] = nan_for_inf(silu(g[i]) * u[i]);
+                m = fmaxf(m, fabsf(g[i]));
+            }
+#pragma unroll
+            for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+            float s, inv;
+            block_scale(m, s, inv);
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row * p.F + ti.f * 128 +
+                                         4 * lane) =
+                cvt_e4m3x4(g[0] * inv, g[1] * inv, g[2] * inv, g[3] * inv);
+            if (lane == 0) p.out_scale[row * (p.F / 128) + ti.f] = s;
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float* v = h ? u : g;
+                const int n = ti.f * 256 + 128 * h + 4 * lane;
+                if (p.f32) {
+                    float* o = static_cast<float*>(p.out) + row * p.ld + n;
+                    if (p.vec && n + 4 <= p.F) {
+                        *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (n + i < p.F) o[i] = v[i];
+                    }
+                } else {
+                    uint16_t* o = static_cast<uint16_t*>(p.out) + row * p.ld + n;
+                    const uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
+                    if (p.vec && n + 4 <= p.F) {
+                        *reinterpret_cast<uint2*>(o) = make_uint2(a, b);
+                    } else {
+                        if (n < p.F) o[0] = (uint16_t)a;
+                        if (n + 1 < p.F) o[1] = (uint16_t)(a >> 16);
+                        if (n + 2 < p.F) o[2] = (uint16_t)b;
+                        if (n + 3 < p.F) o[3] = (uint16_t)(b >> 16);
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int MODE, int FEW, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     scaled_gemm_kernel(const __grid_constant__ CUtensorMap tm_x,     // boxes of 128 rows
                        const __grid_constant__ CUtensorMap tm_x32,   // boxes of 32 rows
@@ -223,6 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tm_s0,
                        const __grid_constant__ CUtensorMap tm_s1, const Params p) {
     constexpr int kFeat = MODE == kSwiglu ? 128 : 256;
+    constexpr int kTile = FEW ? 32 : 128;  // token rows
+    constexpr int RUN = kRun<FEW>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -240,11 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* fempty = ffull + kFSlots;
     float* fac = reinterpret_cast<float*>(smem + kFacOff);
     float* rag = reinterpret_cast<float*>(smem + kEpiOff);
-    float* amax = rag;          // kSwiglu: [tile parity][part][row]
+    float* amax = rag;          // kSwiglu: [tile parity][warps of a row][row]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ngroups = p.offsets ? p.E + p.has_shared : 1;
     const int ftiles = (p.F + kFeat - 1) / kFeat;
+    // SPLIT: a cluster per tile, each CTA its share of the k-blocks
+    const int rank = SPLIT ? (int)cluster_rank() : 0;
+    const int tstart = SPLIT ? (int)blockIdx.x / p.split : (int)blockIdx.x;
+    const int tstep = SPLIT ? (int)gridDim.x / p.split : (int)gridDim.x;
+    const int kb0 = SPLIT ? p.nkb * rank / p.split : 0;
+    const int kb1 = SPLIT ? p.nkb * (rank + 1) / p.split : p.nkb;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -256,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&tempty[b], kEpiWarps);
         }
         mbar_init(done, 1);
-        for (int q = 0; q < 4; ++q) mbar_init(&pair[q], 2);
+        for (int q = 0; q < 4; ++q) mbar_init(&pair[q], FEW ? kEpiWarps : 2);
         for (int f = 0; f < kFSlots; ++f) {
             mbar_init(&ffull[f], 64);
             mbar_init(&fempty[f], kEpiWarps);
@@ -278,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g0 = lane * per, g1 = min(ngroups, g0 + per);
         int local = 0;
         for (int g = g0; g < g1; ++g)
-            local += (int)((rows_of(p, rowoff, g) + 127) / 128) * ftiles;
+            local += (int)((rows_of(p, rowoff, g) + kTile - 1) / kTile) * ftiles;
         int incl = local;
         for (int off = 1; off < 32; off <<= 1) {
             const int v = __shfl_up_sync(0xFFFFFFFFu, incl, off);
@@ -287,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int run = incl - local;
         for (int g = g0; g < g1; ++g) {
             prefix[g] = run;
-            run += (int)((rows_of(p, rowoff, g) + 127) / 128) * ftiles;
+            run += (int)((rows_of(p, rowoff, g) + kTile - 1) / kTile) * ftiles;
         }
         if (lane == 31) prefix[ngroups] = incl;
     }
@@ -297,8 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const int total = prefix[ngroups];
 
-    // 640 threads at 96 registers: the scaling warps take from the other four
-    // (64 * 128 + 104 * 512 = 96 * 640)
+    // 384 threads at 168 registers: the scaling warps take from the other four
     if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == 0) {
@@ -308,14 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0, s = 0;
             uint32_t ph = 0u;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const Tile ti = tile_at(p, prefix, rowoff, ngroups, t);
+            for (int t = tstart; t < total && ok; t += tstep) {
+                const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
                 const CUtensorMap* w0 = ti.shared ? &tm_s0 : &tm_w0;
                 const CUtensorMap* w1 = ti.shared ? &tm_s1 : &tm_w1;
                 const int wrow = (ti.shared || !p.offsets ? 0 : ti.g * p.F) + ti.f * kFeat;
-                // only the rows the tile has (32 at a time): the others' products are unused
-                const int boxes = ti.rows > 96 ? 4 : (ti.rows + 31) / 32;
-                for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+                // only the rows the tile has (32 at a time): the others' products are unused.
+                // FEW: the same 32 rows in every lane quarter
+                const int boxes = FEW || ti.rows > 96 ? 4 : (ti.rows + 31) / 32;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     if (it > 0 && ++s == kStages) { s = 0; ph ^= 1u; }
                     if (!mbar_wait(&empty[s], ph ^ 1u, abort)) {
                         record_timeout(abort);
@@ -328,12 +419,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(st + kABytes, w0, &full[s], kx, wrow, pol_w);
                     tma_load_2d(st + kABytes + kBBytes, MODE == kSwiglu ? w1 : w0, &full[s], kx,
                                 MODE == kSwiglu ? wrow : wrow + 128, pol_w);
-                    if (boxes == 4)
+                    if (!FEW && boxes == 4)
                         tma_load_2d(st, &tm_x, &full[s], kx, (int)ti.row, pol_x);
                     else
                         for (int b = 0; b < boxes; ++b)
                             tma_load_2d(st + b * 32 * kBK, &tm_x32, &full[s], kx,
-                                        (int)ti.row + 32 * b, pol_x);
+                                        (int)ti.row + (FEW ? 0 : 32 * b), pol_x);
                 }
             }
             // no copy may land after the CTA has gone
@@ -346,8 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0, s = 0;
             uint32_t ph = 0u;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+            for (int t = tstart; t < total && ok; t += tstep) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     if (it > 0 && ++s == kStages) { s = 0; ph ^= 1u; }
                     const int b = it & 1;
                     if (!mbar_wait(&full[s], ph, abort) ||
@@ -368,8 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // every UMMA issued has finished before TMEM is given back
-            umma_commit(done);
-            mbar_wait(done, 0u, nullptr, 100000000ull);
+            if (it > 0) {
+                umma_commit(done);
+                mbar_wait(done, 0u, nullptr, 100000000ull);
+            }
         }
     } else {
         // ============================== scale factors ===============================
@@ -378,11 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the row in every k-block (32 lines per load)
         const int w = threadIdx.x - 64;
         const int wblocks = (p.F + 127) / 128;
-        const bool vec = (p.nkb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 15) == 0;
+        const bool vec = ((p.nkb | kb0) & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 15) == 0;
         int n = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const Tile ti = tile_at(p, prefix, rowoff, ngroups, t);
+        for (int t = tstart; t < total && ok; t += tstep) {
+            const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
             const long long wb = (long long)(ti.shared || !p.offsets ? 0 : ti.g) * wblocks;
             const float* sw0 = ti.shared ? p.ssw0 : p.sw0;
             const float* sw1 = MODE == kSwiglu ? (ti.shared ? p.ssw1 : p.sw1) : sw0;
@@ -390,17 +483,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             sw1 += (wb + (MODE == kSwiglu ? ti.f : min(2 * ti.f + 1, wblocks - 1))) * p.nkb;
             const float* sx = p.sx + ti.row * p.nkb;
             const int last = ti.rows - 1;
-            for (int kb = 0; kb < p.nkb; kb += kFKb, ++n) {
+            for (int kb = kb0; kb < kb1; kb += kFKb, ++n) {
                 const int s = n % kFSlots;
-                float a[2][kFKb];  // rows w and w + 64
+                float a[2][kFKb];  // rows w and w + 64 (FEW: the lane's)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float* x = sx + (long long)min(w + 64 * j, last) * p.nkb + kb;
+                    const float* x = sx + (long long)min(FEW ? w & 31 : w + 64 * j, last) * p.nkb + kb;
                     if (vec) {
                         *reinterpret_cast<float4*>(a[j]) = *reinterpret_cast<const float4*>(x);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < kFKb; ++i) a[j][i] = kb + i < p.nkb ? x[i] : 0.0f;
+                        for (int i = 0; i < kFKb; ++i) a[j][i] = kb + i < kb1 ? x[i] : 0.0f;
                     }
                 }
                 if (!mbar_wait(&fempty[s], (((uint32_t)n / kFSlots) & 1u) ^ 1u, abort)) {
@@ -411,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* f = fac + s * kFacFloats + w;
 #pragma unroll
                 for (int i = 0; i < kFKb; ++i) {
-                    if (kb + i >= p.nkb) break;
+                    if (kb + i >= kb1) break;
                     const float g0 = sw0[kb + i], g1 = sw1[kb + i];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -423,70 +516,96 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    if constexpr (SPLIT) {  // around the join of the scaling warps
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
+    }
     } else {
         // ============================ scaling and epilogue ==========================
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
         const int q = warp & 3, part = (warp - kEpiWarp0) >> 2;
-        const int r = q * 32 + lane;  // the thread's row of the tile
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(64 * part);
+        const int c0 = FEW ? 16 * (2 * q + part) : 64 * part;  // the warp's columns of a half
+        const int wr = FEW ? 0 : q * 32;                       // its first row
+        const int r = wr + lane;                               // the thread's row of the tile
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
         Rings rg = {tfull, tempty, ffull, fempty, 0u, 0u};
         int lt = 0;  // tiles so far
-        for (int t = blockIdx.x; t < total; t += gridDim.x, ++lt) {
-            const Tile ti = tile_at(p, prefix, rowoff, ngroups, t);
+        for (int t = tstart; t < total; t += tstep, ++lt) {
+            const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
             const bool mine = r < ti.rows;
-            const bool idle = q * 32 >= ti.rows;  // no row of this warp is in the tile
-            float acc[kCols];
+            const bool idle = wr >= ti.rows;  // no row of this warp is in the tile
+            float acc[2 * RUN];
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
-            if (!(idle ? sums<false>(acc, p.nkb, rg, fac + r, taddr, abort)
-                       : sums<true>(acc, p.nkb, rg, fac + r, taddr, abort))) {
+            for (int i = 0; i < 2 * RUN; ++i) acc[i] = 0.0f;
+            if (!(idle ? sums<RUN, false>(acc, kb1 - kb0, rg, fac + r, taddr, abort)
+                       : sums<RUN, true>(acc, kb1 - kb0, rg, fac + r, taddr, abort))) {
                 record_timeout(abort);
                 break;
             }
-            if constexpr (MODE == kSwiglu) {
+            if constexpr (SPLIT) {
+                // into this CTA's shared memory (every copy into it has been consumed)
+                float* row = reinterpret_cast<float*>(smem) + r * kPartLd + c0;
+                if (mine)
+#pragma unroll
+                    for (int i = 0; i < 2 * RUN; i += 4)
+                        *reinterpret_cast<float4*>(row + (i < RUN ? i : i - RUN + 128)) =
+                            make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                break;  // one tile per cluster
+            }
+            else if constexpr (MODE == kSwiglu) {
                 // h over the gate sums' registers, the row's maximum with the other parts
                 float m = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    acc[i] = nan_for_inf(silu(acc[i]) * acc[64 + i]);
+                for (int i = 0; i < RUN; ++i) {
+                    acc[i] = nan_for_inf(silu(acc[i]) * acc[RUN + i]);
                     m = fmaxf(m, fabsf(acc[i]));
                 }
                 float* am = amax + (lt & 1) * 256 + r;
-                am[part * 128] = m;
+                uint64_t* bar = FEW ? &pair[0] : &pair[q];
+                am[FEW ? 32 * (2 * q + part) : 128 * part] = m;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&pair[q]);
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&pair[q], (uint32_t)lt & 1u, abort))) {
+                if (lane == 0) mbar_arrive(bar);
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, (uint32_t)lt & 1u, abort))) {
                     record_timeout(abort);
                     break;
                 }
-                m = fmaxf(m, am[(part ^ 1) * 128]);
+#pragma unroll
+                for (int o = 0; o < 256; o += kTile) m = fmaxf(m, am[o]);
                 float s, inv;
                 block_scale(m, s, inv);
                 if (mine) {
-                    uint8_t* o = static_cast<uint8_t*>(p.out) + (ti.row + r) * p.F + ti.f * 128 +
-                                 64 * part;
+                    uint8_t* o = static_cast<uint8_t*>(p.out) + (ti.row + r) * p.F + ti.f * 128 + c0;
+                    if constexpr (FEW) {
+                        *reinterpret_cast<uint4*>(o) = make_uint4(
+                            cvt_e4m3x4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv),
+                            cvt_e4m3x4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv),
+                            cvt_e4m3x4(acc[8] * inv, acc[9] * inv, acc[10] * inv, acc[11] * inv),
+                            cvt_e4m3x4(acc[12] * inv, acc[13] * inv, acc[14] * inv, acc[15] * inv));
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t w[8];
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t w[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float* x = acc + 32 * i + 4 * j;
-                            w[j] = cvt_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                            for (int j = 0; j < 8; ++j) {
+                                const float* x = acc + 32 * i + 4 * j;
+                                w[j] = cvt_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                            }
+                            st_global_32B(o + 32 * i, w);
                         }
-                        st_global_32B(o + 32 * i, w);
                     }
-                    if (part == 0) p.out_scale[(ti.row + r) * (p.F / 128) + ti.f] = s;
+                    if (c0 == 0) p.out_scale[(ti.row + r) * (p.F / 128) + ti.f] = s;
                 }
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int n0 = ti.f * 256 + 128 * h + 64 * part;
-                    const float* sum = acc + 64 * h;
-                    if (p.vec && n0 + 64 <= p.F) {
+                    const int n0 = ti.f * 256 + 128 * h + c0;
+                    const float* sum = acc + RUN * h;
+                    if (p.vec && n0 + RUN <= p.F) {
                         if (mine && p.f32) {
                             float* o = static_cast<float*>(p.out) + (ti.row + r) * p.ld + n0;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
+                            for (int i = 0; i < RUN / 8; ++i) {
                                 uint32_t w[8];
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(sum[8 * i + j]);
@@ -495,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (mine) {
                             uint16_t* o = static_cast<uint16_t*>(p.out) + (ti.row + r) * p.ld + n0;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < RUN / 16; ++i) {
                                 uint32_t w[8];
 #pragma unroll
                                 for (int j = 0; j < 8; ++j)
@@ -510,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float* piece = rag + (warp - kEpiWarp0) * (32 * kRagLd);
                         const int pr = lane >> 2, pc = lane & 3;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < RUN / 4; ++i) {
                             __syncwarp();
 #pragma unroll
                             for (int j = 0; j < 4; ++j) piece[lane * kRagLd + j] = sum[4 * i + j];
@@ -519,8 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const int rr = 8 * k + pr;
-                                if (q * 32 + rr < ti.rows && n < p.F) {
-                                    const long long at = (ti.row + q * 32 + rr) * p.ld + n;
+                                if (wr + rr < ti.rows && n < p.F) {
+                                    const long long at = (ti.row + wr + rr) * p.ld + n;
                                     const float v = piece[rr * kRagLd + pc];
                                     if (p.f32) static_cast<float*>(p.out)[at] = v;
                                     else static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
@@ -530,6 +649,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+        }
+        if constexpr (SPLIT) {
+            __syncwarp();
+            cluster_sync();  // all partial sums are written
+            if (tstart < total)
+                join_rows<MODE>(p, tile_at<kTile>(p, prefix, rowoff, ngroups, tstart),
+                                reinterpret_cast<const float*>(smem), rank);
+            __syncwarp();
+            cluster_sync();  // and read: the CTAs may leave
         }
     }
 
@@ -580,11 +708,20 @@ bool code_map(CUtensorMap* m, const void* base, long long rows, long long cols, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE>
-cudaError_t run(const ScaledGemmArgs& a, cudaStream_t s) {
+// At most this many tiles of `tr` token rows (the offsets are on the device): a group that has
+// rows adds one ragged tile.
+long long max_tiles(const ScaledGemmArgs& a, long long tr) {
+    const long long per = a.swiglu ? 128 : 256, ft = (a.F + per - 1) / per;
+    if (!a.offsets) return (a.rows + tr - 1) / tr * ft;
+    const long long P = a.shared_row0, hit = P < a.E ? P : a.E;
+    return (P / tr + hit + (a.shared_rows + tr - 1) / tr) * ft;
+}
+
+template <int MODE, int FEW, int SPLIT>
+cudaError_t run(const ScaledGemmArgs& a, int split, cudaStream_t s) {
     static DeviceOnce attr_once;
     cudaError_t err = attr_once.run([] {
-        return cudaFuncSetAttribute(scaled_gemm_kernel<MODE>,
+        return cudaFuncSetAttribute(scaled_gemm_kernel<MODE, FEW, SPLIT>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     });
     if (err != cudaSuccess) return err;
@@ -620,21 +757,53 @@ cudaError_t run(const ScaledGemmArgs& a, cudaStream_t s) {
     p.vec = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.F % (a.f32 ? 8 : 16) == 0;
     p.out_scale = a.out_scale;
 
-    // at most this many tiles (the offsets are on the device): a group adds one ragged tile
-    const long long ft = (a.F + (MODE == kSwiglu ? 127 : 255)) / (MODE == kSwiglu ? 128 : 256);
-    const long long mt = a.offsets ? a.shared_row0 / 128 + a.E + (a.shared_rows + 127) / 128
-                                   : (a.rows + 127) / 128;
-    long long grid = num_sms();
-    if (mt * ft < grid) grid = mt * ft;
-    if (grid < 1) return cudaSuccess;
-    return launch_kernel(scaled_gemm_kernel<MODE>, dim3((unsigned)grid), dim3(kThreads),
-                         (size_t)kSmemBytes, s, x, x32, w0, w1, s0, s1, p);
+    p.split = split;
+    const long long tiles = max_tiles(a, FEW ? 32 : 128);
+    if (tiles < 1) return cudaSuccess;
+    if constexpr (SPLIT) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)split;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = pdl_enabled() ? 2 : 1;
+        err = cudaLaunchKernelEx(&cfg, scaled_gemm_kernel<MODE, FEW, SPLIT>, x, x32, w0, w1, s0, s1, p);
+        return err != cudaSuccess ? err : cudaGetLastError();
+    } else {
+        const long long sms = num_sms();
+        return launch_kernel(scaled_gemm_kernel<MODE, FEW, SPLIT>,
+                             dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kThreads),
+                             (size_t)kSmemBytes, s, x, x32, w0, w1, s0, s1, p);
+    }
+}
+
+template <int MODE>
+cudaError_t choose(const ScaledGemmArgs& a, cudaStream_t s) {
+    // Tiles of 32 rows where groups have few: the same rows in every lane quarter of a tile, so
+    // that all scaling warps share its columns.
+    const bool few = a.offsets ? a.shared_row0 <= (long long)16 * a.E : a.rows <= 32;
+    // Too few tiles for the SMs: 2, 4 or 8 CTAs share a tile's k-blocks (two at least each) and
+    // join their sums through the cluster's shared memory, in rank order.
+    const long long tiles = max_tiles(a, few ? 32 : 128), sms = num_sms();
+    const int nkb = (a.K + kBK - 1) / kBK;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= sms && nkb >= 4 * split) split *= 2;
+    if (split > 1) return few ? run<MODE, 1, 1>(a, split, s) : run<MODE, 0, 1>(a, split, s);
+    return few ? run<MODE, 1, 0>(a, 1, s) : run<MODE, 0, 0>(a, 1, s);
 }
 
 }  // namespace
 
 cudaError_t launch_scaled_gemm(const ScaledGemmArgs& a, cudaStream_t s) {
-    return a.swiglu ? run<kSwiglu>(a, s) : run<kLinear>(a, s);
+    return a.swiglu ? choose<kSwiglu>(a, s) : choose<kLinear>(a, s);
 }
 
 cudaError_t read_scaled_status(unsigned int* out, int clear, cudaStream_t s) {

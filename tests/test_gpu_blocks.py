@@ -167,6 +167,17 @@ def test_matmul_shapes(M, N, K, pad, dtype):
     check_matmul(*operands(M, N, K, M + N + K, pad), dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [
+    # many tiles of one CTA each: of 32 rows, of 128 rows, with and without a ragged last column
+    (5, 40000, 256), (30, 39001, 144), (2500, 2304, 256), (2470, 2401, 272),
+    # two, four and eight CTAs on a tile, k-blocks that do not divide evenly
+    (32, 8192, 1424), (128, 8192, 640), (20, 4097, 2064), (260, 1600, 1680), (17, 700, 7168),
+    (3, 256, 4112), (128, 256, 5264), (100, 131, 4000)])
+def test_matmul_tile_forms(M, N, K, dtype):
+    check_matmul(*operands(M, N, K, M + N + K), dtype)
+
+
 def test_matmul_every_row_and_column_lands_in_its_place():
     """One-hot rows pick single weight columns: exact, and wrong as soon as a row, a column, a
     block or its scale is taken from elsewhere."""
@@ -308,6 +319,15 @@ def check_experts(T, d, I, E, K, shared, seed, skew=0.0, drop=False):
     (700, 512, 384, 4, 4, True), (1500, 256, 128, 3, 2, False)])
 def test_experts(T, d, I, E, K, shared):
     check_experts(T, d, I, E, K, shared, T + d)
+
+
+@pytest.mark.parametrize("T,d,I,E,K,shared", [
+    # many tiles of 32 rows, some experts with more rows than one; then of 128 rows
+    (64, 512, 1024, 40, 4, True), (100, 256, 2048, 48, 7, False), (1200, 640, 1024, 8, 4, True),
+    # few tiles, several CTAs on each: of 32 rows and of 128
+    (2, 2048, 256, 16, 3, True), (40, 1152, 128, 6, 2, True), (200, 1408, 128, 2, 2, False)])
+def test_experts_tile_forms(T, d, I, E, K, shared):
+    check_experts(T, d, I, E, K, shared, T + d + I)
 
 
 def test_experts_skewed_and_undispatched():
