@@ -285,7 +285,7 @@ struct SwigluWs {
 // With e4m3 experts the same space holds the codes and scales of the rows [P + T, d] and of h
 // [P + T, I].  They fit wherever top_k >= 2; the sizes reported cover both.
 struct ScaledWs {
-    size_t x, sx, h, sh, total;
+    size_t x, sx, h, sh, inv, total;
 };
 ScaledWs scaled_ws(int64_t T, int32_t d, int32_t I, int32_t K, int has_shared) {
     ScaledWs w;
@@ -295,6 +295,7 @@ ScaledWs scaled_ws(int64_t T, int32_t d, int32_t I, int32_t K, int has_shared) {
     w.sx = off; off += align256((size_t)R * (d / 128) * 4);
     w.h = off;  off += align256((size_t)R * I);
     w.sh = off; off += align256((size_t)R * (I / 128) * 4);
+    w.inv = off; off += align256((size_t)T * K * 4);
     w.total = off;
     return w;
 }
@@ -342,11 +343,14 @@ ForwardWs forward_ws(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K, int 
 // so no plan splits more than d/512 ways.
 int router_ksplit_bound(int32_t d) { return d / 512 > 1 ? d / 512 : 1; }
 
+constexpr int64_t kInvertMin = 4096;
+
 // e4m3 experts: quantised rows of the dispatch, gate/up product with SwiGLU and quantisation in
 // its epilogue, down product.
 int run_swiglu_scaled(const void* x, int64_t T, int32_t d, int32_t I, int32_t E, int32_t K,
-                      const int32_t* offsets, const int32_t* perm, const moe_expert_weights_t* ex,
-                      const moe_expert_weights_t* sh, void* out, uint8_t* ws, cudaStream_t s) {
+                      const int32_t* offsets, const int32_t* perm, const int32_t* inv,
+                      const moe_expert_weights_t* ex, const moe_expert_weights_t* sh, void* out,
+                      uint8_t* ws, cudaStream_t s) {
     const int64_t P = T * K;
     const ScaledWs lw = scaled_ws(T, d, I, K, sh != nullptr);
     uint8_t* xq = ws + lw.x;
@@ -354,8 +358,20 @@ int run_swiglu_scaled(const void* x, int64_t T, int32_t d, int32_t I, int32_t E,
     uint8_t* hq = ws + lw.h;
     float* shq = reinterpret_cast<float*>(ws + lw.sh);
     const int64_t shared_rows = sh ? T : 0;
-    MOE_LAUNCH(moe::launch_quantize_dispatched(x, perm, offsets, E, K, P, shared_rows, d, xq, sx, s),
+    // Quantising from the tokens' side reads and rounds a row once instead of K + 1 times, but
+    // needs the inverse of perm: the layer has it, a call of the experts alone makes it first
+    // when there are enough rows to pay for two more launches.
+    if (!inv && P >= kInvertMin) {
+        int32_t* own = reinterpret_cast<int32_t*>(ws + lw.inv);
+        MOE_LAUNCH(moe::launch_invert(perm, offsets, E, P, own, s), "invert dispatch");
+        inv = own;
+    }
+    MOE_LAUNCH(moe::launch_quantize_dispatched(x, perm, offsets, inv, E, K, P, shared_rows, d, xq,
+                                             sx, s),
              "quantise rows");
+    // small batches: the products' prologues overlap the tail of the kernel before them
+    PdlScope pdl;
+    if (g_phase_n == 0 && P < moe::kPermMultiMin) pdl.on();
     MOE_CUDA(phase(4, s), "phase event");
     const auto fp = [](const void* q) { return static_cast<const float*>(q); };
     moe::ScaledGemmArgs g = {};
@@ -394,10 +410,11 @@ int run_swiglu_scaled(const void* x, int64_t T, int32_t d, int32_t I, int32_t E,
 }
 
 int run_swiglu(const void* x, int64_t T, int32_t d, int32_t I, int32_t E, int32_t K,
-               const int32_t* offsets, const int32_t* perm, const moe_expert_weights_t* ex,
-               const moe_expert_weights_t* sh, void* out, uint8_t* ws, cudaStream_t s) {
+               const int32_t* offsets, const int32_t* perm, const int32_t* inv,
+               const moe_expert_weights_t* ex, const moe_expert_weights_t* sh, void* out,
+               uint8_t* ws, cudaStream_t s) {
     if (is_scaled(ex))
-        return run_swiglu_scaled(x, T, d, I, E, K, offsets, perm, ex, sh, out, ws, s);
+        return run_swiglu_scaled(x, T, d, I, E, K, offsets, perm, inv, ex, sh, out, ws, s);
     const int64_t P = T * K;
     const SwigluWs lw = swiglu_ws(T, d, I, K, sh != nullptr);
     void* x_perm = ws + lw.x_perm;
@@ -593,8 +610,8 @@ int forward_impl(const moe_layer_args_t& A, void* ws, size_t ws_bytes, cudaStrea
     MOE_CUDA(phase(3, s), "phase event");
 
     // a4 + a5 (+ a7): expert SwiGLU GEMMs, shared expert as the last group
-    rc = run_swiglu(A.x, T, d, I, E, K, offsets, perm, A.experts, A.shared, eo, w + lw.swiglu,
-                    s);
+    rc = run_swiglu(A.x, T, d, I, E, K, offsets, perm, inv, A.experts, A.shared, eo,
+                    w + lw.swiglu, s);
     if (rc) return rc;
 
     // a6: combine (the gated shared expert weighs its row by sigmoid(x . w_shared_gate))
@@ -797,7 +814,7 @@ int moe_grouped_swiglu(const void* x, int64_t T, int32_t d, int32_t I, int32_t E
     if (T == 0) return MOE_OK;
     rc = check_device();
     if (rc) return rc;
-    return run_swiglu(x, T, d, I, E, K, offsets, perm, experts, shared, out,
+    return run_swiglu(x, T, d, I, E, K, offsets, perm, nullptr, experts, shared, out,
                       static_cast<uint8_t*>(ws), (cudaStream_t)stream);
 }
 

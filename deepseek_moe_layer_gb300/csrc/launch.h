@@ -152,10 +152,15 @@ cudaError_t launch_quantize_rows(const void* x, int bf16, long long rows, int n,
 cudaError_t launch_quantize_square(const void* x, int bf16, long long rows, int n, long long ld,
                                    uint8_t* codes, float* scales, cudaStream_t s);
 // Rows of the dispatch: row j < offsets[E] from token perm[j] / K, row P + t from token t
-// (shared_rows of them), of bf16 x [T, d].
+// (shared_rows of them), of bf16 x [T, d].  With inv (pair -> slot, -1: none) each token is
+// quantised once and written to its slots.
 cudaError_t launch_quantize_dispatched(const void* x, const int32_t* perm, const int32_t* offsets,
-                                       int E, int K, long long P, long long shared_rows, int d,
-                                       uint8_t* codes, float* scales, cudaStream_t s);
+                                       const int32_t* inv, int E, int K, long long P,
+                                       long long shared_rows, int d, uint8_t* codes, float* scales,
+                                       cudaStream_t s);
+// inv [P] of perm: -1 for the pairs that are not dispatched.
+cudaError_t launch_invert(const int32_t* perm, const int32_t* offsets, int E, long long P,
+                          int32_t* inv, cudaStream_t s);
 
 struct ScaledWeights {           // e4m3 codes [groups, F, K] and scales, one or two (gate, up)
     const void *w0, *w1;

@@ -59,8 +59,12 @@ MOE_DEV void inf_to_nan(float (&v)[8]) {
         if (fabsf(v[i]) == kInf) v[i] = __int_as_float(0x7FFFFFFF);
 }
 
-// Rows.  GATHER: output row j < P is row perm[j] / K of x when j < *dispatched (else it is left
-// alone), and row P + t (shared rows) is row t.
+// Rows, plain or of a dispatch:
+//   kGather : output row j < P is row perm[j] / K of x when j < *dispatched (else it is left
+//             alone), and row P + t is row t for the shared rows;
+//   kScatter: the same rows from the tokens' side: row t of x is quantised once and written to
+//             the slots inv[t K + k] >= 0, and to P + t.
+enum { kPlain = 0, kGather = 1, kScatter = 2 };
 struct QuantRows {
     const void* x;
     unsigned units;      // half warps with work: rows * ceil(nb / kPer)
@@ -69,15 +73,16 @@ struct QuantRows {
     int n, nb;           // columns (a multiple of 16), blocks of 128 per row
     uint8_t* codes;      // [rows, n]
     float* scales;       // [rows, nb]
-    const int32_t* perm; // GATHER
+    const int32_t* perm; // kGather
     const int32_t* dispatched;
+    const int32_t* inv;  // kScatter
     long long P;
-    int K;
+    int K, shared;
 };
 
 constexpr int kPer = 4;
 
-template <bool BF16, bool GATHER>
+template <bool BF16, int FORM>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantRows a) {
     const int lane = threadIdx.x & 15;
     const unsigned unit = blockIdx.x * 16u + (threadIdx.x >> 4);
@@ -86,9 +91,9 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantRows a) {
     const long long row = r;
     bool on = unit < a.units;
     pdl_launch_dependents();
-    pdl_wait();  // the dispatch (GATHER) or x come from the kernels before
+    pdl_wait();  // the dispatch or x come from the kernels before
     long long src = row;
-    if (GATHER && on) {
+    if (FORM == kGather && on) {
         if (src >= a.P) src -= a.P;
         else if (src < *a.dispatched) src = a.perm[src] / a.K;
         else on = false;
@@ -101,9 +106,10 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantRows a) {
         for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
         if (on && col < a.n) load8<BF16>(a.x, src * a.ld + col, v[u]);
     }
+    uint2 q[kPer];
+    float sc[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-        const int col = (b0 + u) * 128 + lane * 8;
         float m = amax8(v[u]);
 #pragma unroll
         for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
@@ -113,12 +119,35 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantRows a) {
             for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
             inf_to_nan(v[u]);
         }
-        float s, inv;
-        block_scale(m, s, inv);
-        if (on && col < a.n)
-            *reinterpret_cast<uint2*>(a.codes + row * a.n + col) = codes8(v[u], inv);
-        if (on && lane == 0 && b0 + u < a.nb) a.scales[row * a.nb + b0 + u] = s;
+        float inv;
+        block_scale(m, sc[u], inv);
+        q[u] = codes8(v[u], inv);
     }
+    if (!on) return;
+    auto put = [&](long long to) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int col = (b0 + u) * 128 + lane * 8;
+            if (col < a.n) *reinterpret_cast<uint2*>(a.codes + to * a.n + col) = q[u];
+            if (lane == 0 && b0 + u < a.nb) a.scales[to * a.nb + b0 + u] = sc[u];
+        }
+    };
+    if (FORM == kScatter) {
+        for (int k = 0; k < a.K; ++k) {
+            const int32_t to = __ldg(a.inv + row * a.K + k);
+            if (to >= 0) put(to);
+        }
+        if (a.shared) put(a.P + row);
+    } else {
+        put(row);
+    }
+}
+
+// inv[perm[j]] = j for the dispatched slots (the others' pairs keep what inv held).
+__global__ void __launch_bounds__(256) invert_kernel(const int32_t* perm, const int32_t* dispatched,
+                                                     int P, int32_t* inv) {
+    const int j = (int)(blockIdx.x * 256u + threadIdx.x);
+    if (j < P && j < *dispatched) inv[perm[j]] = j;
 }
 
 // 128 x 128 blocks (weights): one CTA per block, its 16 half warps take eight rows each and
@@ -189,8 +218,8 @@ cudaError_t launch_quantize_rows(const void* x, int bf16, long long rows, int n,
                                  uint8_t* codes, float* scales, cudaStream_t s) {
     const QuantRows a = quant_rows(x, rows, ld, n, codes, scales);
     const unsigned grid = (a.units + 15) / 16;
-    return bf16 ? launch_kernel(quant_rows_kernel<true, false>, dim3(grid), dim3(256), 0, s, a)
-                : launch_kernel(quant_rows_kernel<false, false>, dim3(grid), dim3(256), 0, s, a);
+    return bf16 ? launch_kernel(quant_rows_kernel<true, kPlain>, dim3(grid), dim3(256), 0, s, a)
+                : launch_kernel(quant_rows_kernel<false, kPlain>, dim3(grid), dim3(256), 0, s, a);
 }
 
 cudaError_t launch_quantize_square(const void* x, int bf16, long long rows, int n, long long ld,
@@ -203,16 +232,28 @@ cudaError_t launch_quantize_square(const void* x, int bf16, long long rows, int 
                                 ld, n, nb, codes, scales);
 }
 
+cudaError_t launch_invert(const int32_t* perm, const int32_t* offsets, int E, long long P,
+                          int32_t* inv, cudaStream_t s) {
+    const cudaError_t err = cudaMemsetAsync(inv, 0xFF, sizeof(int32_t) * (size_t)P, s);
+    if (err != cudaSuccess) return err;
+    invert_kernel<<<(unsigned)((P + 255) / 256), 256, 0, s>>>(perm, offsets + E, (int)P, inv);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_quantize_dispatched(const void* x, const int32_t* perm, const int32_t* offsets,
-                                       int E, int K, long long P, long long shared_rows, int d,
-                                       uint8_t* codes, float* scales, cudaStream_t s) {
-    QuantRows a = quant_rows(x, P + shared_rows, d, d, codes, scales);
+                                       const int32_t* inv, int E, int K, long long P,
+                                       long long shared_rows, int d, uint8_t* codes, float* scales,
+                                       cudaStream_t s) {
+    QuantRows a = quant_rows(x, inv ? P / K : P + shared_rows, d, d, codes, scales);
     a.perm = perm;
     a.dispatched = offsets + E;
+    a.inv = inv;
     a.P = P;
     a.K = K;
-    const unsigned grid = (a.units + 15) / 16;
-    return launch_kernel(quant_rows_kernel<true, true>, dim3(grid), dim3(256), 0, s, a);
+    a.shared = shared_rows > 0;
+    const dim3 grid((a.units + 15) / 16);
+    return inv ? launch_kernel(quant_rows_kernel<true, kScatter>, grid, dim3(256), 0, s, a)
+               : launch_kernel(quant_rows_kernel<true, kGather>, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace moe

@@ -120,9 +120,9 @@ def test_scaled_experts_need_a_scaled_shared_expert():
 def test_scaled_experts_workspace_and_sizes():
     L = binding.lib()
     need = L.moe_grouped_swiglu_workspace_bytes(4, 256, 128, 16, 1, 1)
-    R = 4 * 1 + 4  # slots: the codes and fp32 scales of the rows and of h, 256-byte aligned
+    R = 4 * 1 + 4  # slots: codes and fp32 scales of the rows and of h, the inverse dispatch
     al = lambda v: (v + 255) // 256 * 256  # noqa: E731
-    scaled = al(R * 256) + al(R * 2 * 4) + al(R * 128) + al(R * 4)
+    scaled = al(R * 256) + al(R * 2 * 4) + al(R * 128) + al(R * 4) + al(4 * 1 * 4)
     assert need >= scaled
     assert _swiglu(_ew(), shared=_ew(), K=1, ws_bytes=scaled - 1) == BAD and "ws_bytes" in _err()
     assert _swiglu(_ew(), E=1024, d=1 << 22, I=128, T=1, K=1) == BAD and "too large" in _err()
