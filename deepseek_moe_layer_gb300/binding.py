@@ -140,6 +140,18 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(t, stream):
+    """cudaStream_t (an int) for a call on tensor t: `stream`, or the current one.  The library
+    launches on the current device, so t has to be there."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    dev = torch._C._cuda_getDevice()
+    if t.get_device() != dev:
+        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{dev}")
+    # (the raw query: torch.cuda.current_stream() alone costs as much as the launch)
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _need(t, dtype, name, device=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -149,6 +161,12 @@ def _need(t, dtype, name, device=None):
         raise ValueError(f"{name} must be contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _need_out(t, dtype, name, shape, device):
+    _need(t, dtype, name, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def route_params(top_k, n_group, topk_group, norm_topk_prob, routed_scaling_factor):
@@ -249,23 +267,28 @@ def route_softmax_grouped(logits, top_k, n_group, topk_group, norm_topk_prob,
     fp32 or None -> (inds int32, scores fp32) [..., K]."""
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("logits must be fp32 or bf16")
-    _need(logits, logits.dtype, "logits")
+    if not logits.is_contiguous():
+        raise ValueError("logits must be contiguous")
     E = logits.shape[-1]
     if bias is not None:
         if bias.dim() != 1 or bias.shape[0] != E:
             raise ValueError("bias must have rank 1 and length E (the last dim of logits)")
         _need(bias, torch.float32, "bias", logits.device)
     rows = logits.numel() // E if E else 0
-    shape = tuple(logits.shape[:-1]) + (int(top_k),)
+    shape = (*logits.shape[:-1], int(top_k))
     if inds is None:
         inds = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    else:
+        _need_out(inds, torch.int32, "inds", shape, logits.device)
     if scores is None:
         scores = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    else:
+        _need_out(scores, torch.float32, "scores", shape, logits.device)
     p = route_params(top_k, n_group, topk_group, norm_topk_prob, routed_scaling_factor)
     dt = MOE_DTYPE_F32 if logits.dtype == torch.float32 else MOE_DTYPE_BF16
-    _check(lib().moe_route_softmax_grouped(_ptr(logits), dt, rows, E, _ptr(bias),
-                                           ctypes.byref(p), _ptr(inds), _ptr(scores),
-                                           _stream(stream)))
+    _check((_lib or lib()).moe_route_softmax_grouped(
+        logits.data_ptr(), dt, rows, E, None if bias is None else bias.data_ptr(),
+        ctypes.byref(p), inds.data_ptr(), scores.data_ptr(), _raw_stream(logits, stream)))
     return inds, scores
 
 
@@ -277,19 +300,21 @@ def quantize_blocks(x, block_rows=1, codes=None, scales=None, stream=None):
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x must be [rows, n] with unit stride along n")
     rows, n = x.shape
-    ld = x.stride(0) if rows > 1 else max(n, 1)
-    R = -(-rows // int(block_rows)) if int(block_rows) > 0 else 0
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows = {block_rows} (1 or 128)")
+    blocks = (-(-rows // block_rows), -(-n // 128))
     if codes is None:
-        codes = torch.empty(rows, n, dtype=torch.float8_e4m3fn, device=x.device)
+        codes = torch.empty((rows, n), dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _need_out(codes, torch.float8_e4m3fn, "codes", (rows, n), x.device)
     if scales is None:
-        scales = torch.empty(R, -(-n // 128), dtype=torch.float32, device=x.device)
-    _need(codes, torch.float8_e4m3fn, "codes", x.device)
-    _need(scales, torch.float32, "scales", x.device)
-    if codes.shape != x.shape or tuple(scales.shape) != (R, -(-n // 128)):
-        raise ValueError(f"codes must be {tuple(x.shape)} and scales {(R, -(-n // 128))}")
-    dt = MOE_DTYPE_F32 if x.dtype == torch.float32 else MOE_DTYPE_BF16
-    _check(lib().moe_quantize_blocks(_ptr(x), dt, rows, n, ld, int(block_rows), _ptr(codes),
-                                     _ptr(scales), _stream(stream)))
+        scales = torch.empty(blocks, dtype=torch.float32, device=x.device)
+    else:
+        _need_out(scales, torch.float32, "scales", blocks, x.device)
+    _check((_lib or lib()).moe_quantize_blocks(
+        x.data_ptr(), MOE_DTYPE_F32 if x.dtype == torch.float32 else MOE_DTYPE_BF16, rows, n,
+        x.stride(0) if rows > 1 else n, block_rows, codes.data_ptr(), scales.data_ptr(),
+        _raw_stream(x, stream)))
     return codes, scales
 
 
@@ -301,26 +326,24 @@ def matmul_blocks(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, st
         raise TypeError(f"a: dtype {a.dtype}, expected {torch.float8_e4m3fn}")
     if a.dim() != 2 or (a.shape[1] > 1 and a.stride(1) != 1):
         raise ValueError("a must be [M, K] with unit stride along K")
-    _need(w, torch.float8_e4m3fn, "w", a.device)
-    _need(a_scale, torch.float32, "a_scale", a.device)
-    _need(w_scale, torch.float32, "w_scale", a.device)
-    if w.dim() != 2 or w.shape[1] != a.shape[1]:
-        raise ValueError(f"w must be [N, {a.shape[1]}]")
-    (M, K), N = a.shape, w.shape[0]
-    kb = -(-K // 128)
-    if tuple(a_scale.shape) != (M, kb) or tuple(w_scale.shape) != (-(-N // 128), kb):
-        raise ValueError(f"a_scale must be {(M, kb)} and w_scale {(-(-N // 128), kb)}")
+    M, K = a.shape
+    if w.dim() != 2 or w.shape[1] != K:
+        raise ValueError(f"w must be [N, {K}]")
+    N, kb, dev = w.shape[0], -(-K // 128), a.device
+    _need(w, torch.float8_e4m3fn, "w", dev)
+    _need_out(a_scale, torch.float32, "a_scale", (M, kb), dev)
+    _need_out(w_scale, torch.float32, "w_scale", (-(-N // 128), kb), dev)
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype, device=a.device)
-    if out.dtype not in (torch.float32, torch.bfloat16):
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        out_dtype = out.dtype
+        _need_out(out, out_dtype, "out", (M, N), dev)
+    if out_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("out must be fp32 or bf16")
-    _need(out, out.dtype, "out", a.device)
-    if tuple(out.shape) != (M, N):
-        raise ValueError(f"out must be {(M, N)}")
-    dt = MOE_DTYPE_F32 if out.dtype == torch.float32 else MOE_DTYPE_BF16
-    lda = a.stride(0) if M > 1 else max(K, 1)
-    _check(lib().moe_matmul_blocks(_ptr(a), _ptr(a_scale), M, lda, _ptr(w), _ptr(w_scale), N, K,
-                                   dt, _ptr(out), _stream(stream)))
+    _check((_lib or lib()).moe_matmul_blocks(
+        a.data_ptr(), a_scale.data_ptr(), M, a.stride(0) if M > 1 else K, w.data_ptr(),
+        w_scale.data_ptr(), N, K, MOE_DTYPE_F32 if out_dtype == torch.float32 else MOE_DTYPE_BF16,
+        out.data_ptr(), _raw_stream(a, stream)))
     return out
 
 
