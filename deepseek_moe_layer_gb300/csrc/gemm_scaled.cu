@@ -100,12 +100,21 @@ struct Params {
     int split;               // SPLIT: CTAs per tile (the cluster's size), k-blocks shared out
 };
 
-MOE_DEV void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t accumulate) {
+// One k-block: four K = 32 steps (32 codes = 32 bytes further each) into one buffer, then the
+// arrivals on `tfull` (the buffer is done) and `empty` (the stage has been read).
+MOE_DEV void umma_block(uint32_t d_tmem, uint64_t dx, uint64_t dw, uint64_t* tfull, uint64_t* empty) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(kIdesc), "r"(accumulate)
+        "{\n\t.reg .pred t;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %9, !t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %3, %4, %9, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %5, %6, %9, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %7, %8, %9, t;\n\t"
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t"
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%11];\n\t}" ::"r"(
+            d_tmem),
+        "l"(dx), "l"(dw), "l"(dx + 2), "l"(dw + 2), "l"(dx + 4), "l"(dw + 4), "l"(dx + 6), "l"(dw + 6),
+        "r"(kIdesc), "r"(smem_u32(tfull)), "r"(smem_u32(empty))
         : "memory");
 }
 
@@ -435,33 +444,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ================================ UMMA issuer ===============================
+        // (few instructions between a buffer's release and its next UMMA: they are on the way
+        // round, 213 -> 209 us)
         if (lane == 0) {
-            int it = 0, s = 0;
+            const int mine = tstart < total ? (total - 1 - tstart) / tstep + 1 : 0;
+            const int n = SPLIT ? (mine > 0 ? kb1 - kb0 : 0) : mine * p.nkb;
+            const uint64_t dx = sdesc_k128(smem_u32(smem)), dw = sdesc_k128(smem_u32(smem) + kABytes);
+            constexpr uint64_t kStep = kStageBytes >> 4;  // descriptors count 16 bytes
+            uint64_t ax = dx, aw = dw;
             uint32_t ph = 0u;
-            bool ok = true;
-            for (int t = tstart; t < total && ok; t += tstep) {
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    if (it > 0 && ++s == kStages) { s = 0; ph ^= 1u; }
-                    const int b = it & 1;
-                    if (!mbar_wait(&full[s], ph, abort) ||
-                        !mbar_wait(&tempty[b], (((uint32_t)it >> 1) & 1u) ^ 1u, abort)) {
-                        record_timeout(abort);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t xs = smem_u32(smem + s * kStageBytes);
-                    const uint64_t dx = sdesc_k128(xs), dw = sdesc_k128(xs + kABytes);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)  // 32 codes = 32 bytes further each
-                        umma_e4m3(tmem + (uint32_t)(b * 256), dx + (uint64_t)(2 * kk),
-                                  dw + (uint64_t)(2 * kk), kk > 0 ? 1u : 0u);
-                    umma_commit(&tfull[b]);
-                    umma_commit(&empty[s]);
+            int s = 0;
+#pragma unroll 1
+            for (int it = 0; it < n; ++it) {
+                const uint32_t b = (uint32_t)it & 1u;
+                if (!mbar_wait(&full[s], ph, abort) ||
+                    !mbar_wait(&tempty[b], (((uint32_t)it >> 1) & 1u) ^ 1u, abort)) {
+                    record_timeout(abort);
+                    break;
+                }
+                tc_fence_after();
+                umma_block(tmem + b * 256u, ax, aw, &tfull[b], &empty[s]);
+                ax += kStep;
+                aw += kStep;
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                    ax = dx;
+                    aw = dw;
                 }
             }
             // every UMMA issued has finished before TMEM is given back
-            if (it > 0) {
+            if (n > 0) {
                 umma_commit(done);
                 mbar_wait(done, 0u, nullptr, 100000000ull);
             }

@@ -193,6 +193,31 @@ def test_matmul_every_row_and_column_lands_in_its_place():
     assert torch.equal(y.double(), ref)
 
 
+def test_matmul_takes_strided_rows_and_a_given_output():
+    a, sa, w, sw = operands(70, 96, 256, 8, pad=64)
+    out = torch.full((72, 96), 5.0, dtype=torch.float32, device=DEV)
+    y = binding.matmul_blocks(a, sa, w, sw, out=out[1:71])
+    assert y.data_ptr() == out[1:71].data_ptr()
+    assert torch.equal(y, binding.matmul_blocks(a.contiguous(), sa, w, sw, out_dtype=torch.float32))
+    assert bool((out[0] == 5).all()) and bool((out[71] == 5).all())
+    # an output that starts off a 32-byte border
+    buf = torch.full((70 * 96 + 1,), 5.0, dtype=torch.float32, device=DEV)
+    z = binding.matmul_blocks(a, sa, w, sw, out=buf[1:].view(70, 96))
+    assert torch.equal(z, y) and float(buf[0]) == 5.0
+
+
+def test_cpu_tensors_are_refused():
+    a, sa, w, sw = operands(4, 16, 128, 1)
+    with pytest.raises(ValueError):
+        binding.matmul_blocks(a.cpu(), sa.cpu(), w.cpu(), sw.cpu())
+    with pytest.raises(ValueError):
+        binding.matmul_blocks(a, sa, w.cpu(), sw)
+    with pytest.raises(ValueError):
+        binding.quantize_blocks(torch.randn(4, 128))
+    with pytest.raises(ValueError):
+        binding.route_softmax_grouped(torch.randn(4, 16), 2, 4, 2, True, 1.0)
+
+
 def test_matmul_nan_stays_in_its_row_and_column():
     a, sa, w, sw = operands(200, 300, 512, 11)
     a, w = a.clone(), w.clone()
@@ -333,6 +358,64 @@ def test_experts_tile_forms(T, d, I, E, K, shared):
 def test_experts_skewed_and_undispatched():
     check_experts(400, 256, 256, 32, 4, True, 1, skew=3.0)
     check_experts(200, 256, 128, 8, 3, True, 2, drop=True)
+
+
+@pytest.mark.parametrize("T,shared", [(3, True), (3, False), (900, True), (2100, False)])
+def test_experts_with_nothing_dispatched(T, shared):
+    """Every pair without an expert: only the shared rows are computed."""
+    g = gen(T)
+    d, I, E, K = 256, 128, 5, 2
+    x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+    ex, sh = make_experts(E, d, I, g), make_experts(1, d, I, g) if shared else None
+    inds = torch.full((T, K), -1, dtype=torch.int32, device=DEV)
+    _, offsets, perm, _ = binding.permute(inds, E)
+    y = binding.grouped_swiglu(x, offsets, perm, K, ex, sh)
+    torch.cuda.synchronize()
+    binding.device_status()
+    if shared:
+        ref, tol = expert_ref(x, sh, 0)
+        check_within(y[T * K:], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs())
+
+
+def test_experts_same_bits_on_another_stream_and_twice():
+    g = gen(31)
+    d, I, E, K = 512, 256, 8, 3
+    ex, sh = make_experts(E, d, I, g), make_experts(1, d, I, g)
+    cases = []
+    for T in (1, 50, 1700):
+        x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+        _, offsets, perm, _ = binding.permute(dispatch(T, E, K, g), E)
+        cases.append((x, offsets, perm, binding.grouped_swiglu(x, offsets, perm, K, ex, sh)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(4):  # all at once, each on a stream and a workspace of its own
+        got = []
+        for (x, o, p, _), st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                got.append(binding.grouped_swiglu(x, o, p, K, ex, sh, stream=st))
+        torch.cuda.synchronize()
+        for c, y in zip(cases, got):
+            assert torch.equal(c[3], y)
+
+
+def test_weights_quantised_by_the_library_serve_as_experts():
+    """bf16 weights through moe_quantize_blocks (128 x 128) into the experts' format."""
+    g = gen(41)
+    d, I, E, K, T = 256, 256, 3, 2, 20
+    ex = {"bits": binding.MOE_BITS_E4M3}
+    for k, (n, m) in (("gate", (I, d)), ("up", (I, d)), ("down", (d, I))):
+        w = (torch.randn(E, n, m, generator=g, device=DEV) / m ** 0.5).to(torch.bfloat16)
+        q = [binding.quantize_blocks(w[e], block_rows=128) for e in range(E)]
+        ex[k] = torch.stack([c.view(torch.uint8) for c, _ in q]).view(F8)
+        ex[k + "_s"] = torch.stack([s for _, s in q])
+    x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+    _, offsets, perm, _ = binding.permute(dispatch(T, E, K, g), E)
+    y = binding.grouped_swiglu(x, offsets, perm, K, ex)
+    off, tok = offsets.tolist(), perm.long() // K
+    for e in range(E):
+        at = slice(off[e], off[e + 1])
+        ref, tol = expert_ref(x[tok[at]], ex, e)
+        check_within(y[at], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs())
 
 
 def test_experts_rows_behind_the_last_slot_are_left_alone():
