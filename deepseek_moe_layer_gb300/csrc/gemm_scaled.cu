@@ -123,6 +123,20 @@ MOE_DEV float nan_for_inf(float v) {
     return fabsf(v) == __int_as_float(0x7F800000) ? __int_as_float(0x7FFFFFFF) : v;
 }
 
+// 16 TMEM columns of the thread's lane, loaded and waited for in one statement: no use of the
+// registers can move ahead of the wait.
+MOE_DEV void tmem_get16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 // acc (16 sums) += 16 TMEM columns of the thread's lane * f.
 MOE_DEV void fold16(float* acc, const uint32_t (&r)[16], float f) {
 #pragma unroll
@@ -175,8 +189,7 @@ MOE_DEV bool sums(float (&acc)[2 * RUN], int n, Rings& rg, const float* f, uint3
             uint32_t u[16];
 #pragma unroll
             for (int c = 0; c < 2 * RUN; c += 16) {
-                tmem_ld16(taddr + b * 256u + (uint32_t)(c < RUN ? c : c - RUN + 128), u);
-                tmem_ld_wait();
+                tmem_get16(taddr + b * 256u + (uint32_t)(c < RUN ? c : c - RUN + 128), u);
                 if (c == 2 * RUN - 16) {  // the last load: the buffer is free before the last sums
                     tc_fence_before();
                     __syncwarp();

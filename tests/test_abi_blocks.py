@@ -169,6 +169,11 @@ def test_binding_checks_types_and_shapes():
         binding.matmul_blocks(a, sa, w, sw, out_dtype=torch.float16)
     with pytest.raises(ValueError):
         binding.route_softmax_grouped(x, 2, 4, 2, True, 1.0, bias=torch.zeros(4))
+    # host memory never reaches the library
+    for call in (lambda: binding.quantize_blocks(x), lambda: binding.matmul_blocks(a, sa, w, sw),
+                 lambda: binding.route_softmax_grouped(x, 2, 4, 2, True, 1.0)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
     e = {"bits": binding.MOE_BITS_E4M3, "gate": torch.zeros(2, 128, 256).to(F8),
          "up": torch.zeros(2, 128, 256).to(F8), "down": torch.zeros(2, 256, 128).to(F8),
          "gate_s": torch.ones(2, 1, 2), "up_s": torch.ones(2, 1, 2), "down_s": torch.ones(2, 2, 1)}
