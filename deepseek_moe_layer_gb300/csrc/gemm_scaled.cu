@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ================================ UMMA issuer ===============================
         // (few instructions between a buffer's release and its next UMMA: they are on the way
-        // round, 213 -> 209 us)
+        // round)
         if (lane == 0) {
             const int mine = tstart < total ? (total - 1 - tstart) / tstep + 1 : 0;
             const int n = SPLIT ? (mine > 0 ? kb1 - kb0 : 0) : mine * p.nkb;
@@ -815,15 +815,22 @@ cudaError_t run(const ScaledGemmArgs& a, int split, cudaStream_t s) {
 
 template <int MODE>
 cudaError_t choose(const ScaledGemmArgs& a, cudaStream_t s) {
-    // Tiles of 32 rows where groups have few: the same rows in every lane quarter of a tile, so
-    // that all scaling warps share its columns.
-    const bool few = a.offsets ? a.shared_row0 <= (long long)16 * a.E : a.rows <= 32;
+    // Experts with few rows: tiles of 32 rows, the same rows in every lane quarter, so that all
+    // scaling warps share the columns instead of two of them doing all (64 experts, 7168 x 2048,
+    // up to 8 / 24 / 32 rows per expert on average: 413 / 472 / 536 us against 473 / 505 / 514 for
+    // tiles of 128 rows).  Not for a single group's product (32 x 32768 x 2048: 13.0 against 12.4
+    // us, 8 rows 12.4 against 12.2; 1 x 2112 x 7168 alone 7.4 against 8.5).
+    const bool few = a.offsets && a.shared_row0 <= (long long)24 * a.E;
     // Too few tiles for the SMs: 2, 4 or 8 CTAs share a tile's k-blocks (two at least each) and
-    // join their sums through the cluster's shared memory, in rank order.
+    // join their sums through the cluster's shared memory, in rank order, if that spares a CTA
+    // at least six k-blocks, which the join costs (1 x 2112 x 7168: 8.5 us against 24.0 for a CTA
+    // per tile; 128 x 16384 x 2048, two CTAs: 12.9 against 13.6; 600 x 3840 x 1024, where two
+    // would spare four k-blocks: 11.3 against 9.6).
     const long long tiles = max_tiles(a, few ? 32 : 128), sms = num_sms();
     const int nkb = (a.K + kBK - 1) / kBK;
     int split = 1;
     while (split < 8 && tiles * split * 2 <= sms && nkb >= 4 * split) split *= 2;
+    if (nkb - nkb / split < 6) split = 1;
     if (split > 1) return few ? run<MODE, 1, 1>(a, split, s) : run<MODE, 0, 1>(a, split, s);
     return few ? run<MODE, 1, 0>(a, 1, s) : run<MODE, 0, 0>(a, 1, s);
 }

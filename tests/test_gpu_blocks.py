@@ -358,9 +358,10 @@ def test_experts_tile_forms(T, d, I, E, K, shared):
 def test_experts_skewed_and_undispatched():
     check_experts(400, 256, 256, 32, 4, True, 1, skew=3.0)
     check_experts(200, 256, 128, 8, 3, True, 2, drop=True)
+    check_experts(3000, 256, 128, 8, 3, True, 3, drop=True)  # by the inverse dispatch
 
 
-@pytest.mark.parametrize("T,shared", [(3, True), (3, False), (900, True), (2100, False)])
+@pytest.mark.parametrize("T,shared", [(3, True), (3, False), (900, True), (4200, False)])
 def test_experts_with_nothing_dispatched(T, shared):
     """Every pair without an expert: only the shared rows are computed."""
     g = gen(T)
