@@ -439,6 +439,42 @@ def test_experts_rows_behind_the_last_slot_are_left_alone():
     assert bool((out[7:] == 7.0).all()) and not bool((out[:7] == 7.0).all())
 
 
+def test_failed_launches_leave_outputs_and_recover():
+    """The host-side fault hook at each launch of the new calls: an error, the outputs of the
+    launches not made as they were, and the same call right afterwards."""
+    g = gen(51)
+    x = torch.randn(40, 256, generator=g, device=DEV)
+    codes = torch.full((40, 256), 1.0, device=DEV).to(F8)
+    scales = torch.full((40, 2), 3.0, device=DEV)
+    ops = operands(40, 96, 256, 2)
+    out = torch.full((40, 96), 5.0, device=DEV)
+    logits = torch.randn(40, 16, generator=g, device=DEV)
+    inds = torch.full((40, 2), 9, dtype=torch.int32, device=DEV)
+    ex = make_experts(4, 256, 128, g)
+    _, offsets, perm, _ = binding.permute(dispatch(40, 4, 2, g), 4)
+    xb = x.to(torch.bfloat16)
+    before = binding.get_fault()
+    try:
+        for at, call in ((0, lambda: binding.quantize_blocks(x, codes=codes, scales=scales)),
+                         (0, lambda: binding.matmul_blocks(*ops, out=out)),
+                         (0, lambda: binding.route_softmax_grouped(logits, 2, 4, 2, True, 1.0, inds=inds)),
+                         (0, lambda: binding.grouped_swiglu(xb, offsets, perm, 2, ex)),
+                         (1, lambda: binding.grouped_swiglu(xb, offsets, perm, 2, ex)),
+                         (2, lambda: binding.grouped_swiglu(xb, offsets, perm, 2, ex))):
+            binding.set_fault(binding.MOE_FAULT_LAUNCH, at)
+            with pytest.raises(binding.MoeError) as e:
+                call()
+            assert e.value.code == binding.MOE_ERR_CUDA and "injected" in str(e.value)
+        torch.cuda.synchronize()
+        assert bool((codes.float() == 1).all()) and bool((scales == 3).all())
+        assert bool((out == 5).all()) and bool((inds == 9).all())
+    finally:
+        binding.set_fault(*before)
+    check_quantize(x, 1)
+    check_matmul(*ops, torch.float32)
+    check_experts(40, 256, 128, 4, 2, False, 52)
+
+
 def test_layer_of_the_parts():
     """moe_forward(_ex) with e4m3 experts is its parts: the gate on the layer's own logits, the
     dispatch, the experts and the combine give the same bits, for both gates."""
