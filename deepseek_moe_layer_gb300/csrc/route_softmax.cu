@@ -13,8 +13,9 @@
 //           is 0), times the scaling factor
 //
 // Selection is exact.  Without a bias it compares the logits themselves (softmax is strictly
-// increasing).  With a bias v is computed in fp32, and where two neighbours in the order stand
-// closer than its rounding can tell (kNear below) the row is selected again in fp64.
+// increasing).  With a bias v is computed in fp32, and where that cannot tell the order (two
+// neighbours among the chosen, or the last of them and any of the others, closer than far_apart
+// below) the row is selected again in fp64.
 //
 // One warp per row; lane l holds the experts l EPL, .. l EPL + EPL - 1.  An arg-max is one
 // redux.max over order-preserving keys and one redux.min over the indices of the maxima; a group
@@ -273,9 +274,7 @@ __global__ void __launch_bounds__(256, EPL <= 8 ? (BIAS ? 4 : 5) : 1)
         int bi = 0, idx = 0;
         look(key, bk, bi);
         float p = 0.0f, before = 0.0f, pb = 0.0f;
-        const int selectable = a.topk_group * (E / a.n_group);
-        const int rounds = BIAS && K < selectable ? K + 1 : K;
-        for (int r = 0; r < rounds; ++r) {
+        for (int r = 0; r < K; ++r) {
             float pe = 0.0f;
             if (BIAS) {
 #pragma unroll
@@ -293,6 +292,19 @@ __global__ void __launch_bounds__(256, EPL <= 8 ? (BIAS ? 4 : 5) : 1)
             if (lane == r) {
                 idx = w;
                 p = BIAS ? pe : v;
+            }
+        }
+        if (BIAS && K < a.topk_group * (E / a.n_group)) {
+            // the last one chosen has to stand clear of all the others, not of the best of them
+            // alone: one further behind with a larger p is off by more (the bound is convex in p,
+            // so its ends 0 and rz cover them all; each one's own p decides where they do not)
+            if (!(before - key_value(warp_max(bk)) > fmaxf(far_apart<EPL>(pb, 0.0f, rz, before),
+                                                           far_apart<EPL>(pb, rz, rz, before)))) {
+                bool close = false;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    close |= key[i] && !(before - key_value(key[i]) > far_apart<EPL>(pb, e[i], rz, before));
+                near |= __any_sync(kFull, close);
             }
         }
         if (BIAS) {

@@ -119,3 +119,41 @@ def test_leading_dims_and_large_batch():
     i2, s2 = binding.route_softmax_grouped(l.view(-1, 96), 4, 3, 2, True, 1.0)
     assert i1.shape == (3, 700, 4) and torch.equal(i1.view(-1, 4), i2) and torch.equal(s1.view(-1, 4), s2)
     check(l.view(-1, 96)[:500], 4, 3, 2, True, 1.0)
+
+
+def dominant_rows(E, K, G, seed, rows=256):
+    """Rows whose border between K and K + 1 lies between two experts of tiny probability some
+    2^-24 apart, and an expert of probability near 1 whose bias puts its value beside theirs: what
+    fp32 leaves of that value is off by many times the gap, in either direction."""
+    r = np.random.default_rng(seed)
+    eg = E // G
+    base = r.normal(0, 0.3, E)
+    J = int(r.integers(E // 2, E))
+    base[J] = np.log(E) + r.uniform(1.5, 4.0)
+    base = base.astype(np.float32).astype(np.float64)
+    p = np.exp(base - base.max())
+    p /= p.sum()
+    c = 0.01
+    want = c - 0.001 * (1 + r.random(E))
+    rest = [x for x in r.permutation(E) if x != J]
+    a, b, top = rest[0], rest[1], rest[2:1 + K]
+    gap = 2.0 ** -24 * r.uniform(1.0, 2.0)
+    want[a], want[b] = c + gap / 2, c - gap / 2
+    want[J] = c + 2.0 ** -24 * r.uniform(-1, 2)
+    want[top] = c + 0.1 + 0.01 * r.random(len(top))
+    bias = (want - p).astype(np.float32)
+    logits = np.repeat(base.astype(np.float32)[None], rows, 0)
+    # the dominant logit a few steps of fp32 to either side: its value moves past the border
+    step = np.spacing(logits[0, J])
+    logits[:, J] += (step * r.integers(-3, 4, rows)).astype(np.float32)
+    logits[:, a] += (1e-5 * r.normal(size=rows)).astype(np.float32)
+    return torch.from_numpy(logits).to(DEV), torch.from_numpy(bias).to(DEV)
+
+
+@pytest.mark.parametrize("E,K,G,tg", [(32, 1, 1, 1), (32, 3, 4, 4), (64, 1, 8, 8), (160, 6, 1, 1),
+                                      (160, 1, 1, 1), (256, 8, 8, 8), (288, 2, 1, 1), (1024, 4, 1, 1)])
+def test_bias_hides_a_dominant_expert(E, K, G, tg):
+    """An expert that fp32 ranks behind the first K + 1 is chosen where 64 bits choose it."""
+    for seed in range(24):
+        logits, bias = dominant_rows(E, K, G, 1000 * E + seed)
+        check(logits, K, G, tg, False, bias=bias)
