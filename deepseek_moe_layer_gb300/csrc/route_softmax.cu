@@ -213,12 +213,13 @@ __device__ __noinline__ void select_exact(const RouteArgs& a, long long row, int
 }
 
 // Above this gap two fp32 values v = p + b stand in their true order.  In units of 2^-24: an own
-// numerator is off by 4 of itself (expf) and its product and Z's reciprocal by 2 more; Z by 4 and
-// EPL + 4 sums, which moves both values alike and so counts for their difference; l - m by |l - m|
-// of it, and x exp(-x) < 0.4; the two sums with the bias by |v| each.
+// numerator is off by 4 of itself (expf), its product and Z's reciprocal by 2 more, and the rounding
+// of l - m by |l - m| of it, with x exp(-x) < 0.4 of the largest; Z by 4, by EPL + 4 sums and by the
+// mean of |l - m| under p (< 5 with 1024 experts), which moves both values alike and so counts for
+// their difference; the two sums with the bias by |v| each.
 template <int EPL>
 MOE_DEV float far_apart(float p, float q, float pmax, float v) {
-    return 0x1p-24f * (6.0f * (p + q) + (EPL + 8) * fabsf(p - q) + 0.8f * pmax + 2.0f * fabsf(v)) *
+    return 0x1p-24f * (6.0f * (p + q) + (EPL + 13) * fabsf(p - q) + 0.8f * pmax + 2.0f * fabsf(v)) *
            1.001f;
 }
 
