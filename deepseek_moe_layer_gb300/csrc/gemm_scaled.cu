@@ -63,9 +63,9 @@ constexpr int kBBytes = 128 * kBK;             // per half
 constexpr int kStageBytes = kABytes + 2 * kBBytes;
 constexpr int kStages = 4;
 constexpr int kBarOff = kStages * kStageBytes;
-// full, empty, tfull, tempty, done, row maxima, ffull, fempty
-constexpr int kNumBars = 2 * kStages + 2 + 2 + 1 + 4 + 2 * kFSlots;
-constexpr int kMiscOff = kBarOff + 8 * kNumBars;
+// full, empty, tfull, tempty, done, row maxima, ffull, fempty, decided
+constexpr int kNumBars = 2 * kStages + 2 + 2 + 1 + 4 + 2 * kFSlots + 1;
+constexpr int kMiscOff = kBarOff + 8 * kNumBars;  // TMEM address, abort, lost
 constexpr int kPrefixOff = (kMiscOff + 16 + 15) / 16 * 16;
 constexpr int kRowOffOff = kPrefixOff + 4 * (kMaxGroups + 1);
 constexpr int kFacOff = (kRowOffOff + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
@@ -146,6 +146,51 @@ MOE_DEV void fold16(float* acc, const uint32_t (&r)[16], float f) {
         acc[i] = v.x;
         acc[i + 1] = v.y;
     }
+}
+
+// A block's sum is 0 or between 2^-18 and 2^25, so it can make a normal number with two scales
+// whose own fp32 product is none: such a factor has lost what its scales hold.  A CTA that met one
+// goes over its tiles a second time and writes them again, now three times over the k-blocks of
+// each: with the factors too large for fp32 (kLarge: less 2^128), with those too small (kSmall:
+// times 2^100) and with all the others, each time 0 for the rest.  The sums are put right in
+// between; the loop over the k-blocks is the same one (a branch for it in there, or a second loop:
+// 8192 x 4096 x 7168 231 .. 269 us against 210).
+enum { kLarge = 0, kSmall = 1, kUsual = 2 };
+constexpr float kFltMax = 0x1.fffffep127f;
+
+MOE_DEV int factor_class(float f, float a, float g) {
+    const float v = fabsf(f);
+    if (v < 0x1p-126f && a != 0.0f && g != 0.0f) return kSmall;
+    return v > kFltMax && fabsf(a) <= kFltMax && fabsf(g) <= kFltMax ? kLarge : kUsual;
+}
+
+// The factor of the scales a and g in the round `cls` of a second time.  A small one's scales are
+// both below 2^23, a large one's both at least 1.
+MOE_DEV float class_factor(float a, float g, int cls) {
+    const float f = a * g;
+    if (factor_class(f, a, g) != cls) return 0.0f;
+    if (cls == kLarge) return (a * 0x1p-64f) * (g * 0x1p-64f);
+    return cls == kSmall ? (a * 0x1p50f) * (g * 0x1p50f) : f;
+}
+
+// What a round left, as the next one needs it.  After the large factors a sum is 0, or so large
+// that the small ones do not move it, neither by what they are nor by 2^100 times that; so the
+// second step leaves it alone, and the others leave 2^100.
+MOE_DEV float after_round(float v, int cls) {
+    if (cls == kLarge) return v * 0x1p64f * 0x1p64f;
+    return cls == kSmall && fabsf(v) < 0x1p60f ? v * 0x1p-100f : v;
+}
+
+// Whether one of a slot's products is lost: n k-blocks of two rows' scales with the halves'.
+__device__ __noinline__ bool any_lost(const float* x0, const float* x1, const float* sw0,
+                                      const float* sw1, int n) {
+    bool any = false;
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < 4; ++j) {
+            const float a = j & 1 ? x1[i] : x0[i], g = j & 2 ? sw1[i] : sw0[i];
+            any |= factor_class(a * g, a, g) != kUsual;
+        }
+    return any;
 }
 
 // One 32-byte store (a whole sector).
@@ -345,6 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t* rowoff = reinterpret_cast<int32_t*>(smem + kRowOffOff);
     uint64_t* ffull = pair + 4;
     uint64_t* fempty = ffull + kFSlots;
+    uint64_t* decided = fempty + kFSlots;
+    volatile int* lost = reinterpret_cast<volatile int*>(smem + kMiscOff + 8);
     float* fac = reinterpret_cast<float*>(smem + kFacOff);
     float* rag = reinterpret_cast<float*>(smem + kEpiOff);
     float* amax = rag;          // kSwiglu: [tile parity][warps of a row][row]
@@ -374,7 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ffull[f], 64);
             mbar_init(&fempty[f], kEpiWarps);
         }
+        mbar_init(decided, 64);
         *abort = 0;
+        *lost = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_x);
         prefetch_tmap(&tm_x32);
@@ -420,35 +469,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0, s = 0;
             uint32_t ph = 0u;
             bool ok = true;
-            for (int t = tstart; t < total && ok; t += tstep) {
-                const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
-                const CUtensorMap* w0 = ti.shared ? &tm_s0 : &tm_w0;
-                const CUtensorMap* w1 = ti.shared ? &tm_s1 : &tm_w1;
-                const int wrow = (ti.shared || !p.offsets ? 0 : ti.g * p.F) + ti.f * kFeat;
-                // only the rows the tile has (32 at a time): the others' products are unused.
-                // FEW: the same rows in every lane quarter, 8 or 32 of them (one token's experts:
-                // 84 -> 77 us)
-                const int boxes = FEW || ti.rows > 96 ? 4 : (ti.rows + 31) / 32;
-                const int per = FEW && ti.rows <= 8 ? 8 : 32;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    if (it > 0 && ++s == kStages) { s = 0; ph ^= 1u; }
-                    if (!mbar_wait(&empty[s], ph ^ 1u, abort)) {
-                        record_timeout(abort);
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* st = smem + s * kStageBytes;
-                    const int kx = kb * kBK;
-                    mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * per * kBK + 2 * kBBytes));
-                    tma_load_2d(st + kABytes, w0, &full[s], kx, wrow, pol_w);
-                    tma_load_2d(st + kABytes + kBBytes, MODE == kSwiglu ? w1 : w0, &full[s], kx,
-                                MODE == kSwiglu ? wrow : wrow + 128, pol_w);
-                    if (!FEW && boxes == 4)
-                        tma_load_2d(st, &tm_x, &full[s], kx, (int)ti.row, pol_x);
-                    else
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(st + b * 32 * kBK, per == 8 ? &tm_x : &tm_x32, &full[s], kx,
-                                        (int)ti.row + (FEW ? 0 : 32 * b), pol_x);
+            int rounds = 1;
+            for (int pass = 0; pass < 2 && ok; ++pass, rounds = 3) {
+                if (pass && !(mbar_wait(decided, 0u, abort) && *lost)) break;
+                for (int t = tstart; t < total && ok; t += tstep) {
+                    const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
+                    const CUtensorMap* w0 = ti.shared ? &tm_s0 : &tm_w0;
+                    const CUtensorMap* w1 = ti.shared ? &tm_s1 : &tm_w1;
+                    const int wrow = (ti.shared || !p.offsets ? 0 : ti.g * p.F) + ti.f * kFeat;
+                    // only the rows the tile has (32 at a time): the others' products are unused.
+                    // FEW: the same rows in every lane quarter, 8 or 32 of them (one token's
+                    // experts: 84 -> 74 us)
+                    const int boxes = FEW || ti.rows > 96 ? 4 : (ti.rows + 31) / 32;
+                    const int per = FEW && ti.rows <= 8 ? 8 : 32;
+                    for (int round = 0; round < rounds && ok; ++round)
+                        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                            if (it > 0 && ++s == kStages) { s = 0; ph ^= 1u; }
+                            if (!mbar_wait(&empty[s], ph ^ 1u, abort)) {
+                                record_timeout(abort);
+                                ok = false;
+                                break;
+                            }
+                            uint8_t* st = smem + s * kStageBytes;
+                            const int kx = kb * kBK;
+                            mbar_arrive_expect_tx(&full[s],
+                                                  (uint32_t)(boxes * per * kBK + 2 * kBBytes));
+                            tma_load_2d(st + kABytes, w0, &full[s], kx, wrow, pol_w);
+                            tma_load_2d(st + kABytes + kBBytes, MODE == kSwiglu ? w1 : w0,
+                                        &full[s], kx, MODE == kSwiglu ? wrow : wrow + 128, pol_w);
+                            if (!FEW && boxes == 4)
+                                tma_load_2d(st, &tm_x, &full[s], kx, (int)ti.row, pol_x);
+                            else
+                                for (int b = 0; b < boxes; ++b)
+                                    tma_load_2d(st + b * 32 * kBK, per == 8 ? &tm_x : &tm_x32,
+                                                &full[s], kx, (int)ti.row + (FEW ? 0 : 32 * b),
+                                                pol_x);
+                        }
                 }
             }
             // no copy may land after the CTA has gone
@@ -465,13 +521,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dx = sdesc_k128(smem_u32(smem)), dw = sdesc_k128(smem_u32(smem) + kABytes);
             constexpr uint64_t kStep = kStageBytes >> 4;  // descriptors count 16 bytes
             uint64_t ax = dx, aw = dw;
-            uint32_t ph = 0u;
+            uint32_t ph = 0u, it = 0u, end = (uint32_t)n;
             int s = 0;
 #pragma unroll 1
-            for (int it = 0; it < n; ++it) {
-                const uint32_t b = (uint32_t)it & 1u;
+            for (;; ++it) {
+                if (it == end) {  // (3 n + n at most: a second time)
+                    if (it != (uint32_t)n || !(mbar_wait(decided, 0u, abort) && *lost)) break;
+                    end *= 4u;
+                }
+                const uint32_t b = it & 1u;
                 if (!mbar_wait(&full[s], ph, abort) ||
-                    !mbar_wait(&tempty[b], (((uint32_t)it >> 1) & 1u) ^ 1u, abort)) {
+                    !mbar_wait(&tempty[b], ((it >> 1) & 1u) ^ 1u, abort)) {
                     record_timeout(abort);
                     break;
                 }
@@ -502,45 +562,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool vec = ((p.nkb | kb0) & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 15) == 0;
         int n = 0;
         bool ok = true;
-        for (int t = tstart; t < total && ok; t += tstep) {
-            const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
-            const long long wb = (long long)(ti.shared || !p.offsets ? 0 : ti.g) * wblocks;
-            const float* sw0 = ti.shared ? p.ssw0 : p.sw0;
-            const float* sw1 = MODE == kSwiglu ? (ti.shared ? p.ssw1 : p.sw1) : sw0;
-            sw0 += (wb + (MODE == kSwiglu ? ti.f : 2 * ti.f)) * p.nkb;
-            sw1 += (wb + (MODE == kSwiglu ? ti.f : min(2 * ti.f + 1, wblocks - 1))) * p.nkb;
-            const float* sx = p.sx + ti.row * p.nkb;
-            const int last = ti.rows - 1;
-            for (int kb = kb0; kb < kb1; kb += kFKb, ++n) {
-                const int s = n % kFSlots;
-                float a[2][kFKb];  // rows w and w + 64 (FEW: the lane's)
+        int rounds = 1;
+        for (int pass = 0; pass < 2 && ok; ++pass, rounds = 3) {
+            if (pass) {
+                mbar_arrive(decided);
+                if (!(mbar_wait(decided, 0u, abort) && *lost)) break;
+            }
+            for (int t = tstart; t < total && ok; t += tstep) {
+                const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
+                const long long wb = (long long)(ti.shared || !p.offsets ? 0 : ti.g) * wblocks;
+                const float* sw0 = ti.shared ? p.ssw0 : p.sw0;
+                const float* sw1 = MODE == kSwiglu ? (ti.shared ? p.ssw1 : p.sw1) : sw0;
+                sw0 += (wb + (MODE == kSwiglu ? ti.f : 2 * ti.f)) * p.nkb;
+                sw1 += (wb + (MODE == kSwiglu ? ti.f : min(2 * ti.f + 1, wblocks - 1))) * p.nkb;
+                const float* sx = p.sx + ti.row * p.nkb;
+                const int last = ti.rows - 1;
+                for (int round = 0; round < rounds && ok; ++round)
+                    for (int kb = kb0; kb < kb1; kb += kFKb, ++n) {
+                        const int s = n % kFSlots;
+                        float a[2][kFKb];  // rows w and w + 64 (FEW: the lane's)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float* x = sx + (long long)min(FEW ? w & 31 : w + 64 * j, last) * p.nkb + kb;
-                    if (vec) {
-                        *reinterpret_cast<float4*>(a[j]) = *reinterpret_cast<const float4*>(x);
-                    } else {
+                        for (int j = 0; j < 2; ++j) {
+                            const int r = min(FEW ? w & 31 : w + 64 * j, last);
+                            const float* x = sx + (long long)r * p.nkb + kb;
+                            if (vec) {
+                                *reinterpret_cast<float4*>(a[j]) = *reinterpret_cast<const float4*>(x);
+                            } else {
 #pragma unroll
-                        for (int i = 0; i < kFKb; ++i) a[j][i] = kb + i < kb1 ? x[i] : 0.0f;
+                                for (int i = 0; i < kFKb; ++i) a[j][i] = kb + i < kb1 ? x[i] : 0.0f;
+                            }
+                        }
+                        if (!mbar_wait(&fempty[s], (((uint32_t)n / kFSlots) & 1u) ^ 1u, abort)) {
+                            record_timeout(abort);
+                            ok = false;
+                            break;
+                        }
+                        float* f = fac + s * kFacFloats + w;
+                        float low = 1.0f, high = 1.0f;
+#pragma unroll
+                        for (int i = 0; i < kFKb; ++i) {
+                            if (kb + i >= kb1) break;
+                            const float g0 = sw0[kb + i], g1 = sw1[kb + i];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float x = a[j][i];
+                                const float f0 = pass ? class_factor(x, g0, round) : x * g0;
+                                const float f1 = pass ? class_factor(x, g1, round) : x * g1;
+                                f[i * 256 + 64 * j] = f0;
+                                f[i * 256 + 128 + 64 * j] = f1;
+                                low = fminf(low, fminf(fabsf(f0), fabsf(f1)));
+                                high = fmaxf(high, fmaxf(fabsf(f0), fabsf(f1)));
+                            }
+                        }
+                        if (!(low >= 0x1p-126f && high <= kFltMax) && !pass) {
+                            const long long r0 = min(FEW ? w & 31 : w, last);
+                            const long long r1 = min(FEW ? w & 31 : w + 64, last);
+                            if (any_lost(sx + r0 * p.nkb + kb, sx + r1 * p.nkb + kb, sw0 + kb,
+                                         sw1 + kb, min(kFKb, kb1 - kb)))
+                                *lost = 1;
+                        }
+                        mbar_arrive(&ffull[s]);
                     }
-                }
-                if (!mbar_wait(&fempty[s], (((uint32_t)n / kFSlots) & 1u) ^ 1u, abort)) {
-                    record_timeout(abort);
-                    ok = false;
-                    break;
-                }
-                float* f = fac + s * kFacFloats + w;
-#pragma unroll
-                for (int i = 0; i < kFKb; ++i) {
-                    if (kb + i >= kb1) break;
-                    const float g0 = sw0[kb + i], g1 = sw1[kb + i];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        f[i * 256 + 64 * j] = a[j][i] * g0;
-                        f[i * 256 + 128 + 64 * j] = a[j][i] * g1;
-                    }
-                }
-                mbar_arrive(&ffull[s]);
             }
         }
     }
@@ -559,118 +641,134 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
         Rings rg = {tfull, tempty, ffull, fempty, 0u, 0u};
         int lt = 0;  // tiles so far
-        for (int t = tstart; t < total; t += tstep, ++lt) {
-            const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
-            const bool mine = r < ti.rows;
-            const bool idle = wr >= ti.rows;  // no row of this warp is in the tile
-            float acc[2 * RUN];
+        bool ok = true;
+        int rounds = 1;
+        for (int pass = 0; pass < 2 && ok; ++pass, rounds = 3) {
+            // (every factor of the tiles has been waited for, and with them what `lost` says)
+            __syncwarp();
+            if (pass && !*lost) break;
+            for (int t = tstart; t < total; t += tstep, ++lt) {
+                const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
+                const bool mine = r < ti.rows;
+                const bool idle = wr >= ti.rows;  // no row of this warp is in the tile
+                float acc[2 * RUN];
 #pragma unroll
-            for (int i = 0; i < 2 * RUN; ++i) acc[i] = 0.0f;
-            if (!(idle ? sums<RUN, false>(acc, kb1 - kb0, rg, fac + r, taddr, abort)
-                       : sums<RUN, true>(acc, kb1 - kb0, rg, fac + r, taddr, abort))) {
-                record_timeout(abort);
-                break;
-            }
-            if constexpr (SPLIT) {
-                // into this CTA's shared memory (every copy into it has been consumed)
-                float* row = reinterpret_cast<float*>(smem) + r * kPartLd + c0;
-                if (mine)
+                for (int i = 0; i < 2 * RUN; ++i) acc[i] = 0.0f;
+                for (int round = 0; round < rounds && ok; ++round) {
+                    ok = idle ? sums<RUN, false>(acc, kb1 - kb0, rg, fac + r, taddr, abort)
+                              : sums<RUN, true>(acc, kb1 - kb0, rg, fac + r, taddr, abort);
+                    if (rounds > 1) {
 #pragma unroll
-                    for (int i = 0; i < 2 * RUN; i += 4)
-                        *reinterpret_cast<float4*>(row + (i < RUN ? i : i - RUN + 128)) =
-                            make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-                break;  // one tile per cluster
-            }
-            else if constexpr (MODE == kSwiglu) {
-                // h over the gate sums' registers, the row's maximum with the other parts
-                float m = 0.0f;
-#pragma unroll
-                for (int i = 0; i < RUN; ++i) {
-                    acc[i] = nan_for_inf(silu(acc[i]) * acc[RUN + i]);
-                    m = fmaxf(m, fabsf(acc[i]));
+                        for (int i = 0; i < 2 * RUN; ++i) acc[i] = after_round(acc[i], round);
+                    }
                 }
-                float* am = amax + (lt & 1) * 256 + r;
-                uint64_t* bar = FEW ? &pair[0] : &pair[q];
-                am[FEW ? 32 * (2 * q + part) : 128 * part] = m;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar);
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, (uint32_t)lt & 1u, abort))) {
+                if (!ok) {
                     record_timeout(abort);
                     break;
                 }
+                if constexpr (SPLIT) {
+                    // into this CTA's shared memory (every copy into it has been consumed, and no
+                    // second time will follow)
+                    float* row = reinterpret_cast<float*>(smem) + r * kPartLd + c0;
+                    if (mine && !(*lost && rounds == 1))
 #pragma unroll
-                for (int o = 0; o < 256; o += kTile) m = fmaxf(m, am[o]);
-                float s, inv;
-                block_scale(m, s, inv);
-                if (mine) {
-                    uint8_t* o = static_cast<uint8_t*>(p.out) + (ti.row + r) * p.F + ti.f * 128 + c0;
-                    if constexpr (FEW) {
-                        *reinterpret_cast<uint4*>(o) = make_uint4(
-                            cvt_e4m3x4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv),
-                            cvt_e4m3x4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv),
-                            cvt_e4m3x4(acc[8] * inv, acc[9] * inv, acc[10] * inv, acc[11] * inv),
-                            cvt_e4m3x4(acc[12] * inv, acc[13] * inv, acc[14] * inv, acc[15] * inv));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float* x = acc + 32 * i + 4 * j;
-                                w[j] = cvt_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-                            }
-                            st_global_32B(o + 32 * i, w);
-                        }
-                    }
-                    if (c0 == 0) p.out_scale[(ti.row + r) * (p.F / 128) + ti.f] = s;
+                        for (int i = 0; i < 2 * RUN; i += 4)
+                            *reinterpret_cast<float4*>(row + (i < RUN ? i : i - RUN + 128)) =
+                                make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                    break;  // one tile per cluster
                 }
-            } else {
+                else if constexpr (MODE == kSwiglu) {
+                    // h over the gate sums' registers, the row's maximum with the other parts
+                    float m = 0.0f;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int n0 = ti.f * 256 + 128 * h + c0;
-                    const float* sum = acc + RUN * h;
-                    if (p.vec && n0 + RUN <= p.F) {
-                        if (mine && p.f32) {
-                            float* o = static_cast<float*>(p.out) + (ti.row + r) * p.ld + n0;
+                    for (int i = 0; i < RUN; ++i) {
+                        acc[i] = nan_for_inf(silu(acc[i]) * acc[RUN + i]);
+                        m = fmaxf(m, fabsf(acc[i]));
+                    }
+                    float* am = amax + (lt & 1) * 256 + r;
+                    uint64_t* bar = FEW ? &pair[0] : &pair[q];
+                    am[FEW ? 32 * (2 * q + part) : 128 * part] = m;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, (uint32_t)lt & 1u, abort));
+                    if (!ok) {
+                        record_timeout(abort);
+                        break;
+                    }
 #pragma unroll
-                            for (int i = 0; i < RUN / 8; ++i) {
+                    for (int o = 0; o < 256; o += kTile) m = fmaxf(m, am[o]);
+                    float s, inv;
+                    block_scale(m, s, inv);
+                    if (mine) {
+                        uint8_t* o = static_cast<uint8_t*>(p.out) + (ti.row + r) * p.F + ti.f * 128 + c0;
+                        if constexpr (FEW) {
+                            *reinterpret_cast<uint4*>(o) = make_uint4(
+                                cvt_e4m3x4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv),
+                                cvt_e4m3x4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv),
+                                cvt_e4m3x4(acc[8] * inv, acc[9] * inv, acc[10] * inv, acc[11] * inv),
+                                cvt_e4m3x4(acc[12] * inv, acc[13] * inv, acc[14] * inv, acc[15] * inv));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
                                 uint32_t w[8];
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(sum[8 * i + j]);
-                                st_global_32B(o + 8 * i, w);
-                            }
-                        } else if (mine) {
-                            uint16_t* o = static_cast<uint16_t*>(p.out) + (ti.row + r) * p.ld + n0;
-#pragma unroll
-                            for (int i = 0; i < RUN / 16; ++i) {
-                                uint32_t w[8];
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    w[j] = pack_bf16x2(sum[16 * i + 2 * j], sum[16 * i + 2 * j + 1]);
-                                st_global_32B(o + 16 * i, w);
+                                for (int j = 0; j < 8; ++j) {
+                                    const float* x = acc + 32 * i + 4 * j;
+                                    w[j] = cvt_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                                }
+                                st_global_32B(o + 32 * i, w);
                             }
                         }
-                    } else if (!idle && n0 < p.F) {
-                        // rows without 32-byte alignment, or the last columns: four columns at
-                        // a time through shared memory, so that a store covers four columns of
-                        // eight rows instead of one of 32
-                        float* piece = rag + (warp - kEpiWarp0) * (32 * kRagLd);
-                        const int pr = lane >> 2, pc = lane & 3;
+                        if (c0 == 0) p.out_scale[(ti.row + r) * (p.F / 128) + ti.f] = s;
+                    }
+                } else {
 #pragma unroll
-                        for (int i = 0; i < RUN / 4; ++i) {
-                            __syncwarp();
+                    for (int h = 0; h < 2; ++h) {
+                        const int n0 = ti.f * 256 + 128 * h + c0;
+                        const float* sum = acc + RUN * h;
+                        if (p.vec && n0 + RUN <= p.F) {
+                            if (mine && p.f32) {
+                                float* o = static_cast<float*>(p.out) + (ti.row + r) * p.ld + n0;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) piece[lane * kRagLd + j] = sum[4 * i + j];
-                            __syncwarp();
-                            const int n = n0 + 4 * i + pc;
+                                for (int i = 0; i < RUN / 8; ++i) {
+                                    uint32_t w[8];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int rr = 8 * k + pr;
-                                if (wr + rr < ti.rows && n < p.F) {
-                                    const long long at = (ti.row + wr + rr) * p.ld + n;
-                                    const float v = piece[rr * kRagLd + pc];
-                                    if (p.f32) static_cast<float*>(p.out)[at] = v;
-                                    else static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
+                                    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(sum[8 * i + j]);
+                                    st_global_32B(o + 8 * i, w);
+                                }
+                            } else if (mine) {
+                                uint16_t* o = static_cast<uint16_t*>(p.out) + (ti.row + r) * p.ld + n0;
+#pragma unroll
+                                for (int i = 0; i < RUN / 16; ++i) {
+                                    uint32_t w[8];
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j)
+                                        w[j] = pack_bf16x2(sum[16 * i + 2 * j], sum[16 * i + 2 * j + 1]);
+                                    st_global_32B(o + 16 * i, w);
+                                }
+                            }
+                        } else if (!idle && n0 < p.F) {
+                            // rows without 32-byte alignment, or the last columns: four columns at
+                            // a time through shared memory, so that a store covers four columns of
+                            // eight rows instead of one of 32
+                            float* piece = rag + (warp - kEpiWarp0) * (32 * kRagLd);
+                            const int pr = lane >> 2, pc = lane & 3;
+#pragma unroll
+                            for (int i = 0; i < RUN / 4; ++i) {
+                                __syncwarp();
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) piece[lane * kRagLd + j] = sum[4 * i + j];
+                                __syncwarp();
+                                const int n = n0 + 4 * i + pc;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int rr = 8 * k + pr;
+                                    if (wr + rr < ti.rows && n < p.F) {
+                                        const long long at = (ti.row + wr + rr) * p.ld + n;
+                                        const float v = piece[rr * kRagLd + pc];
+                                        if (p.f32) static_cast<float*>(p.out)[at] = v;
+                                        else static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
+                                    }
                                 }
                             }
                         }

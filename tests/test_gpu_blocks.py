@@ -548,3 +548,55 @@ def test_noalloc_with_scaled_experts():
         binding._stream()))
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 600, 400), (5, 300, 144), (100, 300, 2064), (400, 20000, 256)])
+@pytest.mark.parametrize("sx,sw", [(-126, -20), (-126, -25), (-20, -126), (-100, -45), (-140, 20),
+                                   (119, 10), (10, 119), (64, 64), (-149, -10)])
+def test_scales_whose_product_is_no_normal_number(sx, sw, M, N, K):
+    """Any fp32 scales: a sum of e4m3 products (2^-18 to 2^25) brings back into range what the
+    product of its two scales alone leaves.  Beside the bound of check_matmul, each of the blocks'
+    steps may lose half the smallest subnormal, 2^-150."""
+    g = gen(M + sx)
+    kb, nb = -(-K // 128), -(-N // 128)
+    a, w = codes_of((M, K), g), codes_of((N, K), g)
+    if sx + sw > 0:  # subnormal codes: sums below 2^-5, some of them 0
+        a = (torch.randint(-7, 8, (M, K), generator=g, device=DEV) * 2.0 ** -9).to(F8)
+        w = (torch.randint(-7, 8, (N, K), generator=g, device=DEV) * 2.0 ** -9).to(F8)
+    a = a.float().mul_(torch.rand(M, 1, generator=g, device=DEV) < 0.9).to(F8)  # rows of zeros
+    # the first k-block and every third row as scales usually are: lost and whole factors side by side
+    sa = torch.full((M, kb), 2.0 ** sx, dtype=torch.float64, device=DEV)
+    sb = torch.full((nb, kb), 2.0 ** sw, dtype=torch.float64, device=DEV)
+    if sx + sw < 0:
+        sa[::3], sb[:, 0] = 2.0 ** -60, 2.0 ** -70
+        sa[M // 2, kb - 1] = 0.0
+    sa *= 1 if sx < -126 else 1 + torch.rand(M, kb, generator=g, device=DEV) / 2
+    sb *= 1 + torch.rand(nb, kb, generator=g, device=DEV) / 2
+    sa, sb = sa.float(), sb.float()
+    y = binding.matmul_blocks(a, sa, w, sb, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    binding.device_status()
+    ref, tol = product64(a.double() * spread(sa, M, K, 1), w.double() * spread(sb, N, K, 128), kb)
+    assert float(ref.abs().max()) < 2.0 ** 127
+    check_within(y, ref, tol + (kb + 2) * 2.0 ** -149)
+
+
+@pytest.mark.parametrize("T,E", [(3, 8), (40, 6), (600, 3)])
+def test_experts_with_scales_whose_product_is_no_normal_number(T, E):
+    """The down product's two scales together near 2^-147, its rows near 2^-129 (where bf16's own
+    rounding is 2^-134)."""
+    g = gen(T)
+    d, I, K = 256, 128, 2
+    ex = make_experts(E, d, I, g)
+    for k, e in (("gate_s", -46), ("up_s", -52), ("down_s", -30)):
+        ex[k] = (ex[k].double() * 2.0 ** e).float()
+    x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+    _, offsets, perm, _ = binding.permute(dispatch(T, E, K, g), E)
+    y = binding.grouped_swiglu(x, offsets, perm, K, ex)
+    torch.cuda.synchronize()
+    off, tok = offsets.tolist(), perm.long() // K
+    for e in range(E):
+        if off[e + 1] > off[e]:
+            at = slice(off[e], off[e + 1])
+            ref, tol = expert_ref(x[tok[at]], ex, e)
+            check_within(y[at], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs() + 2.0 ** -134)
