@@ -204,10 +204,14 @@ int check_weights(const moe_expert_weights_t* w, const char* what, int shared, b
     return MOE_OK;
 }
 
+// Columns and weight rows of the e4m3 kernels: 32-bit counts, rounded up to tiles of 256 and to
+// four blocks of 128.
+constexpr int64_t kMaxScaledWidth = ((int64_t)1 << 31) - 512;
+
 // A weight row's index is a 32-bit copy coordinate, and so is a tile's.
 int check_scaled_dims(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K) {
     const int64_t wide = d > I ? d : I;
-    MOE_CHECK(E * wide < ((int64_t)1 << 31) &&
+    MOE_CHECK(E * wide <= kMaxScaledWidth &&
                   (T * (K + 1) / 128 + E + 1) * (wide / 128) < ((int64_t)1 << 31) &&
                   T * (K + 1) * (d / 128) < ((int64_t)1 << 31),
               "T = %lld, E = %d, d = %d, I = %d: too large for e4m3 experts", (long long)T, E, d, I);
@@ -950,7 +954,8 @@ int moe_quantize_blocks(const void* x, moe_dtype_t dtype, int64_t rows, int32_t 
     MOE_CHECK(dtype == MOE_DTYPE_F32 || dtype == MOE_DTYPE_BF16, "dtype %d unknown", (int)dtype);
     MOE_CHECK(rows >= 0 && rows < ((int64_t)1 << 31), "rows = %lld outside [0, 2^31)",
               (long long)rows);
-    MOE_CHECK(n >= 16 && n % 16 == 0, "n = %d must be a positive multiple of 16", n);
+    MOE_CHECK(n >= 16 && n % 16 == 0 && n <= kMaxScaledWidth,
+              "n = %d must be a positive multiple of 16, at most 2^31 - 512", n);
     MOE_CHECK(block_rows == 1 || block_rows == 128, "block_rows = %d (1 or 128)", block_rows);
     const int per16 = dtype == MOE_DTYPE_BF16 ? 8 : 4;
     MOE_CHECK(ld >= n && ld % per16 == 0, "ld = %lld must be at least n = %d and a multiple of %d",
@@ -981,8 +986,9 @@ int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t ld
     MOE_CHECK(out_dtype == MOE_DTYPE_F32 || out_dtype == MOE_DTYPE_BF16, "dtype %d unknown",
               (int)out_dtype);
     MOE_CHECK(M >= 0 && M < ((int64_t)1 << 31), "M = %lld outside [0, 2^31)", (long long)M);
-    MOE_CHECK(N >= 1, "N = %d < 1", N);
-    MOE_CHECK(K >= 16 && K % 16 == 0, "K = %d must be a positive multiple of 16", K);
+    MOE_CHECK(N >= 1 && N <= kMaxScaledWidth, "N = %d outside [1, 2^31 - 512]", N);
+    MOE_CHECK(K >= 16 && K % 16 == 0 && K <= kMaxScaledWidth,
+              "K = %d must be a positive multiple of 16, at most 2^31 - 512", K);
     MOE_CHECK(lda >= K && lda % 16 == 0, "lda = %lld must be at least K = %d and a multiple of 16",
               (long long)lda, K);
     MOE_CHECK((M + 127) / 128 * (((int64_t)N + 127) / 128) < ((int64_t)1 << 31),

@@ -200,8 +200,8 @@ int moe_route_softmax_grouped(const void* logits, moe_dtype_t dtype, int64_t row
  * With A the block's largest finite magnitude, its scale s is the smallest power of two
  * >= 2^-126 with A / s <= 448 (1 when A = 0), and a code is x / s rounded to nearest, ties to
  * even.  NaN and infinities become the e4m3 NaN.
- * Errors: MOE_ERR_INVALID for NULL pointers, an unknown dtype, rows < 0, n not a positive
- * multiple of 16, ld < n or not a multiple of 16 bytes, block_rows not 1 or 128, x or codes not
+ * Errors: MOE_ERR_INVALID for NULL pointers, an unknown dtype, rows outside [0, 2^31), n not a
+ * positive multiple of 16 up to 2^31 - 512, ld < n or not a multiple of 16 bytes, block_rows not 1 or 128, x or codes not
  * 16-byte aligned, 2^31 blocks or more.  rows == 0 is a no-op.
  */
 int moe_quantize_blocks(const void* x, moe_dtype_t dtype, int64_t rows, int32_t n, int64_t ld,
@@ -215,8 +215,8 @@ int moe_quantize_blocks(const void* x, moe_dtype_t dtype, int64_t rows, int32_t 
  *   w_scale fp32 [ceil(N / 128), ceil(K / 128)]; the scales are any fp32 numbers.  A block's
  *   sum runs in the tensor cores' fp32, the sum over the blocks in fp32, and out [M, N] is that
  *   (MOE_DTYPE_F32) or rounded once (MOE_DTYPE_BF16).
- * Errors: MOE_ERR_INVALID for NULL pointers, an unknown dtype, M < 0, N < 1, K not a positive
- * multiple of 16, lda < K or not a multiple of 16, a or w not 16-byte aligned, 2^31 tiles of
+ * Errors: MOE_ERR_INVALID for NULL pointers, an unknown dtype, M outside [0, 2^31), N outside
+ * [1, 2^31 - 512], K not a positive multiple of 16 up to 2^31 - 512, lda < K or not a multiple of 16, a or w not 16-byte aligned, 2^31 tiles of
  * 128 x 128 or more.  M == 0 is a no-op.
  */
 int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t lda, const void* w,

@@ -182,3 +182,20 @@ def test_binding_checks_types_and_shapes():
         binding.expert_weights({**e, "down_s": torch.ones(2, 1, 2)})
     with pytest.raises(TypeError):
         binding.expert_weights({**e, "up": torch.zeros(2, 128, 256)})
+
+
+# The kernels count columns in 32 bits, rounded up to their tiles: the last sizes below 2^31 are
+# refused (they would have been counted as negative, past every bound).
+@pytest.mark.parametrize("n", [(1 << 31) - 16, (1 << 31) - 128, (1 << 31) - 496])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_refuses_sizes_that_round_up_past_32_bits(n, block_rows):
+    assert _quant(rows=1, n=n, ld=n, block_rows=block_rows) == BAD
+    assert f"n = {n}" in _err()
+
+
+@pytest.mark.parametrize("kw", [dict(N=(1 << 31) - 1, K=16, lda=16), dict(N=(1 << 31) - 511, K=16, lda=16),
+                                dict(K=(1 << 31) - 16, lda=(1 << 31) - 16, N=1),
+                                dict(K=(1 << 31) - 496, lda=(1 << 31) - 496, N=1)])
+def test_matmul_refuses_sizes_that_round_up_past_32_bits(kw):
+    assert _matmul(M=1, **kw) == BAD
+    assert ("K = " if kw["K"] > 16 else "N = ") in _err()
