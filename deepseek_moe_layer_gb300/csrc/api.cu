@@ -986,13 +986,14 @@ int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t ld
     MOE_CHECK(out_dtype == MOE_DTYPE_F32 || out_dtype == MOE_DTYPE_BF16, "dtype %d unknown",
               (int)out_dtype);
     MOE_CHECK(M >= 0 && M < ((int64_t)1 << 31), "M = %lld outside [0, 2^31)", (long long)M);
-    MOE_CHECK(N >= 1 && N <= kMaxScaledWidth, "N = %d outside [1, 2^31 - 512]", N);
+    MOE_CHECK(N >= 1, "N = %d < 1", N);
     MOE_CHECK(K >= 16 && K % 16 == 0 && K <= kMaxScaledWidth,
               "K = %d must be a positive multiple of 16, at most 2^31 - 512", K);
     MOE_CHECK(lda >= K && lda % 16 == 0, "lda = %lld must be at least K = %d and a multiple of 16",
               (long long)lda, K);
     MOE_CHECK((M + 127) / 128 * (((int64_t)N + 127) / 128) < ((int64_t)1 << 31),
               "M x N = %lld x %d has too many tiles", (long long)M, N);
+    MOE_CHECK(N <= kMaxScaledWidth, "N = %d above 2^31 - 512", N);
     MOE_CHECK(w && w_scale && (M == 0 || (a && a_scale && out)), "NULL pointer argument");
     MOE_CHECK(aligned(a, 16) && aligned(w, 16), "a and w must be 16-byte aligned");
     MOE_CHECK(aligned(a_scale, 4) && aligned(w_scale, 4) &&
