@@ -174,11 +174,17 @@ def route_params(top_k, n_group, topk_group, norm_topk_prob, routed_scaling_fact
                        float(routed_scaling_factor))
 
 
-def expert_weights(w: dict | None):
+def _is_scaled(w):
+    return w is not None and int(w.get("bits", 16)) == MOE_BITS_E4M3
+
+
+def expert_weights(w: dict | None, shape=None, device=None):
     """ExpertWeights from a dict: bits 16 -> gate/up/down bf16; bits 8 or 4 -> gate/up/down
     int32 (packed uint32 words) plus gate_s/gate_b/up_s/up_b/down_s/down_b fp16 and an
     optional 'group' (inputs per scale: 32, 64 or 128; default 64); bits MOE_BITS_E4M3 ->
-    gate/up/down float8_e4m3fn plus gate_s/up_s/down_s fp32 [.., rows/128, inputs/128]."""
+    gate/up/down float8_e4m3fn plus gate_s/up_s/down_s fp32 [.., rows/128, inputs/128], which
+    are held against shape (E, d, I) and device where given: gate, up [E, I, d], down [E, d, I]
+    (E = 1: without it, too)."""
     if w is None:
         return None
     bits = int(w.get("bits", 16))
@@ -190,8 +196,13 @@ def expert_weights(w: dict | None):
     if bits == MOE_BITS_E4M3:
         for k in ("gate", "up", "down"):
             q, sc = w[k], w[k + "_s"]
-            _need(q, torch.float8_e4m3fn, k)
+            _need(q, torch.float8_e4m3fn, k, device)
             _need(sc, torch.float32, k + "_s", q.device)
+            if shape is not None:
+                E, d, I = shape
+                full = (E, d, I) if k == "down" else (E, I, d)
+                if q.shape != full and not (E == 1 and q.shape == full[1:]):
+                    raise ValueError(f"{k}: shape {tuple(q.shape)}, expected {full}")
             want = tuple(q.shape[:-2]) + (-(-q.shape[-2] // 128), -(-q.shape[-1] // 128))
             if tuple(sc.shape) != want:
                 raise ValueError(f"{k}_s: shape {tuple(sc.shape)}, expected {want}")
@@ -436,8 +447,17 @@ def grouped_swiglu(x, offsets, perm, K, experts, shared=None, I=None, ws=None, s
     T, d = x.shape
     E = offsets.numel() - 1
     I = I if I is not None else (experts["gate"].shape[1])
-    ew, sw = expert_weights(experts), expert_weights(shared)
     P = T * K
+    if _is_scaled(experts):
+        ew = expert_weights(experts, (E, d, I), x.device)
+        sw = expert_weights(shared, (1, d, I), x.device)
+        _need(offsets, torch.int32, "offsets", x.device)
+        _need(perm, torch.int32, "perm", x.device)
+        if perm.numel() < P:
+            raise ValueError(f"perm holds {perm.numel()} pairs, not T * K = {P}")
+        _raw_stream(x, stream)  # (on the current device)
+    else:
+        ew, sw = expert_weights(experts), expert_weights(shared)
     out = torch.empty(P + (T if shared is not None else 0), d, dtype=torch.bfloat16,
                       device=x.device)
     need = grouped_swiglu_workspace_bytes(T, d, I, E, K, shared is not None)
@@ -492,7 +512,9 @@ class MoELayer:
         self.I = experts["gate"].shape[1]
         self.params = route_params(top_k, n_group, topk_group, norm_topk_prob,
                                    routed_scaling_factor)
-        self.ew, self.sw = expert_weights(experts), expert_weights(shared)
+        self.scaled = _is_scaled(experts)
+        of = lambda E: ((E, self.d, self.I), self.dev) if self.scaled else ()  # noqa: E731
+        self.ew, self.sw = expert_weights(experts, *of(self.E)), expert_weights(shared, *of(1))
         self.ws = None
 
     def _args(self, x, y, inds, scores, logits):
@@ -531,6 +553,12 @@ class MoELayer:
         _need(x, torch.bfloat16, "x", self.dev)
         T, d = x.shape
         K = self.params.top_k
+        if self.scaled:
+            if d != self.d:
+                raise ValueError(f"x must be [T, {self.d}], not {tuple(x.shape)}")
+            if y is not None:
+                _need_out(y, torch.bfloat16, "y", (T, d), self.dev)
+            _raw_stream(x, stream)  # (on the current device)
         ws = self.workspace(T)
         if y is None:
             y = torch.empty(T, d, dtype=torch.bfloat16, device=self.dev)

@@ -199,3 +199,83 @@ def test_quantize_refuses_sizes_that_round_up_past_32_bits(n, block_rows):
 def test_matmul_refuses_sizes_that_round_up_past_32_bits(kw):
     assert _matmul(M=1, **kw) == BAD
     assert ("K = " if kw["K"] > 16 else "N = ") in _err()
+
+
+def _dict(E, d, I, device="cpu"):
+    z = lambda *s: torch.zeros(*s, device=device).to(F8)  # noqa: E731
+    one = lambda *s: torch.ones(*s, device=device)  # noqa: E731
+    b = lambda n: -(-n // 128)  # noqa: E731
+    return {"bits": binding.MOE_BITS_E4M3, "gate": z(E, I, d), "up": z(E, I, d), "down": z(E, d, I),
+            "gate_s": one(E, b(I), b(d)), "up_s": one(E, b(I), b(d)), "down_s": one(E, b(d), b(I))}
+
+
+def _other(w, key, E, d, I):
+    """w with `key` and its scales of another shape."""
+    o = _dict(E, d, I)
+    return {**w, key: o[key], key + "_s": o[key + "_s"]}
+
+
+GOOD = (4, 256, 128)  # E, d, I
+
+
+@pytest.mark.parametrize("experts,shared,msg", [
+    (_dict(3, 256, 128), None, "gate"),                                   # fewer than E experts
+    (_dict(4, 384, 128), None, "gate"),                                   # another width than x
+    (_other(_dict(*GOOD), "up", 4, 256, 256), None, "up"),                # up of another I
+    (_other(_dict(*GOOD), "up", 2, 256, 128), None, "up"),
+    (_other(_dict(*GOOD), "down", 4, 256, 256), None, "down"),
+    (_other(_dict(*GOOD), "down", 3, 256, 128), None, "down"),
+    (_dict(*GOOD), _dict(1, 256, 256), "gate"),                           # a shared expert of its own I
+    (_dict(*GOOD), _other(_dict(1, 256, 128), "down", 1, 128, 128), "down"),
+])
+def test_experts_of_other_shapes_never_reach_the_library(experts, shared, msg):
+    """Codes and scales agree with each other, but not with x, the dispatch or the other weights."""
+    x = torch.zeros(5, 256, dtype=torch.bfloat16)
+    offsets, perm = torch.zeros(5, dtype=torch.int32), torch.zeros(10, dtype=torch.int32)
+    with pytest.raises(ValueError, match=msg):
+        binding.grouped_swiglu(x, offsets, perm, 2, experts, shared, I=128)
+    with pytest.raises(ValueError, match=msg):
+        binding.MoELayer(torch.zeros(4, 256, dtype=torch.bfloat16), None, {**experts, "gate": experts["gate"]},
+                         shared, 2, 1, 1, True, 1.0, route_kind=binding.MOE_ROUTE_SOFTMAX)
+
+
+def test_shared_experts_may_leave_out_their_only_dimension():
+    one = {k: v[0] if isinstance(v, torch.Tensor) else v for k, v in _dict(1, 256, 128).items()}
+    for shared in (one, _dict(1, 256, 128)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            binding.grouped_swiglu(torch.zeros(5, 256, dtype=torch.bfloat16),
+                                   torch.zeros(5, dtype=torch.int32), torch.zeros(10, dtype=torch.int32),
+                                   2, _dict(*GOOD), shared)
+
+
+def test_e4m3_experts_check_the_dispatch_and_the_device():
+    x = torch.zeros(5, 256, dtype=torch.bfloat16)
+    offsets, perm = torch.zeros(5, dtype=torch.int32), torch.zeros(10, dtype=torch.int32)
+    w = _dict(*GOOD)
+    with pytest.raises(TypeError, match="offsets"):
+        binding.grouped_swiglu(x, offsets.long(), perm, 2, w)
+    with pytest.raises(TypeError, match="perm"):
+        binding.grouped_swiglu(x, offsets, perm.long(), 2, w)
+    with pytest.raises(ValueError, match="perm"):
+        binding.grouped_swiglu(x, offsets, perm[:9].contiguous(), 2, w)
+    with pytest.raises(ValueError, match="perm"):
+        binding.grouped_swiglu(x, offsets, torch.zeros(20, dtype=torch.int32)[::2], 2, w)
+    with pytest.raises(ValueError, match="CUDA device"):
+        binding.grouped_swiglu(x, offsets, perm, 2, w)
+    meta = _dict(*GOOD, device="meta")
+    with pytest.raises(ValueError, match="gate is on meta"):
+        binding.grouped_swiglu(x, offsets, perm, 2, meta)
+    with pytest.raises(ValueError, match="gate is on meta"):
+        binding.MoELayer(torch.zeros(4, 256, dtype=torch.bfloat16), None, meta, None, 2, 1, 1, True, 1.0,
+                         route_kind=binding.MOE_ROUTE_SOFTMAX)
+
+
+def test_e4m3_layer_checks_its_rows():
+    layer = binding.MoELayer(torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(4), _dict(*GOOD), None,
+                             2, 1, 1, True, 1.0)
+    with pytest.raises(ValueError, match="x must be"):
+        layer(torch.zeros(5, 384, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="y must be"):
+        layer(torch.zeros(5, 256, dtype=torch.bfloat16), y=torch.zeros(4, 256, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="CUDA device"):
+        layer(torch.zeros(5, 256, dtype=torch.bfloat16))
