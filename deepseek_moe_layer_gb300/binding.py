@@ -509,6 +509,8 @@ class MoELayer:
         self.w_router, self.bias, self.logit_offset = w_router, bias, logit_offset
         self.experts, self.shared = experts, shared
         self.E, self.d = w_router.shape
+        if self.route_kind == MOE_ROUTE_SOFTMAX_GROUPED and bias is not None and bias.shape != (self.E,):
+            raise ValueError(f"bias must be [{self.E}], not {tuple(bias.shape)}")
         self.I = experts["gate"].shape[1]
         self.params = route_params(top_k, n_group, topk_group, norm_topk_prob,
                                    routed_scaling_factor)

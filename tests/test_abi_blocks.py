@@ -279,3 +279,11 @@ def test_e4m3_layer_checks_its_rows():
         layer(torch.zeros(5, 256, dtype=torch.bfloat16), y=torch.zeros(4, 256, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="CUDA device"):
         layer(torch.zeros(5, 256, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("shape", [(3,), (5,), (1, 4)])
+def test_grouped_gate_of_a_layer_checks_its_bias(shape):
+    """The gate reads E of them."""
+    with pytest.raises(ValueError, match="bias"):
+        binding.MoELayer(torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(shape), _dict(*GOOD), None,
+                         2, 1, 1, True, 1.0, route_kind=binding.MOE_ROUTE_SOFTMAX_GROUPED)
