@@ -152,6 +152,28 @@ def _raw_stream(t, stream):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _torch_stream(stream):
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream)
+
+
+def _empty(shape, dtype, device, stream, returned=True):
+    """Memory that a call on `stream` writes.  It comes from that stream's pool: what the current
+    one's pool hands out may still be in use there by work queued before.  A result that is
+    `returned` is also marked as used by the caller's stream, so that its memory is not written
+    again before what the caller does with it."""
+    stream = _torch_stream(stream)
+    if stream is None or stream.device != device:
+        return torch.empty(shape, dtype=dtype, device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and caller != stream:
+        t.record_stream(caller)
+    return t
+
+
 def _need(t, dtype, name, device=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -243,9 +265,9 @@ def route_deepseek(logits, bias, top_k, n_group, topk_group, norm_topk_prob,
     rows = logits.numel() // E if E else 0
     shape = tuple(logits.shape[:-1]) + (int(top_k),)
     if inds is None:
-        inds = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        inds = _empty(shape, torch.int32, logits.device, stream)
     if scores is None:
-        scores = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        scores = _empty(shape, torch.float32, logits.device, stream)
     p = route_params(top_k, n_group, topk_group, norm_topk_prob, routed_scaling_factor)
     dt = MOE_DTYPE_F32 if logits.dtype == torch.float32 else MOE_DTYPE_BF16
     _check(lib().moe_route_deepseek(_ptr(logits), dt, rows, E, _ptr(bias), ctypes.byref(p),
@@ -262,9 +284,9 @@ def route_softmax(logits, top_k, inds=None, scores=None, stream=None):
     rows = logits.numel() // E if E else 0
     shape = tuple(logits.shape[:-1]) + (int(top_k),)
     if inds is None:
-        inds = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        inds = _empty(shape, torch.int32, logits.device, stream)
     if scores is None:
-        scores = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        scores = _empty(shape, torch.float32, logits.device, stream)
     dt = MOE_DTYPE_F32 if logits.dtype == torch.float32 else MOE_DTYPE_BF16
     _check(lib().moe_route_softmax(_ptr(logits), dt, rows, E, int(top_k), _ptr(inds),
                                    _ptr(scores), _stream(stream)))
@@ -288,11 +310,11 @@ def route_softmax_grouped(logits, top_k, n_group, topk_group, norm_topk_prob,
     rows = logits.numel() // E if E else 0
     shape = (*logits.shape[:-1], int(top_k))
     if inds is None:
-        inds = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        inds = _empty(shape, torch.int32, logits.device, stream)
     else:
         _need_out(inds, torch.int32, "inds", shape, logits.device)
     if scores is None:
-        scores = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        scores = _empty(shape, torch.float32, logits.device, stream)
     else:
         _need_out(scores, torch.float32, "scores", shape, logits.device)
     p = route_params(top_k, n_group, topk_group, norm_topk_prob, routed_scaling_factor)
@@ -315,11 +337,11 @@ def quantize_blocks(x, block_rows=1, codes=None, scales=None, stream=None):
         raise ValueError(f"block_rows = {block_rows} (1 or 128)")
     blocks = (-(-rows // block_rows), -(-n // 128))
     if codes is None:
-        codes = torch.empty((rows, n), dtype=torch.float8_e4m3fn, device=x.device)
+        codes = _empty((rows, n), torch.float8_e4m3fn, x.device, stream)
     else:
         _need_out(codes, torch.float8_e4m3fn, "codes", (rows, n), x.device)
     if scales is None:
-        scales = torch.empty(blocks, dtype=torch.float32, device=x.device)
+        scales = _empty(blocks, torch.float32, x.device, stream)
     else:
         _need_out(scales, torch.float32, "scales", blocks, x.device)
     _check((_lib or lib()).moe_quantize_blocks(
@@ -345,7 +367,7 @@ def matmul_blocks(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, st
     _need_out(a_scale, torch.float32, "a_scale", (M, kb), dev)
     _need_out(w_scale, torch.float32, "w_scale", (-(-N // 128), kb), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = _empty((M, N), out_dtype, dev, stream)
     else:
         out_dtype = out.dtype
         _need_out(out, out_dtype, "out", (M, N), dev)
@@ -363,7 +385,7 @@ def shared_gate(x, w_gate, stream=None):
     _need(x, torch.bfloat16, "x")
     _need(w_gate, torch.bfloat16, "w_gate", x.device)
     T, d = x.shape
-    g = torch.empty(T, dtype=torch.float32, device=x.device)
+    g = _empty(T, torch.float32, x.device, stream)
     _check(lib().moe_shared_gate(_ptr(x), T, d, _ptr(w_gate), _ptr(g), _stream(stream)))
     return g
 
@@ -376,7 +398,7 @@ def combine_gated(expert_out, scores, inv_perm, shared_out, gate, stream=None):
     _need(gate, torch.float32, "gate")
     T, K = scores.shape
     d = expert_out.shape[1]
-    y = torch.empty(T, d, dtype=torch.bfloat16, device=expert_out.device)
+    y = _empty((T, d), torch.bfloat16, expert_out.device, stream)
     _check(lib().moe_combine_gated(_ptr(expert_out), _ptr(scores), _ptr(inv_perm),
                                    _ptr(shared_out), _ptr(gate), T, K, d, _ptr(y),
                                    _stream(stream)))
@@ -399,9 +421,9 @@ def indexer_topk(scores, k, lengths=None, want_mask=False, inds=None, mask=None,
         if lengths.shape != (rows,):
             raise ValueError("lengths must be [rows]")
     if inds is None:
-        inds = torch.empty(rows, int(k), dtype=torch.int32, device=scores.device)
+        inds = _empty((rows, int(k)), torch.int32, scores.device, stream)
     if want_mask and mask is None:
-        mask = torch.empty(rows, n, dtype=torch.uint8, device=scores.device)
+        mask = _empty((rows, n), torch.uint8, scores.device, stream)
     dt = MOE_DTYPE_F32 if scores.dtype == torch.float32 else MOE_DTYPE_BF16
     _check(lib().moe_indexer_topk(_ptr(scores), dt, rows, n, ld, _ptr(lengths), int(k),
                                   _ptr(inds), _ptr(mask), n if mask is not None else 0,
@@ -414,10 +436,10 @@ def permute(inds, E, stream=None):
     _need(inds, torch.int32, "inds")
     T, K = inds.shape
     dev = inds.device
-    counts = torch.empty(E, dtype=torch.int32, device=dev)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    perm = torch.empty(T * K, dtype=torch.int32, device=dev)
-    inv = torch.empty(T * K, dtype=torch.int32, device=dev)
+    counts = _empty(E, torch.int32, dev, stream)
+    offsets = _empty(E + 1, torch.int32, dev, stream)
+    perm = _empty(T * K, torch.int32, dev, stream)
+    inv = _empty(T * K, torch.int32, dev, stream)
     _check(lib().moe_permute(_ptr(inds), T, K, E, _ptr(counts), _ptr(offsets), _ptr(perm),
                              _ptr(inv), _stream(stream)))
     return counts, offsets, perm, inv
@@ -431,7 +453,7 @@ def router_logits(x, w_router, logit_offset=None, stream=None):
     E = w_router.shape[0]
     if logit_offset is not None:
         _need(logit_offset, torch.float32, "logit_offset", x.device)
-    out = torch.empty(T, E, dtype=torch.float32, device=x.device)
+    out = _empty((T, E), torch.float32, x.device, stream)
     _check(lib().moe_router_logits(_ptr(x), T, d, _ptr(w_router), E, _ptr(logit_offset),
                                    _ptr(out), _stream(stream)))
     return out
@@ -458,11 +480,10 @@ def grouped_swiglu(x, offsets, perm, K, experts, shared=None, I=None, ws=None, s
         _raw_stream(x, stream)  # (on the current device)
     else:
         ew, sw = expert_weights(experts), expert_weights(shared)
-    out = torch.empty(P + (T if shared is not None else 0), d, dtype=torch.bfloat16,
-                      device=x.device)
+    out = _empty((P + (T if shared is not None else 0), d), torch.bfloat16, x.device, stream)
     need = grouped_swiglu_workspace_bytes(T, d, I, E, K, shared is not None)
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        ws = _empty(max(need, 256), torch.uint8, x.device, stream, returned=False)
     _check(lib().moe_grouped_swiglu(_ptr(x), T, d, I, E, K, _ptr(offsets), _ptr(perm),
                                     ctypes.byref(ew), _ref(sw), _ptr(out), _ptr(ws),
                                     ws.numel(), _stream(stream)))
@@ -476,7 +497,7 @@ def combine(expert_out, scores, inv_perm, shared_out=None, stream=None):
     _need(inv_perm, torch.int32, "inv_perm")
     T, K = scores.shape
     d = expert_out.shape[1]
-    y = torch.empty(T, d, dtype=torch.bfloat16, device=expert_out.device)
+    y = _empty((T, d), torch.bfloat16, expert_out.device, stream)
     _check(lib().moe_combine(_ptr(expert_out), _ptr(scores), _ptr(inv_perm), _ptr(shared_out),
                              T, K, d, _ptr(y), _stream(stream)))
     return y
@@ -490,7 +511,8 @@ class MoELayer:
     """The whole layer on device-resident weights: ``layer(x) -> y``.
 
     Holds the weights, the gate parameters and a reusable workspace; each call is one
-    ``moe_forward`` on the current stream.  With ``want_intermediates`` it also returns the
+    ``moe_forward`` on the current stream (or ``stream``).  Calls share the workspace: on several
+    streams their caller has to order them.  With ``want_intermediates`` it also returns the
     selected experts, their weights and the router logits.
     """
 
@@ -509,7 +531,8 @@ class MoELayer:
         self.w_router, self.bias, self.logit_offset = w_router, bias, logit_offset
         self.experts, self.shared = experts, shared
         self.E, self.d = w_router.shape
-        if self.route_kind == MOE_ROUTE_SOFTMAX_GROUPED and bias is not None and bias.shape != (self.E,):
+        grouped = self.route_kind == MOE_ROUTE_SOFTMAX_GROUPED
+        if grouped and bias is not None and bias.shape != (self.E,):
             raise ValueError(f"bias must be [{self.E}], not {tuple(bias.shape)}")
         self.I = experts["gate"].shape[1]
         self.params = route_params(top_k, n_group, topk_group, norm_topk_prob,
@@ -517,7 +540,7 @@ class MoELayer:
         self.scaled = _is_scaled(experts)
         of = lambda E: ((E, self.d, self.I), self.dev) if self.scaled else ()  # noqa: E731
         self.ew, self.sw = expert_weights(experts, *of(self.E)), expert_weights(shared, *of(1))
-        self.ws = None
+        self.ws, self.ws_stream = None, None
 
     def _args(self, x, y, inds, scores, logits):
         a = LayerArgs()
@@ -536,7 +559,7 @@ class MoELayer:
         a.logits_out = None if logits is None else logits.data_ptr()
         return a
 
-    def workspace(self, T):
+    def workspace(self, T, stream=None):
         if self.ex:
             a = LayerArgs()
             a.route_kind, a.T, a.d, a.I, a.E = self.route_kind, T, self.d, self.I, self.E
@@ -547,8 +570,15 @@ class MoELayer:
         else:
             need = forward_workspace_bytes(T, self.d, self.I, self.E, self.params.top_k,
                                            self.shared is not None)
+        used = None
+        if self.dev.type == "cuda":
+            used = stream if stream is not None else torch.cuda.current_stream(self.dev)
         if self.ws is None or self.ws.numel() < need:
-            self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.dev)
+            self.ws = _empty(max(need, 256), torch.uint8, self.dev, stream, returned=False)
+            self.ws_stream = used and used.cuda_stream
+        elif used is not None and used.cuda_stream != self.ws_stream:
+            # the memory must outlive this call when a later one needs more
+            self.ws.record_stream(_torch_stream(used))
         return self.ws
 
     def __call__(self, x, y=None, want_intermediates=False, stream=None):
@@ -561,14 +591,14 @@ class MoELayer:
             if y is not None:
                 _need_out(y, torch.bfloat16, "y", (T, d), self.dev)
             _raw_stream(x, stream)  # (on the current device)
-        ws = self.workspace(T)
+        ws = self.workspace(T, stream)
         if y is None:
-            y = torch.empty(T, d, dtype=torch.bfloat16, device=self.dev)
+            y = _empty((T, d), torch.bfloat16, self.dev, stream)
         inds = scores = logits = None
         if want_intermediates:
-            inds = torch.empty(T, K, dtype=torch.int32, device=self.dev)
-            scores = torch.empty(T, K, dtype=torch.float32, device=self.dev)
-            logits = torch.empty(T, self.E, dtype=torch.float32, device=self.dev)
+            inds = _empty((T, K), torch.int32, self.dev, stream)
+            scores = _empty((T, K), torch.float32, self.dev, stream)
+            logits = _empty((T, self.E), torch.float32, self.dev, stream)
         if self.ex:
             a = self._args(x, y, inds, scores, logits)
             _check(lib().moe_forward_ex(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)))

@@ -600,3 +600,84 @@ def test_experts_with_scales_whose_product_is_no_normal_number(T, E):
             at = slice(off[e], off[e + 1])
             ref, tol = expert_ref(x[tok[at]], ex, e)
             check_within(y[at], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs() + 2.0 ** -134)
+
+
+def test_calls_on_a_given_stream_allocate_there(monkeypatch):
+    """With stream= every output and workspace is of that stream's memory (the current stream's may
+    still be in use by work queued there), and the results equal those of the current stream."""
+    g = gen(61)
+    T, d, I, E, K = 40, 256, 128, 8, 2
+    x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+    ex, sh = make_experts(E, d, I, g), make_experts(1, d, I, g)
+    wr = (torch.randn(E, d, generator=g, device=DEV) / d ** 0.5).to(torch.bfloat16)
+    wg, bias = wr[0].contiguous(), torch.zeros(E, device=DEV)
+    logits = binding.router_logits(x, wr)
+    inds, scores = binding.route_softmax_grouped(logits, K, 2, 2, True, 1.0)
+    _, offsets, perm, inv = binding.permute(inds, E)
+    eo = binding.grouped_swiglu(x, offsets, perm, K, ex, sh)
+    gate = binding.shared_gate(x, wg)
+    ops = operands(40, 96, 256, 2)
+    layer = binding.MoELayer(wr, None, ex, sh, K, 2, 2, True, 1.0, route_kind=binding.MOE_ROUTE_SOFTMAX_GROUPED)
+    calls = {
+        "quantize_blocks": lambda st: binding.quantize_blocks(x, stream=st),
+        "matmul_blocks": lambda st: binding.matmul_blocks(*ops, stream=st),
+        "route_softmax_grouped": lambda st: binding.route_softmax_grouped(logits, K, 2, 2, True, 1.0, stream=st),
+        "route_softmax": lambda st: binding.route_softmax(logits, K, stream=st),
+        "route_deepseek": lambda st: binding.route_deepseek(logits, bias, K, 2, 1, True, 1.0, stream=st),
+        "router_logits": lambda st: binding.router_logits(x, wr, stream=st),
+        "permute": lambda st: binding.permute(inds, E, stream=st),
+        "grouped_swiglu": lambda st: binding.grouped_swiglu(x, offsets, perm, K, ex, sh, stream=st),
+        "shared_gate": lambda st: binding.shared_gate(x, wg, stream=st),
+        "combine": lambda st: binding.combine(eo, scores, inv, eo[T * K:], stream=st),
+        "combine_gated": lambda st: binding.combine_gated(eo, scores, inv, eo[T * K:], gate, stream=st),
+        "indexer_topk": lambda st: binding.indexer_topk(logits, 3, want_mask=True, stream=st),
+        "layer": lambda st: layer(x, want_intermediates=True, stream=st),
+    }
+    want = {k: c(None) for k, c in calls.items()}
+    layer.ws = None
+    torch.cuda.synchronize()
+    st, seen, empty = torch.cuda.Stream(), [], torch.empty
+
+    def watched(*a, **kw):
+        seen.append(torch.cuda.current_stream())
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", watched)
+    got = {}
+    for k, c in calls.items():
+        seen.clear()
+        got[k] = c(st)
+        assert seen and all(s == st for s in seen), k
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    for k in calls:
+        a, b = (v if isinstance(v, tuple) else (v,) for v in (want[k], got[k]))
+        assert len(a) == len(b)
+        for u, v in zip(a, b):
+            assert torch.equal(u.contiguous().view(torch.uint8), v.contiguous().view(torch.uint8)), k
+
+
+def test_layer_keeps_its_workspace_for_the_streams_that_use_it():
+    """A workspace used on a second stream is not handed out again when a later call replaces it,
+    before that stream is done with it."""
+    g = gen(62)
+    d, I, E, K = 256, 128, 8, 2
+    ex = make_experts(E, d, I, g)
+    wr = (torch.randn(E, d, generator=g, device=DEV) / d ** 0.5).to(torch.bfloat16)
+    layer = binding.MoELayer(wr, None, ex, None, K, 2, 2, True, 1.0,
+                             route_kind=binding.MOE_ROUTE_SOFTMAX_GROUPED)
+    x = torch.randn(64, d, generator=g, device=DEV).to(torch.bfloat16)
+    big = torch.randn(4096, d, generator=g, device=DEV).to(torch.bfloat16)
+    want = layer(x)
+    torch.cuda.synchronize()
+    old, size = layer.ws.data_ptr(), layer.ws.numel()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(200_000_000)  # some 0.1 s
+        y = layer(x)
+    layer(big)  # replaces the workspace while the call on st waits
+    assert layer.ws.data_ptr() != old
+    taken = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    assert all(t.data_ptr() != old for t in taken)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
