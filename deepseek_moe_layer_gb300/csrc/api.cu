@@ -287,7 +287,8 @@ struct SwigluWs {
     size_t x_perm, h, total;
 };
 // With e4m3 experts the same space holds the codes and scales of the rows [P + T, d] and of h
-// [P + T, I].  They fit wherever top_k >= 2; the sizes reported cover both.
+// [P + T, I].  They fit wherever top_k >= 2; the sizes reported without the experts at hand cover
+// both.
 struct ScaledWs {
     size_t x, sx, h, sh, inv, total;
 };
@@ -314,10 +315,14 @@ SwigluWs swiglu_ws(int64_t T, int32_t d, int32_t I, int32_t K, int has_shared) {
     w.total = off;
     return w;
 }
-size_t swiglu_ws_bytes(int64_t T, int32_t d, int32_t I, int32_t K, int has_shared) {
+enum class Experts { kAny, kPlain, kScaled };  // what a size is for
+Experts kind_of(const moe_expert_weights_t* w) {
+    return w->bits == MOE_BITS_E4M3 ? Experts::kScaled : Experts::kPlain;
+}
+size_t swiglu_ws_bytes(int64_t T, int32_t d, int32_t I, int32_t K, int has_shared, Experts kind) {
     const size_t a = swiglu_ws(T, d, I, K, has_shared).total;
     const size_t b = scaled_ws(T, d, I, K, has_shared).total;
-    return a > b ? a : b;
+    return kind == Experts::kPlain || (kind == Experts::kAny && a > b) ? a : b;
 }
 
 // Whole-layer workspace.
@@ -325,7 +330,7 @@ struct ForwardWs {
     size_t logits_part, inds, scores, counts, offsets, perm, inv, expert_out, swiglu, total;
 };
 ForwardWs forward_ws(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K, int has_shared,
-                     int ksplit) {
+                     int ksplit, Experts kind) {
     ForwardWs w;
     const int64_t P = T * K;
     size_t off = 0;
@@ -337,7 +342,7 @@ ForwardWs forward_ws(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K, int 
     w.perm = off;        off += align256((size_t)P * 4);
     w.inv = off;         off += align256((size_t)P * 4);
     w.expert_out = off;  off += align256((size_t)(P + (has_shared ? T : 0)) * d * 2);
-    w.swiglu = off;      off += swiglu_ws_bytes(T, d, I, K, has_shared);
+    w.swiglu = off;      off += swiglu_ws_bytes(T, d, I, K, has_shared, kind);
     w.total = off;
     return w;
 }
@@ -491,10 +496,10 @@ struct ForwardExWs {
     ForwardWs base;
     size_t gate, total;
 };
-ForwardExWs forward_ex_ws(const moe_layer_args_t& a) {
+ForwardExWs forward_ex_ws(const moe_layer_args_t& a, Experts kind) {
     ForwardExWs w;
     w.base = forward_ws(a.T, a.d, a.I, a.E, a.params.top_k, a.shared != nullptr,
-                        router_ksplit_bound(a.d));
+                        router_ksplit_bound(a.d), kind);
     w.gate = w.base.total;
     w.total = w.gate + (a.w_shared_gate ? align256((size_t)a.T * 4) : 0);
     return w;
@@ -537,7 +542,7 @@ int forward_impl(const moe_layer_args_t& A, void* ws, size_t ws_bytes, cudaStrea
               "x, w_router, w_shared_gate and y must be 16-byte aligned");
     MOE_CHECK(aligned(ws, 256), "ws must be 256-byte aligned");
     const int has_shared = A.shared != nullptr;
-    const ForwardExWs lx = forward_ex_ws(A);
+    const ForwardExWs lx = forward_ex_ws(A, kind_of(A.experts));
     const ForwardWs& lw = lx.base;
     MOE_CHECK(ws_bytes >= lx.total, "ws_bytes = %zu < %zu required", ws_bytes, lx.total);
     if (T == 0) return MOE_OK;
@@ -639,6 +644,13 @@ int moe::set_error(int code, const char* msg) {
 }
 
 bool moe::pdl_enabled() { return g_pdl; }
+
+size_t moe::forward_bytes(int64_t T, int32_t d, int32_t I, int32_t E, int32_t top_k,
+                          bool has_shared, int32_t bits) {
+    if (T < 0 || d < 0 || I < 0 || E < 0 || top_k < 0) return 0;
+    const Experts kind = bits == MOE_BITS_E4M3 ? Experts::kScaled : Experts::kPlain;
+    return forward_ws(T, d, I, E, top_k, has_shared, router_ksplit_bound(d), kind).total;
+}
 
 extern "C" {
 
@@ -793,7 +805,7 @@ size_t moe_grouped_swiglu_workspace_bytes(int64_t T, int32_t d, int32_t I, int32
                                           int32_t has_shared) {
     (void)E;
     if (T < 0 || d < 0 || I < 0 || K < 0) return 0;
-    return swiglu_ws_bytes(T, d, I, K, has_shared != 0);
+    return swiglu_ws_bytes(T, d, I, K, has_shared != 0, Experts::kAny);
 }
 
 int moe_grouped_swiglu(const void* x, int64_t T, int32_t d, int32_t I, int32_t E, int32_t K,
@@ -814,8 +826,7 @@ int moe_grouped_swiglu(const void* x, int64_t T, int32_t d, int32_t I, int32_t E
     if (scaled && (rc = check_scaled_dims(T, d, I, E, K))) return rc;
     MOE_CHECK(aligned(x, 16) && aligned(out, 16), "x and out must be 16-byte aligned");
     MOE_CHECK(aligned(ws, 256), "ws must be 256-byte aligned");
-    const size_t need = scaled ? scaled_ws(T, d, I, K, shared != nullptr).total
-                               : swiglu_ws(T, d, I, K, shared != nullptr).total;
+    const size_t need = swiglu_ws_bytes(T, d, I, K, shared != nullptr, kind_of(experts));
     MOE_CHECK(ws_bytes >= need, "ws_bytes = %zu < %zu required", ws_bytes, need);
     if (T == 0) return MOE_OK;
     rc = check_device();
@@ -846,7 +857,8 @@ int moe_combine(const void* expert_out, const float* scores, const int32_t* inv_
 size_t moe_forward_workspace_bytes(int64_t T, int32_t d, int32_t I, int32_t E, int32_t top_k,
                                    int32_t has_shared) {
     if (T < 0 || d < 0 || I < 0 || E < 0 || top_k < 0) return 0;
-    return forward_ws(T, d, I, E, top_k, has_shared != 0, router_ksplit_bound(d)).total;
+    return forward_ws(T, d, I, E, top_k, has_shared != 0, router_ksplit_bound(d), Experts::kAny)
+        .total;
 }
 
 int moe_forward(const void* x, int64_t T, int32_t d, int32_t I, int32_t E,
@@ -880,7 +892,7 @@ int moe_forward(const void* x, int64_t T, int32_t d, int32_t I, int32_t E,
 
 size_t moe_forward_ex_workspace_bytes(const moe_layer_args_t* a) {
     if (!a || a->T < 0 || a->d < 0 || a->I < 0 || a->E < 0 || a->params.top_k < 0) return 0;
-    return forward_ex_ws(*a).total;
+    return forward_ex_ws(*a, Experts::kAny).total;
 }
 
 int moe_forward_ex(const moe_layer_args_t* args, void* ws, size_t ws_bytes, moe_stream_t stream) {

@@ -195,6 +195,10 @@ int num_sms();
 // Sets the thread-local text returned by moe_last_error() and returns `code`.
 int set_error(int code, const char* msg);
 
+// Workspace of moe_forward for experts of these bits (moe_forward_workspace_bytes: for any).
+size_t forward_bytes(int64_t T, int32_t d, int32_t I, int32_t E, int32_t top_k, bool has_shared,
+                     int32_t bits);
+
 // Programmatic dependent launch for the kernels of one layer call after its first: while set
 // (per host thread), the launchers below launch with programmatic stream serialization, so a
 // kernel's prologue overlaps the tail of the one before it (each kernel waits with

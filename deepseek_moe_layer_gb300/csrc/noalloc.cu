@@ -69,8 +69,8 @@ extern "C" int moe_forward_noalloc(const void* x, int64_t T, int32_t d, int32_t 
                                    int32_t* inds_out, float* scores_out, float* logits_out,
                                    moe_stream_t stream) {
     if (!params) return moe::set_error(MOE_ERR_INVALID, "params is NULL");
-    const size_t need =
-        moe_forward_workspace_bytes(T, d, I, E, params->top_k, shared != nullptr ? 1 : 0);
+    const size_t need = moe::forward_bytes(T, d, I, E, params->top_k, shared != nullptr,
+                                           experts ? experts->bits : 16);
     if (need > kScratchBytes) {
         char msg[256];
         snprintf(msg, sizeof msg,

@@ -287,3 +287,34 @@ def test_grouped_gate_of_a_layer_checks_its_bias(shape):
     with pytest.raises(ValueError, match="bias"):
         binding.MoELayer(torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(shape), _dict(*GOOD), None,
                          2, 1, 1, True, 1.0, route_kind=binding.MOE_ROUTE_SOFTMAX_GROUPED)
+
+
+def test_bf16_layer_with_one_expert_per_token_needs_what_it_always_needed():
+    """The reported size covers e4m3 experts too, which with top_k = 1 and a shared expert can need
+    more; a layer of bf16 experts takes its own size, and the fixed workspace its old batches."""
+    L = binding.lib()
+    T, d, I, E = 600, 7168, 128, 16
+    al = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    fixed = [al(d // 512 * T * E * 4), *[al(T * 4)] * 2, al(E * 4), al((E + 1) * 4), *[al(T * 4)] * 2,
+             al(2 * T * d * 2)]  # logits, choices and dispatch; the experts' outputs
+    bf16 = sum(fixed) + al(T * d * 2) + al(2 * T * I * 2)  # gathered rows and h
+    e4m3 = sum(fixed) + al(2 * T * d) + al(2 * T * d // 128 * 4) + al(2 * T * I) + al(2 * T * I // 128 * 4) + al(T * 4)
+    assert bf16 < e4m3 == L.moe_forward_workspace_bytes(T, d, I, E, 1, 1)
+    ew = binding.ExpertWeights(16, 0, 0x1000, 0x1000, 0x1000, *([None] * 6))
+    p = binding.route_params(1, 1, 1, True, 1.0)
+    f, ref = FAKE, ctypes.byref
+    call = lambda w, n: L.moe_forward(f, T, d, I, E, f, f, None, ref(p), ref(w), ref(w), f, None, None,  # noqa: E731
+                                      None, ctypes.c_void_p(0x10000), n, None)
+    assert call(ew, 1000) == BAD and f"< {bf16} required" in _err()
+    assert call(_ew(), 1000) == BAD and f"< {e4m3} required" in _err()
+    # the largest batch whose bf16 workspace fits the fixed one: refused (if at all) for x's alignment
+    size = 64 << 20
+    T = next(t for t in range(3000, 0, -1) if L.moe_forward_workspace_bytes(t, d, I, E, 1, 1) <= size) + 4
+    odd = ctypes.c_void_p(0x1008)
+    args = (odd, T, d, I, E, f, f, None, ref(p))
+    assert L.moe_forward_workspace_bytes(T, d, I, E, 1, 1) > size
+    L.moe_forward_noalloc(*args, ref(ew), ref(ew), f, None, None, None, None)
+    assert "bytes of workspace" not in _err()
+    e = _ew()
+    assert L.moe_forward_noalloc(*args, ref(e), ref(e), f, None, None, None, None) == BAD
+    assert "bytes of workspace" in _err()
