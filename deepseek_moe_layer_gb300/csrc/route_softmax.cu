@@ -12,8 +12,9 @@
 //     w_k = p_k, divided by sum of the selected p when K > 1 and norm is set (0 when that sum
 //           is 0), times the scaling factor
 //
-// Selection is exact.  Without a bias it compares the logits themselves (softmax is strictly
-// increasing).  With a bias v is computed in fp32, and where that cannot tell the order (two
+// Selection is exact.  Without a bias it compares the logits themselves: softmax is strictly
+// increasing, and where p tells two experts no longer apart (finite logits beside a +inf one, whose
+// p are all 0) the larger logit still comes first.  With a bias v is computed in fp32, and where that cannot tell the order (two
 // neighbours among the chosen, or the last of them and any of the others, closer than far_apart
 // below) the row is selected again in fp64.
 //

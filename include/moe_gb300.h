@@ -180,7 +180,10 @@ int moe_route_softmax(const void* logits, moe_dtype_t dtype, int64_t rows, int32
  *   expert index first among equals; the weights are p (without the bias), divided by their sum
  *   only when K > 1 and norm_topk_prob (0 when that sum is 0), times routed_scaling_factor.
  * The selection is that of exact arithmetic to 64 bits: without a bias it compares the logits,
- * with one it falls back on fp64 where fp32 cannot tell two neighbours apart.
+ * with one it falls back on fp64 where fp32 cannot tell two experts apart.  So where p is 0 for
+ * several experts (the finite logits beside a +inf one; with a bias also those more than 745 below
+ * m) the order without a bias is still the logits', with a bias it is v's: logits inf 1 5 2 give
+ * 0 2 for K = 2, and 0 1 with a bias of zeros.
  * Out: inds [rows, K] int32, scores [rows, K] fp32.
  * Errors: MOE_ERR_INVALID for NULL pointers (bias may be NULL), rows < 0, an unknown dtype, E
  * outside [1, 1024], n_group outside [1, 32] or not dividing E, topk_group outside

@@ -157,3 +157,13 @@ def test_bias_hides_a_dominant_expert(E, K, G, tg):
     for seed in range(24):
         logits, bias = dominant_rows(E, K, G, 1000 * E + seed)
         check(logits, K, G, tg, False, bias=bias)
+
+
+def test_order_among_experts_without_probability():
+    """Beside a +inf logit every finite one has p = 0: without a bias the logits still order them,
+    with a bias of zeros their values are equal and the lower index comes first."""
+    l = torch.tensor([[float("inf"), 1.0, 5.0, 2.0]], device=DEV)
+    inds, scores = binding.route_softmax_grouped(l, 2, 1, 1, False, 1.0)
+    assert inds.tolist() == [[0, 2]] and scores.tolist() == [[1.0, 0.0]]
+    inds, scores = binding.route_softmax_grouped(l, 2, 1, 1, False, 1.0, bias=torch.zeros(4, device=DEV))
+    assert inds.tolist() == [[0, 1]] and scores.tolist() == [[1.0, 0.0]]
