@@ -681,3 +681,28 @@ def test_layer_keeps_its_workspace_for_the_streams_that_use_it():
     assert all(t.data_ptr() != old for t in taken)
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,d,I,E,K,shared", [
+    (64, 512, 1024, 40, 4, True), (1200, 640, 1024, 8, 4, True),   # tiles of 32 rows, of 128
+    (2, 2048, 256, 16, 3, True), (200, 1408, 128, 2, 2, False)])   # several CTAs on a tile
+def test_experts_write_an_output_off_a_32_byte_border(T, d, I, E, K, shared):
+    """The call asks for 16 bytes: the same bits as on a whole border, and nothing around them."""
+    import ctypes
+    g = gen(T + d)
+    x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+    ex, sh = make_experts(E, d, I, g), make_experts(1, d, I, g) if shared else None
+    _, offsets, perm, _ = binding.permute(dispatch(T, E, K, g), E)
+    want = binding.grouped_swiglu(x, offsets, perm, K, ex, sh)
+    buf = torch.full((want.numel() + 24,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[8:8 + want.numel()].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    need = binding.grouped_swiglu_workspace_bytes(T, d, I, E, K, shared)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    ew, sw = binding.expert_weights(ex), binding.expert_weights(sh)
+    binding._check(binding.lib().moe_grouped_swiglu(
+        binding._ptr(x), T, d, I, E, K, binding._ptr(offsets), binding._ptr(perm), ctypes.byref(ew),
+        binding._ref(sw), binding._ptr(out), binding._ptr(ws), need, binding._stream()))
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    assert bool((buf[:8] == 7).all()) and bool((buf[8 + want.numel():] == 7).all())
