@@ -94,7 +94,7 @@ struct Params {
     const float* ssw1;
     void* out;               // kLinear: bf16 or fp32 [rows, ld]; kSwiglu: codes [rows, F]
     long long ld;
-    int f32;                 // kLinear: fp32 out
+    int f32;                 // kLinear: fp32 out (not FEW: the experts' rows are bf16)
     int vec;                 // kLinear: rows of `out` are 32-byte aligned
     float* out_scale;        // kSwiglu: [rows, F / 128]
     int split;               // SPLIT: CTAs per tile (the cluster's size), k-blocks shared out
@@ -297,8 +297,9 @@ MOE_DEV Tile tile_at(const Params& p, const int32_t* prefix, const int32_t* rowo
 
 // SPLIT: adds the partial sums of a tile's CTAs (their shared memory at `part`, in rank order)
 // and writes the rows rank, rank + split, ..: a warp per row, a lane four columns of each half.
-template <int MODE>
+template <int MODE, int FEW>
 MOE_DEV void join_rows(const Params& p, const Tile& ti, const float* part, int rank) {
+    const bool f32 = !FEW && p.f32;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kEpiWarp0;
     for (int r = rank + p.split * w; r < ti.rows; r += p.split * kEpiWarps) {
         const float* at = part + r * kPartLd + 4 * lane;
@@ -338,7 +339,7 @@ MOE_DEV void join_rows(const Params& p, const Tile& ti, const float* part, int r
             for (int h = 0; h < 2; ++h) {
                 const float* v = h ? u : g;
                 const int n = ti.f * 256 + 128 * h + 4 * lane;
-                if (p.f32) {
+                if (f32) {
                     float* o = static_cast<float*>(p.out) + row * p.ld + n;
                     if (p.vec && n + 4 <= p.F) {
                         *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
@@ -639,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wr = FEW ? 0 : q * 32;                       // its first row
         const int r = wr + lane;                               // the thread's row of the tile
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
+        const bool f32 = !FEW && p.f32;
         Rings rg = {tfull, tempty, ffull, fempty, 0u, 0u};
         int lt = 0;  // tiles so far
         bool ok = true;
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int n0 = ti.f * 256 + 128 * h + c0;
                         const float* sum = acc + RUN * h;
                         if (p.vec && n0 + RUN <= p.F) {
-                            if (mine && p.f32) {
+                            if (mine && f32) {
                                 float* o = static_cast<float*>(p.out) + (ti.row + r) * p.ld + n0;
 #pragma unroll
                                 for (int i = 0; i < RUN / 8; ++i) {
@@ -766,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     if (wr + rr < ti.rows && n < p.F) {
                                         const long long at = (ti.row + wr + rr) * p.ld + n;
                                         const float v = piece[rr * kRagLd + pc];
-                                        if (p.f32) static_cast<float*>(p.out)[at] = v;
+                                        if (f32) static_cast<float*>(p.out)[at] = v;
                                         else static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
                                     }
                                 }
@@ -780,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             cluster_sync();  // all partial sums are written
             if (tstart < total)
-                join_rows<MODE>(p, tile_at<kTile>(p, prefix, rowoff, ngroups, tstart),
+                join_rows<MODE, FEW>(p, tile_at<kTile>(p, prefix, rowoff, ngroups, tstart),
                                 reinterpret_cast<const float*>(smem), rank);
             __syncwarp();
             cluster_sync();  // and read: the CTAs may leave
