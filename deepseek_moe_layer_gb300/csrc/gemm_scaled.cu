@@ -181,18 +181,6 @@ MOE_DEV float after_round(float v, int cls) {
     return cls == kSmall && fabsf(v) < 0x1p60f ? v * 0x1p-100f : v;
 }
 
-// Whether one of a slot's products is lost: n k-blocks of two rows' scales with the halves'.
-__device__ __noinline__ bool any_lost(const float* x0, const float* x1, const float* sw0,
-                                      const float* sw1, int n) {
-    bool any = false;
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const float a = j & 1 ? x1[i] : x0[i], g = j & 2 ? sw1[i] : sw0[i];
-            any |= factor_class(a * g, a, g) != kUsual;
-        }
-    return any;
-}
-
 // One 32-byte store (a whole sector).
 MOE_DEV void st_global_32B(void* p, const uint32_t (&w)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
@@ -615,12 +603,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 high = fmaxf(high, fmaxf(fabsf(f0), fabsf(f1)));
                             }
                         }
-                        if (!(low >= 0x1p-126f && high <= kFltMax) && !pass) {
-                            const long long r0 = min(FEW ? w & 31 : w, last);
-                            const long long r1 = min(FEW ? w & 31 : w + 64, last);
-                            if (any_lost(sx + r0 * p.nkb + kb, sx + r1 * p.nkb + kb, sw0 + kb,
-                                         sw1 + kb, min(kFKb, kb1 - kb)))
-                                *lost = 1;
+                        if (!(low >= 0x1p-126f && high <= kFltMax) && !pass) {  // (or scales of 0)
+#pragma unroll
+                            for (int i = 0; i < kFKb; ++i) {
+                                if (kb + i >= kb1) break;
+                                const float g0 = sw0[kb + i], g1 = sw1[kb + i];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const float x = a[j][i];
+                                    if (factor_class(x * g0, x, g0) != kUsual ||
+                                        factor_class(x * g1, x, g1) != kUsual)
+                                        *lost = 1;
+                                }
+                            }
                         }
                         mbar_arrive(&ffull[s]);
                     }
