@@ -706,3 +706,34 @@ def test_experts_write_an_output_off_a_32_byte_border(T, d, I, E, K, shared):
     torch.cuda.synchronize()
     assert torch.equal(out.view(torch.int16), want.view(torch.int16))
     assert bool((buf[:8] == 7).all()) and bool((buf[8 + want.numel():] == 7).all())
+
+
+@pytest.mark.parametrize("T,E,every", [(1, 64, 1), (64, 64, 4), (900, 64, 16), (128, 256, 24)])
+def test_layer_at_a_checkpoints_size(T, E, every):
+    """d = 7168, I = 2048, 8 of E experts and a shared one: the layer is its parts bit for bit, and
+    every `every`-th expert that is hit, and the shared one, match 64 bits."""
+    g = gen(T + E)
+    d, I, K = 7168, 2048, 8
+    ex, sh = {"bits": binding.MOE_BITS_E4M3}, make_experts(1, d, I, g)
+    for k, (n, m) in (("gate", (I, d)), ("up", (I, d)), ("down", (d, I))):
+        ex[k] = torch.empty(E, n, m, dtype=F8, device=DEV)
+        for e in range(E):
+            ex[k][e] = codes_of((n, m), g)
+        ex[k + "_s"] = (torch.rand(E, n // 128, m // 128, generator=g, device=DEV) + 0.5) / (60 * m ** 0.5)
+    wr = (torch.randn(E, d, generator=g, device=DEV) / d ** 0.5).to(torch.bfloat16)
+    bias = 0.01 * torch.randn(E, generator=g, device=DEV)
+    layer = binding.MoELayer(wr, bias, ex, sh, K, 8, 4, True, 2.5)
+    x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+    y, inds, scores, _ = layer(x, want_intermediates=True)
+    _, offsets, perm, inv = binding.permute(inds, E)
+    eo = binding.grouped_swiglu(x, offsets, perm, K, ex, sh)
+    assert torch.equal(y, binding.combine(eo, scores, inv, eo[T * K:]))
+    binding.device_status()
+    off, tok = offsets.tolist(), perm.long() // K
+    hit = [e for e in range(E) if off[e + 1] > off[e]]
+    for e in hit[::every]:
+        at = slice(off[e], off[e + 1])
+        ref, tol = expert_ref(x[tok[at]], ex, e)
+        check_within(eo[at], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs())
+    ref, tol = expert_ref(x, sh, 0)
+    check_within(eo[T * K:], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs())
