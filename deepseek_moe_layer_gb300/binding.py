@@ -477,16 +477,17 @@ def grouped_swiglu(x, offsets, perm, K, experts, shared=None, I=None, ws=None, s
         _need(perm, torch.int32, "perm", x.device)
         if perm.numel() < P:
             raise ValueError(f"perm holds {perm.numel()} pairs, not T * K = {P}")
-        _raw_stream(x, stream)  # (on the current device)
+        st = _raw_stream(x, stream)
     else:
         ew, sw = expert_weights(experts), expert_weights(shared)
+        st = _stream(stream)
     out = _empty((P + (T if shared is not None else 0), d), torch.bfloat16, x.device, stream)
     need = grouped_swiglu_workspace_bytes(T, d, I, E, K, shared is not None)
     if ws is None:
         ws = _empty(max(need, 256), torch.uint8, x.device, stream, returned=False)
     _check(lib().moe_grouped_swiglu(_ptr(x), T, d, I, E, K, _ptr(offsets), _ptr(perm),
                                     ctypes.byref(ew), _ref(sw), _ptr(out), _ptr(ws),
-                                    ws.numel(), _stream(stream)))
+                                    ws.numel(), st))
     return out
 
 
@@ -572,13 +573,14 @@ class MoELayer:
                                            self.shared is not None)
         used = None
         if self.dev.type == "cuda":
-            used = stream if stream is not None else torch.cuda.current_stream(self.dev)
+            used = (stream.cuda_stream if stream is not None
+                    else torch._C._cuda_getCurrentRawStream(self.dev.index))
         if self.ws is None or self.ws.numel() < need:
             self.ws = _empty(max(need, 256), torch.uint8, self.dev, stream, returned=False)
-            self.ws_stream = used and used.cuda_stream
-        elif used is not None and used.cuda_stream != self.ws_stream:
+            self.ws_stream = used
+        elif used != self.ws_stream:
             # the memory must outlive this call when a later one needs more
-            self.ws.record_stream(_torch_stream(used))
+            self.ws.record_stream(_torch_stream(stream) or torch.cuda.current_stream(self.dev))
         return self.ws
 
     def __call__(self, x, y=None, want_intermediates=False, stream=None):
@@ -590,7 +592,9 @@ class MoELayer:
                 raise ValueError(f"x must be [T, {self.d}], not {tuple(x.shape)}")
             if y is not None:
                 _need_out(y, torch.bfloat16, "y", (T, d), self.dev)
-            _raw_stream(x, stream)  # (on the current device)
+            st = _raw_stream(x, stream)
+        else:
+            st = _stream(stream)
         ws = self.workspace(T, stream)
         if y is None:
             y = _empty((T, d), torch.bfloat16, self.dev, stream)
@@ -601,13 +605,13 @@ class MoELayer:
             logits = _empty((T, self.E), torch.float32, self.dev, stream)
         if self.ex:
             a = self._args(x, y, inds, scores, logits)
-            _check(lib().moe_forward_ex(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)))
+            _check(lib().moe_forward_ex(ctypes.byref(a), _ptr(ws), ws.numel(), st))
             return (y, inds, scores, logits) if want_intermediates else y
         _check(lib().moe_forward(_ptr(x), T, d, self.I, self.E, _ptr(self.w_router),
                                  _ptr(self.bias), _ptr(self.logit_offset),
                                  ctypes.byref(self.params), ctypes.byref(self.ew), _ref(self.sw),
                                  _ptr(y), _ptr(inds), _ptr(scores), _ptr(logits), _ptr(ws),
-                                 ws.numel(), _stream(stream)))
+                                 ws.numel(), st))
         if want_intermediates:
             return y, inds, scores, logits
         return y
