@@ -15,12 +15,14 @@
 // UMMAs (128 x 256 x 128, four K = 32 steps) into one of two TMEM buffers, and eight warps fold
 // the finished buffer into fp32 sums in registers, one multiply-add per element (two per
 // instruction), while the tensor core fills the other.  A row is one thread's, so the row scale
-// times the weight scale is one factor per thread, half and k-block.
+// times the weight scale is one factor per thread, half and k-block.  (Scales whose fp32 product is
+// no normal number: factor_class.)
 //
 // What bounds a long product is the way round a buffer: UMMA issue, completion, TMEM loads and
-// multiply-adds, the buffer's release (470, 500, 450 and 190 cycles by the clock, against the
-// UMMAs' own 512): 8192 x 4096 x 7168 takes 210 us, 170 with the scaling left out, 107 for the
-// UMMAs alone.  Tried and slower there: sixteen warps of 64 columns (242 us), halves of 128
+// multiply-adds, the buffer's release (410 .. 470, 500 .. 600, 450 .. 490 and 190 cycles by the
+// clock; with the 150 .. 350 that the trace does not place about 1900 for each of the two buffers,
+// so some 950 .. 1000 per k-block against the UMMAs' own 512): 8192 x 4096 x 7168 takes 212 us, 170
+// with the scaling left out, 107 for the UMMAs alone.  Tried and slower there: sixteen warps of 64 columns (242 us), halves of 128
 // columns with barriers, issuers or warps of their own (261 .. 277), an issuer per buffer (225),
 // looking at the next k-block's barriers between UMMAs (223), CTA pairs with cta_group::2 (513:
 // the way round crosses the cluster twice).
@@ -913,14 +915,15 @@ cudaError_t choose(const ScaledGemmArgs& a, cudaStream_t s) {
     // Experts with few rows: tiles of 32 rows, the same rows in every lane quarter, so that all
     // scaling warps share the columns instead of two of them doing all (64 experts, 7168 x 2048,
     // up to 8 / 24 / 32 rows per expert on average: 413 / 472 / 536 us against 473 / 505 / 514 for
-    // tiles of 128 rows).  Not for a single group's product (32 x 32768 x 2048: 13.0 against 12.4
-    // us, 8 rows 12.4 against 12.2; 1 x 2112 x 7168 alone 7.4 against 8.5).
+    // tiles of 128 rows).  A single group's product keeps tiles of 128, though the others would be the
+    // faster ones by now for up to 32 rows (32 x 32768 x 2048: 12.6 us against 11.7, 8 rows 12.1
+    // against 11.1, 1 x 2112 x 7168 9.1 against 8.3).
     const bool few = a.offsets && a.shared_row0 <= (long long)24 * a.E;
     // Too few tiles for the SMs: 2, 4 or 8 CTAs share a tile's k-blocks (two at least each) and
     // join their sums through the cluster's shared memory, in rank order, if that spares a CTA
-    // at least six k-blocks, which the join costs (1 x 2112 x 7168: 8.5 us against 24.0 for a CTA
-    // per tile; 128 x 16384 x 2048, two CTAs: 12.9 against 13.6; 600 x 3840 x 1024, where two
-    // would spare four k-blocks: 11.3 against 9.6).
+    // at least six k-blocks, which the join costs (1 x 2112 x 7168: 9.1 us against 29.4 for a CTA
+    // per tile; 128 x 16384 x 2048, two CTAs: 14.4 against 14.6; 600 x 3840 x 1024, where two
+    // would spare four k-blocks: 11.8 against 10.1).
     const long long tiles = max_tiles(a, few ? 32 : 128), sms = num_sms();
     const int nkb = (a.K + kBK - 1) / kBK;
     int split = 1;

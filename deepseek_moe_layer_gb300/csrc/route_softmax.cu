@@ -25,7 +25,9 @@
 // experts, 6 chosen from 3 of 8 groups; the issue slots are three quarters full) with enough rows
 // under way to hide the chain of some thirty warp steps: the gate without a bias carries neither
 // probabilities nor the fp64 path, and that path is a function of its own that reads the row
-// again, so that it takes no registers.  16384 such rows: 15.6 us (10.5 MB of logits: 1.7 us).
+// again, so that it takes no registers.  16384 such rows: 15.6 us (10.5 MB of logits: 1.7 us), with
+// a bias 22.5 .. 29; 16384 x 256, 8 from 4 of 8 groups, with a bias 33 .. 47, as few or many of the
+// rows go through fp64 (one of them is ten times a row's time, which shows when it comes last).
 #include "common.cuh"
 #include "launch.h"
 
