@@ -166,7 +166,7 @@ MOE_DEV int factor_class(float f, float a, float g) {
     return v > kFltMax && fabsf(a) <= kFltMax && fabsf(g) <= kFltMax ? kLarge : kUsual;
 }
 
-// The factor of the scales a and g in the round `cls` of a second time.  A small one's scales are
+// The factor of the scales a and g in the sweep `cls` of a second time.  A small one's scales are
 // both below 2^23, a large one's both at least 1.
 MOE_DEV float class_factor(float a, float g, int cls) {
     const float f = a * g;
@@ -175,10 +175,10 @@ MOE_DEV float class_factor(float a, float g, int cls) {
     return cls == kSmall ? (a * 0x1p50f) * (g * 0x1p50f) : f;
 }
 
-// What a round left, as the next one needs it.  After the large factors a sum is 0, or so large
+// What a sweep left, as the next one needs it.  After the large factors a sum is 0, or so large
 // that the small ones do not move it, neither by what they are nor by 2^100 times that; so the
 // second step leaves it alone, and the others leave 2^100.
-MOE_DEV float after_round(float v, int cls) {
+MOE_DEV float after_sweep(float v, int cls) {
     if (cls == kLarge) return v * 0x1p64f * 0x1p64f;
     return cls == kSmall && fabsf(v) < 0x1p60f ? v * 0x1p-100f : v;
 }
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0, s = 0;
             uint32_t ph = 0u;
             bool ok = true;
-            int rounds = 1;
-            for (int pass = 0; pass < 2 && ok; ++pass, rounds = 3) {
+            int sweeps = 1;
+            for (int pass = 0; pass < 2 && ok; ++pass, sweeps = 3) {
                 if (pass && !(mbar_wait(decided, 0u, abort) && *lost)) break;
                 for (int t = tstart; t < total && ok; t += tstep) {
                     const Tile ti = tile_at<kTile>(p, prefix, rowoff, ngroups, t);
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // experts: 84 -> 74 us)
                     const int boxes = FEW || ti.rows > 96 ? 4 : (ti.rows + 31) / 32;
                     const int per = FEW && ti.rows <= 8 ? 8 : 32;
-                    for (int round = 0; round < rounds && ok; ++round)
+                    for (int sweep = 0; sweep < sweeps && ok; ++sweep)
                         for (int kb = kb0; kb < kb1; ++kb, ++it) {
                             if (it > 0 && ++s == kStages) { s = 0; ph ^= 1u; }
                             if (!mbar_wait(&empty[s], ph ^ 1u, abort)) {
@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool vec = ((p.nkb | kb0) & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 15) == 0;
         int n = 0;
         bool ok = true;
-        int rounds = 1;
-        for (int pass = 0; pass < 2 && ok; ++pass, rounds = 3) {
+        int sweeps = 1;
+        for (int pass = 0; pass < 2 && ok; ++pass, sweeps = 3) {
             if (pass) {
                 mbar_arrive(decided);
                 if (!(mbar_wait(decided, 0u, abort) && *lost)) break;
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sw1 += (wb + (MODE == kSwiglu ? ti.f : min(2 * ti.f + 1, wblocks - 1))) * p.nkb;
                 const float* sx = p.sx + ti.row * p.nkb;
                 const int last = ti.rows - 1;
-                for (int round = 0; round < rounds && ok; ++round)
+                for (int sweep = 0; sweep < sweeps && ok; ++sweep)
                     for (int kb = kb0; kb < kb1; kb += kFKb, ++n) {
                         const int s = n % kFSlots;
                         float a[2][kFKb];  // rows w and w + 64 (FEW: the lane's)
@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const float x = a[j][i];
-                                const float f0 = pass ? class_factor(x, g0, round) : x * g0;
-                                const float f1 = pass ? class_factor(x, g1, round) : x * g1;
+                                const float f0 = pass ? class_factor(x, g0, sweep) : x * g0;
+                                const float f1 = pass ? class_factor(x, g1, sweep) : x * g1;
                                 f[i * 256 + 64 * j] = f0;
                                 f[i * 256 + 128 + 64 * j] = f1;
                                 low = fminf(low, fminf(fabsf(f0), fabsf(f1)));
@@ -641,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Rings rg = {tfull, tempty, ffull, fempty, 0u, 0u};
         int lt = 0;  // tiles so far
         bool ok = true;
-        int rounds = 1;
-        for (int pass = 0; pass < 2 && ok; ++pass, rounds = 3) {
+        int sweeps = 1;
+        for (int pass = 0; pass < 2 && ok; ++pass, sweeps = 3) {
             // (every factor of the tiles has been waited for, and with them what `lost` says)
             __syncwarp();
             if (pass && !*lost) break;
@@ -653,12 +653,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float acc[2 * RUN];
 #pragma unroll
                 for (int i = 0; i < 2 * RUN; ++i) acc[i] = 0.0f;
-                for (int round = 0; round < rounds && ok; ++round) {
+                for (int sweep = 0; sweep < sweeps && ok; ++sweep) {
                     ok = idle ? sums<RUN, false>(acc, kb1 - kb0, rg, fac + r, taddr, abort)
                               : sums<RUN, true>(acc, kb1 - kb0, rg, fac + r, taddr, abort);
-                    if (rounds > 1) {
+                    if (sweeps > 1) {
 #pragma unroll
-                        for (int i = 0; i < 2 * RUN; ++i) acc[i] = after_round(acc[i], round);
+                        for (int i = 0; i < 2 * RUN; ++i) acc[i] = after_sweep(acc[i], sweep);
                     }
                 }
                 if (!ok) {
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // into this CTA's shared memory (every copy into it has been consumed, and no
                     // second time will follow)
                     float* row = reinterpret_cast<float*>(smem) + r * kPartLd + c0;
-                    if (mine && !(*lost && rounds == 1))
+                    if (mine && !(*lost && sweeps == 1))
 #pragma unroll
                         for (int i = 0; i < 2 * RUN; i += 4)
                             *reinterpret_cast<float4*>(row + (i < RUN ? i : i - RUN + 128)) =
