@@ -737,3 +737,35 @@ def test_layer_at_a_checkpoints_size(T, E, every):
         check_within(eo[at], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs())
     ref, tol = expert_ref(x, sh, 0)
     check_within(eo[T * K:], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs())
+
+
+@pytest.mark.parametrize("T,d,I,E,K,shared", [
+    (64, 512, 1024, 40, 4, True), (1200, 640, 1024, 8, 4, True),   # tiles of 32 rows, of 128
+    (2, 2048, 256, 16, 3, True), (200, 1408, 128, 2, 2, False)])   # several CTAs on a tile
+def test_up_weights_whose_scale_and_the_rows_make_no_normal_number(T, d, I, E, K, shared):
+    """u near 2^-130 from scales whose product is near 2^-147 (three bits left in fp32), in some
+    blocks of some experts only: h and its codes, and the rows after the down product, as 64 bits
+    have them."""
+    g = gen(T + d + 1)
+    x = (torch.randn(T, d, generator=g, device=DEV) * 2.0 ** -60).to(torch.bfloat16)
+    sets = [make_experts(E, d, I, g)] + ([make_experts(1, d, I, g)] if shared else [])
+    for ex in sets:
+        for k, e in (("gate_s", 66), ("up_s", -70), ("down_s", 20)):
+            ex[k] = (ex[k].double() * 2.0 ** e).float()
+        ex["up_s"][:, :, ::3] *= 2.0 ** 8
+        ex["up_s"][::3] *= 2.0 ** 20
+    ex, sh = sets[0], sets[1] if shared else None
+    _, offsets, perm, _ = binding.permute(dispatch(T, E, K, g), E)
+    y = binding.grouped_swiglu(x, offsets, perm, K, ex, sh)
+    torch.cuda.synchronize()
+    binding.device_status()
+    off, tok = offsets.tolist(), perm.long() // K
+    for e in range(E):
+        if off[e + 1] > off[e]:
+            at = slice(off[e], off[e + 1])
+            ref, tol = expert_ref(x[tok[at]], ex, e)
+            assert 2.0 ** -126 < float(ref.abs().max()) < 1
+            check_within(y[at], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs() + 2.0 ** -134)
+    if shared:
+        ref, tol = expert_ref(x, sh, 0)
+        check_within(y[T * K:], ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs() + 2.0 ** -134)
