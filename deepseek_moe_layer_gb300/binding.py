@@ -27,7 +27,7 @@ EXPORTS = ("moe_last_error", "moe_version", "moe_device_status", "moe_route_deep
            "moe_route_softmax", "moe_shared_gate", "moe_combine_gated", "moe_forward_ex",
            "moe_forward_ex_workspace_bytes", "moe_watchdog_selftest", "moe_indexer_topk",
            "moe_set_fault", "moe_get_fault", "moe_route_softmax_grouped", "moe_quantize_blocks",
-           "moe_matmul_blocks")
+           "moe_matmul_blocks", "moe_cache_append", "moe_indexer_scores")
 MOE_ROUTE_DEEPSEEK, MOE_ROUTE_SOFTMAX, MOE_ROUTE_SOFTMAX_GROUPED = 0, 1, 2
 MOE_BITS_E4M3 = 0x108  # expert weights: e4m3 codes with an fp32 scale per 128 x 128 block
 
@@ -61,6 +61,26 @@ class LayerArgs(ctypes.Structure):
                 ("shared", ctypes.POINTER(ExpertWeights)), ("w_shared_gate", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("inds_out", ctypes.c_void_p),
                 ("scores_out", ctypes.c_void_p), ("logits_out", ctypes.c_void_p)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("T", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("W", ctypes.c_int32), ("slots", ctypes.c_void_p), ("cache", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("norm_weight", ctypes.c_void_p), ("norm_bias", ctypes.c_void_p),
+                ("norm_cols", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("rope_cols", ctypes.c_int32), ("rope_at", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("H", ctypes.c_int32), ("q_token", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("q_out_token", ctypes.c_int64),
+                ("q_out_head", ctypes.c_int64)]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("sequences", ctypes.c_int32),
+                ("width", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -113,6 +133,9 @@ def lib(path: str | None = None):
                                                     ctypes.POINTER(RouteParams), P, P, P]
             L.moe_quantize_blocks.argtypes = [P, ctypes.c_int, i64, i32, i64, i32, P, P, P]
             L.moe_matmul_blocks.argtypes = [P, P, i64, i64, P, P, i32, i32, ctypes.c_int, P, P]
+            L.moe_cache_append.argtypes = [ctypes.POINTER(AppendArgs), P]
+            L.moe_indexer_scores.argtypes = [P, P, i64, i32, ctypes.POINTER(PagedCache), P, P, P,
+                                             i32, P, i64, P]
             L.moe_get_fault.argtypes = [ctypes.POINTER(i32), ctypes.POINTER(i32)]
             for name in ("moe_device_status", "moe_route_deepseek", "moe_permute",
                          "moe_router_logits", "moe_grouped_swiglu", "moe_combine",
@@ -120,7 +143,8 @@ def lib(path: str | None = None):
                          "moe_route_softmax", "moe_shared_gate", "moe_combine_gated",
                          "moe_forward_ex", "moe_watchdog_selftest", "moe_indexer_topk",
                          "moe_set_fault", "moe_get_fault", "moe_route_softmax_grouped",
-                         "moe_quantize_blocks", "moe_matmul_blocks"):
+                         "moe_quantize_blocks", "moe_matmul_blocks", "moe_cache_append",
+                         "moe_indexer_scores"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -429,6 +453,128 @@ def indexer_topk(scores, k, lengths=None, want_mask=False, inds=None, mask=None,
                                   _ptr(inds), _ptr(mask), n if mask is not None else 0,
                                   _stream(stream)))
     return (inds, mask) if want_mask else inds
+
+
+def _need_vector(t, dtype, name, n, device):
+    _need(t, dtype, name, device)
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be [{n}], not {tuple(t.shape)}")
+
+
+def cache_append(x, slots, cache, scales=None, norm_weight=None, norm_bias=None, eps=1e-6,
+                 positions=None, inv_freq=None, rope_at=0, interleaved=True, q=None, q_out=None,
+                 stream=None):
+    """Rows of new tokens into a paged cache: x bf16 [T, W] (rows may be strided) -> row slots[t]
+    (int64 [T]; outside the cache: not written) of cache [pages, page, W], bf16, or float8_e4m3fn with
+    fp32 scales [pages, page, W/128].  The first len(norm_weight) columns are normalised (fp32
+    weight: RMS; with a bias: layer norm), 2 len(inv_freq) columns from rope_at on are rotated by
+    positions (int32 [T]) * inv_freq (fp32), in pairs of neighbours (interleaved) or of halves.
+    q bf16 [T, H, 2 len(inv_freq)] (tokens and heads may be strided) is rotated too, into q_out (a new
+    tensor, or given: q itself, a slice of wider queries).  Returns cache, or (cache, q_out) with q."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x: dtype {x.dtype}, expected {torch.bfloat16}")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [T, W] with unit stride along W")
+    T, W = x.shape
+    dev = x.device
+    _need_vector(slots, torch.int64, "slots", T, dev)
+    if cache.dim() != 3 or cache.shape[2] != W:
+        raise ValueError(f"cache must be [pages, page, {W}], not {tuple(cache.shape)}")
+    _need(cache, torch.bfloat16 if scales is None else torch.float8_e4m3fn, "cache", dev)
+    if scales is not None:
+        _need_out(scales, torch.float32, "scales", (*cache.shape[:2], W // 128), dev)
+    a = AppendArgs()
+    a.x, a.T, a.W, a.ldx = x.data_ptr(), T, W, x.stride(0) if T > 1 else W
+    a.slots, a.cache, a.rows = slots.data_ptr(), cache.data_ptr(), cache.shape[0] * cache.shape[1]
+    a.scales = None if scales is None else scales.data_ptr()
+    if norm_weight is not None:
+        a.norm_cols, a.eps = norm_weight.numel(), eps
+        _need_vector(norm_weight, torch.float32, "norm_weight", a.norm_cols, dev)
+        a.norm_weight = norm_weight.data_ptr()
+        if norm_bias is not None:
+            _need_vector(norm_bias, torch.float32, "norm_bias", a.norm_cols, dev)
+            a.norm_bias = norm_bias.data_ptr()
+    elif norm_bias is not None:
+        raise ValueError("norm_bias given without norm_weight")
+    if inv_freq is not None:
+        R = 2 * inv_freq.numel()
+        _need_vector(inv_freq, torch.float32, "inv_freq", R // 2, dev)
+        if positions is None:
+            raise ValueError("inv_freq given without positions")
+        _need_vector(positions, torch.int32, "positions", T, dev)
+        a.positions, a.inv_freq = positions.data_ptr(), inv_freq.data_ptr()
+        a.rope_cols, a.rope_at, a.interleaved = R, rope_at, int(bool(interleaved))
+    if q is not None:
+        if inv_freq is None:
+            raise ValueError("q given without inv_freq")
+        if q_out is None:
+            q_out = _empty(q.shape, torch.bfloat16, dev, stream)
+        for t, name in ((q, "q"), (q_out, "q_out")):
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+            if t.dim() != 3 or t.shape[0] != T or t.shape[2] != R or t.stride(2) != 1 or \
+                    t.shape[1] != q.shape[1]:
+                raise ValueError(f"{name} must be [{T}, H, {R}] with unit stride along its columns")
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        a.q, a.q_out, a.H = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+        # (the stride of an axis of one is arbitrary)
+        a.q_token, a.q_head = (q.stride(i) if q.shape[i] > 1 else 0 for i in (0, 1))
+        a.q_out_token, a.q_out_head = (q_out.stride(i) if q.shape[i] > 1 else 0 for i in (0, 1))
+    elif q_out is not None:
+        raise ValueError("q_out given without q")
+    _check((_lib or lib()).moe_cache_append(ctypes.byref(a), _raw_stream(x, stream)))
+    return cache if q is None else (cache, q_out)
+
+
+def _paged_cache(rows, dtype, name, width, table, lengths, cu_tokens, T, dev):
+    if rows.dim() != 3 or rows.shape[2] != width:
+        raise ValueError(f"{name} must be [pages, page, {width}], not {tuple(rows.shape)}")
+    _need(rows, dtype, name, dev)
+    if table.dim() != 2:
+        raise ValueError("block_table must be [sequences, pages]")
+    _need(table, torch.int32, "block_table", dev)
+    _need_vector(lengths, torch.int32, "lengths", T, dev)
+    if cu_tokens is not None:
+        _need_vector(cu_tokens, torch.int32, "cu_tokens", table.shape[0] + 1, dev)
+    elif table.shape[0] != T:
+        raise ValueError(f"block_table has {table.shape[0]} rows for {T} tokens, and cu_tokens is None")
+    return PagedCache(rows.data_ptr(), rows.shape[0], rows.shape[1], table.data_ptr(),
+                      table.shape[0], table.shape[1])
+
+
+def indexer_scores(q, weights, keys, block_table, lengths, n, key_scales=None, cu_tokens=None,
+                   out=None, stream=None):
+    """The indexer's scores of the cached positions: q [T, H, 128] and keys [pages, page, 128] bf16, or
+    both float8_e4m3fn with fp32 key_scales [pages, page, 1] (or [pages, page]); weights fp32 [T, H];
+    block_table int32 [B, pages of a sequence]; lengths int32 [T], the positions each token may see;
+    cu_tokens int32 [B + 1], or None for one token per sequence -> fp32 [T, n] (rows of a given `out` may
+    be strided), s_j sum_h weights[t, h] max(q[t, h] . k_j, 0) for j < lengths[t], -inf for the others."""
+    dtype = torch.bfloat16 if key_scales is None else torch.float8_e4m3fn
+    if q.dim() != 3 or q.shape[2] != 128:
+        raise ValueError(f"q must be [T, H, 128], not {tuple(q.shape)}")
+    _need(q, dtype, "q")
+    T, H, dev = q.shape[0], q.shape[1], q.device
+    _need_out(weights, torch.float32, "weights", (T, H), dev)
+    c = _paged_cache(keys, dtype, "keys", 128, block_table, lengths, cu_tokens, T, dev)
+    if key_scales is not None:
+        _need(key_scales, torch.float32, "key_scales", dev)
+        if key_scales.shape not in (keys.shape[:2], (*keys.shape[:2], 1)):
+            raise ValueError(f"key_scales must be {(*keys.shape[:2], 1)}, not {tuple(key_scales.shape)}")
+    n = int(n)
+    if out is None:
+        out = _empty((T, n), torch.float32, dev, stream)
+    else:
+        if out.dtype != torch.float32:
+            raise TypeError(f"out: dtype {out.dtype}, expected {torch.float32}")
+        if out.shape != (T, n) or (n > 1 and out.stride(1) != 1) or out.device != dev:
+            raise ValueError(f"out must be [{T}, {n}] on {dev} with unit stride along its rows")
+    _check((_lib or lib()).moe_indexer_scores(
+        q.data_ptr(), weights.data_ptr(), T, H, ctypes.byref(c),
+        None if key_scales is None else key_scales.data_ptr(),
+        None if cu_tokens is None else cu_tokens.data_ptr(), lengths.data_ptr(), n, out.data_ptr(),
+        out.stride(0) if T > 1 else n, _raw_stream(q, stream)))
+    return out
 
 
 def permute(inds, E, stream=None):

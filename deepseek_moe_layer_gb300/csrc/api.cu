@@ -218,6 +218,29 @@ int check_scaled_dims(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K) {
     return MOE_OK;
 }
 
+// Positions are 32-bit, and rounded up to tiles.
+constexpr int64_t kMaxPositions = ((int64_t)1 << 31) - 512;
+
+// What the readers of a paged cache have in common.
+int check_paged(const moe_paged_cache_t* c, int64_t T, const int32_t* cu, const int32_t* lengths) {
+    MOE_CHECK(c, "cache is NULL");
+    MOE_CHECK(T >= 0 && T < kMaxPositions, "T = %lld outside [0, 2^31 - 512)", (long long)T);
+    MOE_CHECK(c->page >= 1, "page = %d < 1", c->page);
+    MOE_CHECK(c->pages >= 0 && c->pages < ((int64_t)1 << 31), "pages = %lld outside [0, 2^31)",
+              (long long)c->pages);
+    MOE_CHECK(c->width >= 0 && (int64_t)c->width * c->page <= kMaxPositions,
+              "width x page = %d x %d: more than 2^31 - 512 positions", c->width, c->page);
+    MOE_CHECK(c->sequences >= 0, "sequences = %d < 0", c->sequences);
+    MOE_CHECK(cu || c->sequences == T, "sequences = %d, but T = %lld tokens without cu_tokens",
+              c->sequences, (long long)T);
+    MOE_CHECK(T == 0 || (lengths && c->sequences > 0), "NULL lengths, or tokens without a sequence");
+    MOE_CHECK(c->width == 0 || c->sequences == 0 || c->pages == 0 || (c->table && c->rows),
+              "NULL pointer in the cache");
+    MOE_CHECK(aligned(c->table, 4) && aligned(cu, 4) && aligned(lengths, 4),
+              "table, cu_tokens and lengths must be 4-byte aligned");
+    return MOE_OK;
+}
+
 bool is_scaled(const moe_expert_weights_t* w) { return w && w->bits == MOE_BITS_E4M3; }
 
 int check_dims(int64_t T, int32_t d, int32_t I, int32_t E, int32_t K) {
@@ -666,6 +689,8 @@ int moe_device_status(int32_t clear, moe_stream_t stream) {
     unsigned int st8 = 0;
     MOE_CUDA(moe::read_scaled_status(&st8, clear, (cudaStream_t)stream), "status read");
     if (st == 0) st = st8;
+    MOE_CUDA(moe::read_scores_status(&st8, clear, (cudaStream_t)stream), "status read");
+    if (st == 0) st = st8;
     if (st == 5)
         return fail(MOE_ERR_CUDA, "a CTA pair of an expert GEMM held different TMEM columns "
                                   "(status %u); the GEMM did no work", st);
@@ -1026,6 +1051,111 @@ int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t ld
     g.out = out;
     g.f32 = out_dtype == MOE_DTYPE_F32;
     MOE_LAUNCH(moe::launch_scaled_gemm(g, (cudaStream_t)stream), "block-scaled product");
+    return MOE_OK;
+}
+
+int moe_cache_append(const moe_append_args_t* args, moe_stream_t stream) {
+    begin_call();
+    MOE_CHECK(args, "args is NULL");
+    const moe_append_args_t& a = *args;
+    MOE_CHECK(a.T >= 0 && a.T < ((int64_t)1 << 31), "T = %lld outside [0, 2^31)", (long long)a.T);
+    MOE_CHECK(a.W >= 8 && a.W % 8 == 0 && a.W <= 1024, "W = %d must be a multiple of 8 up to 1024", a.W);
+    MOE_CHECK(a.ldx >= a.W && a.ldx % 8 == 0, "ldx = %lld must be at least W = %d and a multiple of 8",
+              (long long)a.ldx, a.W);
+    MOE_CHECK(a.rows >= 0 && a.rows < ((int64_t)1 << 40), "rows = %lld outside [0, 2^40)",
+              (long long)a.rows);
+    MOE_CHECK(a.norm_cols >= 0 && a.norm_cols <= a.W && a.norm_cols % 8 == 0,
+              "norm_cols = %d must be a multiple of 8 in [0, W = %d]", a.norm_cols, a.W);
+    MOE_CHECK(!a.norm_cols || a.eps >= 0.0f, "eps = %g < 0", (double)a.eps);
+    MOE_CHECK(a.rope_cols >= 0 && a.rope_cols % 16 == 0, "rope_cols = %d must be a multiple of 16",
+              a.rope_cols);
+    MOE_CHECK(a.rope_at >= 0 && a.rope_at % 8 == 0 && a.rope_at <= a.W - a.rope_cols,
+              "rope_at = %d must be a multiple of 8 in [0, W - rope_cols = %d]", a.rope_at,
+              a.W - a.rope_cols);
+    MOE_CHECK(!a.scales || a.W % 128 == 0, "W = %d of an e4m3 cache must be a multiple of 128", a.W);
+    MOE_CHECK(!a.q || a.rope_cols, "q given without a rotation");
+    if (a.q) {
+        MOE_CHECK(a.H >= 1 && a.H <= 1024, "H = %d outside [1, 1024]", a.H);
+        MOE_CHECK(a.q_token % 8 == 0 && a.q_head % 8 == 0 && a.q_out_token % 8 == 0 &&
+                      a.q_out_head % 8 == 0,
+                  "strides of q and q_out must be multiples of 8");
+    }
+    MOE_CHECK(a.T == 0 || (a.x && a.slots && a.cache && (!a.norm_cols || a.norm_weight) &&
+                           (!a.rope_cols || (a.positions && a.inv_freq)) && (!a.q || a.q_out)),
+              "NULL pointer argument");
+    MOE_CHECK(aligned(a.x, 16) && aligned(a.cache, 16) && aligned(a.q, 16) && aligned(a.q_out, 16),
+              "x, cache, q and q_out must be 16-byte aligned");
+    MOE_CHECK(aligned(a.slots, 8) && aligned(a.scales, 4) && aligned(a.norm_weight, 4) &&
+                  aligned(a.norm_bias, 4) && aligned(a.positions, 4) && aligned(a.inv_freq, 4),
+              "slots, scales, norm_weight, norm_bias, positions and inv_freq must be aligned to "
+              "their type");
+    if (a.T == 0) return MOE_OK;
+    int rc = check_device();
+    if (rc) return rc;
+    moe::AppendArgs k = {};
+    k.x = a.x;
+    k.T = a.T;
+    k.ldx = a.ldx;
+    k.W = a.W;
+    k.slots = reinterpret_cast<const long long*>(a.slots);
+    k.cache = a.cache;
+    k.scales = a.scales;
+    k.rows = a.rows;
+    k.norm_weight = a.norm_weight;
+    k.norm_bias = a.norm_bias;
+    k.norm_cols = a.norm_cols;
+    k.eps = a.eps;
+    k.positions = a.positions;
+    k.inv_freq = a.inv_freq;
+    k.R = a.rope_cols;
+    k.rope_at = a.rope_at;
+    k.interleaved = a.interleaved != 0;
+    k.q = a.q;
+    k.q_out = a.q_out;
+    k.H = a.H;
+    k.q_token = a.q_token;
+    k.q_head = a.q_head;
+    k.o_token = a.q_out_token;
+    k.o_head = a.q_out_head;
+    MOE_LAUNCH(moe::launch_append(k, (cudaStream_t)stream), "append kernel");
+    return MOE_OK;
+}
+
+int moe_indexer_scores(const void* q, const float* weights, int64_t T, int32_t H,
+                       const moe_paged_cache_t* keys, const float* key_scales,
+                       const int32_t* cu_tokens, const int32_t* lengths, int32_t n, float* out,
+                       int64_t ld, moe_stream_t stream) {
+    begin_call();
+    int rc = check_paged(keys, T, cu_tokens, lengths);
+    if (rc) return rc;
+    MOE_CHECK(H >= 1 && H <= 128, "H = %d outside [1, 128]", H);
+    MOE_CHECK(n >= 0 && n <= kMaxPositions, "n = %d outside [0, 2^31 - 512]", n);
+    MOE_CHECK(ld >= n, "ld = %lld < n = %d", (long long)ld, n);
+    MOE_CHECK(T == 0 || n == 0 || (q && weights && out), "NULL pointer argument");
+    MOE_CHECK(aligned(q, 16) && aligned(keys->rows, 16), "q and the cache must be 16-byte aligned");
+    MOE_CHECK(aligned(weights, 4) && aligned(key_scales, 4) && aligned(out, 4),
+              "weights, key_scales and out must be 4-byte aligned");
+    if (T == 0 || n == 0) return MOE_OK;
+    rc = check_device();
+    if (rc) return rc;
+    moe::ScoresArgs a = {};
+    a.q = q;
+    a.weights = weights;
+    a.T = T;
+    a.H = H;
+    a.keys = keys->rows;
+    a.key_scales = key_scales;
+    a.pages = keys->pages;
+    a.page = keys->page;
+    a.table = keys->table;
+    a.B = keys->sequences;
+    a.width = keys->width;
+    a.cu = cu_tokens;
+    a.lengths = lengths;
+    a.n = n;
+    a.out = out;
+    a.ld = ld;
+    MOE_LAUNCH(moe::launch_scores(a, (cudaStream_t)stream), "scores kernel");
     return MOE_OK;
 }
 

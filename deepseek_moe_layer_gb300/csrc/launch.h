@@ -183,6 +183,49 @@ struct ScaledGemmArgs {
 };
 cudaError_t launch_scaled_gemm(const ScaledGemmArgs& a, cudaStream_t s);
 
+// ---- operators over a paged cache ---------------------------------------------------
+struct AppendArgs {
+    const void* x;               // bf16 [T, W], rows ldx elements apart
+    long long T, ldx;
+    int W;
+    const long long* slots;      // [T] row of the cache, outside [0, rows): not written
+    void* cache;                 // [rows, W] bf16, or e4m3 with scales
+    float* scales;               // [rows, W / 128] or nullptr
+    long long rows;
+    const float* norm_weight;    // [norm_cols]
+    const float* norm_bias;      // [norm_cols] or nullptr (RMS)
+    int norm_cols;               // 0: no normalisation
+    float eps;
+    const int32_t* positions;    // [T]
+    const float* inv_freq;       // [R / 2]
+    int R, rope_at, interleaved; // R = 0: no rotation
+    const void* q;               // bf16 [T, H, R], or nullptr
+    void* q_out;
+    int H;
+    long long q_token, q_head, o_token, o_head;  // strides in elements
+};
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
+
+struct ScoresArgs {
+    const void* q;               // [T, H, 128] bf16, or e4m3 with key_scales
+    const float* weights;        // [T, H]
+    long long T;
+    int H;
+    const void* keys;            // [pages * page, 128]
+    const float* key_scales;     // [pages * page] or nullptr
+    long long pages;
+    int page;
+    const int32_t* table;        // [B, width]
+    int B, width;
+    const int32_t* cu;           // [B + 1] or nullptr
+    const int32_t* lengths;      // [T]
+    int n;
+    float* out;                  // [T, ld]
+    long long ld;
+};
+cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s);
+cudaError_t read_scores_status(unsigned int* out, int clear, cudaStream_t s);
+
 // Per-device status word of the kernels with bounded waits.
 cudaError_t read_device_status(unsigned int* out, int clear, cudaStream_t s);
 // The block-scaled products' own.

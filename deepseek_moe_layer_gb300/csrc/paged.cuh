@@ -1,0 +1,63 @@
+// paged.cuh -- device helpers of the operators over a paged cache: where a sequence's position
+// lies, which sequence a token belongs to, asynchronous 16-byte copies.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// A cache of `pages` pages of `page` rows; sequence b's position j lies in row j % page of page
+// table[b * width + j / page].
+struct Paged {
+    const int32_t* table;
+    int width, page;
+    long long pages;
+};
+
+// Row of the cache that holds position pos of sequence b, -1 for a page outside the cache.
+MOE_DEV long long paged_row(const Paged& c, int b, int pos) {
+    const unsigned at = (unsigned)pos / (unsigned)c.page;
+    const int id = __ldg(c.table + (long long)b * c.width + at);
+    return (unsigned)id < (unsigned long long)c.pages
+               ? (long long)id * c.page + ((unsigned)pos - at * (unsigned)c.page)
+               : -1;
+}
+
+// Sequences of tokens: sequence b's are cu[b] .. cu[b + 1] - 1, or token b alone without cu.
+struct Sequences {
+    const int32_t* cu;       // [B + 1] or nullptr
+    const int32_t* lengths;  // [T] positions a token may see
+    int B, T;
+    int most;                // positions a table row has room for
+};
+
+MOE_DEV int seq_tokens(const Sequences& q) {  // tokens that belong to a sequence
+    return q.cu ? max(0, min(q.T, __ldg(q.cu + q.B))) : q.T;
+}
+// The sequence of token t < seq_tokens(): the last b with cu[b] <= t.
+MOE_DEV int seq_of(const Sequences& q, int t) {
+    if (!q.cu) return t;
+    int lo = 0, hi = q.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(q.cu + mid) <= t) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+MOE_DEV int seq_end(const Sequences& q, int b) { return q.cu ? min(q.T, __ldg(q.cu + b + 1)) : b + 1; }
+MOE_DEV int seq_length(const Sequences& q, int t) { return max(0, min(q.most, __ldg(q.lengths + t))); }
+
+// 16 bytes global -> shared, of which the first `bytes` (16 or 0) are read and the rest is zero.
+MOE_DEV void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+MOE_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+MOE_DEV void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// What this thread wrote to shared memory becomes visible to the tensor cores and the bulk copies.
+MOE_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+}  // namespace moe

@@ -227,6 +227,89 @@ int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t ld
                       moe_stream_t stream);
 
 /*
+ * moe_cache_append -- new tokens' rows into a paged cache and the rotation of their queries,
+ * without a counterpart in the pages: what fills the caches that moe_indexer_scores and
+ * moe_latent_attention read.
+ *   x bf16 [T, W], rows ldx elements apart; W a multiple of 8 up to 1024.
+ *   y[t] = x[t], then in this order
+ *     - columns c < norm_cols (a multiple of 8; 0: none) normalised: without norm_bias
+ *       x / sqrt(mean(x^2) + eps) * norm_weight, with it (x - mean) / sqrt(var + eps) * norm_weight +
+ *       norm_bias (mean, mean(x^2) and var over those columns);
+ *     - columns rope_at .. rope_at + rope_cols - 1 (rope_cols a multiple of 16, 0: none; rope_at of 8)
+ *       rotated: pair i, columns (2i, 2i + 1) if interleaved, else (i, i + rope_cols / 2), is turned
+ *       by the angle positions[t] * inv_freq[i]: (u, v) -> (u cos - v sin, v cos + u sin).
+ *   Out: row slots[t] of the cache [rows, W] (row = page id * rows per page + row in the page; a
+ *   slot outside [0, rows) is not written, -1 for tokens without a place), rounded once: bf16, or
+ *   with scales != NULL e4m3 codes and fp32 scales [rows, W / 128] as of moe_quantize_blocks (W a
+ *   multiple of 128).  The slots inside [0, rows) must differ from each other: of two tokens with
+ *   one slot any part of either may stay.  The cache and x must not overlap.
+ *   q != NULL: queries bf16 [T, H, rope_cols], token and head strides q_token and q_head (in
+ *   elements, multiples of 8), rotated in the same way into q_out (strides q_out_token,
+ *   q_out_head); q_out may be q itself.  Tokens without a slot are rotated too.
+ * Errors: MOE_ERR_INVALID for NULL pointers, T outside [0, 2^31), sizes and strides against the
+ * rules above, H outside [1, 1024], x, cache, q or q_out not 16-byte aligned.  T == 0 is a no-op.
+ */
+typedef struct {
+    const void* x;
+    int64_t T, ldx;
+    int32_t W;
+    const int64_t* slots;
+    void* cache;
+    float* scales;
+    int64_t rows;
+    const float* norm_weight;
+    const float* norm_bias;
+    int32_t norm_cols;
+    float eps;
+    const int32_t* positions;
+    const float* inv_freq;
+    int32_t rope_cols, rope_at, interleaved;
+    const void* q;
+    void* q_out;
+    int32_t H;
+    int64_t q_token, q_head, q_out_token, q_out_head;
+} moe_append_args_t;
+
+int moe_cache_append(const moe_append_args_t* args, moe_stream_t stream);
+
+/*
+ * A paged cache as its readers see it: `pages` pages of `page` rows each, one row per position;
+ * sequence b's position j is row j % page of page table[b * width + j / page].  A table entry
+ * outside [0, pages) is a page that is not there: its positions count as not visible.
+ * Tokens and sequences: T tokens (rows of q); sequence b's tokens are cu_tokens[b] ..
+ * cu_tokens[b + 1] - 1 (cu_tokens [sequences + 1], ascending from 0), or, with cu_tokens NULL, token b
+ * alone (sequences == T).  Rows from cu_tokens[sequences] on belong to no sequence and their outputs
+ * are left as they were.  lengths[t] (clamped to [0, width * page]) is the number of
+ * positions of its sequence that token t may see: its causal length.
+ */
+typedef struct {
+    const void* rows;
+    int64_t pages;
+    int32_t page;
+    const int32_t* table;
+    int32_t sequences, width;
+} moe_paged_cache_t;
+
+/*
+ * moe_indexer_scores -- the indexer's scores of the cached positions (SwiftLM issue #139, "What
+ * needs building" item 1: ReLU(q . k) weighted per head, summed over the heads), what
+ * moe_indexer_topk selects from:
+ *     out[t, j] = s_j * sum_h weights[t, h] * max(q[t, h] . k_j, 0)   for j < lengths[t],
+ *   -inf for the other j < n and for positions whose page is not there.
+ *   q [T, H, 128] and the cache's rows [128] bf16, products and sums in fp32; or, with key_scales
+ *   (fp32, one per cache row) both e4m3, s_j the key's scale (1 without; a query's own scale goes into
+ *   its weights).  weights fp32 [T, H], of any sign.  1 <= H <= 128.  out fp32 [T, ld], n positions
+ *   per row (ld >= n, in elements); what lies between n and ld is left as it was.
+ * Errors: MOE_ERR_INVALID for NULL pointers, H outside [1, 128], n outside [0, 2^31 - 512], ld < n,
+ * a cache with page < 1, pages outside [0, 2^31) or more than 2^31 - 512 positions per sequence,
+ * sequences != T without cu_tokens, q or rows not 16-byte aligned.  T == 0 or n == 0 is a no-op.
+ */
+int moe_indexer_scores(const void* q, const float* weights, int64_t T, int32_t H,
+                       const moe_paged_cache_t* keys, const float* key_scales,
+                       const int32_t* cu_tokens, const int32_t* lengths, int32_t n, float* out,
+                       int64_t ld, moe_stream_t stream);
+
+/*
  * moe_permute -- token-to-expert dispatch ([epic] first paragraph: the grouping that
  * gather_mm / gather_qmm consume).  inds [T, K] int32 expert ids of the P = T*K pairs
  * p = t*K + k.
