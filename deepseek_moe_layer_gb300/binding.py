@@ -27,7 +27,8 @@ EXPORTS = ("moe_last_error", "moe_version", "moe_device_status", "moe_route_deep
            "moe_route_softmax", "moe_shared_gate", "moe_combine_gated", "moe_forward_ex",
            "moe_forward_ex_workspace_bytes", "moe_watchdog_selftest", "moe_indexer_topk",
            "moe_set_fault", "moe_get_fault", "moe_route_softmax_grouped", "moe_quantize_blocks",
-           "moe_matmul_blocks", "moe_cache_append", "moe_indexer_scores")
+           "moe_matmul_blocks", "moe_cache_append", "moe_indexer_scores",
+           "moe_latent_attention", "moe_latent_attention_workspace_bytes")
 MOE_ROUTE_DEEPSEEK, MOE_ROUTE_SOFTMAX, MOE_ROUTE_SOFTMAX_GROUPED = 0, 1, 2
 MOE_BITS_E4M3 = 0x108  # expert weights: e4m3 codes with an fp32 scale per 128 x 128 block
 
@@ -136,6 +137,10 @@ def lib(path: str | None = None):
             L.moe_cache_append.argtypes = [ctypes.POINTER(AppendArgs), P]
             L.moe_indexer_scores.argtypes = [P, P, i64, i32, ctypes.POINTER(PagedCache), P, P, P,
                                              i32, P, i64, P]
+            L.moe_latent_attention.argtypes = [P, i64, i32, i64, i64, ctypes.POINTER(PagedCache), P,
+                                               P, ctypes.c_float, P, i32, P, P, P, sz, P]
+            L.moe_latent_attention_workspace_bytes.argtypes = [i64, i64]
+            L.moe_latent_attention_workspace_bytes.restype = sz
             L.moe_get_fault.argtypes = [ctypes.POINTER(i32), ctypes.POINTER(i32)]
             for name in ("moe_device_status", "moe_route_deepseek", "moe_permute",
                          "moe_router_logits", "moe_grouped_swiglu", "moe_combine",
@@ -144,7 +149,7 @@ def lib(path: str | None = None):
                          "moe_forward_ex", "moe_watchdog_selftest", "moe_indexer_topk",
                          "moe_set_fault", "moe_get_fault", "moe_route_softmax_grouped",
                          "moe_quantize_blocks", "moe_matmul_blocks", "moe_cache_append",
-                         "moe_indexer_scores"):
+                         "moe_indexer_scores", "moe_latent_attention"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -575,6 +580,44 @@ def indexer_scores(q, weights, keys, block_table, lengths, n, key_scales=None, c
         None if cu_tokens is None else cu_tokens.data_ptr(), lengths.data_ptr(), n, out.data_ptr(),
         out.stride(0) if T > 1 else n, _raw_stream(q, stream)))
     return out
+
+
+def latent_attention(q, cache, block_table, lengths, scale, inds=None, cu_tokens=None, out=None,
+                     want_lse=False, ws=None, stream=None):
+    """Attention over cached latent rows, absorbed form: q bf16 [T, H, 576] (tokens and heads may be
+    strided), cache bf16 [pages, page, 576], block_table int32 [B, pages of a sequence], lengths int32 [T]
+    (positions each token may see), cu_tokens int32 [B + 1] or None for one token per sequence, inds int32
+    [T, k] (selected positions, as indexer_topk gives them) or None for all -> bf16 [T, H, 512], and
+    with want_lse also the fp32 [T, H] log-sum-exp of the scaled scores."""
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q: dtype {q.dtype}, expected {torch.bfloat16}")
+    if q.dim() != 3 or q.shape[2] != 576 or q.stride(2) != 1:
+        raise ValueError(f"q must be [T, H, 576] with unit stride along its columns, not {tuple(q.shape)}")
+    T, H, dev = q.shape[0], q.shape[1], q.device
+    c = _paged_cache(cache, torch.bfloat16, "cache", 576, block_table, lengths, cu_tokens, T, dev)
+    k = 0
+    if inds is not None:
+        if inds.dim() != 2 or inds.shape[0] != T:
+            raise ValueError(f"inds must be [{T}, k], not {tuple(inds.shape)}")
+        _need(inds, torch.int32, "inds", dev)
+        k = inds.shape[1]
+    if out is None:
+        out = _empty((T, H, 512), torch.bfloat16, dev, stream)
+    else:
+        _need_out(out, torch.bfloat16, "out", (T, H, 512), dev)
+    lse = _empty((T, H), torch.float32, dev, stream) if want_lse else None
+    L = _lib or lib()
+    if ws is None:
+        need = L.moe_latent_attention_workspace_bytes(T, k if inds is not None else c.width * c.page)
+        ws = _empty(max(need, 256), torch.uint8, dev, stream, returned=False)
+    else:
+        _need(ws, torch.uint8, "ws", dev)
+    _check(L.moe_latent_attention(
+        q.data_ptr(), T, H, q.stride(0) if T > 1 else 0, q.stride(1) if H > 1 else 0, ctypes.byref(c),
+        None if cu_tokens is None else cu_tokens.data_ptr(), lengths.data_ptr(), scale,
+        None if inds is None else inds.data_ptr(), k, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(q, stream)))
+    return (out, lse) if want_lse else out
 
 
 def permute(inds, E, stream=None):

@@ -691,9 +691,11 @@ int moe_device_status(int32_t clear, moe_stream_t stream) {
     if (st == 0) st = st8;
     MOE_CUDA(moe::read_scores_status(&st8, clear, (cudaStream_t)stream), "status read");
     if (st == 0) st = st8;
+    MOE_CUDA(moe::read_attention_status(&st8, clear, (cudaStream_t)stream), "status read");
+    if (st == 0) st = st8;
     if (st == 5)
-        return fail(MOE_ERR_CUDA, "a CTA pair of an expert GEMM held different TMEM columns "
-                                  "(status %u); the GEMM did no work", st);
+        return fail(MOE_ERR_CUDA, "a CTA pair of an expert GEMM or of the attention held different "
+                                  "TMEM columns (status %u); the kernel did no work", st);
     if (st != 0) return fail(MOE_ERR_TIMEOUT, "a device-side wait gave up (status %u)", st);
     return MOE_OK;
 }
@@ -1156,6 +1158,58 @@ int moe_indexer_scores(const void* q, const float* weights, int64_t T, int32_t H
     a.out = out;
     a.ld = ld;
     MOE_LAUNCH(moe::launch_scores(a, (cudaStream_t)stream), "scores kernel");
+    return MOE_OK;
+}
+
+size_t moe_latent_attention_workspace_bytes(int64_t T, int64_t positions) {
+    if (T <= 0 || T >= kMaxPositions || positions < 0 || positions >= ((int64_t)1 << 31)) return 0;
+    return moe::attention_ws_bytes(moe::attention_pairs(T, positions));
+}
+
+int moe_latent_attention(const void* q, int64_t T, int32_t H, int64_t q_token, int64_t q_head,
+                         const moe_paged_cache_t* cache, const int32_t* cu_tokens,
+                         const int32_t* lengths, float scale, const int32_t* inds, int32_t k,
+                         void* out, float* lse, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    begin_call();
+    int rc = check_paged(cache, T, cu_tokens, lengths);
+    if (rc) return rc;
+    MOE_CHECK(H >= 1 && H <= 128, "H = %d outside [1, 128]", H);
+    MOE_CHECK(q_token % 8 == 0 && q_head % 8 == 0, "strides of q must be multiples of 8");
+    MOE_CHECK(!inds || (k >= 1 && k <= kMaxPositions), "k = %d outside [1, 2^31 - 512]", k);
+    MOE_CHECK(T == 0 || (q && out && ws), "NULL pointer argument");
+    MOE_CHECK(aligned(q, 16) && aligned(cache->rows, 16) && aligned(out, 16),
+              "q, the cache and out must be 16-byte aligned");
+    MOE_CHECK(aligned(inds, 4) && aligned(lse, 4), "inds and lse must be 4-byte aligned");
+    MOE_CHECK(aligned(ws, 256), "ws must be 256-byte aligned");
+    const size_t need = moe_latent_attention_workspace_bytes(
+        T, inds ? (int64_t)k : (int64_t)cache->width * cache->page);
+    MOE_CHECK(ws_bytes >= need, "ws_bytes = %zu < %zu required", ws_bytes, need);
+    if (T == 0) return MOE_OK;
+    rc = check_device();
+    if (rc) return rc;
+    moe::AttentionArgs a = {};
+    a.q = q;
+    a.T = T;
+    a.q_token = q_token;
+    a.q_head = q_head;
+    a.H = H;
+    a.rows = cache->rows;
+    a.pages = cache->pages;
+    a.page = cache->page;
+    a.table = cache->table;
+    a.B = cache->sequences;
+    a.width = cache->width;
+    a.cu = cu_tokens;
+    a.lengths = lengths;
+    a.scale = scale;
+    a.inds = inds;
+    a.k = k;
+    a.out = out;
+    a.lse = lse;
+    a.ws = ws;
+    PdlScope pdl;
+    pdl.on();  // the join's launch overlaps the attention kernel's tail
+    MOE_LAUNCH(moe::launch_attention(a, (cudaStream_t)stream), "attention kernel");
     return MOE_OK;
 }
 

@@ -1,0 +1,772 @@
+// latent_attention.cu -- attention over a paged cache of one latent row per position, absorbed form,
+// on the 5th-generation tensor cores:
+//     o[t, h] = sum_j p_j c_j[0:512],   p = softmax_j(scale * q[t, h] . c_j),   c_j 576 columns
+// over the first lengths[t] positions of token t's sequence, or over the selected ones inds[t, :].
+// All heads read the same rows: a cache row is loaded once and is key and value of every head.
+//
+// One pass over the positions with the softmax's running maximum m and sum l per (token, head) row,
+// both fp32 and in base 2.  The maximum is a reference only: it moves (and the sums are
+// rescaled) when a score passes it by more than 8, so p <= 2^8 and the rescaling of 512 columns of
+// TMEM is rare.  p is rounded to bf16 for the second product (2^-9 of each term, the inputs' own
+// precision); l sums the fp32 values.
+//
+// 128 rows x 512 fp32 columns of o are all of an SM's TMEM, so a CTA pair shares them: each CTA
+// has 64 rows, and cta_group::2 UMMAs with M = 128 run both halves at the full rate (a CTA's 64 rows
+// lie in lanes 0..63 for the first half of N and in lanes 64..127 for the second).  A tile is 64
+// positions.  s = q c^T (N = 64, K = 576): each CTA holds 32 of the positions as the K-major B
+// operand.  o += p c (N = 512 as two UMMAs of 256, K = 64): each CTA holds half of the columns of
+// all 64 positions, the same swizzled rows read as an MN-major B operand.  So a pair loads
+// 139 KB per tile where 74 KB are unique: the rest comes from L2.
+//
+// Work is one list of tiles over all segments (up to 128 / H consecutive tokens of a sequence;
+// one token with a selection), cut into equal runs, one per pair, so that sequences of any
+// lengths fill the device; a segment cut apart leaves partial sums (m, l, o in fp32) that a second
+// kernel joins in the order of the pairs: equal calls give equal bits.
+//
+// Warp roles (480 threads): warps 0..3 softmax, rescaling and epilogue (a thread is a row and half of
+// its positions or columns), 4..7 copies of the K-major rows, 8..11 of the MN-major columns (16-byte
+// asynchronous copies, so pages of any size and selected rows are alike; absent rows are zeros),
+// 12 UMMA issuer (of the pair's even CTA), 13 and 14 queries.  Every wait is bounded.
+#include <mutex>
+
+#include "launch.h"
+#include "paged.cuh"
+
+namespace moe {
+
+__device__ unsigned int g_attention_status;
+
+namespace {
+
+constexpr int kWidth = 576, kLatent = 512;
+constexpr int kRowBytes = 2 * kWidth;
+constexpr int kTile = 64;                       // positions per tile
+constexpr int kRows = 128;                      // (token, head) rows of a pair
+constexpr int kSoftWarps = 4, kKWarp = 4, kVWarp = 8, kMmaWarp = 12, kQWarp = 13;
+constexpr int kThreads = 32 * 15;
+
+constexpr int kQOff = 0, kQBlock = 64 * 128;    // 9 blocks of [64 rows x 64 columns]
+constexpr int kKOff = kQOff + 9 * kQBlock, kKBlock = 32 * 128, kKStage = 9 * kKBlock;
+constexpr int kVOff = kKOff + 2 * kKStage, kVBlock = 64 * 128, kVStage = 4 * kVBlock;
+constexpr int kPOff = kVOff + 2 * kVStage, kPStage = 64 * 128;
+constexpr int kBarOff = kPOff + 2 * kPStage;
+// q full, q empty, o free, done, then pairs: k full, k empty, v full, pv done, s full, s free, p full,
+// and four mask barriers
+constexpr int kBars = 4 + 14 + 4;
+constexpr int kMaxOff = kBarOff + 8 * kBars;    // 128 floats: maxima, sums
+constexpr int kMaskOff = kMaxOff + 4 * 128;     // [4][4] 16-bit masks
+constexpr int kScanOff = kMaskOff + 32;         // 16 x int64
+constexpr int kSchedOff = kScanOff + 128;       // Start
+constexpr int kMiscOff = kSchedOff + 32;        // TMEM address, abort
+constexpr int kSmemBytes = kMiscOff + 16;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+
+constexpr uint32_t kSCol = 256;                 // TMEM columns: o 0..255, s 2 x 32
+constexpr uint32_t kIdescS = idesc_bf16(128, 64);
+constexpr uint32_t kIdescO = idesc_bf16(128, 256) | (1u << 16);  // B is MN-major
+constexpr float kInf = __builtin_huge_valf();
+constexpr float kLag = 8.0f;                    // how far a score may pass the reference (base 2)
+
+constexpr int kMaxPairs = 76;
+constexpr int kMinTiles = 4;                    // tiles of a pair at least
+constexpr int kPartFloats = kRows * (kLatent + 2);  // o, m, l
+
+struct Params {
+    Paged cache;
+    Sequences seq;
+    const uint8_t* rows;
+    const uint16_t* q;
+    long long q_token, q_head;   // strides in elements
+    int H, tt;                   // heads; tokens of a segment at most
+    float scale;                 // times log2(e)
+    const int32_t* inds;         // [T, k] or nullptr
+    int k;
+    uint16_t* out;               // [T, H, 512]
+    float* lse;                  // [T, H] or nullptr
+    float* part;                 // [2 pairs][kPartFloats]
+    int4* meta;                  // [2 pairs] valid, token, tokens, last piece of its segment
+    int pairs;
+};
+
+struct Start {
+    int t, b, tile, pad;
+    long long left;
+};
+
+MOE_DEV void record_timeout(volatile int* abort) {
+    *abort = 1;
+    atomicCAS(&g_attention_status, 0u, kStatusTimeout);
+}
+
+// A segment: tokens t .. t + n - 1 of sequence b, `len` positions (or entries of its selection) in
+// `tiles` tiles (one, all masked, where it sees nothing).
+struct Seg {
+    int t, n, b, len, tiles;
+};
+MOE_DEV Seg segment(const Params& p, int t, int b) {
+    Seg s;
+    s.t = t;
+    s.b = b;
+    s.n = max(1, min(p.tt, seq_end(p.seq, b) - t));
+    s.len = 0;
+    for (int i = 0; i < s.n; ++i) s.len = max(s.len, seq_length(p.seq, t + i));
+    if (p.inds) s.len = min(s.len, p.k);
+    s.tiles = max(1, (s.len + kTile - 1) / kTile);
+    return s;
+}
+
+// The pieces of a pair's run, in order.
+struct Walk {
+    int t, b, tile;
+    long long left;
+    Seg s;
+    int i0, i1;  // tiles of the piece
+    MOE_DEV Walk(const Start& st) : t(st.t), b(st.b), tile(st.tile), left(st.left) {}
+    MOE_DEV bool next(const Params& p) {
+        if (left <= 0) return false;
+        s = segment(p, t, b);
+        i0 = tile;
+        i1 = (int)min((long long)s.tiles, i0 + left);
+        left -= i1 - i0;
+        tile = 0;
+        t += s.n;
+        if (!p.seq.cu) b = t;
+        else if (left > 0) while (b < p.seq.B - 1 && t >= seq_end(p.seq, b)) ++b;
+        return true;
+    }
+    MOE_DEV bool begins() const { return i0 == 0; }
+    MOE_DEV bool ends() const { return i1 == s.tiles; }
+};
+
+// The position that entry e of a segment's list stands for, -1 for none.
+MOE_DEV int position(const Params& p, const Seg& s, int e) {
+    if (e >= s.len) return -1;
+    if (!p.inds) return e;
+    const int j = __ldg(p.inds + (long long)s.t * p.k + e);
+    return j >= 0 && j < seq_length(p.seq, s.t) ? j : -1;
+}
+
+MOE_DEV bool wait_c(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait_cluster(bar, parity, 1000u)) return true;
+    return mbar_wait_cluster(bar, parity, abort);
+}
+// Every lane; false (in every lane) when a wait gave up.
+MOE_DEV bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (__all_sync(0xFFFFFFFFu, wait_c(bar, parity, abort))) return true;
+    if ((threadIdx.x & 31) == 0) record_timeout(abort);
+    return false;
+}
+
+// MN-major operand in the 128-byte swizzle: blocks of 64 columns kVBlock apart, groups of 8 rows
+// (along K) 1024 bytes apart.
+MOE_DEV uint64_t sdesc_mn128(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kVBlock >> 4) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+MOE_DEV float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Barrier of the 128 softmax threads: whether v holds for one of them.
+MOE_DEV bool soft_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\t"
+        "setp.ne.b32 a, %1, 0;\n\t"
+        "bar.red.or.pred b, 1, 128, a;\n\t"
+        "selp.u32 %0, 1, 0, b;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+// 16 bytes of bf16 with infinities and NaN as 0.
+MOE_DEV uint32_t finite2(uint32_t v) {
+    if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
+    if ((v & 0x7F800000u) == 0x7F800000u) v &= 0xFFFFu;
+    return v;
+}
+
+// Tiles of the tokens a .. z - 1 (of those that begin a segment).
+template <class F>
+MOE_DEV void for_segments(const Params& p, int a, int z, F&& f) {
+    if (a >= z) return;
+    int b = seq_of(p.seq, a);
+    for (int t = a; t < z; ++t) {
+        if (!p.seq.cu) b = t;
+        else while (b < p.seq.B - 1 && t >= seq_end(p.seq, b)) ++b;
+        const int first = p.seq.cu ? __ldg(p.seq.cu + b) : t;
+        if ((t - first) % p.tt == 0) f(segment(p, t, b));
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
+    uint64_t *qfull = bars, *qempty = bars + 1, *ofree = bars + 2, *done = bars + 3;
+    uint64_t *kfull = bars + 4, *kempty = bars + 6, *vfull = bars + 8, *pvdone = bars + 10;
+    uint64_t *sfull = bars + 12, *sfree = bars + 14, *pfull = bars + 16, *mfull = bars + 18;
+    float* xch = reinterpret_cast<float*>(smem + kMaxOff);
+    volatile uint16_t* mask = reinterpret_cast<volatile uint16_t*>(smem + kMaskOff);
+    long long* scan = reinterpret_cast<long long*>(smem + kScanOff);
+    Start* sched = reinterpret_cast<Start*>(smem + kSchedOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int crank = (int)cluster_rank(), pair = (int)(blockIdx.x >> 1);
+
+    // ---- set-up ----
+    if (threadIdx.x == 0) {
+        // the barriers that the issuer waits on are the even CTA's, with arrivals from both
+        mbar_init(qfull, 4);
+        mbar_init(qempty, 1);
+        mbar_init(ofree, 2 * kSoftWarps);
+        mbar_init(done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&kfull[i], 8);
+            mbar_init(&kempty[i], 1);
+            mbar_init(&vfull[i], 8);
+            mbar_init(&pvdone[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sfree[i], 2 * kSoftWarps);
+            mbar_init(&pfull[i], 2 * kSoftWarps);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&mfull[i], 4);
+        *abort = 0;
+        sched->left = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc_pair(tmem_slot, 512);
+    // this pair's run of the list of tiles: a prefix sum over the tokens
+    {
+        const int tokens = seq_tokens(p.seq);
+        const int per = (tokens + kThreads - 1) / kThreads;
+        const int a = min(tokens, (int)threadIdx.x * per), z = min(tokens, a + per);
+        long long mine = 0;
+        for_segments(p, a, z, [&](const Seg& s) { mine += s.tiles; });
+        long long incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        long long before = incl - mine, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += scan[w];
+            total += scan[w];
+        }
+        const long long runs = max(1ll, min((long long)p.pairs, total / kMinTiles));
+        const long long lo = pair < runs ? total * pair / runs : 0;
+        const long long hi = pair < runs ? total * (pair + 1) / runs : 0;
+        if (lo < hi && before <= lo && lo < before + mine) {
+            long long at = before;
+            for_segments(p, a, z, [&](const Seg& s) {
+                if (at <= lo && lo < at + s.tiles) {
+                    sched->t = s.t;
+                    sched->b = s.b;
+                    sched->tile = (int)(lo - at);
+                    sched->left = hi - lo;
+                }
+                at += s.tiles;
+            });
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    cluster_sync();  // the peer's barriers are initialised and its TMEM allocated
+    Start st = *sched;
+    if (ld_shared_cluster_u32(mapa_shared(tmem_slot, (uint32_t)(crank ^ 1))) != tmem) {
+        st.left = 0;  // the pair's UMMAs address the same columns in both CTAs
+        if (threadIdx.x == 0) atomicCAS(&g_attention_status, 0u, kStatusPairTmem);
+    }
+    Walk w(st);
+    uint32_t g = 0;  // tiles so far
+    bool ok = true;
+
+    if (warp >= kKWarp && warp < kVWarp) {
+        // ====================== rows as keys: 32 of the 64, all columns ======================
+        const int r0 = 8 * (warp - kKWarp);  // this warp's rows of the 32
+        const int sub = lane >> 3, ch = lane & 7;
+        bool pending = false;
+        const auto post = [&](uint32_t n) {
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(&kfull[n & 1u], 0);
+        };
+        while (ok && w.next(p)) {
+            for (int i = w.i0; i < w.i1; ++i, ++g) {
+                const int pos = lane < 8 ? position(p, w.s, i * kTile + crank * 32 + r0 + lane) : -1;
+                const long long row = pos >= 0 ? paged_row(p.cache, w.s.b, pos) : -1;
+                if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&kempty[g & 1u], ((g >> 1) & 1u) ^ 1u))) {
+                    if (pending) {  // announced before the wait
+                        copy_wait<0>();
+                        post(g - 1);
+                        pending = false;
+                    }
+                    if (!wait_all(&kempty[g & 1u], ((g >> 1) & 1u) ^ 1u, abort)) { ok = false; break; }
+                }
+                const uint32_t st0 = smem_u32(smem + kKOff + (g & 1u) * kKStage);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int rr = 4 * h + sub;
+                    const long long at = __shfl_sync(0xFFFFFFFFu, row, rr);
+                    const uint8_t* src = p.rows + (at < 0 ? 0 : at) * kRowBytes + ch * 16;
+                    const uint32_t dst = st0 + (r0 + rr) * 128 + ((ch ^ rr) << 4);
+#pragma unroll
+                    for (int j = 0; j < 9; ++j)
+                        copy16(dst + j * kKBlock, src + j * 128, at < 0 ? 0u : 16u);
+                }
+                copy_commit();
+                if (pending) {
+                    copy_wait<1>();
+                    post(g - 1);
+                }
+                pending = true;
+            }
+        }
+        copy_wait<0>();
+        if (pending && ok) post(g - 1);
+    } else if (warp >= kVWarp && warp < kMmaWarp) {
+        // ================ rows as values: all 64, half of the 512 columns ================
+        const int r0 = 16 * (warp - kVWarp);
+        const int blk = lane >> 3, ch = lane & 7;
+        // block 0, 1: this CTA's 128 columns of the first 256; 2, 3: of the last 256
+        const int col = (blk >> 1) * 256 + crank * 128 + (blk & 1) * 64;
+        bool pending = false;
+        const auto post = [&](uint32_t n) {
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(&vfull[n & 1u], 0);
+        };
+        while (ok && w.next(p)) {
+            // a row that not every token of the segment sees meets zeros of p; an infinity or a
+            // NaN in it must not
+            int fewest = w.s.len;
+            if (!p.inds)
+                for (int i = 0; i < w.s.n; ++i) fewest = min(fewest, seq_length(p.seq, w.s.t + i));
+            for (int i = w.i0; i < w.i1; ++i, ++g) {
+                const int e = i * kTile + r0 + lane;
+                const int pos = lane < 16 ? position(p, w.s, e) : -1;
+                const long long row = pos >= 0 ? paged_row(p.cache, w.s.b, pos) : -1;
+                const uint32_t there = __ballot_sync(0xFFFFFFFFu, row >= 0);
+                if (lane == 0) {
+                    // (read four tiles ago: the columns of the tile before the last are free)
+                    mask[(g & 3u) * 4 + (warp - kVWarp)] = (uint16_t)there;
+                    mbar_arrive(&mfull[g & 3u]);
+                }
+                if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&pvdone[g & 1u], ((g >> 1) & 1u) ^ 1u))) {
+                    if (pending) {
+                        copy_wait<0>();
+                        post(g - 1);
+                        pending = false;
+                    }
+                    if (!wait_all(&pvdone[g & 1u], ((g >> 1) & 1u) ^ 1u, abort)) { ok = false; break; }
+                }
+                const uint32_t st0 = smem_u32(smem + kVOff + (g & 1u) * kVStage) + blk * kVBlock;
+                const bool careful = i * kTile + r0 + 15 >= fewest;
+#pragma unroll 4
+                for (int rr = 0; rr < 16; ++rr) {
+                    const long long at = __shfl_sync(0xFFFFFFFFu, row, rr);
+                    const uint8_t* src = p.rows + (at < 0 ? 0 : at) * kRowBytes + col * 2 + ch * 16;
+                    const uint32_t dst = st0 + (r0 + rr) * 128 + ((ch ^ (rr & 7)) << 4);
+                    if (careful && at >= 0 && i * kTile + r0 + rr >= fewest) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
+                                     "r"(finite2(v.x)), "r"(finite2(v.y)), "r"(finite2(v.z)),
+                                     "r"(finite2(v.w))
+                                     : "memory");
+                    } else {
+                        copy16(dst, src, at < 0 ? 0u : 16u);
+                    }
+                }
+                copy_commit();
+                if (pending) {
+                    copy_wait<1>();
+                    post(g - 1);
+                }
+                pending = true;
+            }
+        }
+        copy_wait<0>();
+        if (pending && ok) post(g - 1);
+    } else if (warp >= kQWarp) {
+        // ================================== queries ==================================
+        uint32_t n = 0;
+        for (; ok && w.next(p); ++n) {
+            if (!wait_all(qempty, (n & 1u) ^ 1u, abort)) { ok = false; break; }
+            const uint32_t base = smem_u32(smem + kQOff);
+            const int rows = w.s.n * p.H;
+            const int r0 = 32 * (warp - kQWarp);
+            const int sub = lane >> 3, ch = lane & 7;
+#pragma unroll 2
+            for (int r = r0; r < r0 + 32; r += 4) {
+                const int rr = r + sub, gr = crank * 64 + rr;
+                const bool live = gr < rows;
+                const uint16_t* src = p.q;
+                if (live) src += (w.s.t + gr / p.H) * p.q_token + (gr % p.H) * p.q_head;
+                const uint32_t dst = base + rr * 128 + ((ch ^ (rr & 7)) << 4);
+#pragma unroll
+                for (int j = 0; j < 9; ++j)
+                    copy16(dst + j * kQBlock, src + j * 64 + ch * 8, live ? 16u : 0u);
+            }
+            copy_commit();
+            copy_wait<0>();
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(qfull, 0);
+        }
+    } else if (warp == kMmaWarp) {
+        // ================================ UMMA issuer ================================
+        if (crank == 0 && lane == 0) {
+            uint32_t n = 0;
+            const auto scores = [&]() -> bool {  // tile g
+                const uint32_t i = g & 1u, ph = (g >> 1) & 1u;
+                if (!wait_c(&kfull[i], ph, abort) || !wait_c(&sfree[i], ph ^ 1u, abort)) return false;
+                tc_fence_after();
+                const uint64_t dq = sdesc_k128(smem_u32(smem + kQOff));
+                const uint64_t dk = sdesc_k128(smem_u32(smem + kKOff + i * kKStage));
+#pragma unroll
+                for (int j = 0; j < 9; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16_pair(tmem + kSCol + 32 * i, dq + (uint64_t)(j * (kQBlock / 16) + 2 * k),
+                                       dk + (uint64_t)(j * (kKBlock / 16) + 2 * k), kIdescS, j + k > 0);
+                umma_commit_pair(&kempty[i], 3);
+                umma_commit_pair(&sfull[i], 3);
+                return true;
+            };
+            const auto values = [&](uint32_t c, bool first) -> bool {  // tile c
+                const uint32_t i = c & 1u, ph = (c >> 1) & 1u;
+                if (!wait_c(&vfull[i], ph, abort) || !wait_c(&pfull[i], ph, abort)) return false;
+                if (first && !wait_c(ofree, (n & 1u) ^ 1u, abort)) return false;
+                tc_fence_after();
+                const uint64_t dp = sdesc_k128(smem_u32(smem + kPOff + i * kPStage));
+                const uint64_t dv = sdesc_mn128(smem_u32(smem + kVOff + i * kVStage));
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)  // 16 positions = 2048 bytes further
+                        umma_bf16_pair(tmem + 128 * half, dp + (uint64_t)(2 * k),
+                                       dv + (uint64_t)(half * 2 * (kVBlock / 16) + k * (2048 / 16)),
+                                       kIdescO, !first || k > 0);
+                umma_commit_pair(&pvdone[i], 3);
+                return true;
+            };
+            for (; ok && w.next(p); ++n) {
+                if (!wait_c(qfull, n & 1u, abort)) { ok = false; break; }
+                for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
+                    ok = scores();
+                    if (ok && i == w.i1 - 1) umma_commit_pair(qempty, 3);
+                    if (ok && i > w.i0) ok = values(g - 1, i - 1 == w.i0);
+                }
+                if (ok) ok = values(g - 1, w.i1 - 1 == w.i0);
+            }
+            if (!ok) record_timeout(abort);
+            umma_commit_pair(done, 1);  // no UMMA is left when the pair frees its TMEM
+            mbar_wait(done, 0u, nullptr, 100000000ull);
+        }
+    } else {
+        // ======================= softmax, rescaling and epilogue =======================
+        const int L = (int)threadIdx.x, row = L & 63, half = L >> 6;
+        const int gr = crank * 64 + row;
+        const uint32_t lane0 = tmem + ((uint32_t)(warp * 32) << 16);
+        if (crank == 0 && L == 0) p.meta[2 * pair] = p.meta[2 * pair + 1] = make_int4(0, 0, 0, 0);
+        uint32_t n = 0;
+        for (; ok && w.next(p); ++n) {
+            const bool live = gr < w.s.n * p.H;
+            const int tok = w.s.t + gr / p.H, head = gr % p.H;
+            const int see = !live ? 0 : p.inds ? w.s.len : seq_length(p.seq, tok);
+            float m = -kInf, l = 0.0f;
+            for (int i = w.i0; i < w.i1; ++i, ++g) {
+                const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
+                // (a warp whose wait gave up keeps to the barriers of the 128 threads until all know)
+                ok = ok && wait_all(&mfull[g & 3u], (g >> 2) & 1u, abort) && wait_all(&sfull[b], ph, abort);
+                tc_fence_after();
+                uint32_t v[32];
+                tmem_ld32(lane0 + kSCol + 32 * b, v);
+                const int left = see - i * kTile - half * 32;
+                uint32_t bits = (uint32_t)mask[(g & 3u) * 4 + 2 * half] |
+                                ((uint32_t)mask[(g & 3u) * 4 + 2 * half + 1] << 16);
+                bits &= left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive_cluster(&sfree[b], 0);
+                float x[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]) * p.scale;
+                if (!__all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!((bits >> c) & 1u)) x[c] = -kInf;
+                }
+                float mx = x[0];
+#pragma unroll
+                for (int c = 1; c < 32; ++c) mx = fmaxf(mx, x[c]);
+                if (soft_any(!ok || mx > m + kLag)) {
+                    xch[L] = mx;
+                    if (soft_any(!ok)) { ok = false; break; }
+                    mx = fmaxf(mx, xch[L ^ 64]);
+                    const float to = mx > m + kLag ? mx : m;
+                    const float f = to == m ? 1.0f : exp2_of(m - to);
+                    m = to;
+                    l *= f;
+                    if (i > w.i0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
+                        // o of the tiles so far; the next product waits for this tile's p
+                        ok = wait_all(&pvdone[b ^ 1u], ((g - 1) >> 1) & 1u, abort);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (uint32_t c = 0; c < 256; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(lane0 + c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st16(lane0 + c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float ref = m == -kInf ? 0.0f : m;
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float p0 = exp2_of(x[c] - ref), p1 = exp2_of(x[c + 1] - ref);
+                    l += p0 + p1;
+                    pk[c / 2] = pack_bf16x2(p0, p1);
+                }
+                ok = ok && wait_all(&pvdone[b], ph ^ 1u, abort);  // p of two tiles ago has been read
+                const uint32_t dst = smem_u32(smem + kPOff + b * kPStage) + row * 128;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     dst + (((half * 4 + c) ^ (row & 7)) << 4)),
+                                 "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
+                                 : "memory");
+                fence_async_shared();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive_cluster(&pfull[b], 0);
+            }
+            ok = ok && wait_all(&pvdone[(g - 1) & 1u], ((g - 1) >> 1) & 1u, abort);
+            xch[L] = l;
+            if (soft_any(!ok)) { ok = false; break; }
+            l += xch[L ^ 64];
+            tc_fence_after();
+            const bool whole = w.begins() && w.ends();
+            const int slot = 2 * pair + (w.begins() ? 1 : 0);
+            float* part = p.part + (long long)slot * kPartFloats;
+            const float f = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            if (live && half == 0) {
+                if (whole) {
+                    if (p.lse)
+                        p.lse[(long long)tok * p.H + head] =
+                            l == 0.0f ? -kInf : (m + log2f(l)) * 0.693147180559945f;
+                } else {
+                    part[kRows * kLatent + gr] = m;
+                    part[kRows * kLatent + kRows + gr] = l;
+                }
+            }
+            if (crank == 0 && L == 0 && !whole)
+                p.meta[slot] = make_int4(1, w.s.t, w.s.n, w.ends() ? 1 : 0);
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(lane0 + (uint32_t)c, o);
+                tmem_ld_wait();
+                const int col = (c >> 7) * 256 + half * 128 + (c & 127);
+                if (live && whole) {
+                    uint32_t r[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        r[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
+                    uint4* d = reinterpret_cast<uint4*>(p.out + ((long long)tok * p.H + head) * kLatent + col);
+                    d[0] = make_uint4(r[0], r[1], r[2], r[3]);
+                    d[1] = make_uint4(r[4], r[5], r[6], r[7]);
+                } else if (live) {
+                    uint4* d = reinterpret_cast<uint4*>(part + gr * kLatent + col);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        d[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(ofree, 0);
+        }
+    }
+
+    pdl_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    // neither CTA leaves while the other's UMMAs or arrivals may still touch its memory
+    cluster_sync();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// Joins the pieces of the blockIdx.y-th segment that was cut apart: its first piece is the second
+// slot of some pair, the others the first slots of the pairs behind it.  A warp per row.
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p) {
+    __shared__ float weight[kJoinWarps][kMaxPairs + 1];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int want = (int)blockIdx.y, owner = -1;
+    for (int q = 0; q < p.pairs && owner < 0; q += 32) {
+        const bool cut = q + lane < p.pairs && p.meta[2 * (q + lane) + 1].x != 0;
+        uint32_t any = __ballot_sync(0xFFFFFFFFu, cut);
+        const int cnt = __popc(any);
+        if (want >= cnt) { want -= cnt; continue; }
+        while (want-- > 0) any &= any - 1;
+        owner = q + __ffs(any) - 1;
+    }
+    if (owner < 0) return;
+    const int4 first = p.meta[2 * owner + 1];
+    int pieces = 1;
+    while (owner + pieces < p.pairs) {
+        const int4 m = p.meta[2 * (owner + pieces)];
+        if (!m.x) return;  // (a pair that gave up)
+        ++pieces;
+        if (m.w) break;
+    }
+    const int row = (int)blockIdx.x * kJoinWarps + w;
+    if (row >= first.z * p.H) return;
+    const auto at = [&](int i) {
+        return p.part + (long long)(i == 0 ? 2 * owner + 1 : 2 * (owner + i)) * kPartFloats;
+    };
+    float m = -kInf;
+    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, at(i)[kRows * kLatent + row]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float l = 0.0f;
+    for (int i = lane; i < pieces; i += 32) {
+        const float mi = at(i)[kRows * kLatent + row];
+        const float f = mi == -kInf ? 0.0f : mi == m ? 1.0f : exp2_of(mi - m);
+        weight[w][i] = f;
+        const float li = at(i)[kRows * kLatent + kRows + row];
+        l += f * li;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    __syncwarp();
+    float4 acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+        const float f = weight[w][i];
+        const float4* o = reinterpret_cast<const float4*>(at(i) + row * kLatent) + lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 v = o[32 * c];
+            acc[c].x = fmaf(f, v.x, acc[c].x);
+            acc[c].y = fmaf(f, v.y, acc[c].y);
+            acc[c].z = fmaf(f, v.z, acc[c].z);
+            acc[c].w = fmaf(f, v.w, acc[c].w);
+        }
+    }
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    const long long o = (long long)(first.y + row / p.H) * p.H + row % p.H;
+    uint2* d = reinterpret_cast<uint2*>(p.out + o * kLatent) + lane;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        d[32 * c] = make_uint2(pack_bf16x2(acc[c].x * f, acc[c].y * f), pack_bf16x2(acc[c].z * f, acc[c].w * f));
+    if (p.lse && lane == 0) p.lse[o] = l == 0.0f ? -kInf : (m + log2f(l)) * 0.693147180559945f;
+}
+
+}  // namespace
+
+int attention_pairs(long long T, long long entries) {
+    const long long tiles = T * ((entries + kTile - 1) / kTile > 0 ? (entries + kTile - 1) / kTile : 1);
+    const long long runs = tiles / kMinTiles;
+    return (int)(runs < 1 ? 1 : runs > kMaxPairs ? kMaxPairs : runs);
+}
+size_t attention_ws_bytes(int pairs) {
+    return (size_t)pairs * 2 * (kPartFloats * sizeof(float) + sizeof(int4));
+}
+
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
+    static DeviceOnce attr_once, occ_once;
+    static int resident[DeviceOnce::kMaxDevices] = {};
+    cudaError_t e = attr_once.run([] {
+        return cudaFuncSetAttribute(attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSmemBytes);
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= DeviceOnce::kMaxDevices) return cudaErrorInvalidDevice;
+    // as many pairs as the device can hold at once (an SM left over in a GPC takes none)
+    e = occ_once.run([&] {
+        cfg.gridDim = dim3(2 * kMaxPairs);
+        int n = 0;
+        const cudaError_t err = cudaOccupancyMaxActiveClusters(&n, attention_kernel, &cfg);
+        if (err == cudaSuccess) resident[dev] = n > 0 ? n : 1;
+        return err;
+    });
+    if (e != cudaSuccess) return e;
+    const long long room = (long long)a.width * a.page;
+    Params p = {};
+    p.cache = {a.table, a.width, a.page, a.pages};
+    p.seq = {a.cu, a.lengths, a.B, (int)a.T, (int)room};
+    p.rows = static_cast<const uint8_t*>(a.rows);
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.q_token = a.q_token;
+    p.q_head = a.q_head;
+    p.H = a.H;
+    p.tt = a.inds || !a.cu ? 1 : kRows / a.H;
+    p.scale = a.scale * 1.44269504088896f;
+    p.inds = a.inds;
+    p.k = a.k;
+    p.out = static_cast<uint16_t*>(a.out);
+    p.lse = a.lse;
+    p.pairs = attention_pairs(a.T, a.inds ? a.k : room);
+    if (resident[dev] < p.pairs) p.pairs = resident[dev];
+    p.part = static_cast<float*>(a.ws);
+    p.meta = reinterpret_cast<int4*>(p.part + (size_t)p.pairs * 2 * kPartFloats);
+    cfg.gridDim = dim3((unsigned)(2 * p.pairs));
+    e = cudaLaunchKernelEx(&cfg, attention_kernel, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess || p.pairs == 1) return e;
+    const long long cut = a.T < p.pairs - 1 ? a.T : p.pairs - 1;  // segments that may be cut apart
+    return launch_kernel(join_kernel, dim3((unsigned)((kRows + kJoinWarps - 1) / kJoinWarps), (unsigned)cut),
+                         dim3(32 * kJoinWarps), 0, s, p);
+}
+
+cudaError_t read_attention_status(unsigned int* out, int clear, cudaStream_t s) {
+    cudaError_t err = cudaMemcpyFromSymbolAsync(out, g_attention_status, sizeof(unsigned int), 0,
+                                                cudaMemcpyDeviceToHost, s);
+    if (err != cudaSuccess) return err;
+    err = cudaStreamSynchronize(s);
+    if (err != cudaSuccess || !clear) return err;
+    const unsigned int zero = 0;
+    err = cudaMemcpyToSymbolAsync(g_attention_status, &zero, sizeof(unsigned int), 0,
+                                  cudaMemcpyHostToDevice, s);
+    if (err != cudaSuccess) return err;
+    return cudaStreamSynchronize(s);
+}
+
+}  // namespace moe

@@ -226,6 +226,29 @@ struct ScoresArgs {
 cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s);
 cudaError_t read_scores_status(unsigned int* out, int clear, cudaStream_t s);
 
+struct AttentionArgs {
+    const void* q;               // bf16 [T, H, 576], strides q_token and q_head (elements)
+    long long T, q_token, q_head;
+    int H;
+    const void* rows;            // bf16 [pages * page, 576]
+    long long pages;
+    int page;
+    const int32_t* table;        // [B, width]
+    int B, width;
+    const int32_t* cu;           // [B + 1] or nullptr
+    const int32_t* lengths;      // [T]
+    float scale;
+    const int32_t* inds;         // [T, k] or nullptr
+    int k;
+    void* out;                   // bf16 [T, H, 512]
+    float* lse;                  // [T, H] or nullptr
+    void* ws;                    // attention_ws_bytes(attention_pairs(T, k or width * page))
+};
+int attention_pairs(long long T, long long entries);
+size_t attention_ws_bytes(int pairs);
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
+cudaError_t read_attention_status(unsigned int* out, int clear, cudaStream_t s);
+
 // Per-device status word of the kernels with bounded waits.
 cudaError_t read_device_status(unsigned int* out, int clear, cudaStream_t s);
 // The block-scaled products' own.

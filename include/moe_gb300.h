@@ -310,6 +310,33 @@ int moe_indexer_scores(const void* q, const float* weights, int64_t T, int32_t H
                        int64_t ld, moe_stream_t stream);
 
 /*
+ * moe_latent_attention -- attention whose keys and values are one cached row per position for all
+ * heads (absorbed form; SwiftLM issue #139, "What needs building" item 3: decode gathers the
+ * selected positions):
+ *     out[t, h] = sum_j p_j c_j[0:512],  p = softmax over j of scale * (q[t, h] . c_j)
+ *   c_j bf16 [576]: row of position j, 512 latent columns and 64 rotated ones.  j runs over the
+ *   positions j < lengths[t], or, with inds int32 [T, k], over the positions named by the first
+ *   min(k, lengths[t]) entries of inds[t] (as moe_indexer_topk writes them: distinct, then -1); an
+ *   entry outside [0, lengths[t]) is skipped, one that is there twice counts twice, entries further
+ *   on are not read.  Positions whose page is not there do not count.
+ *   q bf16 [T, H, 576], token and head strides q_token and q_head (in elements, multiples of 8);
+ *   1 <= H <= 128.  Scores, softmax and sums in fp32; p is rounded to bf16 for its product.
+ *   Out: out bf16 [T, H, 512]; lse fp32 [T, H] or NULL: log of the sum of exp of the scaled scores.
+ *   A token without any position gives out 0 and lse -inf.
+ *   ws: at least moe_latent_attention_workspace_bytes(T, k or width * page) bytes, 256-byte
+ *   aligned, in use until the call's work is done (calls that overlap need one each).
+ * Errors: MOE_ERR_INVALID for NULL pointers, H outside [1, 128], k < 1 with inds, strides that are no
+ * multiple of 8, the cache's rules as at moe_indexer_scores, q, rows or out not 16-byte aligned, a
+ * workspace that is too small.  T == 0 is a no-op.
+ */
+int moe_latent_attention(const void* q, int64_t T, int32_t H, int64_t q_token, int64_t q_head,
+                         const moe_paged_cache_t* cache, const int32_t* cu_tokens,
+                         const int32_t* lengths, float scale, const int32_t* inds, int32_t k,
+                         void* out, float* lse, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+size_t moe_latent_attention_workspace_bytes(int64_t T, int64_t positions);
+
+/*
  * moe_permute -- token-to-expert dispatch ([epic] first paragraph: the grouping that
  * gather_mm / gather_qmm consume).  inds [T, K] int32 expert ids of the P = T*K pairs
  * p = t*K + k.
