@@ -228,6 +228,8 @@ int check_paged(const moe_paged_cache_t* c, int64_t T, const int32_t* cu, const 
     MOE_CHECK(c->page >= 1, "page = %d < 1", c->page);
     MOE_CHECK(c->pages >= 0 && c->pages < ((int64_t)1 << 31), "pages = %lld outside [0, 2^31)",
               (long long)c->pages);
+    MOE_CHECK(c->pages * c->page < ((int64_t)1 << 31), "pages x page = %lld x %d: 2^31 rows or more",
+              (long long)c->pages, c->page);
     MOE_CHECK(c->width >= 0 && (int64_t)c->width * c->page <= kMaxPositions,
               "width x page = %d x %d: more than 2^31 - 512 positions", c->width, c->page);
     MOE_CHECK(c->sequences >= 0, "sequences = %d < 0", c->sequences);
@@ -1207,9 +1209,13 @@ int moe_latent_attention(const void* q, int64_t T, int32_t H, int64_t q_token, i
     a.out = out;
     a.lse = lse;
     a.ws = ws;
-    PdlScope pdl;
-    pdl.on();  // the join's launch overlaps the attention kernel's tail
+    MOE_CUDA(moe::attention_plan(a), "attention plan");
     MOE_LAUNCH(moe::launch_attention(a, (cudaStream_t)stream), "attention kernel");
+    if (a.pairs > 1) {
+        PdlScope pdl;
+        pdl.on();  // the join's launch overlaps the attention kernel's tail
+        MOE_LAUNCH(moe::launch_attention_join(a, (cudaStream_t)stream), "attention join");
+    }
     return MOE_OK;
 }
 

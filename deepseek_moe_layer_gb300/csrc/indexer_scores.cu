@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                     const int pos = c * kKeys + 32 * w + lane;
                     const long long mine = pos < p.seq.most ? paged_row(p.keys, r.b, pos) : -1;
                     if (!__all_sync(0xFFFFFFFFu,
-                                    mbar_try_wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u))) {
+                                    mbar_test(&empty[s], ((it / C::kStages) & 1u) ^ 1u))) {
                         // no slot yet: what has been asked for is announced before the wait
                         copy_wait<0>();
                         while (posted < it) post();
@@ -238,34 +238,31 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         }
     } else if (warp == kMmaWarp) {
         // ================================ UMMA issuer ================================
-        if (lane == 0) {
-            uint32_t it = 0, acc = 0, n = 0;
-            bool ok = true;
-            for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++n) {
-                Unit un(p, u, tokens);
-                if (!mbar_wait(qfull, n & 1u, abort)) { record_timeout(abort); break; }
-                Part r;
-                while (ok && un.part(p, r)) {
-                    for (int c = r.c0; c < r.c1 && ok; ++c, ++it) {
-                        const uint32_t s = it % C::kStages;
-                        if (!mbar_wait(&full[s], (it / C::kStages) & 1u, abort)) {
-                            record_timeout(abort);
-                            ok = false;
-                            break;
-                        }
-                        const uint64_t da = sdesc_k128(smem_u32(smem + C::kStageOff + s * C::kStageBytes));
-                        for (int t = r.t0; t < r.t1; t += gtok, ++acc) {
-                            const uint32_t ab = acc & 1u;
-                            if (!mbar_wait(&aempty[ab], ((acc >> 1) & 1u) ^ 1u, abort)) {
-                                record_timeout(abort);
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const int cols = min(gtok, r.t1 - t) * p.Hp;
-                            const uint32_t idesc = C::kIdesc0 | ((uint32_t)(cols >> 3) << 17);
-                            const uint64_t db =
-                                sdesc_k128(smem_u32(smem) + (uint32_t)((t - un.u0) * p.Hp * 128));
+        uint32_t it = 0, acc = 0, n = 0;
+        bool ok = true;
+        const auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+            if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort))) return true;
+            if (lane == 0) record_timeout(abort);
+            return ok = false;
+        };
+        const uint64_t dq = sdesc_k128(smem_u32(smem)), dk = sdesc_k128(smem_u32(smem + C::kStageOff));
+        for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++n) {
+            Unit un(p, u, tokens);
+            if (!wait(qfull, n & 1u)) break;
+            Part r;
+            while (ok && un.part(p, r)) {
+                for (int c = r.c0; c < r.c1 && ok; ++c, ++it) {
+                    const uint32_t s = it % C::kStages;
+                    if (!wait(&full[s], (it / C::kStages) & 1u)) break;
+                    const uint64_t da = dk + (uint64_t)(s * (C::kStageBytes / 16));
+                    for (int t = r.t0; t < r.t1; t += gtok, ++acc) {
+                        const uint32_t ab = acc & 1u;
+                        if (!wait(&aempty[ab], ((acc >> 1) & 1u) ^ 1u)) break;
+                        tc_fence_after();
+                        const int cols = min(gtok, r.t1 - t) * p.Hp;
+                        const uint32_t idesc = C::kIdesc0 | ((uint32_t)(cols >> 3) << 17);
+                        const uint64_t db = dq + (uint64_t)((t - un.u0) * p.Hp * 8);
+                        if (elect_lane()) {
 #pragma unroll
                             for (int blk = 0; blk < C::kBlocks; ++blk)
 #pragma unroll
@@ -277,14 +274,18 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                                 }
                             umma_commit(&afull[ab]);
                         }
-                        if (ok) umma_commit(&empty[s]);
+                        __syncwarp();
                     }
+                    if (ok && elect_lane()) umma_commit(&empty[s]);
+                    __syncwarp();
                 }
-                if (ok) umma_commit(qempty);
             }
-            umma_commit(done);  // no UMMA is left when the CTA frees its TMEM
-            mbar_wait(done, 0u, nullptr, 100000000ull);
+            if (ok && elect_lane()) umma_commit(qempty);
+            __syncwarp();
         }
+        if (elect_lane()) umma_commit(done);  // no UMMA is left when the CTA frees its TMEM
+        __syncwarp();
+        mbar_wait(done, 0u, nullptr, 100000000ull);
     } else {
         // ================================= epilogue =================================
         const int quarter = warp & 3, set = warp >> 2;

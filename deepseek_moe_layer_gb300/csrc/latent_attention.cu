@@ -23,10 +23,11 @@
 // lengths fill the device; a segment cut apart leaves partial sums (m, l, o in fp32) that a second
 // kernel joins in the order of the pairs: equal calls give equal bits.
 //
-// Warp roles (480 threads): warps 0..3 softmax, rescaling and epilogue (a thread is a row and half of
+// Warp roles (512 threads): warps 0..3 softmax, rescaling and epilogue (a thread is a row and half of
 // its positions or columns), 4..7 copies of the K-major rows, 8..11 of the MN-major columns (16-byte
 // asynchronous copies, so pages of any size and selected rows are alike; absent rows are zeros),
-// 12 UMMA issuer (of the pair's even CTA), 13 and 14 queries.  Every wait is bounded.
+// 12 UMMA issuer (of the pair's even CTA), 13 finds the rows of the tiles ahead, 14 and 15 queries.
+// Every wait is bounded.
 #include <mutex>
 
 #include "launch.h"
@@ -40,35 +41,40 @@ namespace {
 
 constexpr int kWidth = 576, kLatent = 512;
 constexpr int kRowBytes = 2 * kWidth;
-constexpr int kTile = 64;                       // positions per tile
+constexpr int kTile = 128;                      // positions per tile
 constexpr int kRows = 128;                      // (token, head) rows of a pair
-constexpr int kSoftWarps = 4, kKWarp = 4, kVWarp = 8, kMmaWarp = 12, kQWarp = 13;
-constexpr int kThreads = 32 * 15;
+constexpr int kSoftWarps = 4, kKWarp = 4, kVWarp = 8, kMmaWarp = 12, kFindWarp = 13, kQWarp = 14;
+constexpr int kCopyWarps = 4;                   // of the K-major rows, and of the MN-major columns
+constexpr int kThreads = 32 * 16;
+constexpr int kKBlocks = 9;                     // 64 columns of this CTA's 64 positions
+constexpr int kVChunks = 8;                     // 16 positions, this CTA's 256 columns
 
 constexpr int kQOff = 0, kQBlock = 64 * 128;    // 9 blocks of [64 rows x 64 columns]
-constexpr int kKOff = kQOff + 9 * kQBlock, kKBlock = 32 * 128, kKStage = 9 * kKBlock;
-constexpr int kVOff = kKOff + 2 * kKStage, kVBlock = 64 * 128, kVStage = 4 * kVBlock;
-constexpr int kPOff = kVOff + 2 * kVStage, kPStage = 64 * 128;
-constexpr int kBarOff = kPOff + 2 * kPStage;
-// q full, q empty, o free, done, then pairs: k full, k empty, v full, pv done, s full, s free, p full,
-// and four mask barriers
-constexpr int kBars = 4 + 14 + 4;
-constexpr int kMaxOff = kBarOff + 8 * kBars;    // 128 floats: maxima, sums
-constexpr int kMaskOff = kMaxOff + 4 * 128;     // [4][4] 16-bit masks
-constexpr int kScanOff = kMaskOff + 32;         // 16 x int64
+constexpr int kKOff = kQOff + 9 * kQBlock, kKBlock = 64 * 128;
+constexpr int kVOff = kKOff + kKBlocks * kKBlock, kVBlock = kTile * 128;  // 4 of [128 x 64 columns]
+constexpr int kPOff = kVOff + 4 * kVBlock, kPBlock = 64 * 128;  // 2 of [64 rows x 64 positions]
+constexpr int kBarOff = kPOff + 2 * kPBlock;
+// q full, q empty, o free, done, p full, pv done; s full, s free (2 each); k full, k empty (9 each);
+// v full, v empty (8 each); rows full, rows empty (2 each); masks (4)
+constexpr int kBars = 6 + 4 + 2 * kKBlocks + 2 * kVChunks + 4 + 4;
+constexpr int kXchOff = kBarOff + 8 * kBars;    // 128 floats: maxima, sums
+constexpr int kRowOff = kXchOff + 4 * 128;      // [2][128] rows of the cache
+constexpr int kMaskOff = kRowOff + 2 * 4 * kTile;  // [4][4] words
+constexpr int kScanOff = kMaskOff + 64;         // 16 x int64
 constexpr int kSchedOff = kScanOff + 128;       // Start
 constexpr int kMiscOff = kSchedOff + 32;        // TMEM address, abort
 constexpr int kSmemBytes = kMiscOff + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+static_assert(kVChunks == 2 * kCopyWarps, "two chunks of a tile per copying warp");
 
-constexpr uint32_t kSCol = 256;                 // TMEM columns: o 0..255, s 2 x 32
-constexpr uint32_t kIdescS = idesc_bf16(128, 64);
+constexpr uint32_t kSCol = 256;                 // TMEM columns: o 0..255, s 2 x 64
+constexpr uint32_t kIdescS = idesc_bf16(128, 128);
 constexpr uint32_t kIdescO = idesc_bf16(128, 256) | (1u << 16);  // B is MN-major
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLag = 8.0f;                    // how far a score may pass the reference (base 2)
 
 constexpr int kMaxPairs = 76;
-constexpr int kMinTiles = 4;                    // tiles of a pair at least
+constexpr int kMinTiles = 2;                    // tiles of a pair at least
 constexpr int kPartFloats = kRows * (kLatent + 2);  // o, m, l
 
 struct Params {
@@ -146,13 +152,16 @@ MOE_DEV int position(const Params& p, const Seg& s, int e) {
     return j >= 0 && j < seq_length(p.seq, s.t) ? j : -1;
 }
 
-MOE_DEV bool wait_c(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (mbar_try_wait_cluster(bar, parity, 1000u)) return true;
-    return mbar_wait_cluster(bar, parity, abort);
+// What the barriers hand over between the CTAs of a pair are operands that their writers have
+// fenced for the asynchronous proxy and TMEM under the tcgen05 fences; no thread reads what
+// another CTA's thread wrote with ordinary stores.  So arrivals and waits have the default scope
+// (cluster scope on both, measured at 2048 tokens x 2048 selected: 2680 us against 2013).
+MOE_DEV void arrive_even(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
 }
 // Every lane; false (in every lane) when a wait gave up.
 MOE_DEV bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (__all_sync(0xFFFFFFFFu, wait_c(bar, parity, abort))) return true;
+    if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort))) return true;
     if ((threadIdx.x & 31) == 0) record_timeout(abort);
     return false;
 }
@@ -184,7 +193,10 @@ MOE_DEV bool soft_any(bool v) {
     return r != 0;
 }
 
-// 16 bytes of bf16 with infinities and NaN as 0.
+// The lowest n bits.
+MOE_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Two bf16 numbers with infinities and NaN as 0.
 MOE_DEV uint32_t finite2(uint32_t v) {
     if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
     if ((v & 0x7F800000u) == 0x7F800000u) v &= 0xFFFFu;
@@ -208,10 +220,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
     uint64_t *qfull = bars, *qempty = bars + 1, *ofree = bars + 2, *done = bars + 3;
-    uint64_t *kfull = bars + 4, *kempty = bars + 6, *vfull = bars + 8, *pvdone = bars + 10;
-    uint64_t *sfull = bars + 12, *sfree = bars + 14, *pfull = bars + 16, *mfull = bars + 18;
-    float* xch = reinterpret_cast<float*>(smem + kMaxOff);
-    volatile uint16_t* mask = reinterpret_cast<volatile uint16_t*>(smem + kMaskOff);
+    uint64_t *pfull = bars + 4, *pvdone = bars + 5, *sfull = bars + 6, *sfree = bars + 8;
+    uint64_t *kfull = bars + 10, *kempty = kfull + kKBlocks;
+    uint64_t *vfull = kempty + kKBlocks, *vempty = vfull + kVChunks;
+    uint64_t *rfull = vempty + kVChunks, *rempty = rfull + 2, *mfull = rempty + 2;
+    float* xch = reinterpret_cast<float*>(smem + kXchOff);
+    volatile int32_t* rowat = reinterpret_cast<volatile int32_t*>(smem + kRowOff);
+    volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + kMaskOff);
     long long* scan = reinterpret_cast<long long*>(smem + kScanOff);
     Start* sched = reinterpret_cast<Start*>(smem + kSchedOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
@@ -226,16 +241,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
         mbar_init(qempty, 1);
         mbar_init(ofree, 2 * kSoftWarps);
         mbar_init(done, 1);
+        mbar_init(pfull, 2 * kSoftWarps);
+        mbar_init(pvdone, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&kfull[i], 8);
-            mbar_init(&kempty[i], 1);
-            mbar_init(&vfull[i], 8);
-            mbar_init(&pvdone[i], 1);
             mbar_init(&sfull[i], 1);
             mbar_init(&sfree[i], 2 * kSoftWarps);
-            mbar_init(&pfull[i], 2 * kSoftWarps);
+            mbar_init(&rfull[i], 1);
+            mbar_init(&rempty[i], 2 * kCopyWarps);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&mfull[i], 4);
+        for (int i = 0; i < kKBlocks; ++i) {
+            mbar_init(&kfull[i], 2);
+            mbar_init(&kempty[i], 1);
+        }
+        for (int i = 0; i < kVChunks; ++i) {
+            mbar_init(&vfull[i], 2);
+            mbar_init(&vempty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&mfull[i], 1);
         *abort = 0;
         sched->left = 0;
         fence_mbar_init();
@@ -290,112 +312,135 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     uint32_t g = 0;  // tiles so far
     bool ok = true;
 
-    if (warp >= kKWarp && warp < kVWarp) {
-        // ====================== rows as keys: 32 of the 64, all columns ======================
-        const int r0 = 8 * (warp - kKWarp);  // this warp's rows of the 32
+    if (warp >= kKWarp && warp < kMmaWarp) {
+        // A copying warp takes every fourth block (chunk) of the pair's run.  Up to two of its
+        // copies are in flight behind the newest; before it waits for anything it announces them.
+        const bool keys = warp < kVWarp;
+        const int mine = (warp - kKWarp) & (kCopyWarps - 1);
         const int sub = lane >> 3, ch = lane & 7;
-        bool pending = false;
-        const auto post = [&](uint32_t n) {
+        uint64_t* fulls = keys ? kfull : vfull;
+        uint64_t* empties = keys ? kempty : vempty;
+        int flying = 0, b1 = 0, b2 = 0;  // copies not announced; their places, the older one in b2
+        const auto post = [&](int place) {
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(&kfull[n & 1u], 0);
+            if (lane == 0) arrive_even(&fulls[place]);
         };
-        while (ok && w.next(p)) {
-            for (int i = w.i0; i < w.i1; ++i, ++g) {
-                const int pos = lane < 8 ? position(p, w.s, i * kTile + crank * 32 + r0 + lane) : -1;
-                const long long row = pos >= 0 ? paged_row(p.cache, w.s.b, pos) : -1;
-                if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&kempty[g & 1u], ((g >> 1) & 1u) ^ 1u))) {
-                    if (pending) {  // announced before the wait
-                        copy_wait<0>();
-                        post(g - 1);
-                        pending = false;
-                    }
-                    if (!wait_all(&kempty[g & 1u], ((g >> 1) & 1u) ^ 1u, abort)) { ok = false; break; }
-                }
-                const uint32_t st0 = smem_u32(smem + kKOff + (g & 1u) * kKStage);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int rr = 4 * h + sub;
-                    const long long at = __shfl_sync(0xFFFFFFFFu, row, rr);
-                    const uint8_t* src = p.rows + (at < 0 ? 0 : at) * kRowBytes + ch * 16;
-                    const uint32_t dst = st0 + (r0 + rr) * 128 + ((ch ^ rr) << 4);
-#pragma unroll
-                    for (int j = 0; j < 9; ++j)
-                        copy16(dst + j * kKBlock, src + j * 128, at < 0 ? 0u : 16u);
-                }
-                copy_commit();
-                if (pending) {
-                    copy_wait<1>();
-                    post(g - 1);
-                }
-                pending = true;
+        const auto wait_for = [&](uint64_t* bar, uint32_t parity) -> bool {
+            if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+            copy_wait<0>();
+            if (flying > 1) post(b2);
+            if (flying > 0) post(b1);
+            flying = 0;
+            return wait_all(bar, parity, abort);
+        };
+        const auto claim = [&](int place) -> bool {  // tile g may be written there
+            return wait_for(&empties[place], (g & 1u) ^ 1u);
+        };
+        const auto sent = [&](int place) {
+            copy_commit();
+            if (flying == 2) {
+                copy_wait<2>();
+                post(b2);
+                flying = 1;
             }
-        }
-        copy_wait<0>();
-        if (pending && ok) post(g - 1);
-    } else if (warp >= kVWarp && warp < kMmaWarp) {
-        // ================ rows as values: all 64, half of the 512 columns ================
-        const int r0 = 16 * (warp - kVWarp);
-        const int blk = lane >> 3, ch = lane & 7;
-        // block 0, 1: this CTA's 128 columns of the first 256; 2, 3: of the last 256
-        const int col = (blk >> 1) * 256 + crank * 128 + (blk & 1) * 64;
-        bool pending = false;
-        const auto post = [&](uint32_t n) {
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(&vfull[n & 1u], 0);
+            b2 = b1;
+            b1 = place;
+            ++flying;
         };
+        int turn = 0;  // of the block, modulo the number of warps
         while (ok && w.next(p)) {
             // a row that not every token of the segment sees meets zeros of p; an infinity or a
             // NaN in it must not
-            int fewest = w.s.len;
-            if (!p.inds)
+            int fewest = 0x7FFFFFFF;
+            if (!keys && w.s.n > 1)
                 for (int i = 0; i < w.s.n; ++i) fewest = min(fewest, seq_length(p.seq, w.s.t + i));
-            for (int i = w.i0; i < w.i1; ++i, ++g) {
-                const int e = i * kTile + r0 + lane;
-                const int pos = lane < 16 ? position(p, w.s, e) : -1;
-                const long long row = pos >= 0 ? paged_row(p.cache, w.s.b, pos) : -1;
-                const uint32_t there = __ballot_sync(0xFFFFFFFFu, row >= 0);
-                if (lane == 0) {
-                    // (read four tiles ago: the columns of the tile before the last are free)
-                    mask[(g & 3u) * 4 + (warp - kVWarp)] = (uint16_t)there;
-                    mbar_arrive(&mfull[g & 3u]);
-                }
-                if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&pvdone[g & 1u], ((g >> 1) & 1u) ^ 1u))) {
-                    if (pending) {
-                        copy_wait<0>();
-                        post(g - 1);
-                        pending = false;
+            for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
+                if (!wait_for(&rfull[g & 1u], (g >> 1) & 1u)) { ok = false; break; }
+                // keys: the rows of this CTA's 64 positions; values: of the two chunks' 16
+                const volatile int32_t* rows = rowat + (g & 1u) * kTile;
+                const int32_t own0 = rows[keys ? crank * 64 + lane : 16 * mine + (lane & 15)];
+                const int32_t own1 = rows[keys ? crank * 64 + 32 + lane : 16 * (mine + 4) + (lane & 15)];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&rempty[g & 1u]);
+                if (keys) {
+                    for (int j = 0; j < kKBlocks; ++j, turn = (turn + 1) & (kCopyWarps - 1)) {
+                        if (turn != mine) continue;
+                        if (!claim(j)) { ok = false; break; }
+                        const uint32_t dst = smem_u32(smem + kKOff + j * kKBlock);
+#pragma unroll
+                        for (int h = 0; h < 16; ++h) {
+                            const int rr = 4 * h + sub;
+                            const int32_t at = __shfl_sync(0xFFFFFFFFu, h < 8 ? own0 : own1, rr & 31);
+                            const uint8_t* src = p.rows + (long long)max(at, 0) * kRowBytes + j * 128 + ch * 16;
+                            copy16(dst + rr * 128 + ((ch ^ (rr & 7)) << 4), src, at < 0 ? 0u : 16u);
+                        }
+                        sent(j);
                     }
-                    if (!wait_all(&pvdone[g & 1u], ((g >> 1) & 1u) ^ 1u, abort)) { ok = false; break; }
-                }
-                const uint32_t st0 = smem_u32(smem + kVOff + (g & 1u) * kVStage) + blk * kVBlock;
-                const bool careful = i * kTile + r0 + 15 >= fewest;
+                } else {
+                    // block 0, 1: this CTA's 128 columns of the first 256; 2, 3: of the last 256
+                    const int col = (sub >> 1) * 256 + crank * 128 + (sub & 1) * 64;
+                    for (int c = mine; c < kVChunks; c += kCopyWarps) {
+                        const int32_t own = c < kCopyWarps ? own0 : own1;
+                        if (!claim(c)) { ok = false; break; }
+                        const uint32_t dst = smem_u32(smem + kVOff) + sub * kVBlock + c * 2048;
+                        const int first = i * kTile + 16 * c;
+                        if (first + 15 < fewest || first >= w.s.len) {
+#pragma unroll
+                            for (int rr = 0; rr < 16; ++rr) {
+                                const int32_t at = __shfl_sync(0xFFFFFFFFu, own, rr);
+                                const uint8_t* src = p.rows + (long long)max(at, 0) * kRowBytes + col * 2 + ch * 16;
+                                copy16(dst + rr * 128 + ((ch ^ (rr & 7)) << 4), src, at < 0 ? 0u : 16u);
+                            }
+                        } else {
 #pragma unroll 4
-                for (int rr = 0; rr < 16; ++rr) {
-                    const long long at = __shfl_sync(0xFFFFFFFFu, row, rr);
-                    const uint8_t* src = p.rows + (at < 0 ? 0 : at) * kRowBytes + col * 2 + ch * 16;
-                    const uint32_t dst = st0 + (r0 + rr) * 128 + ((ch ^ (rr & 7)) << 4);
-                    if (careful && at >= 0 && i * kTile + r0 + rr >= fewest) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
-                                     "r"(finite2(v.x)), "r"(finite2(v.y)), "r"(finite2(v.z)),
-                                     "r"(finite2(v.w))
-                                     : "memory");
-                    } else {
-                        copy16(dst, src, at < 0 ? 0u : 16u);
+                            for (int rr = 0; rr < 16; ++rr) {
+                                const int32_t at = __shfl_sync(0xFFFFFFFFu, own, rr);
+                                const uint8_t* src = p.rows + (long long)max(at, 0) * kRowBytes + col * 2 + ch * 16;
+                                uint4 v = make_uint4(0, 0, 0, 0);
+                                if (at >= 0) v = __ldg(reinterpret_cast<const uint4*>(src));
+                                if (first + rr >= fewest)
+                                    v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                                 dst + rr * 128 + ((ch ^ (rr & 7)) << 4)),
+                                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                                             : "memory");
+                            }
+                        }
+                        sent(c);
                     }
                 }
-                copy_commit();
-                if (pending) {
-                    copy_wait<1>();
-                    post(g - 1);
-                }
-                pending = true;
             }
         }
         copy_wait<0>();
-        if (pending && ok) post(g - 1);
+        if (ok && flying > 1) post(b2);
+        if (ok && flying > 0) post(b1);
+    } else if (warp == kFindWarp) {
+        // ====================== the rows of the tiles ahead, and which are there ======================
+        while (ok && w.next(p)) {
+            for (int i = w.i0; i < w.i1; ++i, ++g) {
+                int32_t row[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) row[c] = position(p, w.s, i * kTile + 32 * c + lane);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (row[c] >= 0) row[c] = (int32_t)paged_row(p.cache, w.s.b, row[c]);
+                if (!wait_all(&rempty[g & 1u], ((g >> 1) & 1u) ^ 1u, abort)) { ok = false; break; }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    rowat[(g & 1u) * kTile + 32 * c + lane] = row[c];
+                    const uint32_t there = __ballot_sync(0xFFFFFFFFu, row[c] >= 0);
+                    // (its last reader was the softmax of four tiles ago: the copies that have read the
+                    // rows of two tiles ago had waited for the second product of four tiles ago)
+                    if (lane == 0) mask[(g & 3u) * 4 + c] = there;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&rfull[g & 1u]);
+                    mbar_arrive(&mfull[g & 3u]);
+                }
+            }
+        }
     } else if (warp >= kQWarp) {
         // ================================== queries ==================================
         uint32_t n = 0;
@@ -420,56 +465,72 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             copy_wait<0>();
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(qfull, 0);
+            if (lane == 0) arrive_even(qfull);
         }
     } else if (warp == kMmaWarp) {
         // ================================ UMMA issuer ================================
-        if (crank == 0 && lane == 0) {
+        // (the next block's barrier is looked at before a block is issued: a look takes 90 clocks)
+        if (crank == 0) {
             uint32_t n = 0;
+            const uint64_t dq = sdesc_k128(smem_u32(smem + kQOff)), dk = sdesc_k128(smem_u32(smem + kKOff));
+            const uint64_t dp = sdesc_k128(smem_u32(smem + kPOff)), dv = sdesc_mn128(smem_u32(smem + kVOff));
             const auto scores = [&]() -> bool {  // tile g
-                const uint32_t i = g & 1u, ph = (g >> 1) & 1u;
-                if (!wait_c(&kfull[i], ph, abort) || !wait_c(&sfree[i], ph ^ 1u, abort)) return false;
-                tc_fence_after();
-                const uint64_t dq = sdesc_k128(smem_u32(smem + kQOff));
-                const uint64_t dk = sdesc_k128(smem_u32(smem + kKOff + i * kKStage));
+                const uint32_t i = g & 1u;
+                bool here = mbar_test(&kfull[0], g & 1u);
+                if (!wait_all(&sfree[i], ((g >> 1) & 1u) ^ 1u, abort)) return false;
+#pragma unroll 1
+                for (int j = 0; j < kKBlocks; ++j) {
+                    if (!__all_sync(0xFFFFFFFFu, here) && !wait_all(&kfull[j], g & 1u, abort)) return false;
+                    if (j + 1 < kKBlocks) here = mbar_test(&kfull[j + 1], g & 1u);
+                    tc_fence_after();
+                    const uint64_t a = dq + (uint64_t)(j * (kQBlock / 16)), b = dk + (uint64_t)(j * (kKBlock / 16));
+                    if (elect_lane()) {
 #pragma unroll
-                for (int j = 0; j < 9; ++j)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_bf16_pair(tmem + kSCol + 32 * i, dq + (uint64_t)(j * (kQBlock / 16) + 2 * k),
-                                       dk + (uint64_t)(j * (kKBlock / 16) + 2 * k), kIdescS, j + k > 0);
-                umma_commit_pair(&kempty[i], 3);
-                umma_commit_pair(&sfull[i], 3);
+                        for (int k = 0; k < 4; ++k)
+                            umma_bf16_pair(tmem + kSCol + 64 * i, a + (uint64_t)(2 * k), b + (uint64_t)(2 * k),
+                                           kIdescS, j + k > 0);
+                        umma_commit_pair(&kempty[j], 3);
+                        if (j == kKBlocks - 1) umma_commit_pair(&sfull[i], 3);
+                    }
+                    __syncwarp();
+                }
                 return true;
             };
             const auto values = [&](uint32_t c, bool first) -> bool {  // tile c
-                const uint32_t i = c & 1u, ph = (c >> 1) & 1u;
-                if (!wait_c(&vfull[i], ph, abort) || !wait_c(&pfull[i], ph, abort)) return false;
-                if (first && !wait_c(ofree, (n & 1u) ^ 1u, abort)) return false;
-                tc_fence_after();
-                const uint64_t dp = sdesc_k128(smem_u32(smem + kPOff + i * kPStage));
-                const uint64_t dv = sdesc_mn128(smem_u32(smem + kVOff + i * kVStage));
+                bool here = mbar_test(&vfull[0], c & 1u);
+                if (!wait_all(pfull, c & 1u, abort)) return false;
+                if (first && !wait_all(ofree, (n & 1u) ^ 1u, abort)) return false;
+#pragma unroll 1
+                for (int k = 0; k < kVChunks; ++k) {  // 16 positions = 2048 bytes further
+                    if (!__all_sync(0xFFFFFFFFu, here) && !wait_all(&vfull[k], c & 1u, abort)) return false;
+                    if (k + 1 < kVChunks) here = mbar_test(&vfull[k + 1], c & 1u);
+                    tc_fence_after();
+                    const uint64_t a = dp + (uint64_t)((k >> 2) * (kPBlock / 16) + 2 * (k & 3));
+                    if (elect_lane()) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 16 positions = 2048 bytes further
-                        umma_bf16_pair(tmem + 128 * half, dp + (uint64_t)(2 * k),
-                                       dv + (uint64_t)(half * 2 * (kVBlock / 16) + k * (2048 / 16)),
-                                       kIdescO, !first || k > 0);
-                umma_commit_pair(&pvdone[i], 3);
+                        for (int half = 0; half < 2; ++half)
+                            umma_bf16_pair(tmem + 128 * half, a,
+                                           dv + (uint64_t)(half * 2 * (kVBlock / 16) + k * (2048 / 16)),
+                                           kIdescO, !first || k > 0);
+                        umma_commit_pair(&vempty[k], 3);
+                        if (k == kVChunks - 1) umma_commit_pair(pvdone, 3);
+                    }
+                    __syncwarp();
+                }
                 return true;
             };
             for (; ok && w.next(p); ++n) {
-                if (!wait_c(qfull, n & 1u, abort)) { ok = false; break; }
+                if (!wait_all(qfull, n & 1u, abort)) { ok = false; break; }
                 for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
                     ok = scores();
-                    if (ok && i == w.i1 - 1) umma_commit_pair(qempty, 3);
+                    if (ok && i == w.i1 - 1 && elect_lane()) umma_commit_pair(qempty, 3);
+                    __syncwarp();
                     if (ok && i > w.i0) ok = values(g - 1, i - 1 == w.i0);
                 }
                 if (ok) ok = values(g - 1, w.i1 - 1 == w.i0);
             }
-            if (!ok) record_timeout(abort);
-            umma_commit_pair(done, 1);  // no UMMA is left when the pair frees its TMEM
+            if (elect_lane()) umma_commit_pair(done, 1);  // no UMMA is left when the pair frees its TMEM
+            __syncwarp();
             mbar_wait(done, 0u, nullptr, 100000000ull);
         }
     } else {
@@ -485,31 +546,39 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             const int see = !live ? 0 : p.inds ? w.s.len : seq_length(p.seq, tok);
             float m = -kInf, l = 0.0f;
             for (int i = w.i0; i < w.i1; ++i, ++g) {
-                const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
+                const uint32_t b = g & 1u;
                 // (a warp whose wait gave up keeps to the barriers of the 128 threads until all know)
-                ok = ok && wait_all(&mfull[g & 3u], (g >> 2) & 1u, abort) && wait_all(&sfull[b], ph, abort);
+                ok = ok && wait_all(&mfull[g & 3u], (g >> 2) & 1u, abort) &&
+                     wait_all(&sfull[b], (g >> 1) & 1u, abort);
                 tc_fence_after();
-                uint32_t v[32];
-                tmem_ld32(lane0 + kSCol + 32 * b, v);
-                const int left = see - i * kTile - half * 32;
-                uint32_t bits = (uint32_t)mask[(g & 3u) * 4 + 2 * half] |
-                                ((uint32_t)mask[(g & 3u) * 4 + 2 * half + 1] << 16);
-                bits &= left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
-                tmem_ld_wait();
+                float x[64];
+                {
+                    uint32_t v[32], u[32];
+                    tmem_ld32(lane0 + kSCol + 64 * b, v);
+                    tmem_ld32(lane0 + kSCol + 64 * b + 32, u);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        x[c] = __uint_as_float(v[c]) * p.scale;
+                        x[32 + c] = __uint_as_float(u[c]) * p.scale;
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive_cluster(&sfree[b], 0);
-                float x[32];
+                if (lane == 0 && ok) arrive_even(&sfree[b]);
+                const int left = see - i * kTile - half * 64;
+                const uint32_t m0 = mask[(g & 3u) * 4 + 2 * half] & low_bits(left);
+                const uint32_t m1 = mask[(g & 3u) * 4 + 2 * half + 1] & low_bits(left - 32);
+                if (!__all_sync(0xFFFFFFFFu, (m0 & m1) == 0xFFFFFFFFu)) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]) * p.scale;
-                if (!__all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!((bits >> c) & 1u)) x[c] = -kInf;
+                    for (int c = 0; c < 32; ++c) {
+                        if (!((m0 >> c) & 1u)) x[c] = -kInf;
+                        if (!((m1 >> c) & 1u)) x[32 + c] = -kInf;
+                    }
                 }
                 float mx = x[0];
 #pragma unroll
-                for (int c = 1; c < 32; ++c) mx = fmaxf(mx, x[c]);
+                for (int c = 1; c < 64; ++c) mx = fmaxf(mx, x[c]);
                 if (soft_any(!ok || mx > m + kLag)) {
                     xch[L] = mx;
                     if (soft_any(!ok)) { ok = false; break; }
@@ -520,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                     l *= f;
                     if (i > w.i0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
                         // o of the tiles so far; the next product waits for this tile's p
-                        ok = wait_all(&pvdone[b ^ 1u], ((g - 1) >> 1) & 1u, abort);
+                        ok = wait_all(pvdone, (g & 1u) ^ 1u, abort);
                         tc_fence_after();
 #pragma unroll 1
                         for (uint32_t c = 0; c < 256; c += 16) {
@@ -535,27 +604,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                     }
                 }
                 const float ref = m == -kInf ? 0.0f : m;
-                uint32_t pk[16];
+                uint32_t pk[32];
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
+                for (int c = 0; c < 64; c += 2) {
                     const float p0 = exp2_of(x[c] - ref), p1 = exp2_of(x[c + 1] - ref);
                     l += p0 + p1;
                     pk[c / 2] = pack_bf16x2(p0, p1);
                 }
-                ok = ok && wait_all(&pvdone[b], ph ^ 1u, abort);  // p of two tiles ago has been read
-                const uint32_t dst = smem_u32(smem + kPOff + b * kPStage) + row * 128;
+                ok = ok && wait_all(pvdone, (g & 1u) ^ 1u, abort);  // the last tile's p has been read
+                const uint32_t dst = smem_u32(smem + kPOff + half * kPBlock) + row * 128;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     dst + (((half * 4 + c) ^ (row & 7)) << 4)),
+                for (int c = 0; c < 8; ++c)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((c ^ (row & 7)) << 4)),
                                  "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
                                  : "memory");
                 fence_async_shared();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive_cluster(&pfull[b], 0);
+                if (lane == 0 && ok) arrive_even(pfull);
             }
-            ok = ok && wait_all(&pvdone[(g - 1) & 1u], ((g - 1) >> 1) & 1u, abort);
+            ok = ok && wait_all(pvdone, (g - 1) & 1u, abort);
             xch[L] = l;
             if (soft_any(!ok)) { ok = false; break; }
             l += xch[L ^ 64];
@@ -600,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(ofree, 0);
+            if (lane == 0) arrive_even(ofree);
         }
     }
 
@@ -696,38 +764,9 @@ size_t attention_ws_bytes(int pairs) {
     return (size_t)pairs * 2 * (kPartFloats * sizeof(float) + sizeof(int4));
 }
 
-cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
-    static DeviceOnce attr_once, occ_once;
-    static int resident[DeviceOnce::kMaxDevices] = {};
-    cudaError_t e = attr_once.run([] {
-        return cudaFuncSetAttribute(attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kSmemBytes);
-    });
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= DeviceOnce::kMaxDevices) return cudaErrorInvalidDevice;
-    // as many pairs as the device can hold at once (an SM left over in a GPC takes none)
-    e = occ_once.run([&] {
-        cfg.gridDim = dim3(2 * kMaxPairs);
-        int n = 0;
-        const cudaError_t err = cudaOccupancyMaxActiveClusters(&n, attention_kernel, &cfg);
-        if (err == cudaSuccess) resident[dev] = n > 0 ? n : 1;
-        return err;
-    });
-    if (e != cudaSuccess) return e;
+namespace {
+
+Params params_of(const AttentionArgs& a, int pairs) {
     const long long room = (long long)a.width * a.page;
     Params p = {};
     p.cache = {a.table, a.width, a.page, a.pages};
@@ -743,17 +782,67 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
     p.k = a.k;
     p.out = static_cast<uint16_t*>(a.out);
     p.lse = a.lse;
-    p.pairs = attention_pairs(a.T, a.inds ? a.k : room);
-    if (resident[dev] < p.pairs) p.pairs = resident[dev];
+    p.pairs = pairs;
     p.part = static_cast<float*>(a.ws);
-    p.meta = reinterpret_cast<int4*>(p.part + (size_t)p.pairs * 2 * kPartFloats);
-    cfg.gridDim = dim3((unsigned)(2 * p.pairs));
-    e = cudaLaunchKernelEx(&cfg, attention_kernel, p);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess || p.pairs == 1) return e;
-    const long long cut = a.T < p.pairs - 1 ? a.T : p.pairs - 1;  // segments that may be cut apart
+    p.meta = reinterpret_cast<int4*>(p.part + (size_t)pairs * 2 * kPartFloats);
+    return p;
+}
+
+}  // namespace
+
+cudaError_t attention_plan(AttentionArgs& a) {
+    static DeviceOnce once;
+    static int resident[DeviceOnce::kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= DeviceOnce::kMaxDevices) return cudaErrorInvalidDevice;
+    e = once.run([&] {
+        cudaError_t err = cudaFuncSetAttribute(
+            attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (err != cudaSuccess) return err;
+        // as many pairs as the device can hold at once (an SM left over in a GPC takes none)
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * kMaxPairs);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        err = cudaOccupancyMaxActiveClusters(&n, attention_kernel, &cfg);
+        if (err == cudaSuccess) resident[dev] = n > 0 ? n : 1;
+        return err;
+    });
+    if (e != cudaSuccess) return e;
+    a.pairs = attention_pairs(a.T, a.inds ? a.k : (long long)a.width * a.page);
+    if (resident[dev] < a.pairs) a.pairs = resident[dev];
+    return cudaSuccess;
+}
+
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * a.pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_kernel, params_of(a, a.pairs));
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t s) {
+    const long long cut = a.T < a.pairs - 1 ? a.T : a.pairs - 1;  // segments that may be cut apart
     return launch_kernel(join_kernel, dim3((unsigned)((kRows + kJoinWarps - 1) / kJoinWarps), (unsigned)cut),
-                         dim3(32 * kJoinWarps), 0, s, p);
+                         dim3(32 * kJoinWarps), 0, s, params_of(a, a.pairs));
 }
 
 cudaError_t read_attention_status(unsigned int* out, int clear, cudaStream_t s) {

@@ -243,10 +243,14 @@ struct AttentionArgs {
     void* out;                   // bf16 [T, H, 512]
     float* lse;                  // [T, H] or nullptr
     void* ws;                    // attention_ws_bytes(attention_pairs(T, k or width * page))
+    int pairs;                   // CTA pairs (attention_plan)
 };
 int attention_pairs(long long T, long long entries);
 size_t attention_ws_bytes(int pairs);
+cudaError_t attention_plan(AttentionArgs& a);
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
+// With more than one pair: joins what they cut apart.
+cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t s);
 cudaError_t read_attention_status(unsigned int* out, int clear, cudaStream_t s);
 
 // Per-device status word of the kernels with bounded waits.

@@ -57,6 +57,32 @@ template <int N>
 MOE_DEV void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Whether the phase with this parity has completed, without waiting (try_wait suspends the thread
+// until it has, or for some microseconds: copies that are announced behind it arrive late).
+MOE_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// One lane of a converged warp, always the same.  UMMAs are issued by a warp that runs its loops
+// converged, with the issue alone inside `if (elect_lane())`: the operands then are warp-uniform
+// (four UMMAs of 128 x 128 x 16 by a CTA pair, with a wait and a commit: 142 clocks; in a loop
+// that lane 0 runs alone 272).
+MOE_DEV bool elect_lane() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
 // What this thread wrote to shared memory becomes visible to the tensor cores and the bulk copies.
 MOE_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

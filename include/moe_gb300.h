@@ -301,7 +301,7 @@ typedef struct {
  *   its weights).  weights fp32 [T, H], of any sign.  1 <= H <= 128.  out fp32 [T, ld], n positions
  *   per row (ld >= n, in elements); what lies between n and ld is left as it was.
  * Errors: MOE_ERR_INVALID for NULL pointers, H outside [1, 128], n outside [0, 2^31 - 512], ld < n,
- * a cache with page < 1, pages outside [0, 2^31) or more than 2^31 - 512 positions per sequence,
+ * a cache with page < 1, 2^31 rows or more, or more than 2^31 - 512 positions per sequence,
  * sequences != T without cu_tokens, q or rows not 16-byte aligned.  T == 0 or n == 0 is a no-op.
  */
 int moe_indexer_scores(const void* q, const float* weights, int64_t T, int32_t H,
