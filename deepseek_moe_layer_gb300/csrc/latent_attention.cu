@@ -26,7 +26,8 @@
 // Warp roles (512 threads): warps 0..3 softmax, rescaling and epilogue (a thread is a row and half of
 // its positions or columns), 4..7 copies of the K-major rows, 8..11 of the MN-major columns (16-byte
 // asynchronous copies, so pages of any size and selected rows are alike; absent rows are zeros),
-// 12 UMMA issuer (of the pair's even CTA), 13 finds the rows of the tiles ahead, 14 and 15 queries.
+// 12 and 13 issue the two products' UMMAs (of the pair's even CTA; one warp for both waits for
+// barriers as long as the tensor cores work), 14 finds the rows of the tiles ahead, 15 queries.
 // Every wait is bounded.
 #include <mutex>
 
@@ -43,20 +44,23 @@ constexpr int kWidth = 576, kLatent = 512;
 constexpr int kRowBytes = 2 * kWidth;
 constexpr int kTile = 128;                      // positions per tile
 constexpr int kRows = 128;                      // (token, head) rows of a pair
-constexpr int kSoftWarps = 4, kKWarp = 4, kVWarp = 8, kMmaWarp = 12, kFindWarp = 13, kQWarp = 14;
+constexpr int kSoftWarps = 4, kKWarp = 4, kVWarp = 8, kMmaWarp = 12, kFindWarp = 14, kQWarp = 15;
 constexpr int kCopyWarps = 4;                   // of the K-major rows, and of the MN-major columns
 constexpr int kThreads = 32 * 16;
-constexpr int kKBlocks = 9;                     // 64 columns of this CTA's 64 positions
-constexpr int kVChunks = 8;                     // 16 positions, this CTA's 256 columns
+// Operand blocks are freed one by one (their copies take as long as a tile) and waited for in
+// groups (a wait costs the issuing warp more than a block's UMMAs take).
+constexpr int kKBlocks = 9, kKGroups = 3;       // 64 columns of this CTA's 64 positions
+constexpr int kVChunks = 8, kVGroups = 4;       // 16 positions, this CTA's 256 columns
+constexpr int kKPer = kKBlocks / kKGroups, kVPer = kVChunks / kVGroups;
 
 constexpr int kQOff = 0, kQBlock = 64 * 128;    // 9 blocks of [64 rows x 64 columns]
 constexpr int kKOff = kQOff + 9 * kQBlock, kKBlock = 64 * 128;
 constexpr int kVOff = kKOff + kKBlocks * kKBlock, kVBlock = kTile * 128;  // 4 of [128 x 64 columns]
 constexpr int kPOff = kVOff + 4 * kVBlock, kPBlock = 64 * 128;  // 2 of [64 rows x 64 positions]
 constexpr int kBarOff = kPOff + 2 * kPBlock;
-// q full, q empty, o free, done, p full, pv done; s full, s free (2 each); k full, k empty (9 each);
-// v full, v empty (8 each); rows full, rows empty (2 each); masks (4)
-constexpr int kBars = 6 + 4 + 2 * kKBlocks + 2 * kVChunks + 4 + 4;
+// q full, q empty, o free, done, p full, pv done; s full, s free (2 each); k full, k empty; v full,
+// v empty; rows full, rows empty (2 each); masks (4)
+constexpr int kBars = 6 + 4 + kKGroups + kKBlocks + kVGroups + kVChunks + 4 + 4;
 constexpr int kXchOff = kBarOff + 8 * kBars;    // 128 floats: maxima, sums
 constexpr int kRowOff = kXchOff + 4 * 128;      // [2][128] rows of the cache
 constexpr int kMaskOff = kRowOff + 2 * 4 * kTile;  // [4][4] words
@@ -65,6 +69,7 @@ constexpr int kSchedOff = kScanOff + 128;       // Start
 constexpr int kMiscOff = kSchedOff + 32;        // TMEM address, abort
 constexpr int kSmemBytes = kMiscOff + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+static_assert(kVPer == 2 && kVGroups == 4, "descriptors of the second product");
 static_assert(kVChunks == 2 * kCopyWarps, "two chunks of a tile per copying warp");
 
 constexpr uint32_t kSCol = 256;                 // TMEM columns: o 0..255, s 2 x 64
@@ -104,19 +109,19 @@ MOE_DEV void record_timeout(volatile int* abort) {
     atomicCAS(&g_attention_status, 0u, kStatusTimeout);
 }
 
-// A segment: tokens t .. t + n - 1 of sequence b, `len` positions (or entries of its selection) in
-// `tiles` tiles (one, all masked, where it sees nothing).
+// A segment: tokens t .. t + n - 1 of sequence b, which see up to `see` positions; `len` positions (or
+// entries of its selection) in `tiles` tiles (one, all masked, where it sees nothing).
 struct Seg {
-    int t, n, b, len, tiles;
+    int t, n, b, see, len, tiles;
 };
 MOE_DEV Seg segment(const Params& p, int t, int b) {
     Seg s;
     s.t = t;
     s.b = b;
     s.n = max(1, min(p.tt, seq_end(p.seq, b) - t));
-    s.len = 0;
-    for (int i = 0; i < s.n; ++i) s.len = max(s.len, seq_length(p.seq, t + i));
-    if (p.inds) s.len = min(s.len, p.k);
+    s.see = 0;
+    for (int i = 0; i < s.n; ++i) s.see = max(s.see, seq_length(p.seq, t + i));
+    s.len = p.inds ? min(s.see, p.k) : s.see;
     s.tiles = max(1, (s.len + kTile - 1) / kTile);
     return s;
 }
@@ -144,12 +149,10 @@ struct Walk {
     MOE_DEV bool ends() const { return i1 == s.tiles; }
 };
 
-// The position that entry e of a segment's list stands for, -1 for none.
-MOE_DEV int position(const Params& p, const Seg& s, int e) {
+// The entry e of a segment's list: a position, or what its selection holds; -1 behind its end.
+MOE_DEV int entry(const Params& p, const Seg& s, int e) {
     if (e >= s.len) return -1;
-    if (!p.inds) return e;
-    const int j = __ldg(p.inds + (long long)s.t * p.k + e);
-    return j >= 0 && j < seq_length(p.seq, s.t) ? j : -1;
+    return p.inds ? __ldg(p.inds + (long long)s.t * p.k + e) : e;
 }
 
 // What the barriers hand over between the CTAs of a pair are operands that their writers have
@@ -221,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
     uint64_t *qfull = bars, *qempty = bars + 1, *ofree = bars + 2, *done = bars + 3;
     uint64_t *pfull = bars + 4, *pvdone = bars + 5, *sfull = bars + 6, *sfree = bars + 8;
-    uint64_t *kfull = bars + 10, *kempty = kfull + kKBlocks;
-    uint64_t *vfull = kempty + kKBlocks, *vempty = vfull + kVChunks;
+    uint64_t *kfull = bars + 10, *kempty = kfull + kKGroups;
+    uint64_t *vfull = kempty + kKBlocks, *vempty = vfull + kVGroups;
     uint64_t *rfull = vempty + kVChunks, *rempty = rfull + 2, *mfull = rempty + 2;
     float* xch = reinterpret_cast<float*>(smem + kXchOff);
     volatile int32_t* rowat = reinterpret_cast<volatile int32_t*>(smem + kRowOff);
@@ -237,10 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     // ---- set-up ----
     if (threadIdx.x == 0) {
         // the barriers that the issuer waits on are the even CTA's, with arrivals from both
-        mbar_init(qfull, 4);
+        mbar_init(qfull, 2);
         mbar_init(qempty, 1);
         mbar_init(ofree, 2 * kSoftWarps);
-        mbar_init(done, 1);
+        mbar_init(done, 2);
         mbar_init(pfull, 2 * kSoftWarps);
         mbar_init(pvdone, 1);
         for (int i = 0; i < 2; ++i) {
@@ -249,14 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             mbar_init(&rfull[i], 1);
             mbar_init(&rempty[i], 2 * kCopyWarps);
         }
-        for (int i = 0; i < kKBlocks; ++i) {
-            mbar_init(&kfull[i], 2);
-            mbar_init(&kempty[i], 1);
-        }
-        for (int i = 0; i < kVChunks; ++i) {
-            mbar_init(&vfull[i], 2);
-            mbar_init(&vempty[i], 1);
-        }
+        for (int i = 0; i < kKGroups; ++i) mbar_init(&kfull[i], 2 * kKPer);
+        for (int i = 0; i < kVGroups; ++i) mbar_init(&vfull[i], 2 * kVPer);
+        for (int i = 0; i < kKBlocks; ++i) mbar_init(&kempty[i], 1);
+        for (int i = 0; i < kVChunks; ++i) mbar_init(&vempty[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&mfull[i], 1);
         *abort = 0;
         sched->left = 0;
@@ -324,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
         const auto post = [&](int place) {
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) arrive_even(&fulls[place]);
+            if (lane == 0) arrive_even(&fulls[place / (keys ? kKPer : kVPer)]);
         };
         const auto wait_for = [&](uint64_t* bar, uint32_t parity) -> bool {
             if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
@@ -417,41 +416,51 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
         if (ok && flying > 0) post(b1);
     } else if (warp == kFindWarp) {
         // ====================== the rows of the tiles ahead, and which are there ======================
-        while (ok && w.next(p)) {
-            for (int i = w.i0; i < w.i1; ++i, ++g) {
-                int32_t row[4];
+        // the entries are asked for a tile before their rows are: two loads that depend on each
+        // other take longer than a tile under way
+        bool more = w.next(p);
+        int i = w.i0, pos[4];
+        if (more)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) row[c] = position(p, w.s, i * kTile + 32 * c + lane);
+            for (int c = 0; c < 4; ++c) pos[c] = entry(p, w.s, i * kTile + 32 * c + lane);
+        for (; more; ++g) {
+            const int b = w.s.b, see = w.s.see;
+            int32_t row[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (row[c] >= 0) row[c] = (int32_t)paged_row(p.cache, w.s.b, row[c]);
-                if (!wait_all(&rempty[g & 1u], ((g >> 1) & 1u) ^ 1u, abort)) { ok = false; break; }
+            for (int c = 0; c < 4; ++c)
+                row[c] = pos[c] >= 0 && pos[c] < see ? (int32_t)paged_row(p.cache, b, pos[c]) : -1;
+            if (++i == w.i1) {
+                more = w.next(p);
+                i = w.i0;
+            }
+            if (more)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    rowat[(g & 1u) * kTile + 32 * c + lane] = row[c];
-                    const uint32_t there = __ballot_sync(0xFFFFFFFFu, row[c] >= 0);
-                    // (its last reader was the softmax of four tiles ago: the copies that have read the
-                    // rows of two tiles ago had waited for the second product of four tiles ago)
-                    if (lane == 0) mask[(g & 3u) * 4 + c] = there;
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&rfull[g & 1u]);
-                    mbar_arrive(&mfull[g & 3u]);
-                }
+                for (int c = 0; c < 4; ++c) pos[c] = entry(p, w.s, i * kTile + 32 * c + lane);
+            if (!wait_all(&rempty[g & 1u], ((g >> 1) & 1u) ^ 1u, abort)) { ok = false; break; }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                rowat[(g & 1u) * kTile + 32 * c + lane] = row[c];
+                const uint32_t there = __ballot_sync(0xFFFFFFFFu, row[c] >= 0);
+                // (its last reader was the softmax of four tiles ago: the copies that have read the
+                // rows of two tiles ago had waited for the second product of four tiles ago)
+                if (lane == 0) mask[(g & 3u) * 4 + c] = there;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&rfull[g & 1u]);
+                mbar_arrive(&mfull[g & 3u]);
             }
         }
-    } else if (warp >= kQWarp) {
+    } else if (warp == kQWarp) {
         // ================================== queries ==================================
         uint32_t n = 0;
         for (; ok && w.next(p); ++n) {
             if (!wait_all(qempty, (n & 1u) ^ 1u, abort)) { ok = false; break; }
             const uint32_t base = smem_u32(smem + kQOff);
             const int rows = w.s.n * p.H;
-            const int r0 = 32 * (warp - kQWarp);
             const int sub = lane >> 3, ch = lane & 7;
 #pragma unroll 2
-            for (int r = r0; r < r0 + 32; r += 4) {
+            for (int r = 0; r < 64; r += 4) {
                 const int rr = r + sub, gr = crank * 64 + rr;
                 const bool live = gr < rows;
                 const uint16_t* src = p.q;
@@ -467,67 +476,77 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             __syncwarp();
             if (lane == 0) arrive_even(qfull);
         }
-    } else if (warp == kMmaWarp) {
-        // ================================ UMMA issuer ================================
+    } else if (warp >= kMmaWarp && warp < kFindWarp) {
+        // ================================ UMMA issuers ================================
         // (the next block's barrier is looked at before a block is issued: a look takes 90 clocks)
         if (crank == 0) {
-            uint32_t n = 0;
-            const uint64_t dq = sdesc_k128(smem_u32(smem + kQOff)), dk = sdesc_k128(smem_u32(smem + kKOff));
-            const uint64_t dp = sdesc_k128(smem_u32(smem + kPOff)), dv = sdesc_mn128(smem_u32(smem + kVOff));
-            const auto scores = [&]() -> bool {  // tile g
-                const uint32_t i = g & 1u;
-                bool here = mbar_test(&kfull[0], g & 1u);
-                if (!wait_all(&sfree[i], ((g >> 1) & 1u) ^ 1u, abort)) return false;
+            if (warp == kMmaWarp) {
+                const uint64_t dq = sdesc_k128(smem_u32(smem + kQOff)), dk = sdesc_k128(smem_u32(smem + kKOff));
+                for (uint32_t n = 0; ok && w.next(p); ++n) {
+                    ok = wait_all(qfull, n & 1u, abort);
+                    for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
+                        const uint32_t b = g & 1u;
+                        bool here = mbar_test(&kfull[0], g & 1u);
+                        if (!(ok = wait_all(&sfree[b], ((g >> 1) & 1u) ^ 1u, abort))) break;
 #pragma unroll 1
-                for (int j = 0; j < kKBlocks; ++j) {
-                    if (!__all_sync(0xFFFFFFFFu, here) && !wait_all(&kfull[j], g & 1u, abort)) return false;
-                    if (j + 1 < kKBlocks) here = mbar_test(&kfull[j + 1], g & 1u);
-                    tc_fence_after();
-                    const uint64_t a = dq + (uint64_t)(j * (kQBlock / 16)), b = dk + (uint64_t)(j * (kKBlock / 16));
-                    if (elect_lane()) {
+                        for (int j = 0; j < kKGroups; ++j) {
+                            if (!__all_sync(0xFFFFFFFFu, here) && !(ok = wait_all(&kfull[j], g & 1u, abort))) break;
+                            if (j + 1 < kKGroups) here = mbar_test(&kfull[j + 1], g & 1u);
+                            tc_fence_after();
+                            const uint64_t da = dq + (uint64_t)(j * kKPer * (kQBlock / 16));
+                            const uint64_t db = dk + (uint64_t)(j * kKPer * (kKBlock / 16));
+                            if (elect_lane()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_bf16_pair(tmem + kSCol + 64 * i, a + (uint64_t)(2 * k), b + (uint64_t)(2 * k),
-                                           kIdescS, j + k > 0);
-                        umma_commit_pair(&kempty[j], 3);
-                        if (j == kKBlocks - 1) umma_commit_pair(&sfull[i], 3);
+                                for (int c = 0; c < kKPer; ++c) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        umma_bf16_pair(tmem + kSCol + 64 * b,
+                                                       da + (uint64_t)(c * (kQBlock / 16) + 2 * k),
+                                                       db + (uint64_t)(c * (kKBlock / 16) + 2 * k), kIdescS,
+                                                       j + c + k > 0);
+                                    umma_commit_pair(&kempty[j * kKPer + c], 3);
+                                }
+                                if (j == kKGroups - 1) {
+                                    umma_commit_pair(&sfull[b], 3);
+                                    if (i == w.i1 - 1) umma_commit_pair(qempty, 3);
+                                }
+                            }
+                            __syncwarp();
+                        }
                     }
-                    __syncwarp();
                 }
-                return true;
-            };
-            const auto values = [&](uint32_t c, bool first) -> bool {  // tile c
-                bool here = mbar_test(&vfull[0], c & 1u);
-                if (!wait_all(pfull, c & 1u, abort)) return false;
-                if (first && !wait_all(ofree, (n & 1u) ^ 1u, abort)) return false;
+            } else {
+                const uint64_t dp = sdesc_k128(smem_u32(smem + kPOff)), dv = sdesc_mn128(smem_u32(smem + kVOff));
+                for (uint32_t n = 0; ok && w.next(p); ++n) {
+                    for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
+                        const bool first = i == w.i0;
+                        if (first && !(ok = wait_all(ofree, (n & 1u) ^ 1u, abort))) break;
+                        bool here = mbar_test(&vfull[0], g & 1u);
+                        if (!(ok = wait_all(pfull, g & 1u, abort))) break;
 #pragma unroll 1
-                for (int k = 0; k < kVChunks; ++k) {  // 16 positions = 2048 bytes further
-                    if (!__all_sync(0xFFFFFFFFu, here) && !wait_all(&vfull[k], c & 1u, abort)) return false;
-                    if (k + 1 < kVChunks) here = mbar_test(&vfull[k + 1], c & 1u);
-                    tc_fence_after();
-                    const uint64_t a = dp + (uint64_t)((k >> 2) * (kPBlock / 16) + 2 * (k & 3));
-                    if (elect_lane()) {
+                        for (int j = 0; j < kVGroups; ++j) {
+                            if (!__all_sync(0xFFFFFFFFu, here) && !(ok = wait_all(&vfull[j], g & 1u, abort))) break;
+                            if (j + 1 < kVGroups) here = mbar_test(&vfull[j + 1], g & 1u);
+                            tc_fence_after();
+                            // 32 positions: half a block of p's columns, 4096 bytes of rows
+                            const uint64_t da = dp + (uint64_t)((j >> 1) * (kPBlock / 16) + 4 * (j & 1));
+                            const uint64_t db = dv + (uint64_t)(j * (kVPer * 2048 / 16));
+                            if (elect_lane()) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            umma_bf16_pair(tmem + 128 * half, a,
-                                           dv + (uint64_t)(half * 2 * (kVBlock / 16) + k * (2048 / 16)),
-                                           kIdescO, !first || k > 0);
-                        umma_commit_pair(&vempty[k], 3);
-                        if (k == kVChunks - 1) umma_commit_pair(pvdone, 3);
+                                for (int c = 0; c < kVPer; ++c) {
+#pragma unroll
+                                    for (int half = 0; half < 2; ++half)
+                                        umma_bf16_pair(tmem + 128 * half, da + (uint64_t)(2 * c),
+                                                       db + (uint64_t)(half * 2 * (kVBlock / 16) + c * (2048 / 16)),
+                                                       kIdescO, !first || j + c > 0);
+                                    umma_commit_pair(&vempty[j * kVPer + c], 3);
+                                }
+                                if (j == kVGroups - 1) umma_commit_pair(pvdone, 3);
+                            }
+                            __syncwarp();
+                        }
                     }
-                    __syncwarp();
                 }
-                return true;
-            };
-            for (; ok && w.next(p); ++n) {
-                if (!wait_all(qfull, n & 1u, abort)) { ok = false; break; }
-                for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
-                    ok = scores();
-                    if (ok && i == w.i1 - 1 && elect_lane()) umma_commit_pair(qempty, 3);
-                    __syncwarp();
-                    if (ok && i > w.i0) ok = values(g - 1, i - 1 == w.i0);
-                }
-                if (ok) ok = values(g - 1, w.i1 - 1 == w.i0);
             }
             if (elect_lane()) umma_commit_pair(done, 1);  // no UMMA is left when the pair frees its TMEM
             __syncwarp();
