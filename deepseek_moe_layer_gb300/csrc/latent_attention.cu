@@ -23,12 +23,13 @@
 // lengths fill the device; a segment cut apart leaves partial sums (m, l, o in fp32) that a second
 // kernel joins in the order of the pairs: equal calls give equal bits.
 //
-// Warp roles (512 threads): warps 0..3 softmax, rescaling and epilogue (a thread is a row and half of
-// its positions or columns), 4..7 copies of the K-major rows, 8..11 of the MN-major columns (16-byte
-// asynchronous copies, so pages of any size and selected rows are alike; absent rows are zeros),
-// 12 and 13 issue the two products' UMMAs (of the pair's even CTA; one warp for both waits for
-// barriers as long as the tensor cores work), 14 finds the rows of the tiles ahead, 15 queries.
-// Every wait is bounded.
+// Warp roles (896 threads): warps 0..3 softmax, rescaling and epilogue (a thread is a row and half of
+// its positions or columns), 4 and 5 issue the two products' UMMAs (of the pair's even CTA; one warp
+// for both waits for barriers as long as the tensor cores work), 6 finds the rows of the tiles ahead,
+// 7 queries, 8..16 copy the K-major rows, a block of 64 columns each, 17..24 the MN-major columns, 16
+// positions each (16-byte asynchronous copies, so pages of any size and selected rows are alike;
+// absent rows are zeros).  A copying warp has one place in shared memory: it waits until that is
+// free, copies, waits for the data and announces it.  Every wait is bounded.
 #include <mutex>
 
 #include "launch.h"
@@ -44,14 +45,15 @@ constexpr int kWidth = 576, kLatent = 512;
 constexpr int kRowBytes = 2 * kWidth;
 constexpr int kTile = 128;                      // positions per tile
 constexpr int kRows = 128;                      // (token, head) rows of a pair
-constexpr int kSoftWarps = 4, kKWarp = 4, kVWarp = 8, kMmaWarp = 12, kFindWarp = 14, kQWarp = 15;
-constexpr int kCopyWarps = 4;                   // of the K-major rows, and of the MN-major columns
-constexpr int kThreads = 32 * 16;
+constexpr int kSoftWarps = 4, kMmaWarp = 4, kFindWarp = 6, kQWarp = 7, kKWarp = 8;
 // Operand blocks are freed one by one (their copies take as long as a tile) and waited for in
 // groups (a wait costs the issuing warp more than a block's UMMAs take).
 constexpr int kKBlocks = 9, kKGroups = 3;       // 64 columns of this CTA's 64 positions
 constexpr int kVChunks = 8, kVGroups = 4;       // 16 positions, this CTA's 256 columns
 constexpr int kKPer = kKBlocks / kKGroups, kVPer = kVChunks / kVGroups;
+constexpr int kVWarp = kKWarp + kKBlocks, kEndWarp = kVWarp + kVChunks;
+constexpr int kThreads = 32 * 28;               // whole warpgroups
+constexpr int kLowRegs = 56, kHighRegs = 160;   // 160 * 128 + 56 * 768 <= 72 * 896
 
 constexpr int kQOff = 0, kQBlock = 64 * 128;    // 9 blocks of [64 rows x 64 columns]
 constexpr int kKOff = kQOff + 9 * kQBlock, kKBlock = 64 * 128;
@@ -64,13 +66,12 @@ constexpr int kBars = 6 + 4 + kKGroups + kKBlocks + kVGroups + kVChunks + 4 + 4;
 constexpr int kXchOff = kBarOff + 8 * kBars;    // 128 floats: maxima, sums
 constexpr int kRowOff = kXchOff + 4 * 128;      // [2][128] rows of the cache
 constexpr int kMaskOff = kRowOff + 2 * 4 * kTile;  // [4][4] words
-constexpr int kScanOff = kMaskOff + 64;         // 16 x int64
-constexpr int kSchedOff = kScanOff + 128;       // Start
+constexpr int kScanOff = kMaskOff + 64;         // 28 x int64
+constexpr int kSchedOff = kScanOff + 224;       // Start
 constexpr int kMiscOff = kSchedOff + 32;        // TMEM address, abort
 constexpr int kSmemBytes = kMiscOff + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(kVPer == 2 && kVGroups == 4, "descriptors of the second product");
-static_assert(kVChunks == 2 * kCopyWarps, "two chunks of a tile per copying warp");
 
 constexpr uint32_t kSCol = 256;                 // TMEM columns: o 0..255, s 2 x 64
 constexpr uint32_t kIdescS = idesc_bf16(128, 128);
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             mbar_init(&sfull[i], 1);
             mbar_init(&sfree[i], 2 * kSoftWarps);
             mbar_init(&rfull[i], 1);
-            mbar_init(&rempty[i], 2 * kCopyWarps);
+            mbar_init(&rempty[i], kKBlocks + kVChunks);
         }
         for (int i = 0; i < kKGroups; ++i) mbar_init(&kfull[i], 2 * kKPer);
         for (int i = 0; i < kVGroups; ++i) mbar_init(&vfull[i], 2 * kVPer);
@@ -311,145 +312,152 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     uint32_t g = 0;  // tiles so far
     bool ok = true;
 
-    if (warp >= kKWarp && warp < kMmaWarp) {
-        // A copying warp takes every fourth block (chunk) of the pair's run.  Up to two of its
-        // copies are in flight behind the newest; before it waits for anything it announces them.
-        const bool keys = warp < kVWarp;
-        const int mine = (warp - kKWarp) & (kCopyWarps - 1);
-        const int sub = lane >> 3, ch = lane & 7;
-        uint64_t* fulls = keys ? kfull : vfull;
-        uint64_t* empties = keys ? kempty : vempty;
-        int flying = 0, b1 = 0, b2 = 0;  // copies not announced; their places, the older one in b2
-        const auto post = [&](int place) {
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) arrive_even(&fulls[place / (keys ? kKPer : kVPer)]);
-        };
-        const auto wait_for = [&](uint64_t* bar, uint32_t parity) -> bool {
-            if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
-            copy_wait<0>();
-            if (flying > 1) post(b2);
-            if (flying > 0) post(b1);
-            flying = 0;
-            return wait_all(bar, parity, abort);
-        };
-        const auto claim = [&](int place) -> bool {  // tile g may be written there
-            return wait_for(&empties[place], (g & 1u) ^ 1u);
-        };
-        const auto sent = [&](int place) {
-            copy_commit();
-            if (flying == 2) {
-                copy_wait<2>();
-                post(b2);
-                flying = 1;
+    if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+    if (warp >= kKWarp && warp < kVWarp) {
+        // ============== rows as keys: 64 columns of this CTA's 64 positions ==============
+        const int j = warp - kKWarp, sub = lane >> 3, ch = lane & 7;
+        const uint32_t dst = smem_u32(smem + kKOff + j * kKBlock) + sub * 128;
+        const uint8_t* src = p.rows + j * 128 + ch * 16;
+        while (ok && w.next(p)) {
+            for (int i = w.i0; i < w.i1; ++i, ++g) {
+                if (!(ok = wait_all(&rfull[g & 1u], (g >> 1) & 1u, abort))) break;
+                const volatile int32_t* rows = rowat + (g & 1u) * kTile + crank * 64;
+                const int32_t own0 = rows[lane], own1 = rows[32 + lane];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&rempty[g & 1u]);
+                if (!(ok = wait_all(&kempty[j], (g & 1u) ^ 1u, abort))) break;
+#pragma unroll
+                for (int h = 0; h < 16; ++h) {
+                    const int32_t at = __shfl_sync(0xFFFFFFFFu, h < 8 ? own0 : own1, (4 * h + sub) & 31);
+                    copy16(dst + h * 512 + ((ch ^ ((4 * h + sub) & 7)) << 4),
+                           src + (long long)max(at, 0) * kRowBytes, at < 0 ? 0u : 16u);
+                }
+                copy_commit();
+                copy_wait<0>();
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) arrive_even(&kfull[j / kKPer]);
             }
-            b2 = b1;
-            b1 = place;
-            ++flying;
-        };
-        int turn = 0;  // of the block, modulo the number of warps
+        }
+    } else if (warp >= kVWarp && warp < kEndWarp) {
+        // ============ rows as values: 16 positions, half of the 512 columns ============
+        const int c = warp - kVWarp, blk = lane >> 3, ch = lane & 7;
+        // block 0, 1: this CTA's 128 columns of the first 256; 2, 3: of the last 256
+        const int col = (blk >> 1) * 256 + crank * 128 + (blk & 1) * 64;
+        const uint32_t dst = smem_u32(smem + kVOff) + blk * kVBlock + c * 2048;
+        const uint8_t* src = p.rows + col * 2 + ch * 16;
         while (ok && w.next(p)) {
             // a row that not every token of the segment sees meets zeros of p; an infinity or a
             // NaN in it must not
             int fewest = 0x7FFFFFFF;
-            if (!keys && w.s.n > 1)
+            if (w.s.n > 1)
                 for (int i = 0; i < w.s.n; ++i) fewest = min(fewest, seq_length(p.seq, w.s.t + i));
-            for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
-                if (!wait_for(&rfull[g & 1u], (g >> 1) & 1u)) { ok = false; break; }
-                // keys: the rows of this CTA's 64 positions; values: of the two chunks' 16
-                const volatile int32_t* rows = rowat + (g & 1u) * kTile;
-                const int32_t own0 = rows[keys ? crank * 64 + lane : 16 * mine + (lane & 15)];
-                const int32_t own1 = rows[keys ? crank * 64 + 32 + lane : 16 * (mine + 4) + (lane & 15)];
+            for (int i = w.i0; i < w.i1; ++i, ++g) {
+                if (!(ok = wait_all(&rfull[g & 1u], (g >> 1) & 1u, abort))) break;
+                const int32_t own = rowat[(g & 1u) * kTile + 16 * c + (lane & 15)];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&rempty[g & 1u]);
-                if (keys) {
-                    for (int j = 0; j < kKBlocks; ++j, turn = (turn + 1) & (kCopyWarps - 1)) {
-                        if (turn != mine) continue;
-                        if (!claim(j)) { ok = false; break; }
-                        const uint32_t dst = smem_u32(smem + kKOff + j * kKBlock);
+                if (!(ok = wait_all(&vempty[c], (g & 1u) ^ 1u, abort))) break;
+                const int first = i * kTile + 16 * c;
+                if (first + 15 < fewest || first >= w.s.len) {
 #pragma unroll
-                        for (int h = 0; h < 16; ++h) {
-                            const int rr = 4 * h + sub;
-                            const int32_t at = __shfl_sync(0xFFFFFFFFu, h < 8 ? own0 : own1, rr & 31);
-                            const uint8_t* src = p.rows + (long long)max(at, 0) * kRowBytes + j * 128 + ch * 16;
-                            copy16(dst + rr * 128 + ((ch ^ (rr & 7)) << 4), src, at < 0 ? 0u : 16u);
-                        }
-                        sent(j);
+                    for (int rr = 0; rr < 16; ++rr) {
+                        const int32_t at = __shfl_sync(0xFFFFFFFFu, own, rr);
+                        copy16(dst + rr * 128 + ((ch ^ (rr & 7)) << 4),
+                               src + (long long)max(at, 0) * kRowBytes, at < 0 ? 0u : 16u);
                     }
+                    copy_commit();
+                    copy_wait<0>();
                 } else {
-                    // block 0, 1: this CTA's 128 columns of the first 256; 2, 3: of the last 256
-                    const int col = (sub >> 1) * 256 + crank * 128 + (sub & 1) * 64;
-                    for (int c = mine; c < kVChunks; c += kCopyWarps) {
-                        const int32_t own = c < kCopyWarps ? own0 : own1;
-                        if (!claim(c)) { ok = false; break; }
-                        const uint32_t dst = smem_u32(smem + kVOff) + sub * kVBlock + c * 2048;
-                        const int first = i * kTile + 16 * c;
-                        if (first + 15 < fewest || first >= w.s.len) {
-#pragma unroll
-                            for (int rr = 0; rr < 16; ++rr) {
-                                const int32_t at = __shfl_sync(0xFFFFFFFFu, own, rr);
-                                const uint8_t* src = p.rows + (long long)max(at, 0) * kRowBytes + col * 2 + ch * 16;
-                                copy16(dst + rr * 128 + ((ch ^ (rr & 7)) << 4), src, at < 0 ? 0u : 16u);
-                            }
-                        } else {
 #pragma unroll 4
-                            for (int rr = 0; rr < 16; ++rr) {
-                                const int32_t at = __shfl_sync(0xFFFFFFFFu, own, rr);
-                                const uint8_t* src = p.rows + (long long)max(at, 0) * kRowBytes + col * 2 + ch * 16;
-                                uint4 v = make_uint4(0, 0, 0, 0);
-                                if (at >= 0) v = __ldg(reinterpret_cast<const uint4*>(src));
-                                if (first + rr >= fewest)
-                                    v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                                 dst + rr * 128 + ((ch ^ (rr & 7)) << 4)),
-                                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                                             : "memory");
-                            }
-                        }
-                        sent(c);
+                    for (int rr = 0; rr < 16; ++rr) {
+                        const int32_t at = __shfl_sync(0xFFFFFFFFu, own, rr);
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (at >= 0) v = __ldg(reinterpret_cast<const uint4*>(src + (long long)at * kRowBytes));
+                        if (first + rr >= fewest)
+                            v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         dst + rr * 128 + ((ch ^ (rr & 7)) << 4)),
+                                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                                     : "memory");
                     }
                 }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) arrive_even(&vfull[c / kVPer]);
             }
         }
-        copy_wait<0>();
-        if (ok && flying > 1) post(b2);
-        if (ok && flying > 0) post(b1);
     } else if (warp == kFindWarp) {
         // ====================== the rows of the tiles ahead, and which are there ======================
-        // the entries are asked for a tile before their rows are: two loads that depend on each
-        // other take longer than a tile under way
-        bool more = w.next(p);
-        int i = w.i0, pos[4];
-        if (more)
+        // Three tiles are under way: entries asked for, pages asked for, rows handed on.  A load
+        // waits behind the copies for as long as a tile takes (one tile at a time, with its two
+        // loads one after the other: 2048 x 2048 selected 1353 us).
+        bool more = w.next(p), asked = false, paged = false;
+        int i = w.i0, e[4], b = 0, see = 0, id[4], off[4];
+        while (more || asked || paged) {
+            const bool ask = more;
+            int e2[4], b2 = 0, see2 = 0, id2[4], off2[4];
+            if (ask) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) pos[c] = entry(p, w.s, i * kTile + 32 * c + lane);
-        for (; more; ++g) {
-            const int b = w.s.b, see = w.s.see;
-            int32_t row[4];
+                for (int c = 0; c < 4; ++c) e2[c] = entry(p, w.s, i * kTile + 32 * c + lane);
+                b2 = w.s.b;
+                see2 = w.s.see;
+            }
+            if (asked) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                row[c] = pos[c] >= 0 && pos[c] < see ? (int32_t)paged_row(p.cache, b, pos[c]) : -1;
-            if (++i == w.i1) {
+                for (int c = 0; c < 4; ++c) {
+                    const unsigned at = (unsigned)e[c] / (unsigned)p.cache.page;
+                    off2[c] = e[c] - (int)(at * (unsigned)p.cache.page);
+                    id2[c] = e[c] >= 0 && e[c] < see
+                                 ? __ldg(p.cache.table + (long long)b * p.cache.width + at) : -1;
+                }
+            }
+            if (paged) {
+                int32_t row[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    row[c] = (unsigned)id[c] < (unsigned long long)p.cache.pages ? id[c] * p.cache.page + off[c] : -1;
+                // this CTA's 64 rows on their way to L2: they are copied a tile or two later
+                // (line by line: a bulk prefetch of a row takes its lane 90 clocks)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int32_t at = crank ? row[2 + c] : row[c];
+                    const uint8_t* r = p.rows + (long long)at * kRowBytes;
+                    if (at >= 0)
+#pragma unroll
+                        for (int k = 0; k < kRowBytes; k += 128)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(r + k) : "memory");
+                }
+                if (!wait_all(&rempty[g & 1u], ((g >> 1) & 1u) ^ 1u, abort)) { ok = false; break; }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    rowat[(g & 1u) * kTile + 32 * c + lane] = row[c];
+                    const uint32_t there = __ballot_sync(0xFFFFFFFFu, row[c] >= 0);
+                    // (its last reader was the softmax of four tiles ago: the copies that have read
+                    // the rows of two tiles ago had waited for the second product of four tiles ago)
+                    if (lane == 0) mask[(g & 3u) * 4 + c] = there;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&rfull[g & 1u]);
+                    mbar_arrive(&mfull[g & 3u]);
+                }
+                ++g;
+            }
+            if (ask && ++i == w.i1) {
                 more = w.next(p);
                 i = w.i0;
             }
-            if (more)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) pos[c] = entry(p, w.s, i * kTile + 32 * c + lane);
-            if (!wait_all(&rempty[g & 1u], ((g >> 1) & 1u) ^ 1u, abort)) { ok = false; break; }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                rowat[(g & 1u) * kTile + 32 * c + lane] = row[c];
-                const uint32_t there = __ballot_sync(0xFFFFFFFFu, row[c] >= 0);
-                // (its last reader was the softmax of four tiles ago: the copies that have read the
-                // rows of two tiles ago had waited for the second product of four tiles ago)
-                if (lane == 0) mask[(g & 3u) * 4 + c] = there;
+                e[c] = e2[c];
+                id[c] = id2[c];
+                off[c] = off2[c];
             }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&rfull[g & 1u]);
-                mbar_arrive(&mfull[g & 3u]);
-            }
+            b = b2;
+            see = see2;
+            paged = asked;
+            asked = ask;
         }
     } else if (warp == kQWarp) {
         // ================================== queries ==================================
@@ -476,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             __syncwarp();
             if (lane == 0) arrive_even(qfull);
         }
-    } else if (warp >= kMmaWarp && warp < kFindWarp) {
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ================================ UMMA issuers ================================
         // (the next block's barrier is looked at before a block is issued: a look takes 90 clocks)
         if (crank == 0) {
@@ -552,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             __syncwarp();
             mbar_wait(done, 0u, nullptr, 100000000ull);
         }
-    } else {
+    } else if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
         // ======================= softmax, rescaling and epilogue =======================
         const int L = (int)threadIdx.x, row = L & 63, half = L >> 6;
         const int gr = crank * 64 + row;
