@@ -23,13 +23,15 @@
 // lengths fill the device; a segment cut apart leaves partial sums (m, l, o in fp32) that a second
 // kernel joins in the order of the pairs: equal calls give equal bits.
 //
-// Warp roles (896 threads): warps 0..3 softmax, rescaling and epilogue (a thread is a row and half of
-// its positions or columns), 4 and 5 issue the two products' UMMAs (of the pair's even CTA; one warp
-// for both waits for barriers as long as the tensor cores work), 6 finds the rows of the tiles ahead,
-// 7 queries, 8..16 copy the K-major rows, a block of 64 columns each, 17..24 the MN-major columns, 16
-// positions each (16-byte asynchronous copies, so pages of any size and selected rows are alike;
-// absent rows are zeros).  A copying warp has one place in shared memory: it waits until that is
-// free, copies, waits for the data and announces it.  Every wait is bounded.
+// Warp roles (1024 threads): warps 0..7 softmax, rescaling and epilogue (a row's 128 positions are
+// four threads': TMEM lane half x half of its columns), 8 and 9 issue the two products' UMMAs (of the
+// pair's even CTA; one warp for both waits for barriers as long as the tensor cores work), 10
+// finds the rows of the tiles ahead, 11 queries, 12..20 copy the K-major rows, a block of 64 columns
+// each, 21..28 the MN-major columns, 16 positions each (16-byte asynchronous copies, so pages of any
+// size and selected rows are alike; absent rows are zeros).  A copying warp has one place in shared
+// memory: it waits until that is free, copies, waits for the data and announces it.  p goes
+// through two blocks of 64 positions that are freed and filled apart, so that the second product of
+// a tile follows on the last one's.  Every wait is bounded.
 #include <mutex>
 
 #include "launch.h"
@@ -45,29 +47,30 @@ constexpr int kWidth = 576, kLatent = 512;
 constexpr int kRowBytes = 2 * kWidth;
 constexpr int kTile = 128;                      // positions per tile
 constexpr int kRows = 128;                      // (token, head) rows of a pair
-constexpr int kSoftWarps = 4, kMmaWarp = 4, kFindWarp = 6, kQWarp = 7, kKWarp = 8;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kFindWarp = 10, kQWarp = 11, kKWarp = 12;
+constexpr int kSoftThreads = 32 * kSoftWarps;
 // Operand blocks are freed one by one (their copies take as long as a tile) and waited for in
 // groups (a wait costs the issuing warp more than a block's UMMAs take).
 constexpr int kKBlocks = 9, kKGroups = 3;       // 64 columns of this CTA's 64 positions
 constexpr int kVChunks = 8, kVGroups = 4;       // 16 positions, this CTA's 256 columns
 constexpr int kKPer = kKBlocks / kKGroups, kVPer = kVChunks / kVGroups;
 constexpr int kVWarp = kKWarp + kKBlocks, kEndWarp = kVWarp + kVChunks;
-constexpr int kThreads = 32 * 28;               // whole warpgroups
-constexpr int kLowRegs = 56, kHighRegs = 160;   // 160 * 128 + 56 * 768 <= 72 * 896
+constexpr int kThreads = 32 * 32;               // whole warpgroups
+constexpr int kLowRegs = 56, kHighRegs = 88;    // 88 * 256 + 56 * 768 = 64 * 1024
 
 constexpr int kQOff = 0, kQBlock = 64 * 128;    // 9 blocks of [64 rows x 64 columns]
 constexpr int kKOff = kQOff + 9 * kQBlock, kKBlock = 64 * 128;
 constexpr int kVOff = kKOff + kKBlocks * kKBlock, kVBlock = kTile * 128;  // 4 of [128 x 64 columns]
 constexpr int kPOff = kVOff + 4 * kVBlock, kPBlock = 64 * 128;  // 2 of [64 rows x 64 positions]
 constexpr int kBarOff = kPOff + 2 * kPBlock;
-// q full, q empty, o free, done, p full, pv done; s full, s free (2 each); k full, k empty; v full,
-// v empty; rows full, rows empty (2 each); masks (4)
-constexpr int kBars = 6 + 4 + kKGroups + kKBlocks + kVGroups + kVChunks + 4 + 4;
-constexpr int kXchOff = kBarOff + 8 * kBars;    // 128 floats: maxima, sums
-constexpr int kRowOff = kXchOff + 4 * 128;      // [2][128] rows of the cache
+// q full, q empty, o free, done, p free, pv done; p full, s full, s free (2 each); k full, k empty;
+// v full, v empty; rows full, rows empty (2 each); masks (4)
+constexpr int kBars = 6 + 6 + kKGroups + kKBlocks + kVGroups + kVChunks + 4 + 4;
+constexpr int kXchOff = kBarOff + 8 * kBars;    // a float per softmax thread: maxima, sums
+constexpr int kRowOff = kXchOff + 4 * kSoftThreads;      // [2][128] rows of the cache
 constexpr int kMaskOff = kRowOff + 2 * 4 * kTile;  // [4][4] words
-constexpr int kScanOff = kMaskOff + 64;         // 28 x int64
-constexpr int kSchedOff = kScanOff + 224;       // Start
+constexpr int kScanOff = kMaskOff + 64;         // 32 x int64
+constexpr int kSchedOff = kScanOff + 256;       // Start
 constexpr int kMiscOff = kSchedOff + 32;        // TMEM address, abort
 constexpr int kSmemBytes = kMiscOff + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -183,16 +186,16 @@ MOE_DEV float exp2_of(float x) {
     return y;
 }
 
-// Barrier of the 128 softmax threads: whether v holds for one of them.
+// Barrier of the softmax threads: whether v holds for one of them.
 MOE_DEV bool soft_any(bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred a, b;\n\t"
         "setp.ne.b32 a, %1, 0;\n\t"
-        "bar.red.or.pred b, 1, 128, a;\n\t"
+        "bar.red.or.pred b, 1, %2, a;\n\t"
         "selp.u32 %0, 1, 0, b;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "n"(kSoftThreads)
         : "memory");
     return r != 0;
 }
@@ -224,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
     uint64_t *qfull = bars, *qempty = bars + 1, *ofree = bars + 2, *done = bars + 3;
-    uint64_t *pfull = bars + 4, *pvdone = bars + 5, *sfull = bars + 6, *sfree = bars + 8;
-    uint64_t *kfull = bars + 10, *kempty = kfull + kKGroups;
+    uint64_t *pfree = bars + 4, *pvdone = bars + 5, *pfull = bars + 6, *sfull = bars + 8, *sfree = bars + 10;
+    uint64_t *kfull = bars + 12, *kempty = kfull + kKGroups;
     uint64_t *vfull = kempty + kKBlocks, *vempty = vfull + kVGroups;
     uint64_t *rfull = vempty + kVChunks, *rempty = rfull + 2, *mfull = rempty + 2;
     float* xch = reinterpret_cast<float*>(smem + kXchOff);
@@ -245,9 +248,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
         mbar_init(qempty, 1);
         mbar_init(ofree, 2 * kSoftWarps);
         mbar_init(done, 2);
-        mbar_init(pfull, 2 * kSoftWarps);
+        mbar_init(pfree, 1);
         mbar_init(pvdone, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&pfull[i], kSoftWarps);  // half of the warps of both CTAs
             mbar_init(&sfull[i], 1);
             mbar_init(&sfree[i], 2 * kSoftWarps);
             mbar_init(&rfull[i], 1);
@@ -530,11 +534,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                         const bool first = i == w.i0;
                         if (first && !(ok = wait_all(ofree, (n & 1u) ^ 1u, abort))) break;
                         bool here = mbar_test(&vfull[0], g & 1u);
-                        if (!(ok = wait_all(pfull, g & 1u, abort))) break;
+                        if (!(ok = wait_all(&pfull[0], g & 1u, abort))) break;
 #pragma unroll 1
                         for (int j = 0; j < kVGroups; ++j) {
                             if (!__all_sync(0xFFFFFFFFu, here) && !(ok = wait_all(&vfull[j], g & 1u, abort))) break;
                             if (j + 1 < kVGroups) here = mbar_test(&vfull[j + 1], g & 1u);
+                            if (j == kVGroups / 2 && !(ok = wait_all(&pfull[1], g & 1u, abort))) break;
                             tc_fence_after();
                             // 32 positions: half a block of p's columns, 4096 bytes of rows
                             const uint64_t da = dp + (uint64_t)((j >> 1) * (kPBlock / 16) + 4 * (j & 1));
@@ -549,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                                                        kIdescO, !first || j + c > 0);
                                     umma_commit_pair(&vempty[j * kVPer + c], 3);
                                 }
+                                if (j == kVGroups / 2 - 1) umma_commit_pair(pfree, 3);
                                 if (j == kVGroups - 1) umma_commit_pair(pvdone, 3);
                             }
                             __syncwarp();
@@ -563,104 +569,108 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     } else if (warp < kSoftWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
         // ======================= softmax, rescaling and epilogue =======================
-        const int L = (int)threadIdx.x, row = L & 63, half = L >> 6;
+        // thread: row, half of the tile's positions (TMEM lane >= 64), half of those (set)
+        const int L = (int)threadIdx.x, set = warp >> 2, lane128 = L & 127;
+        const int row = lane128 & 63, half = lane128 >> 6;
         const int gr = crank * 64 + row;
-        const uint32_t lane0 = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t lane0 = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        uint64_t* pgone = half ? pvdone : pfree;  // the last tile's p of this half has been read
         if (crank == 0 && L == 0) p.meta[2 * pair] = p.meta[2 * pair + 1] = make_int4(0, 0, 0, 0);
-        uint32_t n = 0;
-        for (; ok && w.next(p); ++n) {
+        const auto of_row = [&](float v, auto&& f) {  // f over the row's four threads
+            return f(f(v, xch[L ^ 64]), f(xch[L ^ 128], xch[L ^ 192]));
+        };
+        for (; ok && w.next(p);) {
             const bool live = gr < w.s.n * p.H;
             const int tok = w.s.t + gr / p.H, head = gr % p.H;
             const int see = !live ? 0 : p.inds ? w.s.len : seq_length(p.seq, tok);
             float m = -kInf, l = 0.0f;
             for (int i = w.i0; i < w.i1; ++i, ++g) {
                 const uint32_t b = g & 1u;
-                // (a warp whose wait gave up keeps to the barriers of the 128 threads until all know)
+                // (a warp whose wait gave up keeps to the softmax barriers until all know)
                 ok = ok && wait_all(&mfull[g & 3u], (g >> 2) & 1u, abort) &&
                      wait_all(&sfull[b], (g >> 1) & 1u, abort);
                 tc_fence_after();
-                float x[64];
+                float x[32];
                 {
-                    uint32_t v[32], u[32];
-                    tmem_ld32(lane0 + kSCol + 64 * b, v);
-                    tmem_ld32(lane0 + kSCol + 64 * b + 32, u);
+                    uint32_t v[32];
+                    tmem_ld32(lane0 + kSCol + 64 * b + 32 * set, v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        x[c] = __uint_as_float(v[c]) * p.scale;
-                        x[32 + c] = __uint_as_float(u[c]) * p.scale;
-                    }
+                    for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]) * p.scale;
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0 && ok) arrive_even(&sfree[b]);
-                const int left = see - i * kTile - half * 64;
-                const uint32_t m0 = mask[(g & 3u) * 4 + 2 * half] & low_bits(left);
-                const uint32_t m1 = mask[(g & 3u) * 4 + 2 * half + 1] & low_bits(left - 32);
-                if (!__all_sync(0xFFFFFFFFu, (m0 & m1) == 0xFFFFFFFFu)) {
+                const uint32_t bits = mask[(g & 3u) * 4 + 2 * half + set] &
+                                      low_bits(see - i * kTile - half * 64 - set * 32);
+                if (!__all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        if (!((m0 >> c) & 1u)) x[c] = -kInf;
-                        if (!((m1 >> c) & 1u)) x[32 + c] = -kInf;
-                    }
+                    for (int c = 0; c < 32; ++c)
+                        if (!((bits >> c) & 1u)) x[c] = -kInf;
                 }
-                float mx = x[0];
+                float mx = fmaxf(x[0], x[1]);
 #pragma unroll
-                for (int c = 1; c < 64; ++c) mx = fmaxf(mx, x[c]);
+                for (int c = 2; c < 32; ++c) mx = fmaxf(mx, x[c]);
                 if (soft_any(!ok || mx > m + kLag)) {
                     xch[L] = mx;
                     if (soft_any(!ok)) { ok = false; break; }
-                    mx = fmaxf(mx, xch[L ^ 64]);
+                    mx = of_row(mx, [](float u, float v) { return fmaxf(u, v); });
                     const float to = mx > m + kLag ? mx : m;
                     const float f = to == m ? 1.0f : exp2_of(m - to);
                     m = to;
                     l *= f;
-                    if (i > w.i0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
+                    if (i > w.i0) {
                         // o of the tiles so far; the next product waits for this tile's p
                         ok = wait_all(pvdone, (g & 1u) ^ 1u, abort);
-                        tc_fence_after();
+                        if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
+                            tc_fence_after();
 #pragma unroll 1
-                        for (uint32_t c = 0; c < 256; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(lane0 + c, o);
-                            tmem_ld_wait();
+                            for (uint32_t c = 128 * set; c < 128u * set + 128u; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(lane0 + c, o);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st16(lane0 + c, o);
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st16(lane0 + c, o);
+                            }
+                            tmem_st_wait();
+                            tc_fence_before();
                         }
-                        tmem_st_wait();
                     }
+                    // (nor may a warp hand over its p, or write its sum there, before the others are done)
+                    if (soft_any(!ok)) { ok = false; break; }
                 }
                 const float ref = m == -kInf ? 0.0f : m;
-                uint32_t pk[32];
+                uint32_t pk[16];
 #pragma unroll
-                for (int c = 0; c < 64; c += 2) {
+                for (int c = 0; c < 32; c += 2) {
                     const float p0 = exp2_of(x[c] - ref), p1 = exp2_of(x[c + 1] - ref);
                     l += p0 + p1;
                     pk[c / 2] = pack_bf16x2(p0, p1);
                 }
-                ok = ok && wait_all(pvdone, (g & 1u) ^ 1u, abort);  // the last tile's p has been read
+                ok = ok && wait_all(pgone, (g & 1u) ^ 1u, abort);
                 const uint32_t dst = smem_u32(smem + kPOff + half * kPBlock) + row * 128;
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((c ^ (row & 7)) << 4)),
+                for (int c = 0; c < 4; ++c)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     dst + (((4 * set + c) ^ (row & 7)) << 4)),
                                  "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
                                  : "memory");
                 fence_async_shared();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) arrive_even(pfull);
+                if (lane == 0 && ok) arrive_even(&pfull[half]);
             }
             ok = ok && wait_all(pvdone, (g - 1) & 1u, abort);
             xch[L] = l;
             if (soft_any(!ok)) { ok = false; break; }
-            l += xch[L ^ 64];
+            l = of_row(l, [](float u, float v) { return u + v; });
             tc_fence_after();
             const bool whole = w.begins() && w.ends();
             const int slot = 2 * pair + (w.begins() ? 1 : 0);
             float* part = p.part + (long long)slot * kPartFloats;
             const float f = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
-            if (live && half == 0) {
+            if (live && half == 0 && set == 0) {
                 if (whole) {
                     if (p.lse)
                         p.lse[(long long)tok * p.H + head] =
@@ -673,11 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             if (crank == 0 && L == 0 && !whole)
                 p.meta[slot] = make_int4(1, w.s.t, w.s.n, w.ends() ? 1 : 0);
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 16) {
+            for (int c = 0; c < 128; c += 16) {
                 uint32_t o[16];
-                tmem_ld16(lane0 + (uint32_t)c, o);
+                tmem_ld16(lane0 + (uint32_t)(128 * set + c), o);
                 tmem_ld_wait();
-                const int col = (c >> 7) * 256 + half * 128 + (c & 127);
+                const int col = set * 256 + half * 128 + c;
                 if (live && whole) {
                     uint32_t r[8];
 #pragma unroll
