@@ -21,12 +21,14 @@
 // Work is one list of tiles over all segments (up to 128 / H consecutive tokens of a sequence;
 // one token with a selection), cut into equal runs, one per pair, so that sequences of any
 // lengths fill the device; a segment cut apart leaves partial sums (m, l, o in fp32) that a second
-// kernel joins in the order of the pairs: equal calls give equal bits.
+// kernel joins in the order of the pairs: equal calls give equal bits.  Where whole segments give
+// a longest run that is no longer than an equal one and the cost of cutting (kCutTiles), runs are
+// whole segments.
 //
 // Warp roles (1024 threads): warps 0..7 softmax, rescaling and epilogue (a row's 128 positions are
 // four threads': TMEM lane half x half of its columns), 8 and 9 issue the two products' UMMAs (of the
 // pair's even CTA; one warp for both waits for barriers as long as the tensor cores work), 10
-// finds the rows of the tiles ahead, 11 queries, 12..20 copy the K-major rows, a block of 64 columns
+// finds the rows of the tiles ahead, 11 and 29..31 load the queries, 12..20 copy the K-major rows, a block of 64 columns
 // each, 21..28 the MN-major columns, 16 positions each (16-byte asynchronous copies, so pages of any
 // size and selected rows are alike; absent rows are zeros).  A copying warp has one place in shared
 // memory: it waits until that is free, copies, waits for the data and announces it.  p goes
@@ -55,6 +57,7 @@ constexpr int kKBlocks = 9, kKGroups = 3;       // 64 columns of this CTA's 64 p
 constexpr int kVChunks = 8, kVGroups = 4;       // 16 positions, this CTA's 256 columns
 constexpr int kKPer = kKBlocks / kKGroups, kVPer = kVChunks / kVGroups;
 constexpr int kVWarp = kKWarp + kKBlocks, kEndWarp = kVWarp + kVChunks;
+constexpr int kQWarps = 4;                      // kQWarp and those from kEndWarp on
 constexpr int kThreads = 32 * 32;               // whole warpgroups
 constexpr int kLowRegs = 56, kHighRegs = 88;    // 88 * 256 + 56 * 768 = 64 * 1024
 
@@ -71,9 +74,10 @@ constexpr int kRowOff = kXchOff + 4 * kSoftThreads;      // [2][128] rows of the
 constexpr int kMaskOff = kRowOff + 2 * 4 * kTile;  // [4][4] words
 constexpr int kScanOff = kMaskOff + 64;         // 32 x int64
 constexpr int kSchedOff = kScanOff + 256;       // Start
-constexpr int kMiscOff = kSchedOff + 32;        // TMEM address, abort
+constexpr int kMiscOff = kSchedOff + 32;        // TMEM address, abort, the peer's TMEM address
 constexpr int kSmemBytes = kMiscOff + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+static_assert(kThreads == 32 * (kEndWarp + kQWarps - 1), "every warp has a role");
 static_assert(kVPer == 2 && kVGroups == 4, "descriptors of the second product");
 
 constexpr uint32_t kSCol = 256;                 // TMEM columns: o 0..255, s 2 x 64
@@ -83,8 +87,15 @@ constexpr float kInf = __builtin_huge_valf();
 constexpr float kLag = 8.0f;                    // how far a score may pass the reference (base 2)
 
 constexpr int kMaxPairs = 76;
-constexpr int kMinTiles = 2;                    // tiles of a pair at least
-constexpr int kPartFloats = kRows * (kLatent + 2);  // o, m, l
+constexpr int kMinTiles = 1;                    // tiles of a pair at least
+// What cutting costs a call, in tiles: partial sums written (2 us) and joined (8 us).  64 segments of
+// 16 tiles on 76 pairs: 62 us cut into runs of 13 or 14 tiles, XX us whole.
+constexpr int kCutTiles = 6;
+// A piece's partial sums: o as the epilogue's warps hold it, in blocks of 32 rows x 16 columns
+// ([CTA][warp][8]), a block as [4][32 rows][4 columns], so that stores and the join's loads are whole
+// lines; then m and l of the 128 rows.
+constexpr int kBlockFloats = 32 * 16, kBlocks = kRows * kLatent / kBlockFloats;
+constexpr int kPartFloats = kRows * (kLatent + 2);
 
 struct Params {
     Paged cache;
@@ -104,8 +115,8 @@ struct Params {
 };
 
 struct Start {
-    int t, b, tile, pad;
-    long long left;
+    int t, b, tile, segments;  // (segments: at most so many)
+    long long left;            // tiles, at most
 };
 
 MOE_DEV void record_timeout(volatile int* abort) {
@@ -132,13 +143,14 @@ MOE_DEV Seg segment(const Params& p, int t, int b) {
 
 // The pieces of a pair's run, in order.
 struct Walk {
-    int t, b, tile;
+    int t, b, tile, segments;
     long long left;
     Seg s;
     int i0, i1;  // tiles of the piece
-    MOE_DEV Walk(const Start& st) : t(st.t), b(st.b), tile(st.tile), left(st.left) {}
+    MOE_DEV Walk(const Start& st) : t(st.t), b(st.b), tile(st.tile), segments(st.segments), left(st.left) {}
     MOE_DEV bool next(const Params& p) {
-        if (left <= 0) return false;
+        if (left <= 0 || segments <= 0) return false;
+        --segments;
         s = segment(p, t, b);
         i0 = tile;
         i1 = (int)min((long long)s.tiles, i0 + left);
@@ -146,7 +158,7 @@ struct Walk {
         tile = 0;
         t += s.n;
         if (!p.seq.cu) b = t;
-        else if (left > 0) while (b < p.seq.B - 1 && t >= seq_end(p.seq, b)) ++b;
+        else if (left > 0 && segments > 0) while (b < p.seq.B - 1 && t >= seq_end(p.seq, b)) ++b;
         return true;
     }
     MOE_DEV bool begins() const { return i0 == 0; }
@@ -234,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     float* xch = reinterpret_cast<float*>(smem + kXchOff);
     volatile int32_t* rowat = reinterpret_cast<volatile int32_t*>(smem + kRowOff);
     volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + kMaskOff);
-    long long* scan = reinterpret_cast<long long*>(smem + kScanOff);
+    unsigned long long* scan = reinterpret_cast<unsigned long long*>(smem + kScanOff);
+    int* tops = reinterpret_cast<int*>(smem + kXchOff);  // (before the softmax needs it)
     Start* sched = reinterpret_cast<Start*>(smem + kSchedOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
@@ -242,9 +255,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     const int crank = (int)cluster_rank(), pair = (int)(blockIdx.x >> 1);
 
     // ---- set-up ----
+    // tiles, segments (from bit 40 on) and the longest segment of this thread's tokens
+    const int tokens = seq_tokens(p.seq);
+    const int per = (tokens + kThreads - 1) / kThreads;
+    const int a = min(tokens, (int)threadIdx.x * per), z = min(tokens, a + per);
+    unsigned long long mine = 0;
+    int longest = 0;
+    for_segments(p, a, z, [&](const Seg& s) {
+        mine += (unsigned)s.tiles + (1ull << 40);
+        longest = max(longest, s.tiles);
+    });
     if (threadIdx.x == 0) {
         // the barriers that the issuer waits on are the even CTA's, with arrivals from both
-        mbar_init(qfull, 2);
+        mbar_init(qfull, 2 * kQWarps);
         mbar_init(qempty, 1);
         mbar_init(ofree, 2 * kSoftWarps);
         mbar_init(done, 2);
@@ -267,49 +290,94 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
         fence_mbar_init();
     }
     if (warp == kMmaWarp) tmem_alloc_pair(tmem_slot, 512);
-    // this pair's run of the list of tiles: a prefix sum over the tokens
-    {
-        const int tokens = seq_tokens(p.seq);
-        const int per = (tokens + kThreads - 1) / kThreads;
-        const int a = min(tokens, (int)threadIdx.x * per), z = min(tokens, a + per);
-        long long mine = 0;
-        for_segments(p, a, z, [&](const Seg& s) { mine += s.tiles; });
-        long long incl = mine;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) scan[warp] = incl;
-        __syncthreads();
-        long long before = incl - mine, total = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += scan[w];
-            total += scan[w];
-        }
-        const long long runs = max(1ll, min((long long)p.pairs, total / kMinTiles));
-        const long long lo = pair < runs ? total * pair / runs : 0;
-        const long long hi = pair < runs ? total * (pair + 1) / runs : 0;
-        if (lo < hi && before <= lo && lo < before + mine) {
-            long long at = before;
-            for_segments(p, a, z, [&](const Seg& s) {
-                if (at <= lo && lo < at + s.tiles) {
-                    sched->t = s.t;
-                    sched->b = s.b;
-                    sched->tile = (int)(lo - at);
-                    sched->left = hi - lo;
-                }
-                at += s.tiles;
-            });
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    cluster_sync();  // the peer's barriers are initialised and its TMEM allocated
+    // the pair's UMMAs address the same columns in both CTAs: each tells the other its address
+    if (threadIdx.x == 0)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(tmem_slot + 2, (uint32_t)(crank ^ 1))),
+                     "r"(tmem)
+                     : "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    // this pair's run of the list of tiles: a prefix sum over the tokens (tiles in the low 40 bits,
+    // segments above) and the longest segment
+    {
+        constexpr unsigned long long kTiles = (1ull << 40) - 1;
+        unsigned long long incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const int warp_longest = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)longest);
+        if (lane == 31) {
+            scan[warp] = incl;
+            tops[warp] = warp_longest;
+        }
+        __syncthreads();
+        if (__any_sync(0xFFFFFFFFu, a < z)) {  // (a few tokens are one warp's)
+            unsigned long long upto = scan[lane];
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const unsigned top = __reduce_max_sync(0xFFFFFFFFu, (unsigned)tops[lane]);
+            const unsigned long long all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+            const unsigned long long before =
+                (warp ? __shfl_sync(0xFFFFFFFFu, upto, max(warp, 1) - 1) : 0) + incl - mine;
+            const long long total = (long long)(all & kTiles);
+            const unsigned segs = (unsigned)(all >> 40), pairs = (unsigned)p.pairs;
+            // 32-bit divisions where they do (64-bit ones take a microsecond)
+            const bool small = total < (1 << 24);
+            const unsigned fair = small ? (unsigned)total / pairs : 0u;
+            const unsigned whole_runs = min(segs, pairs);
+            const unsigned longest_run = small ? (segs + pairs - 1) / pairs * top : 0xFFFFFFFFu;
+            const bool whole = small && longest_run <= fair + kCutTiles &&
+                               (segs <= pairs || (long long)top * segs == total);
+            long long lo = 0, hi = 0, mine0, mine1;
+            if (whole) {
+                if ((unsigned)pair < whole_runs) {
+                    lo = segs * (unsigned)pair / whole_runs;
+                    hi = segs * (unsigned)(pair + 1) / whole_runs;
+                }
+                mine0 = (long long)(before >> 40);
+                mine1 = (long long)((before + mine) >> 40);
+            } else {
+                if (small) {
+                    const unsigned runs = max(1u, min(pairs, (unsigned)total / kMinTiles));
+                    if ((unsigned)pair < runs) {
+                        lo = (unsigned)total * pair / runs;
+                        hi = (unsigned)total * (pair + 1) / runs;
+                    }
+                } else {
+                    lo = total * pair / pairs;
+                    hi = total * (pair + 1) / pairs;
+                }
+                mine0 = (long long)(before & kTiles);
+                mine1 = (long long)((before + mine) & kTiles);
+            }
+            if (lo < hi && mine0 <= lo && lo < mine1) {
+                long long at = mine0;
+                for_segments(p, a, z, [&](const Seg& s) {
+                    const int n = whole ? 1 : s.tiles;
+                    if (at <= lo && lo < at + n) {
+                        sched->t = s.t;
+                        sched->b = s.b;
+                        sched->tile = (int)(lo - at);
+                        sched->segments = whole ? (int)(hi - lo) : 0x7FFFFFFF;
+                        sched->left = whole ? 0x7FFFFFFFFFFFll : hi - lo;
+                    }
+                    at += n;
+                });
+            }
+        }
+    }
+    __syncthreads();
+    // the peer's barriers are initialised and its TMEM allocated
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     Start st = *sched;
-    if (ld_shared_cluster_u32(mapa_shared(tmem_slot, (uint32_t)(crank ^ 1))) != tmem) {
-        st.left = 0;  // the pair's UMMAs address the same columns in both CTAs
+    if (tmem_slot[2] != tmem) {
+        st.left = 0;
         if (threadIdx.x == 0) atomicCAS(&g_attention_status, 0u, kStatusPairTmem);
     }
     Walk w(st);
@@ -463,30 +531,41 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             paged = asked;
             asked = ask;
         }
-    } else if (warp == kQWarp) {
+    } else if (warp == kQWarp || warp >= kEndWarp) {
         // ================================== queries ==================================
-        uint32_t n = 0;
-        for (; ok && w.next(p); ++n) {
-            if (!wait_all(qempty, (n & 1u) ^ 1u, abort)) { ok = false; break; }
-            const uint32_t base = smem_u32(smem + kQOff);
-            const int rows = w.s.n * p.H;
-            const int sub = lane >> 3, ch = lane & 7;
-#pragma unroll 2
-            for (int r = 0; r < 64; r += 4) {
-                const int rr = r + sub, gr = crank * 64 + rr;
-                const bool live = gr < rows;
-                const uint16_t* src = p.q;
-                if (live) src += (w.s.t + gr / p.H) * p.q_token + (gr % p.H) * p.q_head;
-                const uint32_t dst = base + rr * 128 + ((ch ^ (rr & 7)) << 4);
+        const int r0 = 16 * (warp == kQWarp ? 0 : warp - kEndWarp + 1);  // of the CTA's 64 rows
+        const int sub = lane >> 3, ch = lane & 7;
+        const uint32_t dst = smem_u32(smem + kQOff) + (r0 + sub) * 128;
+        const auto row_of = [&](const Seg& q, int gr) {
+            return p.q + (q.t + gr / p.H) * p.q_token + (gr % p.H) * p.q_head;
+        };
+        bool more = w.next(p);
+        for (uint32_t n = 0; more; ++n) {
+            const Seg q = w.s;
+            more = w.next(p);
+            if (!(ok = wait_all(qempty, (n & 1u) ^ 1u, abort))) break;
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const int gr = crank * 64 + r0 + r + sub;
+                const bool live = gr < q.n * p.H;
+                const uint16_t* src = live ? row_of(q, gr) : p.q;
 #pragma unroll
                 for (int j = 0; j < 9; ++j)
-                    copy16(dst + j * kQBlock, src + j * 64 + ch * 8, live ? 16u : 0u);
+                    copy16(dst + r * 128 + ((ch ^ ((r + sub) & 7)) << 4) + j * kQBlock, src + j * 64 + ch * 8,
+                           live ? 16u : 0u);
             }
             copy_commit();
             copy_wait<0>();
             fence_async_shared();
             __syncwarp();
             if (lane == 0) arrive_even(qfull);
+            // the next piece's on their way to L2
+            if (more)
+                for (int i = lane; i < 16 * 9; i += 32) {
+                    const int gr = crank * 64 + r0 + i / 9;
+                    if (gr < w.s.n * p.H)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(w.s, gr) + i % 9 * 64) : "memory");
+                }
         }
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ================================ UMMA issuers ================================
@@ -682,27 +761,57 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             }
             if (crank == 0 && L == 0 && !whole)
                 p.meta[slot] = make_int4(1, w.s.t, w.s.n, w.ends() ? 1 : 0);
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(lane0 + (uint32_t)(128 * set + c), o);
-                tmem_ld_wait();
-                const int col = set * 256 + half * 128 + c;
-                if (live && whole) {
-                    uint32_t r[8];
+            // 32 rows of 64 bytes at a time through this warp's part of p's place (its last reader is
+            // done, its next writers are these warps), so that a store has 64 consecutive bytes of 8
+            // rows: a row per lane takes the stores four times as long
+            const uint32_t stage = smem_u32(smem + kPOff) + warp * 2048;
+            const int col0 = set * 256 + half * 128;
+            const int first = crank * 64 + (warp & 1) * 32;  // of the warp's rows
+            const int rows = w.s.n * p.H;
+            const long long out0 = (long long)w.s.t * p.H;
+            const auto put = [&](const uint32_t (&v)[16], int col) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        r[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
-                    uint4* d = reinterpret_cast<uint4*>(p.out + ((long long)tok * p.H + head) * kLatent + col);
-                    d[0] = make_uint4(r[0], r[1], r[2], r[3]);
-                    d[1] = make_uint4(r[4], r[5], r[6], r[7]);
-                } else if (live) {
-                    uint4* d = reinterpret_cast<uint4*>(part + gr * kLatent + col);
+                for (int k = 0; k < 4; ++k)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)),
+                                 "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
+                                 : "memory");
+                __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        d[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 8 * k + (lane >> 2);
+                    uint4 q;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                                 : "r"(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4))
+                                 : "memory");
+                    if (first + r < rows)
+                        *reinterpret_cast<uint4*>(p.out + (out0 + first + r) * kLatent + col + (lane & 3) * 8) = q;
                 }
                 __syncwarp();
+            };
+            if (whole) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t o[32], v[16];
+                    tmem_ld32(lane0 + (uint32_t)(128 * set + c), o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        v[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
+                    put(v, col0 + c);
+                }
+            } else {
+                uint4* at = reinterpret_cast<uint4*>(part + (crank * kSoftWarps + warp) * 8 * kBlockFloats) + lane;
+#pragma unroll 2
+                for (int c = 0; c < 128; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(lane0 + (uint32_t)(128 * set + c), o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        at[c * 8 + 32 * k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -722,10 +831,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
 }
 
 // Joins the pieces of the blockIdx.y-th segment that was cut apart: its first piece is the second
-// slot of some pair, the others the first slots of the pairs behind it.  A warp per row.
+// slot of some pair, the others the first slots of the pairs behind it.  A lane has a row of a block.
+// SPLIT 1: a warp takes a block and all its pieces, in their order.  SPLIT 8: eight warps share the
+// pieces of one block (warp w: w, w + 8, ..) and join their sums in the order of the warps; for
+// the few tokens whose pieces are many (one token of 4096 positions: 30 us with SPLIT 1, 20 with 8).
 constexpr int kJoinWarps = 4;
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p) {
-    __shared__ float weight[kJoinWarps][kMaxPairs + 1];
+constexpr int kJoinFew = 8;  // tokens up to which SPLIT is 8
+template <int SPLIT>
+__global__ void __launch_bounds__(SPLIT == 1 ? 32 * kJoinWarps : 32 * SPLIT) join_kernel(const Params p) {
+    __shared__ float held[SPLIT == 1 ? 1 : SPLIT][18][32];
     pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     int want = (int)blockIdx.y, owner = -1;
@@ -739,56 +853,77 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p) {
     }
     if (owner < 0) return;
     const int4 first = p.meta[2 * owner + 1];
-    int pieces = 1;
-    while (owner + pieces < p.pairs) {
-        const int4 m = p.meta[2 * (owner + pieces)];
-        if (!m.x) return;  // (a pair that gave up)
-        ++pieces;
-        if (m.w) break;
+    const int blk = SPLIT == 1 ? (int)blockIdx.x * kJoinWarps + w : (int)blockIdx.x;
+    const int warp = (blk >> 3) & (kSoftWarps - 1), quarter = warp & 3;
+    const int row = (blk >> 6) * 64 + (quarter & 1) * 32 + lane;
+    const int col = (warp >> 2) * 256 + (quarter >> 1) * 128 + (blk & 7) * 16;
+    // the pieces behind the first: up to the one that ends the segment
+    int pieces = 0;
+    for (int q = 1; owner + q < p.pairs && !pieces; q += 32) {
+        const bool in = owner + q + lane < p.pairs;
+        const int4 m = in ? p.meta[2 * (owner + q + lane)] : make_int4(0, 0, 0, 0);
+        const uint32_t last = __ballot_sync(0xFFFFFFFFu, m.x && m.w);
+        const uint32_t gone = __ballot_sync(0xFFFFFFFFu, !m.x);
+        const int e = last ? __ffs(last) - 1 : 32;
+        if (gone & low_bits(e)) return;  // (a pair gave up)
+        if (last) pieces = q + e + 1;
     }
-    const int row = (int)blockIdx.x * kJoinWarps + w;
-    if (row >= first.z * p.H) return;
-    const auto at = [&](int i) {
-        return p.part + (long long)(i == 0 ? 2 * owner + 1 : 2 * (owner + i)) * kPartFloats;
-    };
-    float m = -kInf;
-    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, at(i)[kRows * kLatent + row]);
+    if (!pieces || row - lane >= first.z * p.H) return;
+    const float* const p0 = p.part + (long long)(2 * owner + 1) * kPartFloats;
+    const float* const p1 = p.part + (long long)(2 * owner) * kPartFloats;  // + 2 i pieces for i > 0
+    const auto at = [&](int i) { return i == 0 ? p0 : p1 + (long long)(2 * i) * kPartFloats; };
+    // (one pass with a running maximum, so that all of a piece's loads go out at once)
+    float m = -kInf, l = 0.0f, acc[16];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    float l = 0.0f;
-    for (int i = lane; i < pieces; i += 32) {
-        const float mi = at(i)[kRows * kLatent + row];
-        const float f = mi == -kInf ? 0.0f : mi == m ? 1.0f : exp2_of(mi - m);
-        weight[w][i] = f;
-        const float li = at(i)[kRows * kLatent + kRows + row];
-        l += f * li;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    __syncwarp();
-    float4 acc[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c = 0; c < 16; ++c) acc[c] = 0.0f;
 #pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-        const float f = weight[w][i];
-        const float4* o = reinterpret_cast<const float4*>(at(i) + row * kLatent) + lane;
+    for (int i = SPLIT == 1 ? 0 : w; i < pieces; i += SPLIT) {
+        const float* const a = at(i);
+        const float mi = a[kRows * kLatent + row], li = a[kRows * kLatent + kRows + row];
+        const float4* o = reinterpret_cast<const float4*>(a + blk * kBlockFloats) + lane;
+        const float to = fmaxf(m, mi);
+        const float f = mi == -kInf ? 0.0f : mi == to ? 1.0f : exp2_of(mi - to);
+        const float g = m == to ? 1.0f : exp2_of(m - to);
+        m = to;
+        l = fmaf(f, li, l * g);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float4 v = o[32 * c];
-            acc[c].x = fmaf(f, v.x, acc[c].x);
-            acc[c].y = fmaf(f, v.y, acc[c].y);
-            acc[c].z = fmaf(f, v.z, acc[c].z);
-            acc[c].w = fmaf(f, v.w, acc[c].w);
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = o[32 * k];
+            acc[4 * k] = fmaf(f, v.x, acc[4 * k] * g);
+            acc[4 * k + 1] = fmaf(f, v.y, acc[4 * k + 1] * g);
+            acc[4 * k + 2] = fmaf(f, v.z, acc[4 * k + 2] * g);
+            acc[4 * k + 3] = fmaf(f, v.w, acc[4 * k + 3] * g);
         }
     }
-    const float f = l == 0.0f ? 0.0f : 1.0f / l;
-    const long long o = (long long)(first.y + row / p.H) * p.H + row % p.H;
-    uint2* d = reinterpret_cast<uint2*>(p.out + o * kLatent) + lane;
+    if constexpr (SPLIT > 1) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-        d[32 * c] = make_uint2(pack_bf16x2(acc[c].x * f, acc[c].y * f), pack_bf16x2(acc[c].z * f, acc[c].w * f));
-    if (p.lse && lane == 0) p.lse[o] = l == 0.0f ? -kInf : (m + log2f(l)) * 0.693147180559945f;
+        for (int c = 0; c < 16; ++c) held[w][c][lane] = acc[c];
+        held[w][16][lane] = m;
+        held[w][17][lane] = l;
+        __syncthreads();
+        if (w) return;
+        for (int k = 0; k < SPLIT; ++k) m = fmaxf(m, held[k][16][lane]);
+        l = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) acc[c] = 0.0f;
+        for (int k = 0; k < SPLIT; ++k) {
+            const float mi = held[k][16][lane];
+            const float f = mi == -kInf ? 0.0f : mi == m ? 1.0f : exp2_of(mi - m);
+            l = fmaf(f, held[k][17][lane], l);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) acc[c] = fmaf(f, held[k][c][lane], acc[c]);
+        }
+    }
+    if (row >= first.z * p.H) return;
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    const long long o = (long long)first.y * p.H + row;
+    uint32_t r[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) r[c] = pack_bf16x2(acc[2 * c] * f, acc[2 * c + 1] * f);
+    uint4* d = reinterpret_cast<uint4*>(p.out + o * kLatent + col);
+    d[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    d[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    if (p.lse && col == 0) p.lse[o] = l == 0.0f ? -kInf : (m + log2f(l)) * 0.693147180559945f;
 }
 
 }  // namespace
@@ -879,7 +1014,10 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t s) {
     const long long cut = a.T < a.pairs - 1 ? a.T : a.pairs - 1;  // segments that may be cut apart
-    return launch_kernel(join_kernel, dim3((unsigned)((kRows + kJoinWarps - 1) / kJoinWarps), (unsigned)cut),
+    if (a.T <= kJoinFew)
+        return launch_kernel(join_kernel<8>, dim3((unsigned)kBlocks, (unsigned)cut), dim3(32 * 8), 0, s,
+                             params_of(a, a.pairs));
+    return launch_kernel(join_kernel<1>, dim3((unsigned)(kBlocks / kJoinWarps), (unsigned)cut),
                          dim3(32 * kJoinWarps), 0, s, params_of(a, a.pairs));
 }
 
