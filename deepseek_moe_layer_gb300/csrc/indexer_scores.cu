@@ -8,13 +8,15 @@
 // and a token's scores leave as consecutive numbers.  A unit is `tt` consecutive tokens (up to 512
 // columns, in shared memory for the whole unit) and `kc` key tiles that stream past them; tokens
 // of several sequences in one unit are taken sequence by sequence, with the columns of that
-// sequence's tokens only.  Columns run in groups of up to 256 (whole tokens) through two TMEM
-// accumulators of 256, so the epilogue of one overlaps the UMMAs of the next.
+// sequence's tokens only.  Columns run in groups of up to 128 (whole tokens) through four TMEM
+// accumulators; two sets of four warps take every other one, so the epilogue (a maximum and half a
+// packed multiply-add per product) runs beside the UMMAs of the groups ahead.
 //
-// Warp roles (448 threads, one CTA per SM, persistent over units): warps 0..7 epilogue (warp % 4 =
-// TMEM lane quarter, warp / 4 takes every other token), 8..11 key copies (16-byte asynchronous
-// copies, so that pages of any size and any order do; rows without a page or behind the end are
-// zeros), 12 UMMA issuer, 13 queries and weights.  Every wait is bounded.
+// Warp roles (512 threads, one CTA per SM, persistent over units): warps 0..7 epilogue (warp % 4 =
+// TMEM lane quarter, warp / 4 = set), 8..11 key copies (16-byte asynchronous copies, so that
+// pages of any size and any order do; rows without a page or behind the end are zeros; the pages of
+// the tiles ahead are looked up two tiles early), 12 UMMA issuer, 13..15 queries and weights.  Every
+// wait is bounded.
 #include <mutex>
 
 #include "launch.h"
@@ -29,10 +31,11 @@ namespace {
 constexpr int kD = 128;             // columns of an index key
 constexpr int kKeys = 128;          // keys per tile
 constexpr int kCols = 512;          // (token, head) columns of a unit
-constexpr int kGroupCols = 256;     // of them per accumulator
-constexpr int kEpiWarps = 8, kLoadWarps = 4;
+constexpr int kAccCols = 128;       // of them per accumulator
+constexpr int kAccs = 4;
+constexpr int kEpiWarps = 8, kLoadWarps = 4, kQueryWarps = 3;
 constexpr int kMmaWarp = kEpiWarps + kLoadWarps, kQueryWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kQueryWarp + 1);
+constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 
 template <bool F8>
 struct Cfg {
@@ -42,11 +45,20 @@ struct Cfg {
     static constexpr int kStageBytes = kKeys * kRowBytes;
     static constexpr int kStages = F8 ? 8 : 3;
     static constexpr int kLag = F8 ? 4 : 1;                 // tiles in flight behind the newest
+    // Which keys of a tile are there, and their scales, for the epilogue: written before the tile is
+    // announced, read until its last accumulator is.  A place is taken again kRing tiles later, when
+    // the UMMAs of tile kRing - kStages behind are done, which had waited for all but kAccs of the
+    // accumulators before theirs.
+    static constexpr int kRing = F8 ? 16 : 8;
+    static_assert(kRing - kStages > kAccs, "the epilogue is done with a place that is taken again");
     static constexpr int kStageOff = kQBytes;
     static constexpr int kWOff = kStageOff + kStages * kStageBytes;
-    static constexpr int kBarOff = kWOff + 4 * kCols;
-    // full, empty, query full, query empty, accumulator full (2), empty (2), done
-    static constexpr int kBars = 2 * kStages + 2 + 4 + 1;
+    static constexpr int kLenOff = kWOff + 4 * kCols;       // a unit's lengths
+    static constexpr int kScaleOff = kLenOff + 4 * (kCols / 16);
+    static constexpr int kThereOff = kScaleOff + (F8 ? 4 * kKeys * kRing : 0);
+    static constexpr int kBarOff = kThereOff + 16 * kRing;
+    // full, empty, known (per place of the ring), query full, query empty, accumulator full, empty, done
+    static constexpr int kBars = 2 * kStages + kRing + 2 + 2 * kAccs + 1;
     static constexpr int kMiscOff = kBarOff + 8 * kBars;
     static constexpr int kSmemBytes = kMiscOff + 16;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -116,18 +128,68 @@ struct Unit {
     }
 };
 
+// The key tiles of a CTA's units, in order.
+struct Tiles {
+    long long u;
+    int tokens, c;
+    bool more;
+    Unit un;
+    Part r;
+    MOE_DEV Tiles(const Params& p, int tokens) : u(blockIdx.x), tokens(tokens), un(p, blockIdx.x, tokens) {
+        r.c0 = r.c1 = 0;
+        c = 0;
+        more = u < p.units;
+        step(p);
+    }
+    MOE_DEV void step(const Params& p) {  // to a tile, or to the end
+        while (more && c >= r.c1) {
+            if (un.part(p, r)) {
+                c = r.c0;
+            } else {
+                u += gridDim.x;
+                more = u < p.units;
+                if (more) un = Unit(p, u, tokens);
+            }
+        }
+    }
+    MOE_DEV void next(const Params& p) {
+        ++c;
+        step(p);
+    }
+};
+
+// sum += 16 products' maximum with 0 times their heads' weights.
+MOE_DEV void weigh16(const uint32_t* v, const float* w, float2& s0, float2& s1) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(w + e);
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[k] = __uint_as_float(v[e + k]);
+            asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(x[k]));
+        }
+        s0 = __ffma2_rn(make_float2(x[0], x[1]), make_float2(q.x, q.y), s0);
+        s1 = __ffma2_rn(make_float2(x[2], x[3]), make_float2(q.z, q.w), s1);
+    }
+}
+
 template <bool F8>
 __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     using C = Cfg<F8>;
     extern __shared__ __align__(1024) uint8_t smem[];
     float* wts = reinterpret_cast<float*>(smem + C::kWOff);
+    int* lens = reinterpret_cast<int*>(smem + C::kLenOff);
+    float* scales = reinterpret_cast<float*>(smem + C::kScaleOff);
+    uint32_t* there = reinterpret_cast<uint32_t*>(smem + C::kThereOff);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
     uint64_t* empty = full + C::kStages;
-    uint64_t* qfull = empty + C::kStages;
+    uint64_t* known = empty + C::kStages;
+    uint64_t* qfull = known + C::kRing;
     uint64_t* qempty = qfull + 1;
     uint64_t* afull = qfull + 2;
-    uint64_t* aempty = afull + 2;
-    uint64_t* done = aempty + 2;
+    uint64_t* aempty = afull + kAccs;
+    uint64_t* done = aempty + kAccs;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -137,11 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
             mbar_init(&full[s], kLoadWarps);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(qfull, 32);
+        for (int i = 0; i < C::kRing; ++i) mbar_init(&known[i], kLoadWarps);
+        mbar_init(qfull, 32 * kQueryWarps);
         mbar_init(qempty, 1 + kEpiWarps);  // the unit's last UMMA, and the weights read
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kAccs; ++i) {
             mbar_init(&afull[i], 1);
-            mbar_init(&aempty[i], kEpiWarps);
+            mbar_init(&aempty[i], kEpiWarps / 2);
         }
         mbar_init(done, 1);
         *abort = 0;
@@ -153,7 +216,13 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int tokens = seq_tokens(p.seq);
-    const int gtok = max(1, kGroupCols / p.Hp);  // tokens of an accumulator
+    const int gtok = kAccCols / p.Hp;  // tokens of an accumulator
+    bool ok = true;
+    const auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort))) return true;
+        if (lane == 0) record_timeout(abort);
+        return ok = false;
+    };
 
     if (warp >= kEpiWarps && warp < kMmaWarp) {
         // ================================ key copies ================================
@@ -161,77 +230,103 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         constexpr int kPer = C::kRowBytes / 16;   // 16-byte pieces of a row
         constexpr int kRows = 32 / kPer;          // rows that a warp copies at once
         uint32_t it = 0, posted = 0;              // tiles copied, tiles announced
-        bool ok = true;
         const auto post = [&] {
             fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[posted % C::kStages]);
             ++posted;
         };
-        for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-            Unit un(p, u, tokens);
-            Part r;
-            while (ok && un.part(p, r)) {
-                for (int c = r.c0; c < r.c1; ++c, ++it) {
-                    const uint32_t s = it % C::kStages;
-                    const int pos = c * kKeys + 32 * w + lane;
-                    const long long mine = pos < p.seq.most ? paged_row(p.keys, r.b, pos) : -1;
-                    if (!__all_sync(0xFFFFFFFFu,
-                                    mbar_test(&empty[s], ((it / C::kStages) & 1u) ^ 1u))) {
-                        // no slot yet: what has been asked for is announced before the wait
-                        copy_wait<0>();
-                        while (posted < it) post();
-                        if (!__all_sync(0xFFFFFFFFu,
-                                        mbar_wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u, abort))) {
-                            if (lane == 0) record_timeout(abort);
-                            ok = false;
-                            break;
-                        }
-                    }
-                    __syncwarp();
-                    const uint32_t st = smem_u32(smem + C::kStageOff + s * C::kStageBytes);
+        // a lane's row: the page is asked for two tiles, the scale one tile before the copy (each
+        // waits behind the copies for about as long as a tile takes)
+        Tiles ahead(p, tokens);
+        int id = -1, off = 0, id1 = -1, off1 = 0;
+        long long row = -1;
+        float ks = 0.0f;
+        bool has = false, has1 = false, has2 = false;
+        const auto ask = [&] {  // the next tile's page
+            id1 = -1;
+            has1 = ahead.more;
+            if (!ahead.more) return;
+            const int pos = ahead.c * kKeys + 32 * w + lane;
+            const unsigned at = (unsigned)pos / (unsigned)p.keys.page;
+            off1 = pos - (int)(at * (unsigned)p.keys.page);
+            if (pos < p.seq.most) id1 = __ldg(p.keys.table + (long long)ahead.r.b * p.keys.width + at);
+            ahead.next(p);
+        };
+        const auto shift = [&] {
+            has = has2;
+            has2 = has1;
+            row = (unsigned)id < (unsigned long long)p.keys.pages ? (long long)id * p.keys.page + off : -1;
+            if (F8 && has) ks = row >= 0 ? __ldg(p.ks + row) : 0.0f;
+            id = id1;
+            off = off1;
+            ask();
+        };
+        ask();
+        shift();
+        shift();
+        while (has) {
+            const uint32_t s = it % C::kStages, ring = it % C::kRing;
+            const long long mine = row;
+            const float scale = ks;
+            shift();
+            const bool last = !has;
+            if (!__all_sync(0xFFFFFFFFu, mbar_test(&empty[s], ((it / C::kStages) & 1u) ^ 1u))) {
+                // no slot yet: what has been asked for is announced before the wait
+                copy_wait<0>();
+                while (posted < it) post();
+                if (!wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u)) break;
+            }
+            const uint32_t st = smem_u32(smem + C::kStageOff + s * C::kStageBytes);
 #pragma unroll
-                    for (int i = 0; i < 32 / kRows; ++i) {
-                        const int rr = i * kRows + lane / kPer, piece = lane % kPer;
-                        const long long row = __shfl_sync(0xFFFFFFFFu, mine, rr);
-                        const int tr = 32 * w + rr;
-                        copy16(st + (piece / 8) * (kKeys * 128) + tr * 128 + (((piece & 7) ^ (tr & 7)) << 4),
-                               p.k + (row < 0 ? 0 : row) * C::kRowBytes + piece * 16, row < 0 ? 0u : 16u);
-                    }
-                    copy_commit();
-                    if (it - posted >= C::kLag) {
-                        copy_wait<C::kLag>();
-                        post();
-                    }
-                }
+            for (int i = 0; i < 32 / kRows; ++i) {
+                const int rr = i * kRows + lane / kPer, piece = lane % kPer;
+                const int at = (int)__shfl_sync(0xFFFFFFFFu, (int)mine, rr);
+                const int tr = 32 * w + rr;
+                copy16(st + (piece / 8) * (kKeys * 128) + tr * 128 + (((piece & 7) ^ (tr & 7)) << 4),
+                       p.k + (long long)max(at, 0) * C::kRowBytes + piece * 16, at < 0 ? 0u : 16u);
+            }
+            copy_commit();
+            if (F8) scales[ring * kKeys + 32 * w + lane] = scale;
+            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, mine >= 0);
+            __syncwarp();
+            if (lane == 0) {
+                there[ring * 4 + w] = bits;
+                mbar_arrive(&known[ring]);
+            }
+            ++it;
+            if (last) break;
+            if (it - posted > C::kLag) {
+                copy_wait<C::kLag>();
+                post();
             }
         }
         copy_wait<0>();
-        while (posted < it) post();
-    } else if (warp == kQueryWarp) {
+        while (ok && posted < it) post();
+    } else if (warp >= kQueryWarp) {
         // ============================ queries and weights ============================
+        const int tid = (int)threadIdx.x - 32 * kQueryWarp;
         uint32_t n = 0;
         for (long long u = blockIdx.x; u < p.units; u += gridDim.x, ++n) {
             Unit un(p, u, tokens);
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(qempty, (n & 1u) ^ 1u, abort))) {
-                if (lane == 0) record_timeout(abort);
-                break;
-            }
+            if (!wait(qempty, (n & 1u) ^ 1u)) break;
             const uint32_t base = smem_u32(smem);
             constexpr int kPer = C::kRowBytes / 16;
-            const int rows = (un.u1 - un.u0) * p.Hp;
-            for (int i = lane; i < rows * kPer; i += 32) {
-                const int rr = i / kPer, piece = i % kPer;
+            const int rows = max(0, un.u1 - un.u0) * p.Hp;
+            const int piece = tid % kPer;
+#pragma unroll 8
+            for (int rr = tid / kPer; rr < rows; rr += 32 * kQueryWarps / kPer) {
                 const int t = rr / p.Hp, h = rr % p.Hp;
                 const long long at = ((long long)(un.u0 + t) * p.H + (h < p.H ? h : 0)) * C::kRowBytes;
                 copy16(base + (piece / 8) * (kCols * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4),
                        p.q + at + piece * 16, h < p.H ? 16u : 0u);
             }
             copy_commit();
-            for (int i = lane; i < rows; i += 32) {
+            for (int i = tid; i < rows; i += 32 * kQueryWarps) {
                 const int t = i / p.Hp, h = i % p.Hp;
                 wts[i] = h < p.H ? __ldg(p.w + (long long)(un.u0 + t) * p.H + h) : 0.0f;
             }
+            for (int t = tid; t < un.u1 - un.u0; t += 32 * kQueryWarps) lens[t] = seq_length(p.seq, un.u0 + t);
             copy_wait<0>();
             fence_async_shared();
             mbar_arrive(qfull);
@@ -239,12 +334,6 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     } else if (warp == kMmaWarp) {
         // ================================ UMMA issuer ================================
         uint32_t it = 0, acc = 0, n = 0;
-        bool ok = true;
-        const auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-            if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort))) return true;
-            if (lane == 0) record_timeout(abort);
-            return ok = false;
-        };
         const uint64_t dq = sdesc_k128(smem_u32(smem)), dk = sdesc_k128(smem_u32(smem + C::kStageOff));
         for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++n) {
             Unit un(p, u, tokens);
@@ -253,11 +342,14 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
             while (ok && un.part(p, r)) {
                 for (int c = r.c0; c < r.c1 && ok; ++c, ++it) {
                     const uint32_t s = it % C::kStages;
+                    bool here = mbar_test(&aempty[acc & (kAccs - 1)], ((acc / kAccs) & 1u) ^ 1u);
                     if (!wait(&full[s], (it / C::kStages) & 1u)) break;
                     const uint64_t da = dk + (uint64_t)(s * (C::kStageBytes / 16));
-                    for (int t = r.t0; t < r.t1; t += gtok, ++acc) {
-                        const uint32_t ab = acc & 1u;
-                        if (!wait(&aempty[ab], ((acc >> 1) & 1u) ^ 1u)) break;
+                    for (int t = r.t0; t < r.t1; t += gtok) {
+                        const uint32_t ab = acc & (kAccs - 1);
+                        if (!__all_sync(0xFFFFFFFFu, here) && !wait(&aempty[ab], ((acc / kAccs) & 1u) ^ 1u)) break;
+                        ++acc;
+                        here = mbar_test(&aempty[acc & (kAccs - 1)], ((acc / kAccs) & 1u) ^ 1u);
                         tc_fence_after();
                         const int cols = min(gtok, r.t1 - t) * p.Hp;
                         const uint32_t idesc = C::kIdesc0 | ((uint32_t)(cols >> 3) << 17);
@@ -269,15 +361,14 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                                 for (int k = 0; k < 4; ++k) {
                                     const uint64_t a = da + (uint64_t)(blk * (kKeys * 128 / 16) + 2 * k);
                                     const uint64_t b = db + (uint64_t)(blk * (kCols * 128 / 16) + 2 * k);
-                                    if (F8) umma_f8(tmem + ab * kGroupCols, a, b, idesc, blk + k > 0);
-                                    else umma_bf16(tmem + ab * kGroupCols, a, b, idesc, blk + k > 0);
+                                    if (F8) umma_f8(tmem + ab * kAccCols, a, b, idesc, blk + k > 0);
+                                    else umma_bf16(tmem + ab * kAccCols, a, b, idesc, blk + k > 0);
                                 }
                             umma_commit(&afull[ab]);
+                            if (t + gtok >= r.t1) umma_commit(&empty[s]);
                         }
                         __syncwarp();
                     }
-                    if (ok && elect_lane()) umma_commit(&empty[s]);
-                    __syncwarp();
                 }
             }
             if (ok && elect_lane()) umma_commit(qempty);
@@ -288,58 +379,70 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         mbar_wait(done, 0u, nullptr, 100000000ull);
     } else {
         // ================================= epilogue =================================
-        const int quarter = warp & 3, set = warp >> 2;
+        const int quarter = warp & 3;
+        const uint32_t set = warp >> 2;
         const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16);
-        uint32_t acc = 0, n = 0;
-        bool ok = true;
+        uint32_t it = 0, acc = 0, n = 0;
         for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++n) {
             Unit un(p, u, tokens);
-            // (the weights are read behind this wait)
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(qfull, n & 1u, abort))) {
-                if (lane == 0) record_timeout(abort);
-                break;
-            }
+            if (!wait(qfull, n & 1u)) break;  // (the weights and lengths)
             Part r;
             while (ok && un.part(p, r)) {
-                for (int c = r.c0; c < r.c1 && ok; ++c) {
+                for (int c = r.c0; c < r.c1 && ok; ++c, ++it) {
                     const int pos = c * kKeys + quarter * 32 + lane;
-                    const long long row = pos < p.seq.most ? paged_row(p.keys, r.b, pos) : -1;
+                    const uint32_t ring = it % C::kRing;
+                    bool told = false, seen = false;
                     float ks = 1.0f;
-                    if (F8 && row >= 0) ks = __ldg(p.ks + row);
                     for (int t = r.t0; t < r.t1; t += gtok, ++acc) {
-                        const uint32_t ab = acc & 1u;
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&afull[ab], (acc >> 1) & 1u, abort))) {
-                            if (lane == 0) record_timeout(abort);
-                            ok = false;
-                            break;
+                        if ((acc & 1u) != set) continue;
+                        const uint32_t ab = acc & (kAccs - 1);
+                        if (!told) {
+                            if (!wait(&known[ring], (it / C::kRing) & 1u)) break;
+                            seen = pos < p.n && (there[ring * 4 + quarter] >> lane & 1u);
+                            if (F8) ks = scales[ring * kKeys + 32 * quarter + lane];
+                            told = true;
                         }
+                        if (!wait(&afull[ab], (acc / kAccs) & 1u)) break;
                         tc_fence_after();
                         const int cnt = min(gtok, r.t1 - t);
-                        for (int i = (int)((set + acc) & 1u); i < cnt; i += 2) {
-                            const uint32_t ta = taddr0 + ab * kGroupCols + (uint32_t)(i * p.Hp);
-                            const float* w = wts + (t + i - un.u0) * p.Hp;
-                            float sum = 0.0f;
-                            for (int h = 0; h < p.Hp; h += 16) {
-                                uint32_t v[16];
-                                tmem_ld16(ta + (uint32_t)h, v);
-                                float wv[16];
-#pragma unroll
-                                for (int e = 0; e < 16; e += 4)
-                                    *reinterpret_cast<float4*>(wv + e) =
-                                        *reinterpret_cast<const float4*>(w + h + e);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    float x = __uint_as_float(v[e]);
-                                    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(x));
-                                    sum = fmaf(x, wv[e], sum);
-                                }
-                            }
+                        const uint32_t ta = taddr0 + ab * kAccCols;
+                        const float* w = wts + (t - un.u0) * p.Hp;
+                        float* out = p.out + (long long)t * p.ld + pos;
+                        float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+                        int tok = 0, left = p.Hp;
+                        // 16 more columns of the token are summed: its score, if they were the last
+                        const auto summed = [&] {
+                            if ((left -= 16) > 0) return;
+                            const float sum = (s0.x + s0.y) + (s1.x + s1.y);
                             if (pos < p.n)
-                                p.out[(long long)(t + i) * p.ld + pos] =
-                                    row >= 0 && pos < seq_length(p.seq, t + i)
-                                        ? sum * ks
-                                        : -__int_as_float(0x7F800000);
+                                out[(long long)tok * p.ld] =
+                                    seen && pos < lens[t - un.u0 + tok] ? sum * ks : -__int_as_float(0x7F800000);
+                            s0 = s1 = make_float2(0.0f, 0.0f);
+                            left = p.Hp;
+                            ++tok;
+                        };
+                        // 32 columns at a time, the next ones on their way
+                        const int cols = cnt * p.Hp;
+                        uint32_t v[32], v1[32];
+                        tmem_ld32(ta, v);
+                        for (int k = 0; k < cols; k += 64) {
+                            tmem_ready(v);
+                            if (k + 32 < cols) tmem_ld32(ta + (uint32_t)(k + 32), v1);
+                            weigh16(v, w + k, s0, s1);
+                            summed();
+                            if (k + 16 < cols) {
+                                weigh16(v + 16, w + k + 16, s0, s1);
+                                summed();
+                            }
+                            if (k + 32 >= cols) break;
+                            tmem_ready(v1);
+                            if (k + 64 < cols) tmem_ld32(ta + (uint32_t)(k + 64), v);
+                            weigh16(v1, w + k + 32, s0, s1);
+                            summed();
+                            if (k + 48 < cols) {
+                                weigh16(v1 + 16, w + k + 48, s0, s1);
+                                summed();
+                            }
                         }
                         tc_fence_before();
                         __syncwarp();
@@ -394,10 +497,22 @@ cudaError_t run(const ScoresArgs& a, cudaStream_t s) {
     p.tt = kCols / p.Hp;
     if (avg < p.tt) p.tt = avg;
     const long long groups = (a.T + p.tt - 1) / p.tt;
-    // key tiles of a unit: eight units per SM where there are as many, so that sequences of
-    // different lengths even out, and no more than 64
-    long long kc = groups * p.tiles / (8 * num_sms());
-    p.kc = (int)(kc < 1 ? 1 : kc > 64 ? 64 : kc);
+    // key tiles of a unit: the number of rounds of units times their clocks, at the least (queries
+    // loaded, then 280 clocks per accumulator and tile, or what 128 keys take from HBM)
+    const int accs = (p.tt + kAccCols / p.Hp - 1) / (kAccCols / p.Hp);
+    const long long tile = accs * 280 > 3 * C::kRowBytes * 2 ? accs * 280 : 3 * C::kRowBytes * 2;
+    const long long query = p.tt * p.Hp > kAccCols ? 3000 + p.tt * p.Hp * C::kRowBytes / 32 : 300;
+    long long best = -1;
+    for (long long cuts = 1; cuts <= p.tiles && cuts <= 512; ++cuts) {
+        const long long kc = (p.tiles + cuts - 1) / cuts;
+        const long long units = groups * ((p.tiles + kc - 1) / kc);
+        const long long t = (units + num_sms() - 1) / num_sms() * (query + kc * tile);
+        // (as long, and more units: sequences of different lengths even out)
+        if (best < 0 || t <= best) {
+            best = t;
+            p.kc = (int)kc;
+        }
+    }
     p.units = groups * ((p.tiles + p.kc - 1) / p.kc);
     long long grid = num_sms();
     if (p.units < grid) grid = p.units;

@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                 {
                     uint32_t v[32];
                     tmem_ld32(lane0 + kSCol + 64 * b + 32 * set, v);
-                    tmem_ld_wait();
+                    tmem_ready(v);
 #pragma unroll
                     for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]) * p.scale;
                 }
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                             for (uint32_t c = 128 * set; c < 128u * set + 128u; c += 16) {
                                 uint32_t o[16];
                                 tmem_ld16(lane0 + c, o);
-                                tmem_ld_wait();
+                                tmem_ready(o);
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                                 tmem_st16(lane0 + c, o);
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                 for (int c = 0; c < 128; c += 32) {
                     uint32_t o[32], v[16];
                     tmem_ld32(lane0 + (uint32_t)(128 * set + c), o);
-                    tmem_ld_wait();
+                    tmem_ready(o);
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
                         v[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                 for (int c = 0; c < 128; c += 16) {
                     uint32_t o[16];
                     tmem_ld16(lane0 + (uint32_t)(128 * set + c), o);
-                    tmem_ld_wait();
+                    tmem_ready(o);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         at[c * 8 + 32 * k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
