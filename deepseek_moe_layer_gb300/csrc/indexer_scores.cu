@@ -9,13 +9,14 @@
 // columns, in shared memory for the whole unit) and `kc` key tiles that stream past them; tokens
 // of several sequences in one unit are taken sequence by sequence, with the columns of that
 // sequence's tokens only.  Columns run in groups of up to 128 (whole tokens) through four TMEM
-// accumulators; two sets of four warps take every other one, so the epilogue (a maximum and half a
-// packed multiply-add per product) runs beside the UMMAs of the groups ahead.
+// accumulators of four warps each, so that the epilogue (a maximum and half a packed
+// multiply-add per product) runs beside the UMMAs of the groups ahead and four of its warps share
+// a scheduler (two, with the next columns loaded ahead: 4096 x 16384 in 1288 us against XX).
 //
-// Warp roles (512 threads, one CTA per SM, persistent over units): warps 0..7 epilogue (warp % 4 =
-// TMEM lane quarter, warp / 4 = set), 8..11 key copies (16-byte asynchronous copies, so that
+// Warp roles (768 threads, one CTA per SM, persistent over units): warps 0..15 epilogue (warp % 4 =
+// TMEM lane quarter, warp / 4 = accumulator), 16..19 key copies (16-byte asynchronous copies, so that
 // pages of any size and any order do; rows without a page or behind the end are zeros; the pages of
-// the tiles ahead are looked up two tiles early), 12 UMMA issuer, 13..15 queries and weights.  Every
+// the tiles ahead are looked up two tiles early), 20 UMMA issuer, 21..23 queries and weights.  Every
 // wait is bounded.
 #include <mutex>
 
@@ -33,7 +34,7 @@ constexpr int kKeys = 128;          // keys per tile
 constexpr int kCols = 512;          // (token, head) columns of a unit
 constexpr int kAccCols = 128;       // of them per accumulator
 constexpr int kAccs = 4;
-constexpr int kEpiWarps = 8, kLoadWarps = 4, kQueryWarps = 3;
+constexpr int kEpiWarps = 4 * kAccs, kLoadWarps = 4, kQueryWarps = 3;
 constexpr int kMmaWarp = kEpiWarps + kLoadWarps, kQueryWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         mbar_init(qempty, 1 + kEpiWarps);  // the unit's last UMMA, and the weights read
         for (int i = 0; i < kAccs; ++i) {
             mbar_init(&afull[i], 1);
-            mbar_init(&aempty[i], kEpiWarps / 2);
+            mbar_init(&aempty[i], 4);
         }
         mbar_init(done, 1);
         *abort = 0;
@@ -380,73 +381,59 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     } else {
         // ================================= epilogue =================================
         const int quarter = warp & 3;
-        const uint32_t set = warp >> 2;
-        const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t mine = warp >> 2;  // its accumulator
+        const uint32_t ta0 = tmem + ((uint32_t)(quarter * 32) << 16) + mine * kAccCols;
         uint32_t it = 0, acc = 0, n = 0;
         for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++n) {
             Unit un(p, u, tokens);
             if (!wait(qfull, n & 1u)) break;  // (the weights and lengths)
             Part r;
             while (ok && un.part(p, r)) {
-                for (int c = r.c0; c < r.c1 && ok; ++c, ++it) {
+                const int accs = (r.t1 - r.t0 + gtok - 1) / gtok;  // of a tile
+                for (int c = r.c0; c < r.c1 && ok; ++c, ++it, acc += accs) {
                     const int pos = c * kKeys + quarter * 32 + lane;
                     const uint32_t ring = it % C::kRing;
-                    bool told = false, seen = false;
+                    bool seen = false;
                     float ks = 1.0f;
-                    for (int t = r.t0; t < r.t1; t += gtok, ++acc) {
-                        if ((acc & 1u) != set) continue;
-                        const uint32_t ab = acc & (kAccs - 1);
+                    // the tile's accumulators k with (acc + k) % kAccs == mine
+                    for (int k = (int)((mine - acc) & (kAccs - 1)), told = 0; k < accs; k += kAccs) {
                         if (!told) {
                             if (!wait(&known[ring], (it / C::kRing) & 1u)) break;
                             seen = pos < p.n && (there[ring * 4 + quarter] >> lane & 1u);
                             if (F8) ks = scales[ring * kKeys + 32 * quarter + lane];
-                            told = true;
+                            told = 1;
                         }
-                        if (!wait(&afull[ab], (acc / kAccs) & 1u)) break;
+                        if (!wait(&afull[mine], ((acc + k) / kAccs) & 1u)) break;
                         tc_fence_after();
-                        const int cnt = min(gtok, r.t1 - t);
-                        const uint32_t ta = taddr0 + ab * kAccCols;
+                        const int t = r.t0 + k * gtok, cnt = min(gtok, r.t1 - t);
                         const float* w = wts + (t - un.u0) * p.Hp;
                         float* out = p.out + (long long)t * p.ld + pos;
-                        float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-                        int tok = 0, left = p.Hp;
-                        // 16 more columns of the token are summed: its score, if they were the last
-                        const auto summed = [&] {
-                            if ((left -= 16) > 0) return;
+                        uint32_t ta = ta0;
+                        for (int i = 0; i < cnt; ++i, out += p.ld) {
+                            float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+                            int h = p.Hp;
+                            for (; h >= 32; h -= 32, ta += 32, w += 32) {
+                                uint32_t v[32];
+                                tmem_ld32(ta, v);
+                                tmem_ready(v);
+                                weigh16(v, w, s0, s1);
+                                weigh16(v + 16, w + 16, s0, s1);
+                            }
+                            if (h) {
+                                uint32_t v[16];
+                                tmem_ld16(ta, v);
+                                tmem_ready(v);
+                                weigh16(v, w, s0, s1);
+                                ta += 16;
+                                w += 16;
+                            }
                             const float sum = (s0.x + s0.y) + (s1.x + s1.y);
                             if (pos < p.n)
-                                out[(long long)tok * p.ld] =
-                                    seen && pos < lens[t - un.u0 + tok] ? sum * ks : -__int_as_float(0x7F800000);
-                            s0 = s1 = make_float2(0.0f, 0.0f);
-                            left = p.Hp;
-                            ++tok;
-                        };
-                        // 32 columns at a time, the next ones on their way
-                        const int cols = cnt * p.Hp;
-                        uint32_t v[32], v1[32];
-                        tmem_ld32(ta, v);
-                        for (int k = 0; k < cols; k += 64) {
-                            tmem_ready(v);
-                            if (k + 32 < cols) tmem_ld32(ta + (uint32_t)(k + 32), v1);
-                            weigh16(v, w + k, s0, s1);
-                            summed();
-                            if (k + 16 < cols) {
-                                weigh16(v + 16, w + k + 16, s0, s1);
-                                summed();
-                            }
-                            if (k + 32 >= cols) break;
-                            tmem_ready(v1);
-                            if (k + 64 < cols) tmem_ld32(ta + (uint32_t)(k + 64), v);
-                            weigh16(v1, w + k + 32, s0, s1);
-                            summed();
-                            if (k + 48 < cols) {
-                                weigh16(v1 + 16, w + k + 48, s0, s1);
-                                summed();
-                            }
+                                *out = seen && pos < lens[t - un.u0 + i] ? sum * ks : -__int_as_float(0x7F800000);
                         }
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&aempty[ab]);
+                        if (lane == 0) mbar_arrive(&aempty[mine]);
                     }
                 }
                 if (!ok) break;
