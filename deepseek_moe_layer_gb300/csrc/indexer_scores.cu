@@ -6,7 +6,7 @@
 // Keys lie on the tensor cores' M side (128 per tile) and (token, head) pairs on the N side: a
 // thread then holds one key's dot products with all heads, the sum over the heads is its own
 // and a token's scores leave as consecutive numbers.  A unit is `tt` consecutive tokens (up to 512
-// columns, in shared memory for the whole unit) and `kc` key tiles that stream past them; tokens
+// columns, of bf16 384, in shared memory for the whole unit) and `kc` key tiles that stream past them; tokens
 // of several sequences in one unit are taken sequence by sequence, with the columns of that
 // sequence's tokens only.  Columns run in groups of up to 128 (whole tokens) through four TMEM
 // accumulators of four warps each, so that the epilogue (a maximum and half a packed
@@ -15,8 +15,8 @@
 //
 // Warp roles (768 threads, one CTA per SM, persistent over units): warps 0..15 epilogue (warp % 4 =
 // TMEM lane quarter, warp / 4 = accumulator), 16..19 key copies (16-byte asynchronous copies, so that
-// pages of any size and any order do; rows without a page or behind the end are zeros; the pages of
-// the tiles ahead are looked up two tiles early), 20 UMMA issuer, 21..23 queries and weights.  Every
+// pages of any size and any order do; rows without a page or behind the end are zeros; a warp takes
+// every fourth tile, so that four are in flight, and looks its next one's pages up meanwhile), 20 UMMA issuer, 21..23 queries and weights.  Every
 // wait is bounded.
 #include <mutex>
 
@@ -31,7 +31,6 @@ namespace {
 
 constexpr int kD = 128;             // columns of an index key
 constexpr int kKeys = 128;          // keys per tile
-constexpr int kCols = 512;          // (token, head) columns of a unit
 constexpr int kAccCols = 128;       // of them per accumulator
 constexpr int kAccs = 4;
 constexpr int kEpiWarps = 4 * kAccs, kLoadWarps = 4, kQueryWarps = 3;
@@ -42,15 +41,16 @@ template <bool F8>
 struct Cfg {
     static constexpr int kRowBytes = F8 ? kD : 2 * kD;
     static constexpr int kBlocks = kRowBytes / 128;         // 128-byte blocks of a row
+    static constexpr int kCols = F8 ? 512 : 384;            // (token, head) columns of a unit
     static constexpr int kQBytes = kCols * kRowBytes;
     static constexpr int kStageBytes = kKeys * kRowBytes;
-    static constexpr int kStages = F8 ? 8 : 3;
-    static constexpr int kLag = F8 ? 4 : 1;                 // tiles in flight behind the newest
+    static constexpr int kStages = F8 ? 8 : 4;
+    static_assert(kStages % kLoadWarps == 0, "a stage is one warp's, so its waits are in order");
     // Which keys of a tile are there, and their scales, for the epilogue: written before the tile is
     // announced, read until its last accumulator is.  A place is taken again kRing tiles later, when
     // the UMMAs of tile kRing - kStages behind are done, which had waited for all but kAccs of the
     // accumulators before theirs.
-    static constexpr int kRing = F8 ? 16 : 8;
+    static constexpr int kRing = 16;
     static_assert(kRing - kStages > kAccs, "the epilogue is done with a place that is taken again");
     static constexpr int kStageOff = kQBytes;
     static constexpr int kWOff = kStageOff + kStages * kStageBytes;
@@ -197,10 +197,10 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&full[s], kLoadWarps);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int i = 0; i < C::kRing; ++i) mbar_init(&known[i], kLoadWarps);
+        for (int i = 0; i < C::kRing; ++i) mbar_init(&known[i], 1);
         mbar_init(qfull, 32 * kQueryWarps);
         mbar_init(qempty, 1 + kEpiWarps);  // the unit's last UMMA, and the weights read
         for (int i = 0; i < kAccs; ++i) {
@@ -227,83 +227,60 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
 
     if (warp >= kEpiWarps && warp < kMmaWarp) {
         // ================================ key copies ================================
-        const int w = warp - kEpiWarps;  // rows 32 w .. 32 w + 31 of a tile
         constexpr int kPer = C::kRowBytes / 16;   // 16-byte pieces of a row
         constexpr int kRows = 32 / kPer;          // rows that a warp copies at once
-        uint32_t it = 0, posted = 0;              // tiles copied, tiles announced
-        const auto post = [&] {
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[posted % C::kStages]);
-            ++posted;
-        };
-        // a lane's row: the page is asked for two tiles, the scale one tile before the copy (each
-        // waits behind the copies for about as long as a tile takes)
-        Tiles ahead(p, tokens);
-        int id = -1, off = 0, id1 = -1, off1 = 0;
-        long long row = -1;
-        float ks = 0.0f;
-        bool has = false, has1 = false, has2 = false;
-        const auto ask = [&] {  // the next tile's page
-            id1 = -1;
-            has1 = ahead.more;
-            if (!ahead.more) return;
-            const int pos = ahead.c * kKeys + 32 * w + lane;
-            const unsigned at = (unsigned)pos / (unsigned)p.keys.page;
-            off1 = pos - (int)(at * (unsigned)p.keys.page);
-            if (pos < p.seq.most) id1 = __ldg(p.keys.table + (long long)ahead.r.b * p.keys.width + at);
-            ahead.next(p);
-        };
-        const auto shift = [&] {
-            has = has2;
-            has2 = has1;
-            row = (unsigned)id < (unsigned long long)p.keys.pages ? (long long)id * p.keys.page + off : -1;
-            if (F8 && has) ks = row >= 0 ? __ldg(p.ks + row) : 0.0f;
-            id = id1;
-            off = off1;
-            ask();
-        };
-        ask();
-        shift();
-        shift();
-        while (has) {
-            const uint32_t s = it % C::kStages, ring = it % C::kRing;
-            const long long mine = row;
-            const float scale = ks;
-            shift();
-            const bool last = !has;
-            if (!__all_sync(0xFFFFFFFFu, mbar_test(&empty[s], ((it / C::kStages) & 1u) ^ 1u))) {
-                // no slot yet: what has been asked for is announced before the wait
-                copy_wait<0>();
-                while (posted < it) post();
-                if (!wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u)) break;
-            }
-            const uint32_t st = smem_u32(smem + C::kStageOff + s * C::kStageBytes);
+        const int piece = lane % kPer, sub = lane / kPer;
+        const uint32_t dst0 = (piece / 8) * (kKeys * 128) + sub * 128;
+        Tiles tile(p, tokens);
+        uint32_t it = 0;
+        for (; (int)it < warp - kEpiWarps && tile.more; ++it) tile.next(p);
+        int id[4], off[4];                        // page and row in it of the keys 32 k + lane
+        const auto ask = [&] {
 #pragma unroll
-            for (int i = 0; i < 32 / kRows; ++i) {
-                const int rr = i * kRows + lane / kPer, piece = lane % kPer;
-                const int at = (int)__shfl_sync(0xFFFFFFFFu, (int)mine, rr);
-                const int tr = 32 * w + rr;
-                copy16(st + (piece / 8) * (kKeys * 128) + tr * 128 + (((piece & 7) ^ (tr & 7)) << 4),
+            for (int k = 0; k < 4; ++k) {
+                const int pos = tile.c * kKeys + 32 * k + lane;
+                const unsigned at = (unsigned)pos / (unsigned)p.keys.page;
+                off[k] = pos - (int)(at * (unsigned)p.keys.page);
+                id[k] = pos < p.seq.most
+                            ? __ldg(p.keys.table + (long long)tile.r.b * p.keys.width + at) : -1;
+            }
+        };
+        if (tile.more) ask();
+        while (tile.more) {
+            const uint32_t s = it % C::kStages, ring = it % C::kRing;
+            int row[4];
+            float ks[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                row[k] = (unsigned)id[k] < (unsigned long long)p.keys.pages ? id[k] * p.keys.page + off[k] : -1;
+                if (F8) ks[k] = row[k] >= 0 ? __ldg(p.ks + row[k]) : 0.0f;
+            }
+            if (!wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u)) break;
+            const uint32_t st = smem_u32(smem + C::kStageOff + s * C::kStageBytes) + dst0;
+#pragma unroll
+            for (int i = 0; i < kKeys / kRows; ++i) {
+                const int at = __shfl_sync(0xFFFFFFFFu, row[i * kRows / 32], (i * kRows + sub) & 31);
+                copy16(st + i * kRows * 128 + (((piece & 7) ^ ((i * kRows + sub) & 7)) << 4),
                        p.k + (long long)max(at, 0) * C::kRowBytes + piece * 16, at < 0 ? 0u : 16u);
             }
             copy_commit();
-            if (F8) scales[ring * kKeys + 32 * w + lane] = scale;
-            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, mine >= 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (F8) scales[ring * kKeys + 32 * k + lane] = ks[k];
+                const uint32_t bits = __ballot_sync(0xFFFFFFFFu, row[k] >= 0);
+                if (lane == 0) there[ring * 4 + k] = bits;
+            }
             __syncwarp();
-            if (lane == 0) {
-                there[ring * 4 + w] = bits;
-                mbar_arrive(&known[ring]);
-            }
-            ++it;
-            if (last) break;
-            if (it - posted > C::kLag) {
-                copy_wait<C::kLag>();
-                post();
-            }
+            if (lane == 0) mbar_arrive(&known[ring]);
+            it += kLoadWarps;
+            for (int k = 0; k < kLoadWarps && tile.more; ++k) tile.next(p);
+            if (tile.more) ask();
+            copy_wait<0>();
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
         }
         copy_wait<0>();
-        while (ok && posted < it) post();
     } else if (warp >= kQueryWarp) {
         // ============================ queries and weights ============================
         const int tid = (int)threadIdx.x - 32 * kQueryWarp;
@@ -319,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
             for (int rr = tid / kPer; rr < rows; rr += 32 * kQueryWarps / kPer) {
                 const int t = rr / p.Hp, h = rr % p.Hp;
                 const long long at = ((long long)(un.u0 + t) * p.H + (h < p.H ? h : 0)) * C::kRowBytes;
-                copy16(base + (piece / 8) * (kCols * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4),
+                copy16(base + (piece / 8) * (C::kCols * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4),
                        p.q + at + piece * 16, h < p.H ? 16u : 0u);
             }
             copy_commit();
@@ -361,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     const uint64_t a = da + (uint64_t)(blk * (kKeys * 128 / 16) + 2 * k);
-                                    const uint64_t b = db + (uint64_t)(blk * (kCols * 128 / 16) + 2 * k);
+                                    const uint64_t b = db + (uint64_t)(blk * (C::kCols * 128 / 16) + 2 * k);
                                     if (F8) umma_f8(tmem + ab * kAccCols, a, b, idesc, blk + k > 0);
                                     else umma_bf16(tmem + ab * kAccCols, a, b, idesc, blk + k > 0);
                                 }
@@ -481,7 +458,7 @@ cudaError_t run(const ScoresArgs& a, cudaStream_t s) {
     p.tiles = (a.n + kKeys - 1) / kKeys;
     // tokens of a unit: what a sequence has on average, as far as the columns go
     const int avg = a.cu ? (int)((a.T + a.B - 1) / a.B) : 1;
-    p.tt = kCols / p.Hp;
+    p.tt = C::kCols / p.Hp;
     if (avg < p.tt) p.tt = avg;
     const long long groups = (a.T + p.tt - 1) / p.tt;
     // key tiles of a unit: the number of rounds of units times their clocks, at the least (queries
