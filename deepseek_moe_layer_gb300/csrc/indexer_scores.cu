@@ -16,7 +16,9 @@
 // Warp roles (768 threads, one CTA per SM, persistent over units): warps 0..15 epilogue (warp % 4 =
 // TMEM lane quarter, warp / 4 = accumulator), 16..19 key copies (16-byte asynchronous copies, so that
 // pages of any size and any order do; rows without a page or behind the end are zeros; a warp takes
-// every fourth tile, so that four are in flight, and looks its next one's pages up meanwhile), 20 UMMA issuer, 21..23 queries and weights.  Every
+// every fourth tile, so that four are in flight, and looks its next one's pages up meanwhile), 20 and 21 issue the UMMAs of
+// every other accumulator (an issuer's waits and commits take as long as the UMMAs), 22 and 23
+// queries and weights.  Every
 // wait is bounded.
 #include <mutex>
 
@@ -33,8 +35,8 @@ constexpr int kD = 128;             // columns of an index key
 constexpr int kKeys = 128;          // keys per tile
 constexpr int kAccCols = 128;       // of them per accumulator
 constexpr int kAccs = 4;
-constexpr int kEpiWarps = 4 * kAccs, kLoadWarps = 4, kQueryWarps = 3;
-constexpr int kMmaWarp = kEpiWarps + kLoadWarps, kQueryWarp = kMmaWarp + 1;
+constexpr int kEpiWarps = 4 * kAccs, kLoadWarps = 4, kMmaWarps = 2, kQueryWarps = 2;
+constexpr int kMmaWarp = kEpiWarps + kLoadWarps, kQueryWarp = kMmaWarp + kMmaWarps;
 constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 
 template <bool F8>
@@ -198,16 +200,16 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], kMmaWarps);
         }
         for (int i = 0; i < C::kRing; ++i) mbar_init(&known[i], 1);
         mbar_init(qfull, 32 * kQueryWarps);
-        mbar_init(qempty, 1 + kEpiWarps);  // the unit's last UMMA, and the weights read
+        mbar_init(qempty, kMmaWarps + kEpiWarps);  // the unit's last UMMAs, and the weights read
         for (int i = 0; i < kAccs; ++i) {
             mbar_init(&afull[i], 1);
             mbar_init(&aempty[i], 4);
         }
-        mbar_init(done, 1);
+        mbar_init(done, kMmaWarps);
         *abort = 0;
         fence_mbar_init();
     }
@@ -309,8 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
             fence_async_shared();
             mbar_arrive(qfull);
         }
-    } else if (warp == kMmaWarp) {
-        // ================================ UMMA issuer ================================
+    } else if (warp >= kMmaWarp) {
+        // ================================ UMMA issuers ================================
+        const uint32_t mine = warp - kMmaWarp;  // accumulators of this parity
         uint32_t it = 0, acc = 0, n = 0;
         const uint64_t dq = sdesc_k128(smem_u32(smem)), dk = sdesc_k128(smem_u32(smem + C::kStageOff));
         for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++n) {
@@ -318,35 +321,38 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
             if (!wait(qfull, n & 1u)) break;
             Part r;
             while (ok && un.part(p, r)) {
-                for (int c = r.c0; c < r.c1 && ok; ++c, ++it) {
+                const int accs = (r.t1 - r.t0 + gtok - 1) / gtok;  // of a tile
+                for (int c = r.c0; c < r.c1 && ok; ++c, ++it, acc += accs) {
                     const uint32_t s = it % C::kStages;
-                    bool here = mbar_test(&aempty[acc & (kAccs - 1)], ((acc / kAccs) & 1u) ^ 1u);
+                    int k = (int)((mine - acc) & (kMmaWarps - 1));
+                    bool here = mbar_test(&aempty[(acc + k) & (kAccs - 1)], (((acc + k) / kAccs) & 1u) ^ 1u);
                     if (!wait(&full[s], (it / C::kStages) & 1u)) break;
+                    tc_fence_after();
                     const uint64_t da = dk + (uint64_t)(s * (C::kStageBytes / 16));
-                    for (int t = r.t0; t < r.t1; t += gtok) {
-                        const uint32_t ab = acc & (kAccs - 1);
-                        if (!__all_sync(0xFFFFFFFFu, here) && !wait(&aempty[ab], ((acc / kAccs) & 1u) ^ 1u)) break;
-                        ++acc;
-                        here = mbar_test(&aempty[acc & (kAccs - 1)], ((acc / kAccs) & 1u) ^ 1u);
+                    for (; k < accs; k += kMmaWarps) {
+                        const uint32_t a1 = acc + k, ab = a1 & (kAccs - 1), a2 = a1 + kMmaWarps;
+                        if (!__all_sync(0xFFFFFFFFu, here) && !wait(&aempty[ab], ((a1 / kAccs) & 1u) ^ 1u)) break;
+                        here = mbar_test(&aempty[a2 & (kAccs - 1)], ((a2 / kAccs) & 1u) ^ 1u);
                         tc_fence_after();
-                        const int cols = min(gtok, r.t1 - t) * p.Hp;
+                        const int t = r.t0 + k * gtok, cols = min(gtok, r.t1 - t) * p.Hp;
                         const uint32_t idesc = C::kIdesc0 | ((uint32_t)(cols >> 3) << 17);
                         const uint64_t db = dq + (uint64_t)((t - un.u0) * p.Hp * 8);
                         if (elect_lane()) {
 #pragma unroll
                             for (int blk = 0; blk < C::kBlocks; ++blk)
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const uint64_t a = da + (uint64_t)(blk * (kKeys * 128 / 16) + 2 * k);
-                                    const uint64_t b = db + (uint64_t)(blk * (C::kCols * 128 / 16) + 2 * k);
-                                    if (F8) umma_f8(tmem + ab * kAccCols, a, b, idesc, blk + k > 0);
-                                    else umma_bf16(tmem + ab * kAccCols, a, b, idesc, blk + k > 0);
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint64_t a = da + (uint64_t)(blk * (kKeys * 128 / 16) + 2 * e);
+                                    const uint64_t b = db + (uint64_t)(blk * (C::kCols * 128 / 16) + 2 * e);
+                                    if (F8) umma_f8(tmem + ab * kAccCols, a, b, idesc, blk + e > 0);
+                                    else umma_bf16(tmem + ab * kAccCols, a, b, idesc, blk + e > 0);
                                 }
                             umma_commit(&afull[ab]);
-                            if (t + gtok >= r.t1) umma_commit(&empty[s]);
                         }
                         __syncwarp();
                     }
+                    if (ok && elect_lane()) umma_commit(&empty[s]);
+                    __syncwarp();
                 }
             }
             if (ok && elect_lane()) umma_commit(qempty);
