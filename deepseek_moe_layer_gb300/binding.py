@@ -192,8 +192,10 @@ def _empty(shape, dtype, device, stream, returned=True):
     one's pool hands out may still be in use there by work queued before.  A result that is
     `returned` is also marked as used by the caller's stream, so that its memory is not written
     again before what the caller does with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     stream = _torch_stream(stream)
-    if stream is None or stream.device != device:
+    if stream.device != device:
         return torch.empty(shape, dtype=dtype, device=device)
     caller = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
@@ -460,6 +462,14 @@ def indexer_topk(scores, k, lengths=None, want_mask=False, inds=None, mask=None,
     return (inds, mask) if want_mask else inds
 
 
+def _fits(t, dtype, shape, dev):
+    """Whether t is a contiguous tensor of this type, shape and device (an index; -1: the host).  The
+    calls below ask this first and look for what is wrong only where it is not so: a check by
+    check costs a call as much as its launch."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous())
+
+
 def _need_vector(t, dtype, name, n, device):
     _need(t, dtype, name, device)
     if t.shape != (n,):
@@ -476,76 +486,86 @@ def cache_append(x, slots, cache, scales=None, norm_weight=None, norm_bias=None,
     positions (int32 [T]) * inv_freq (fp32), in pairs of neighbours (interleaved) or of halves.
     q bf16 [T, H, 2 len(inv_freq)] (tokens and heads may be strided) is rotated too, into q_out (a new
     tensor, or given: q itself, a slice of wider queries).  Returns cache, or (cache, q_out) with q."""
-    if x.dtype != torch.bfloat16:
+    if x.dtype is not torch.bfloat16:
         raise TypeError(f"x: dtype {x.dtype}, expected {torch.bfloat16}")
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x must be [T, W] with unit stride along W")
     T, W = x.shape
-    dev = x.device
-    _need_vector(slots, torch.int64, "slots", T, dev)
+    dev = x.get_device()
+    if not _fits(slots, torch.int64, (T,), dev):
+        _need_vector(slots, torch.int64, "slots", T, x.device)
     if cache.dim() != 3 or cache.shape[2] != W:
         raise ValueError(f"cache must be [pages, page, {W}], not {tuple(cache.shape)}")
-    _need(cache, torch.bfloat16 if scales is None else torch.float8_e4m3fn, "cache", dev)
+    pages, page, _ = cache.shape
+    _need(cache, torch.bfloat16 if scales is None else torch.float8_e4m3fn, "cache", x.device)
     if scales is not None:
-        _need_out(scales, torch.float32, "scales", (*cache.shape[:2], W // 128), dev)
-    a = AppendArgs()
-    a.x, a.T, a.W, a.ldx = x.data_ptr(), T, W, x.stride(0) if T > 1 else W
-    a.slots, a.cache, a.rows = slots.data_ptr(), cache.data_ptr(), cache.shape[0] * cache.shape[1]
-    a.scales = None if scales is None else scales.data_ptr()
+        _need_out(scales, torch.float32, "scales", (pages, page, W // 128), x.device)
+    n = R = at = 0
+    weight = bias = pos = freq = None
     if norm_weight is not None:
-        a.norm_cols, a.eps = norm_weight.numel(), eps
-        _need_vector(norm_weight, torch.float32, "norm_weight", a.norm_cols, dev)
-        a.norm_weight = norm_weight.data_ptr()
+        n = norm_weight.numel()
+        if not _fits(norm_weight, torch.float32, (n,), dev):
+            _need_vector(norm_weight, torch.float32, "norm_weight", n, x.device)
+        weight = norm_weight.data_ptr()
         if norm_bias is not None:
-            _need_vector(norm_bias, torch.float32, "norm_bias", a.norm_cols, dev)
-            a.norm_bias = norm_bias.data_ptr()
+            if not _fits(norm_bias, torch.float32, (n,), dev):
+                _need_vector(norm_bias, torch.float32, "norm_bias", n, x.device)
+            bias = norm_bias.data_ptr()
     elif norm_bias is not None:
         raise ValueError("norm_bias given without norm_weight")
     if inv_freq is not None:
-        R = 2 * inv_freq.numel()
-        _need_vector(inv_freq, torch.float32, "inv_freq", R // 2, dev)
+        half = inv_freq.numel()
+        if not _fits(inv_freq, torch.float32, (half,), dev):
+            _need_vector(inv_freq, torch.float32, "inv_freq", half, x.device)
         if positions is None:
             raise ValueError("inv_freq given without positions")
-        _need_vector(positions, torch.int32, "positions", T, dev)
-        a.positions, a.inv_freq = positions.data_ptr(), inv_freq.data_ptr()
-        a.rope_cols, a.rope_at, a.interleaved = R, rope_at, int(bool(interleaved))
+        if not _fits(positions, torch.int32, (T,), dev):
+            _need_vector(positions, torch.int32, "positions", T, x.device)
+        R, at, pos, freq = 2 * half, rope_at, positions.data_ptr(), inv_freq.data_ptr()
+    H, src, dst, st = 0, None, None, (0, 0, 0, 0)
     if q is not None:
         if inv_freq is None:
             raise ValueError("q given without inv_freq")
         if q_out is None:
-            q_out = _empty(q.shape, torch.bfloat16, dev, stream)
+            q_out = _empty(q.shape, torch.bfloat16, x.device, stream)
         for t, name in ((q, "q"), (q_out, "q_out")):
-            if t.dtype != torch.bfloat16:
+            if t.dtype is not torch.bfloat16:
                 raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
-            if t.dim() != 3 or t.shape[0] != T or t.shape[2] != R or t.stride(2) != 1 or \
-                    t.shape[1] != q.shape[1]:
+            if t.dim() != 3 or t.shape != (T, q.shape[1], R) or t.stride(2) != 1:
                 raise ValueError(f"{name} must be [{T}, H, {R}] with unit stride along its columns")
-            if t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, expected {dev}")
-        a.q, a.q_out, a.H = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+        H, src, dst = q.shape[1], q.data_ptr(), q_out.data_ptr()
         # (the stride of an axis of one is arbitrary)
-        a.q_token, a.q_head = (q.stride(i) if q.shape[i] > 1 else 0 for i in (0, 1))
-        a.q_out_token, a.q_out_head = (q_out.stride(i) if q.shape[i] > 1 else 0 for i in (0, 1))
+        (q0, q1, _), (o0, o1, _) = q.stride(), q_out.stride()
+        st = (q0 if T > 1 else 0, q1 if H > 1 else 0, o0 if T > 1 else 0, o1 if H > 1 else 0)
     elif q_out is not None:
         raise ValueError("q_out given without q")
+    a = AppendArgs(x.data_ptr(), T, x.stride(0) if T > 1 else W, W, slots.data_ptr(),
+                   cache.data_ptr(), None if scales is None else scales.data_ptr(), pages * page,
+                   weight, bias, n, eps, pos, freq, R, at, int(bool(interleaved)), src, dst, H, *st)
     _check((_lib or lib()).moe_cache_append(ctypes.byref(a), _raw_stream(x, stream)))
     return cache if q is None else (cache, q_out)
 
 
-def _paged_cache(rows, dtype, name, width, table, lengths, cu_tokens, T, dev):
+def _paged_cache(rows, dtype, name, width, table, lengths, cu_tokens, T, device, dev):
     if rows.dim() != 3 or rows.shape[2] != width:
         raise ValueError(f"{name} must be [pages, page, {width}], not {tuple(rows.shape)}")
-    _need(rows, dtype, name, dev)
+    pages, page, _ = rows.shape
+    if not _fits(rows, dtype, (pages, page, width), dev):
+        _need(rows, dtype, name, device)
     if table.dim() != 2:
         raise ValueError("block_table must be [sequences, pages]")
-    _need(table, torch.int32, "block_table", dev)
-    _need_vector(lengths, torch.int32, "lengths", T, dev)
+    B, wide = table.shape
+    if not _fits(table, torch.int32, (B, wide), dev):
+        _need(table, torch.int32, "block_table", device)
+    if not _fits(lengths, torch.int32, (T,), dev):
+        _need_vector(lengths, torch.int32, "lengths", T, device)
     if cu_tokens is not None:
-        _need_vector(cu_tokens, torch.int32, "cu_tokens", table.shape[0] + 1, dev)
-    elif table.shape[0] != T:
-        raise ValueError(f"block_table has {table.shape[0]} rows for {T} tokens, and cu_tokens is None")
-    return PagedCache(rows.data_ptr(), rows.shape[0], rows.shape[1], table.data_ptr(),
-                      table.shape[0], table.shape[1])
+        _need_vector(cu_tokens, torch.int32, "cu_tokens", B + 1, device)
+    elif B != T:
+        raise ValueError(f"block_table has {B} rows for {T} tokens, and cu_tokens is None")
+    return PagedCache(rows.data_ptr(), pages, page, table.data_ptr(), B, wide)
 
 
 def indexer_scores(q, weights, keys, block_table, lengths, n, key_scales=None, cu_tokens=None,
@@ -558,27 +578,32 @@ def indexer_scores(q, weights, keys, block_table, lengths, n, key_scales=None, c
     dtype = torch.bfloat16 if key_scales is None else torch.float8_e4m3fn
     if q.dim() != 3 or q.shape[2] != 128:
         raise ValueError(f"q must be [T, H, 128], not {tuple(q.shape)}")
-    _need(q, dtype, "q")
-    T, H, dev = q.shape[0], q.shape[1], q.device
-    _need_out(weights, torch.float32, "weights", (T, H), dev)
-    c = _paged_cache(keys, dtype, "keys", 128, block_table, lengths, cu_tokens, T, dev)
+    T, H, _ = q.shape
+    device, dev = q.device, q.get_device()
+    if not _fits(q, dtype, (T, H, 128), dev):
+        _need(q, dtype, "q")
+    if not _fits(weights, torch.float32, (T, H), dev):
+        _need_out(weights, torch.float32, "weights", (T, H), device)
+    c = _paged_cache(keys, dtype, "keys", 128, block_table, lengths, cu_tokens, T, device, dev)
     if key_scales is not None:
-        _need(key_scales, torch.float32, "key_scales", dev)
+        _need(key_scales, torch.float32, "key_scales", device)
         if key_scales.shape not in (keys.shape[:2], (*keys.shape[:2], 1)):
             raise ValueError(f"key_scales must be {(*keys.shape[:2], 1)}, not {tuple(key_scales.shape)}")
+        key_scales = key_scales.data_ptr()
     n = int(n)
     if out is None:
-        out = _empty((T, n), torch.float32, dev, stream)
+        out = _empty((T, n), torch.float32, device, stream)
+        ld = n
     else:
-        if out.dtype != torch.float32:
+        if out.dtype is not torch.float32:
             raise TypeError(f"out: dtype {out.dtype}, expected {torch.float32}")
-        if out.shape != (T, n) or (n > 1 and out.stride(1) != 1) or out.device != dev:
-            raise ValueError(f"out must be [{T}, {n}] on {dev} with unit stride along its rows")
+        if out.shape != (T, n) or (n > 1 and out.stride(1) != 1) or out.get_device() != dev:
+            raise ValueError(f"out must be [{T}, {n}] on {device} with unit stride along its rows")
+        ld = out.stride(0) if T > 1 else n
     _check((_lib or lib()).moe_indexer_scores(
-        q.data_ptr(), weights.data_ptr(), T, H, ctypes.byref(c),
-        None if key_scales is None else key_scales.data_ptr(),
+        q.data_ptr(), weights.data_ptr(), T, H, ctypes.byref(c), key_scales,
         None if cu_tokens is None else cu_tokens.data_ptr(), lengths.data_ptr(), n, out.data_ptr(),
-        out.stride(0) if T > 1 else n, _raw_stream(q, stream)))
+        ld, _raw_stream(q, stream)))
     return out
 
 
@@ -589,34 +614,36 @@ def latent_attention(q, cache, block_table, lengths, scale, inds=None, cu_tokens
     (positions each token may see), cu_tokens int32 [B + 1] or None for one token per sequence, inds int32
     [T, k] (selected positions, as indexer_topk gives them) or None for all -> bf16 [T, H, 512], and
     with want_lse also the fp32 [T, H] log-sum-exp of the scaled scores."""
-    if q.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16:
         raise TypeError(f"q: dtype {q.dtype}, expected {torch.bfloat16}")
     if q.dim() != 3 or q.shape[2] != 576 or q.stride(2) != 1:
         raise ValueError(f"q must be [T, H, 576] with unit stride along its columns, not {tuple(q.shape)}")
-    T, H, dev = q.shape[0], q.shape[1], q.device
-    c = _paged_cache(cache, torch.bfloat16, "cache", 576, block_table, lengths, cu_tokens, T, dev)
-    k = 0
+    T, H, _ = q.shape
+    device, dev = q.device, q.get_device()
+    c = _paged_cache(cache, torch.bfloat16, "cache", 576, block_table, lengths, cu_tokens, T, device, dev)
+    k, chosen = 0, None
     if inds is not None:
         if inds.dim() != 2 or inds.shape[0] != T:
             raise ValueError(f"inds must be [{T}, k], not {tuple(inds.shape)}")
-        _need(inds, torch.int32, "inds", dev)
-        k = inds.shape[1]
+        _need(inds, torch.int32, "inds", device)
+        k, chosen = inds.shape[1], inds.data_ptr()
     if out is None:
-        out = _empty((T, H, 512), torch.bfloat16, dev, stream)
+        out = _empty((T, H, 512), torch.bfloat16, device, stream)
     else:
-        _need_out(out, torch.bfloat16, "out", (T, H, 512), dev)
-    lse = _empty((T, H), torch.float32, dev, stream) if want_lse else None
+        _need_out(out, torch.bfloat16, "out", (T, H, 512), device)
+    lse = _empty((T, H), torch.float32, device, stream) if want_lse else None
     L = _lib or lib()
     if ws is None:
         need = L.moe_latent_attention_workspace_bytes(T, k if inds is not None else c.width * c.page)
-        ws = _empty(max(need, 256), torch.uint8, dev, stream, returned=False)
+        ws = _empty((max(need, 256),), torch.uint8, device, stream, returned=False)
     else:
-        _need(ws, torch.uint8, "ws", dev)
+        _need(ws, torch.uint8, "ws", device)
+    q0, q1, _ = q.stride()
     _check(L.moe_latent_attention(
-        q.data_ptr(), T, H, q.stride(0) if T > 1 else 0, q.stride(1) if H > 1 else 0, ctypes.byref(c),
-        None if cu_tokens is None else cu_tokens.data_ptr(), lengths.data_ptr(), scale,
-        None if inds is None else inds.data_ptr(), k, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(q, stream)))
+        q.data_ptr(), T, H, q0 if T > 1 else 0, q1 if H > 1 else 0, ctypes.byref(c),
+        None if cu_tokens is None else cu_tokens.data_ptr(), lengths.data_ptr(), scale, chosen, k,
+        out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+        _raw_stream(q, stream)))
     return (out, lse) if want_lse else out
 
 

@@ -4,8 +4,9 @@
 // bias the layer norm: (x - mean) / std * w + b), the R columns from r0 on turned pair by pair by
 // the angle positions[t] * inv_freq[i], then rounded once, to bf16 or to e4m3 codes with one
 // power-of-two scale per 128 columns, into row slots[t] of the cache.  Sums and values in fp32.  The
-// angle is formed and reduced to half a turn in 64 bits: at position 10^6 an fp32 product is off
-// by 0.03 radians.
+// angle is formed in turns from exact fp32 products (turn_of): at position 10^6 a rounded one is
+// off by 0.03 radians, and the device's 64-bit rate is a hundredth of its 32-bit one (4001 index
+// keys: 18 us with angles in 64 bits, XX so).
 //
 // The bound is HBM (8192 rows of 576 columns with 128 heads' rotations move 287 MB) or, for a few
 // tokens, the launch.  A row is a warp's, 8 columns per lane and step, its sums five shuffles; queries
@@ -23,11 +24,20 @@ constexpr int kMaxChunks = 4;      // of 8 columns per lane: rows up to 1024 col
 constexpr int kMaxAngles = 2048;   // of a query block: tokens * R / 2
 constexpr int kQueryUnits = 4;     // 16-byte columns (or pairs of them) in flight per thread
 
+// cos and sin of the angle pos * f.  f / (2 pi) is g1 + g2 (g1 rounded, its rounding error and the
+// constant's own in g2), pos the sum of hi, a multiple of 4096, and lo; the products hi g1 and
+// lo g1 and what their rounding leaves are exact, and so is every difference to the nearest
+// whole number.  Off by less than 2^-25 turns to position 2^26, 2^-20 to 2^31 (f <= 1).
 MOE_DEV void turn_of(int pos, float f, float& c, float& s) {
-    constexpr double kTurn = 6.283185307179586477;
-    const double a = (double)pos * (double)f;
-    const double r = a - rint(a * (1.0 / kTurn)) * kTurn;
-    sincosf((float)r, &s, &c);
+    constexpr float kInv1 = 0x1.45f306p-3f, kInv2 = 0x1.b93910p-28f;  // 1 / (2 pi)
+    const float g1 = f * kInv1, g2 = fmaf(f, kInv2, fmaf(f, kInv1, -g1));
+    const float hi = (float)(pos & ~0xFFF), lo = (float)(pos & 0xFFF);
+    const float h = hi * g1, l = lo * g1;
+    const float eh = fmaf(hi, g1, -h), el = fmaf(lo, g1, -l);
+    float t = (eh - rintf(eh)) + el + (hi + lo) * g2;
+    t = (h - rintf(h)) + (l - rintf(l)) + (t - rintf(t));
+    t -= rintf(t);
+    sincospif(2.0f * t, &s, &c);
 }
 
 MOE_DEV void unpack8(const uint4& q, float (&v)[8]) {
@@ -220,7 +230,7 @@ MOE_DEV void rotate_queries(const AppendArgs& a, long long t0, int tokens) {
 }
 
 template <bool F8>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, unsigned row_blocks, int per) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendArgs a, unsigned row_blocks, int per) {
     if (blockIdx.x < row_blocks) {
         const long long t = (long long)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5);
         if (t < a.T) append_row<F8>(a, t);
