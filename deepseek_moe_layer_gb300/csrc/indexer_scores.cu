@@ -473,7 +473,7 @@ cudaError_t run(const ScoresArgs& a, cudaStream_t s) {
     const long long tile = accs * 280 > 3 * C::kRowBytes * 2 ? accs * 280 : 3 * C::kRowBytes * 2;
     const long long query = p.tt * p.Hp > kAccCols ? 3000 + p.tt * p.Hp * C::kRowBytes / 32 : 300;
     long long best = -1;
-    for (long long cuts = 1; cuts <= p.tiles && cuts <= 512; ++cuts) {
+    for (long long cuts = 1; cuts <= p.tiles; cuts += 1 + cuts / 8) {
         const long long kc = (p.tiles + cuts - 1) / cuts;
         const long long units = groups * ((p.tiles + kc - 1) / kc);
         const long long t = (units + num_sms() - 1) / num_sms() * (query + kc * tile);

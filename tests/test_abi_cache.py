@@ -1,0 +1,234 @@
+"""The operators over a paged cache on a machine without a GPU: every argument check of
+moe_cache_append, moe_indexer_scores and moe_latent_attention runs on the host before any CUDA call,
+and the binding refuses tensors that do not fit before it reaches the library."""
+import ctypes
+
+import pytest
+import torch
+
+from deepseek_moe_layer_gb300 import binding
+
+FAKE = 0x10000  # never dereferenced: every call below fails its host checks
+I31 = 1 << 31
+
+
+def _rc(rc):
+    return rc, binding.lib().moe_last_error().decode()
+
+
+def _append(**kw):
+    f = dict(x=FAKE, T=4, ldx=576, W=576, slots=FAKE, cache=FAKE, scales=None, rows=256,
+             norm_weight=FAKE, norm_bias=None, norm_cols=512, eps=1e-6, positions=FAKE,
+             inv_freq=FAKE, rope_cols=64, rope_at=512, interleaved=1, q=FAKE, q_out=FAKE, H=8,
+             q_token=8 * 64, q_head=64, q_out_token=8 * 64, q_out_head=64)
+    f.update(kw)
+    return _rc(binding.lib().moe_cache_append(ctypes.byref(binding.AppendArgs(**f)), None))
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(x=None), "NULL"), (dict(slots=None), "NULL"), (dict(cache=None), "NULL"),
+    (dict(norm_weight=None), "NULL"), (dict(positions=None), "NULL"), (dict(inv_freq=None), "NULL"),
+    (dict(q_out=None), "NULL"),
+    (dict(T=-1), "T = -1"), (dict(T=I31), "T = "),
+    (dict(W=0), "W = 0"), (dict(W=12, ldx=16), "W = 12"), (dict(W=1032, ldx=1032), "W = 1032"),
+    (dict(ldx=568), "ldx = 568"), (dict(ldx=580), "ldx = 580"),
+    (dict(rows=-1), "rows = -1"),
+    (dict(norm_cols=584), "norm_cols = 584"), (dict(norm_cols=12), "norm_cols = 12"),
+    (dict(norm_cols=-8), "norm_cols = -8"), (dict(eps=-1.0), "eps"),
+    (dict(rope_cols=24), "rope_cols = 24"), (dict(rope_cols=-16), "rope_cols = -16"),
+    (dict(rope_at=520), "rope_at = 520"), (dict(rope_at=4), "rope_at = 4"),
+    (dict(rope_at=-8), "rope_at = -8"),
+    (dict(scales=FAKE), "multiple of 128"),
+    (dict(rope_cols=0, rope_at=0), "q given without a rotation"),
+    (dict(H=0), "H = 0"), (dict(H=1025), "H = 1025"),
+    (dict(q_token=4), "strides"), (dict(q_head=4), "strides"), (dict(q_out_token=4), "strides"),
+    (dict(q_out_head=4), "strides"),
+    (dict(x=FAKE + 8), "16-byte"), (dict(cache=FAKE + 8), "16-byte"), (dict(q=FAKE + 8), "16-byte"),
+    (dict(q_out=FAKE + 8), "16-byte"), (dict(slots=FAKE + 4), "aligned to"),
+    (dict(positions=FAKE + 2), "aligned to"),
+])
+def test_append_refusals(kw, msg):
+    rc, err = _append(**kw)
+    assert rc == binding.MOE_ERR_INVALID and msg in err, err
+
+
+def test_append_nothing_to_do():
+    assert _append(T=0, x=None, slots=None, q=None)[0] == binding.MOE_OK
+    rc, err = _rc(binding.lib().moe_cache_append(None, None))
+    assert rc == binding.MOE_ERR_INVALID and "args" in err
+
+
+def _cache(**kw):
+    f = dict(rows=FAKE, pages=16, page=64, table=FAKE, sequences=4, width=8)
+    f.update(kw)
+    return binding.PagedCache(**f)
+
+
+PAGED = [
+    (dict(page=0), "page = 0"), (dict(pages=-1), "pages = -1"), (dict(pages=I31), "pages = "),
+    (dict(pages=I31 // 64), "2^31 rows"), (dict(width=-1), "width"),
+    (dict(width=1 << 25), "positions"), (dict(sequences=-1), "sequences"),
+    (dict(sequences=3), "without cu_tokens"), (dict(table=None), "NULL pointer in the cache"),
+    (dict(rows=None), "NULL pointer in the cache"), (dict(table=FAKE + 2), "4-byte"),
+    (dict(rows=FAKE + 8), "16-byte"),
+]
+
+
+def _scores(cache=None, q=FAKE, w=FAKE, T=4, H=64, ks=None, cu=None, lengths=FAKE, n=512, out=FAKE,
+            ld=512, null=False):
+    c = None if null else ctypes.byref(_cache(**(cache or {})))
+    return _rc(binding.lib().moe_indexer_scores(q, w, T, H, c, ks, cu, lengths, n, out, ld, None))
+
+
+@pytest.mark.parametrize("cache,msg", PAGED)
+def test_scores_cache_refusals(cache, msg):
+    rc, err = _scores(cache)
+    assert rc == binding.MOE_ERR_INVALID and msg in err, err
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(null=True), "cache is NULL"), (dict(q=None), "NULL"), (dict(w=None), "NULL"),
+    (dict(out=None), "NULL"), (dict(lengths=None), "NULL lengths"), (dict(T=-1), "T = -1"),
+    (dict(T=I31), "T = "), (dict(H=0), "H = 0"), (dict(H=129), "H = 129"), (dict(n=-1), "n = -1"),
+    (dict(n=I31 - 1, ld=I31), "n = "), (dict(ld=511), "ld = 511"), (dict(q=FAKE + 8), "16-byte"),
+    (dict(w=FAKE + 2), "4-byte"), (dict(out=FAKE + 2), "4-byte"), (dict(ks=FAKE + 2), "4-byte"),
+    (dict(cu=FAKE + 2), "4-byte"), (dict(lengths=FAKE + 2), "4-byte"),
+    (dict(cu=FAKE, cache=dict(sequences=0)), "without a sequence"),
+])
+def test_scores_refusals(kw, msg):
+    rc, err = _scores(**kw)
+    assert rc == binding.MOE_ERR_INVALID and msg in err, err
+
+
+def test_scores_nothing_to_do():
+    assert _scores(dict(sequences=0), T=0, q=None, w=None, out=None, lengths=None)[0] == binding.MOE_OK
+    assert _scores(n=0, ld=0, out=None)[0] == binding.MOE_OK
+
+
+def _attention(cache=None, q=FAKE, T=4, H=128, qt=128 * 576, qh=576, cu=None, lengths=FAKE, inds=None,
+               k=0, out=FAKE, lse=None, ws=FAKE, ws_bytes=1 << 40, null=False):
+    c = None if null else ctypes.byref(_cache(**(cache or {})))
+    return _rc(binding.lib().moe_latent_attention(q, T, H, qt, qh, c, cu, lengths, 0.1, inds, k, out,
+                                                  lse, ws, ws_bytes, None))
+
+
+@pytest.mark.parametrize("cache,msg", PAGED)
+def test_attention_cache_refusals(cache, msg):
+    rc, err = _attention(cache)
+    assert rc == binding.MOE_ERR_INVALID and msg in err, err
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(null=True), "cache is NULL"), (dict(q=None), "NULL"), (dict(out=None), "NULL"),
+    (dict(ws=None), "NULL"), (dict(lengths=None), "NULL lengths"), (dict(T=-1), "T = -1"),
+    (dict(H=0), "H = 0"), (dict(H=129), "H = 129"), (dict(qt=4), "strides"), (dict(qh=4), "strides"),
+    (dict(inds=FAKE, k=0), "k = 0"), (dict(q=FAKE + 8), "16-byte"), (dict(out=FAKE + 8), "16-byte"),
+    (dict(inds=FAKE + 2, k=4), "4-byte"), (dict(lse=FAKE + 2), "4-byte"), (dict(ws=FAKE + 16), "256-byte"),
+    (dict(ws_bytes=1024), "ws_bytes = 1024"),
+])
+def test_attention_refusals(kw, msg):
+    rc, err = _attention(**kw)
+    assert rc == binding.MOE_ERR_INVALID and msg in err, err
+
+
+def test_attention_workspace():
+    L = binding.lib()
+    size = L.moe_latent_attention_workspace_bytes
+    assert size(0, 100) == 0 and size(-1, 100) == 0 and size(1, -1) == 0
+    assert 0 < size(1, 0) <= size(1, 4096) <= size(64, 4096) <= size(1 << 20, 1 << 20) < 64 << 20
+    assert _attention(dict(sequences=0), T=0, q=None, out=None, ws=None, lengths=None,
+                      ws_bytes=0)[0] == binding.MOE_OK
+
+
+def test_valid_calls_without_gpu_fail_loudly():
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    for rc, err in (_append(), _scores(), _attention()):
+        assert rc == binding.MOE_ERR_NODEVICE and err
+
+
+# ---- the binding --------------------------------------------------------------------------------
+
+BF, F8, F32, I32, I64 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32, torch.int64
+
+
+def z(*shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def _call_append(**kw):
+    a = dict(x=z(3, 576), slots=z(3, dtype=I64), cache=z(2, 64, 576), norm_weight=z(512, dtype=F32),
+             positions=z(3, dtype=I32), inv_freq=z(32, dtype=F32), rope_at=512, q=z(3, 8, 64))
+    a.update(kw)
+    return binding.cache_append(**a)
+
+
+@pytest.mark.parametrize("kw,exc,msg", [
+    (dict(x=z(3, 576, dtype=F32)), TypeError, "x: dtype"), (dict(x=z(3 * 576)), ValueError, "x must"),
+    (dict(x=z(576, 3).t()), ValueError, "unit stride"),
+    (dict(slots=z(3, dtype=I32)), TypeError, "slots"), (dict(slots=z(4, dtype=I64)), ValueError, "slots"),
+    (dict(slots=[1, 2, 3]), TypeError, "slots"),
+    (dict(cache=z(2, 64, 512)), ValueError, "cache"), (dict(cache=z(2, 64, 576, dtype=F8)), TypeError, "cache"),
+    (dict(cache=z(2, 64, 1152)[..., ::2]), ValueError, "contiguous"),
+    (dict(scales=z(2, 64, 4, dtype=F32)), TypeError, "cache"),
+    (dict(norm_weight=z(512)), TypeError, "norm_weight"),
+    (dict(norm_bias=z(511, dtype=F32)), ValueError, "norm_bias"),
+    (dict(norm_weight=None, norm_bias=z(512, dtype=F32)), ValueError, "without norm_weight"),
+    (dict(positions=None), ValueError, "without positions"), (dict(positions=z(3, dtype=I64)), TypeError, "positions"),
+    (dict(inv_freq=z(32)), TypeError, "inv_freq"), (dict(inv_freq=None), ValueError, "q given without inv_freq"),
+    (dict(q=z(3, 8, 32)), ValueError, "q must"), (dict(q=z(3, 8, 64, dtype=F32)), TypeError, "q: dtype"),
+    (dict(q_out=z(3, 9, 64)), ValueError, "q_out must"), (dict(q=None, q_out=z(3, 8, 64)), ValueError, "without q"),
+    (dict(), ValueError, "CUDA device"),
+])
+def test_binding_append(kw, exc, msg):
+    with pytest.raises(exc, match=msg):
+        _call_append(**kw)
+
+
+def _call_scores(**kw):
+    a = dict(q=z(3, 64, 128), weights=z(3, 64, dtype=F32), keys=z(4, 64, 128),
+             block_table=z(3, 2, dtype=I32), lengths=z(3, dtype=I32), n=100)
+    a.update(kw)
+    return binding.indexer_scores(**a)
+
+
+@pytest.mark.parametrize("kw,exc,msg", [
+    (dict(q=z(3, 64, 64)), ValueError, "q must"), (dict(q=z(3, 64, 128, dtype=F8)), TypeError, "q: dtype"),
+    (dict(q=z(3, 64, 256)[..., ::2]), ValueError, "q must be contiguous"),
+    (dict(weights=z(3, 64)), TypeError, "weights"), (dict(weights=z(3, 63, dtype=F32)), ValueError, "weights"),
+    (dict(keys=z(4, 64, 64)), ValueError, "keys"), (dict(keys=z(4, 64, 128, dtype=F8)), TypeError, "keys"),
+    (dict(key_scales=z(4, 64, 1, dtype=F32)), TypeError, "q: dtype"),
+    (dict(q=z(3, 64, 128, dtype=F8), keys=z(4, 64, 128, dtype=F8), key_scales=z(4, 63, 1, dtype=F32)), ValueError,
+     "key_scales"),
+    (dict(block_table=z(2, 2, dtype=I32)), ValueError, "cu_tokens is None"),
+    (dict(block_table=z(6, dtype=I32)), ValueError, "block_table"), (dict(block_table=z(3, 2, dtype=I64)), TypeError, "block_table"),
+    (dict(lengths=z(3, dtype=I64)), TypeError, "lengths"), (dict(lengths=z(2, dtype=I32)), ValueError, "lengths"),
+    (dict(cu_tokens=z(3, dtype=I32)), ValueError, "cu_tokens"), (dict(cu_tokens=z(4, dtype=I64)), TypeError, "cu_tokens"),
+    (dict(out=z(3, 100)), TypeError, "out"), (dict(out=z(3, 99, dtype=F32)), ValueError, "out"),
+    (dict(out=z(100, 3, dtype=F32).t()), ValueError, "out"),
+    (dict(), ValueError, "CUDA device"),
+])
+def test_binding_scores(kw, exc, msg):
+    with pytest.raises(exc, match=msg):
+        _call_scores(**kw)
+
+
+def _call_attention(**kw):
+    a = dict(q=z(3, 16, 576), cache=z(4, 64, 576), block_table=z(3, 2, dtype=I32),
+             lengths=z(3, dtype=I32), scale=0.1)
+    a.update(kw)
+    return binding.latent_attention(**a)
+
+
+@pytest.mark.parametrize("kw,exc,msg", [
+    (dict(q=z(3, 16, 512)), ValueError, "q must"), (dict(q=z(3, 16, 576, dtype=F32)), TypeError, "q: dtype"),
+    (dict(q=z(3, 16, 1152)[..., ::2]), ValueError, "unit stride"),
+    (dict(cache=z(4, 64, 512)), ValueError, "cache"), (dict(cache=z(4, 64, 576, dtype=F32)), TypeError, "cache"),
+    (dict(inds=z(2, 8, dtype=I32)), ValueError, "inds"), (dict(inds=z(3, 8, dtype=I64)), TypeError, "inds"),
+    (dict(out=z(3, 16, 576)), ValueError, "out"), (dict(out=z(3, 16, 512, dtype=F32)), TypeError, "out"),
+    (dict(ws=z(16)), TypeError, "ws"), (dict(lengths=z(4, dtype=I32)), ValueError, "lengths"),
+    (dict(), ValueError, "CUDA device"),
+])
+def test_binding_attention(kw, exc, msg):
+    with pytest.raises(exc, match=msg):
+        _call_attention(**kw)
