@@ -11,7 +11,8 @@
 // sequence's tokens only.  Columns run in groups of up to 128 (whole tokens) through four TMEM
 // accumulators of four warps each, so that the epilogue (a maximum and half a packed
 // multiply-add per product) runs beside the UMMAs of the groups ahead and four of its warps share
-// a scheduler (two, with the next columns loaded ahead: 4096 x 16384 in 1288 us against XX).
+// a scheduler (4096 x 16384 in 804 us; 1288 with two and 32 columns loaded ahead, 1016 with four and
+// 16 ahead).
 //
 // Warp roles (768 threads, one CTA per SM, persistent over units): warps 0..15 epilogue (warp % 4 =
 // TMEM lane quarter, warp / 4 = accumulator), 16..19 key copies (16-byte asynchronous copies, so that
@@ -376,21 +377,22 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                 for (int c = r.c0; c < r.c1 && ok; ++c, ++it, acc += accs) {
                     const int pos = c * kKeys + quarter * 32 + lane;
                     const uint32_t ring = it % C::kRing;
-                    bool seen = false;
+                    int hidden = 0x7FFFFFFF;  // the key's position, if it is there
                     float ks = 1.0f;
                     // the tile's accumulators k with (acc + k) % kAccs == mine
                     for (int k = (int)((mine - acc) & (kAccs - 1)), told = 0; k < accs; k += kAccs) {
                         if (!told) {
                             if (!wait(&known[ring], (it / C::kRing) & 1u)) break;
-                            seen = pos < p.n && (there[ring * 4 + quarter] >> lane & 1u);
+                            if (there[ring * 4 + quarter] >> lane & 1u) hidden = pos;
                             if (F8) ks = scales[ring * kKeys + 32 * quarter + lane];
                             told = 1;
                         }
-                        if (!wait(&afull[mine], ((acc + k) / kAccs) & 1u)) break;
-                        tc_fence_after();
                         const int t = r.t0 + k * gtok, cnt = min(gtok, r.t1 - t);
                         const float* w = wts + (t - un.u0) * p.Hp;
+                        const int* len = lens + (t - un.u0);
                         float* out = p.out + (long long)t * p.ld + pos;
+                        if (!wait(&afull[mine], ((acc + k) / kAccs) & 1u)) break;
+                        tc_fence_after();
                         uint32_t ta = ta0;
                         for (int i = 0; i < cnt; ++i, out += p.ld) {
                             float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
@@ -411,8 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                                 w += 16;
                             }
                             const float sum = (s0.x + s0.y) + (s1.x + s1.y);
-                            if (pos < p.n)
-                                *out = seen && pos < lens[t - un.u0 + i] ? sum * ks : -__int_as_float(0x7F800000);
+                            if (pos < p.n) *out = hidden < len[i] ? sum * ks : -__int_as_float(0x7F800000);
                         }
                         tc_fence_before();
                         __syncwarp();

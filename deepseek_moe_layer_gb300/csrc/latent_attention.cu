@@ -180,7 +180,7 @@ MOE_DEV void arrive_even(uint64_t* bar) {
 }
 // Every lane; false (in every lane) when a wait gave up.
 MOE_DEV bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort))) return true;
+    if (__all_sync(0xFFFFFFFFu, mbar_wait_lean(bar, parity, abort))) return true;
     if ((threadIdx.x & 31) == 0) record_timeout(abort);
     return false;
 }

@@ -70,6 +70,15 @@ MOE_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// mbar_wait with a clock that is looked at only after some microseconds: a try returns after a while
+// of its own accord, so waits go round more than once, and a warp that waits takes issue slots
+// from those that share its scheduler (23 instructions a round with the clock in it, 5 without).
+MOE_DEV bool mbar_wait_lean(uint64_t* bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, abort);
+}
 // One lane of a converged warp, always the same.  UMMAs are issued by a warp that runs its loops
 // converged, with the issue alone inside `if (elect_lane())`: the operands then are warp-uniform
 // (four UMMAs of 128 x 128 x 16 by a CTA pair, with a wait and a commit: 142 clocks; in a loop
