@@ -73,8 +73,8 @@ constexpr int kXchOff = kBarOff + 8 * kBars;    // a float per softmax thread: m
 constexpr int kRowOff = kXchOff + 4 * kSoftThreads;      // [2][128] rows of the cache
 constexpr int kMaskOff = kRowOff + 2 * 4 * kTile;  // [4][4] words
 constexpr int kScanOff = kMaskOff + 64;         // 32 x int64
-constexpr int kSchedOff = kScanOff + 256;       // Start
-constexpr int kMiscOff = kSchedOff + 32;        // TMEM address, abort, the peer's TMEM address
+constexpr int kSchedOff = kScanOff + 256;       // Start (40 bytes)
+constexpr int kMiscOff = kSchedOff + 48;        // TMEM address, abort, the peer's TMEM address
 constexpr int kSmemBytes = kMiscOff + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(kThreads == 32 * (kEndWarp + kQWarps - 1), "every warp has a role");
@@ -114,11 +114,6 @@ struct Params {
     int pairs;
 };
 
-struct Start {
-    int t, b, tile, segments;  // (segments: at most so many)
-    long long left;            // tiles, at most
-};
-
 MOE_DEV void record_timeout(volatile int* abort) {
     *abort = 1;
     atomicCAS(&g_attention_status, 0u, kStatusTimeout);
@@ -129,17 +124,24 @@ MOE_DEV void record_timeout(volatile int* abort) {
 struct Seg {
     int t, n, b, see, len, tiles;
 };
-MOE_DEV Seg segment(const Params& p, int t, int b) {
+MOE_DEV Seg segment(const Params& p, const Sequences& q, int t, int b) {
     Seg s;
     s.t = t;
     s.b = b;
-    s.n = max(1, min(p.tt, seq_end(p.seq, b) - t));
+    s.n = max(1, min(p.tt, seq_end(q, b) - t));
     s.see = 0;
-    for (int i = 0; i < s.n; ++i) s.see = max(s.see, seq_length(p.seq, t + i));
+    for (int i = 0; i < s.n; ++i) s.see = max(s.see, seq_length(q, t + i));
     s.len = p.inds ? min(s.see, p.k) : s.see;
     s.tiles = max(1, (s.len + kTile - 1) / kTile);
     return s;
 }
+
+// A pair's run: its first segment, the tile in it, and at most so many segments and tiles.
+struct Start {
+    Seg s;
+    int tile, segments;
+    long long left;
+};
 
 // The pieces of a pair's run, in order.
 struct Walk {
@@ -147,18 +149,22 @@ struct Walk {
     long long left;
     Seg s;
     int i0, i1;  // tiles of the piece
-    MOE_DEV Walk(const Start& st) : t(st.t), b(st.b), tile(st.tile), segments(st.segments), left(st.left) {}
+    MOE_DEV Walk(const Start& st)
+        : t(-1), b(0), tile(st.tile), segments(st.segments), left(st.left), s(st.s) {}
     MOE_DEV bool next(const Params& p) {
         if (left <= 0 || segments <= 0) return false;
         --segments;
-        s = segment(p, t, b);
+        if (t >= 0) {  // (the first segment is at hand)
+            b = s.b;
+            if (!p.seq.cu) b = t;
+            else while (b < p.seq.B - 1 && t >= seq_end(p.seq, b)) ++b;
+            s = segment(p, p.seq, t, b);
+        }
         i0 = tile;
         i1 = (int)min((long long)s.tiles, i0 + left);
         left -= i1 - i0;
         tile = 0;
-        t += s.n;
-        if (!p.seq.cu) b = t;
-        else if (left > 0 && segments > 0) while (b < p.seq.B - 1 && t >= seq_end(p.seq, b)) ++b;
+        t = s.t + s.n;
         return true;
     }
     MOE_DEV bool begins() const { return i0 == 0; }
@@ -224,14 +230,14 @@ MOE_DEV uint32_t finite2(uint32_t v) {
 
 // Tiles of the tokens a .. z - 1 (of those that begin a segment).
 template <class F>
-MOE_DEV void for_segments(const Params& p, int a, int z, F&& f) {
+MOE_DEV void for_segments(const Params& p, const Sequences& q, int a, int z, F&& f) {
     if (a >= z) return;
-    int b = seq_of(p.seq, a);
+    int b = seq_of(q, a);
     for (int t = a; t < z; ++t) {
-        if (!p.seq.cu) b = t;
-        else while (b < p.seq.B - 1 && t >= seq_end(p.seq, b)) ++b;
-        const int first = p.seq.cu ? __ldg(p.seq.cu + b) : t;
-        if ((t - first) % p.tt == 0) f(segment(p, t, b));
+        if (!q.cu) b = t;
+        else while (b < q.B - 1 && t >= seq_end(q, b)) ++b;
+        const int first = q.cu ? q.cu[b] : t;
+        if ((t - first) % p.tt == 0) f(segment(p, q, t, b));
     }
 }
 
@@ -255,13 +261,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     const int crank = (int)cluster_rank(), pair = (int)(blockIdx.x >> 1);
 
     // ---- set-up ----
-    // tiles, segments (from bit 40 on) and the longest segment of this thread's tokens
-    const int tokens = seq_tokens(p.seq);
+    // tiles, segments (from bit 40 on) and the longest segment of this thread's tokens; the sequences'
+    // ends are searched in shared memory, where the rows of the first tiles will be
+    Sequences seq = p.seq;
+    if (seq.cu && seq.B < 4 * kVBlock / 4) {
+        int32_t* ends = reinterpret_cast<int32_t*>(smem + kVOff);
+        for (int i = threadIdx.x; i <= seq.B; i += kThreads) ends[i] = __ldg(p.seq.cu + i);
+        seq.cu = ends;
+        __syncthreads();
+    }
+    const int tokens = seq_tokens(seq);
     const int per = (tokens + kThreads - 1) / kThreads;
     const int a = min(tokens, (int)threadIdx.x * per), z = min(tokens, a + per);
     unsigned long long mine = 0;
     int longest = 0;
-    for_segments(p, a, z, [&](const Seg& s) {
+    for_segments(p, seq, a, z, [&](const Seg& s) {
         mine += (unsigned)s.tiles + (1ull << 40);
         longest = max(longest, s.tiles);
     });
@@ -358,11 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             }
             if (lo < hi && mine0 <= lo && lo < mine1) {
                 long long at = mine0;
-                for_segments(p, a, z, [&](const Seg& s) {
+                for_segments(p, seq, a, z, [&](const Seg& s) {
                     const int n = whole ? 1 : s.tiles;
                     if (at <= lo && lo < at + n) {
-                        sched->t = s.t;
-                        sched->b = s.b;
+                        sched->s = s;
                         sched->tile = (int)(lo - at);
                         sched->segments = whole ? (int)(hi - lo) : 0x7FFFFFFF;
                         sched->left = whole ? 0x7FFFFFFFFFFFll : hi - lo;

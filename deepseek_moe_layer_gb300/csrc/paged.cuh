@@ -23,7 +23,8 @@ MOE_DEV long long paged_row(const Paged& c, int b, int pos) {
                : -1;
 }
 
-// Sequences of tokens: sequence b's are cu[b] .. cu[b + 1] - 1, or token b alone without cu.
+// Sequences of tokens: sequence b's are cu[b] .. cu[b + 1] - 1, or token b alone without cu.  (cu may
+// be a copy in shared memory.)
 struct Sequences {
     const int32_t* cu;       // [B + 1] or nullptr
     const int32_t* lengths;  // [T] positions a token may see
@@ -32,7 +33,7 @@ struct Sequences {
 };
 
 MOE_DEV int seq_tokens(const Sequences& q) {  // tokens that belong to a sequence
-    return q.cu ? max(0, min(q.T, __ldg(q.cu + q.B))) : q.T;
+    return q.cu ? max(0, min(q.T, q.cu[q.B])) : q.T;
 }
 // The sequence of token t < seq_tokens(): the last b with cu[b] <= t.
 MOE_DEV int seq_of(const Sequences& q, int t) {
@@ -40,11 +41,11 @@ MOE_DEV int seq_of(const Sequences& q, int t) {
     int lo = 0, hi = q.B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(q.cu + mid) <= t) lo = mid; else hi = mid - 1;
+        if (q.cu[mid] <= t) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
-MOE_DEV int seq_end(const Sequences& q, int b) { return q.cu ? min(q.T, __ldg(q.cu + b + 1)) : b + 1; }
+MOE_DEV int seq_end(const Sequences& q, int b) { return q.cu ? min(q.T, q.cu[b + 1]) : b + 1; }
 MOE_DEV int seq_length(const Sequences& q, int t) { return max(0, min(q.most, __ldg(q.lengths + t))); }
 
 // 16 bytes global -> shared, of which the first `bytes` (16 or 0) are read and the rest is zero.
