@@ -374,26 +374,36 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
             Part r;
             while (ok && un.part(p, r)) {
                 const int accs = (r.t1 - r.t0 + gtok - 1) / gtok;  // of a tile
-                for (int c = r.c0; c < r.c1 && ok; ++c, ++it, acc += accs) {
-                    const int pos = c * kKeys + quarter * 32 + lane;
+                // of the accumulator `was` of a tile (always the same one, where a tile has kAccs)
+                int was = -1, cnt = 0, pos = r.c0 * kKeys + quarter * 32 + lane;
+                const float* w0 = wts;
+                const int* len = lens;
+                float* out0 = p.out;
+                for (int c = r.c0; c < r.c1 && ok; ++c, ++it, acc += accs, pos += kKeys) {
                     const uint32_t ring = it % C::kRing;
                     int hidden = 0x7FFFFFFF;  // the key's position, if it is there
                     float ks = 1.0f;
                     // the tile's accumulators k with (acc + k) % kAccs == mine
                     for (int k = (int)((mine - acc) & (kAccs - 1)), told = 0; k < accs; k += kAccs) {
+                        if (k != was) {
+                            was = k;
+                            const int t = r.t0 + k * gtok;
+                            cnt = min(gtok, r.t1 - t);
+                            w0 = wts + (t - un.u0) * p.Hp;
+                            len = lens + (t - un.u0);
+                            out0 = p.out + (long long)t * p.ld;
+                        }
                         if (!told) {
                             if (!wait(&known[ring], (it / C::kRing) & 1u)) break;
                             if (there[ring * 4 + quarter] >> lane & 1u) hidden = pos;
                             if (F8) ks = scales[ring * kKeys + 32 * quarter + lane];
                             told = 1;
                         }
-                        const int t = r.t0 + k * gtok, cnt = min(gtok, r.t1 - t);
-                        const float* w = wts + (t - un.u0) * p.Hp;
-                        const int* len = lens + (t - un.u0);
-                        float* out = p.out + (long long)t * p.ld + pos;
                         if (!wait(&afull[mine], ((acc + k) / kAccs) & 1u)) break;
                         tc_fence_after();
                         uint32_t ta = ta0;
+                        const float* w = w0;
+                        float* out = out0 + pos;
                         for (int i = 0; i < cnt; ++i, out += p.ld) {
                             float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
                             int h = p.Hp;
