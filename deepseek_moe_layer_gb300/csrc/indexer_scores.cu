@@ -11,8 +11,8 @@
 // sequence's tokens only.  Columns run in groups of up to 128 (whole tokens) through four TMEM
 // accumulators of four warps each, so that the epilogue (a maximum and half a packed
 // multiply-add per product) runs beside the UMMAs of the groups ahead and four of its warps share
-// a scheduler (4096 x 16384 in 804 us; 1288 with two and 32 columns loaded ahead, 1016 with four and
-// 16 ahead).
+// a scheduler (4096 x 16384 in 770 us; 1288 with two and 32 columns loaded ahead, 1016 with four and
+// 16 ahead, 955 with eight accumulators of 64 columns).
 //
 // Warp roles (768 threads, one CTA per SM, persistent over units): warps 0..15 epilogue (warp % 4 =
 // TMEM lane quarter, warp / 4 = accumulator), 16..19 key copies (16-byte asynchronous copies, so that
