@@ -5,16 +5,20 @@
 //
 // Keys lie on the tensor cores' M side (128 per tile) and (token, head) pairs on the N side: a
 // thread then holds one key's dot products with all heads, the sum over the heads is its own
-// and a token's scores leave as consecutive numbers.  A unit is `tt` consecutive tokens (up to 512
-// columns, of bf16 384, in shared memory for the whole unit) and `kc` key tiles that stream past them; tokens
-// of several sequences in one unit are taken sequence by sequence, with the columns of that
-// sequence's tokens only.  Columns run in groups of up to 128 (whole tokens) through four TMEM
-// accumulators of four warps each, so that the epilogue (a maximum and half a packed
-// multiply-add per product) runs beside the UMMAs of the groups ahead and four of its warps share
-// a scheduler (4096 x 16384 in 770 us; 1288 with two and 32 columns loaded ahead, 1016 with four and
-// 16 ahead, 955 with eight accumulators of 64 columns).
+// and a token's scores leave as consecutive numbers.  A group is `tt` consecutive tokens (e4m3 up to 512
+// columns, bf16 384), whose queries stay in shared memory while key tiles stream past them; tokens of
+// several sequences in one group are taken sequence by sequence, with the columns of that
+// sequence's tokens only.  Columns run in accumulators of up to 128 (whole tokens), four in
+// TMEM with four warps each, so that the epilogue (a maximum and half a packed multiply-add per
+// product) runs beside the UMMAs of the accumulators ahead and four of its warps share a scheduler
+// (4096 x 16384 in 643 us; before runs 770, 1288 with two and 32 columns loaded ahead, 1016 with four and 16 ahead,
+// 955 with eight accumulators of 64 columns).
 //
-// Warp roles (768 threads, one CTA per SM, persistent over units): warps 0..15 epilogue (warp % 4 =
+// Work is one list of (tile, accumulator) over all groups and their sequences, as many tiles as the
+// tokens can see, cut into equal runs, one per CTA (units of as many tiles, some of them out of sight:
+// 64 sequences of 8192 to 32768 positions 59 us, 42 so).
+//
+// Warp roles (768 threads, one CTA per SM): warps 0..15 epilogue (warp % 4 =
 // TMEM lane quarter, warp / 4 = accumulator), 16..19 key copies (16-byte asynchronous copies, so that
 // pages of any size and any order do; rows without a page or behind the end are zeros; a warp takes
 // every fourth tile, so that four are in flight, and looks its next one's pages up meanwhile), 20 and 21 issue the UMMAs of
@@ -44,7 +48,7 @@ template <bool F8>
 struct Cfg {
     static constexpr int kRowBytes = F8 ? kD : 2 * kD;
     static constexpr int kBlocks = kRowBytes / 128;         // 128-byte blocks of a row
-    static constexpr int kCols = F8 ? 512 : 384;            // (token, head) columns of a unit
+    static constexpr int kCols = F8 ? 512 : 384;            // (token, head) columns of a group
     static constexpr int kQBytes = kCols * kRowBytes;
     static constexpr int kStageBytes = kKeys * kRowBytes;
     static constexpr int kStages = F8 ? 8 : 4;
@@ -57,7 +61,7 @@ struct Cfg {
     static_assert(kRing - kStages > kAccs, "the epilogue is done with a place that is taken again");
     static constexpr int kStageOff = kQBytes;
     static constexpr int kWOff = kStageOff + kStages * kStageBytes;
-    static constexpr int kLenOff = kWOff + 4 * kCols;       // a unit's lengths
+    static constexpr int kLenOff = kWOff + 4 * kCols;       // a group's lengths
     static constexpr int kScaleOff = kLenOff + 4 * (kCols / 16);
     static constexpr int kThereOff = kScaleOff + (F8 ? 4 * kKeys * kRing : 0);
     static constexpr int kBarOff = kThereOff + 16 * kRing;
@@ -82,9 +86,7 @@ struct Params {
     int n;                   // positions of an output row
     float* out;              // [T, ld]
     long long ld;
-    int tt, kc;              // tokens of a unit, key tiles of a unit
-    int tiles;               // key tiles of n
-    long long units;
+    int tt, gtok;            // tokens of a group, of an accumulator
 };
 
 MOE_DEV void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -102,63 +104,67 @@ MOE_DEV void record_timeout(volatile int* abort) {
     atomicCAS(&g_scores_status, 0u, kStatusTimeout);
 }
 
-// The part of a unit that belongs to one sequence: tokens t0 .. t1 - 1 of sequence b, key tiles
-// c0 .. c1 - 1 hold positions that one of them may see.
+// The part of a group (tokens u0 .. u1 - 1) that belongs to one sequence: tokens t0 .. t1 - 1 of
+// sequence b, `accs` accumulators for each of the tiles that one of them can see; c0 .. c1 - 1 of
+// these tiles are this CTA's.
 struct Part {
-    int b, t0, t1, c0, c1;
+    int b, u0, u1, t0, t1, accs, tiles, c0, c1;
 };
-// Walks a unit's parts; every thread that walks sees the same ones.
-struct Unit {
-    int u0, u1, c0, c1, next;
-    MOE_DEV Unit(const Params& p, long long u, int tokens) {
-        const int chunks = (p.tiles + p.kc - 1) / p.kc;
-        u0 = (int)(u / chunks) * p.tt;
-        u1 = min(tokens, u0 + p.tt);
-        c0 = (int)(u % chunks) * p.kc;
-        c1 = min(p.tiles, c0 + p.kc);
-        next = u0;
-    }
+MOE_DEV void part_at(const Params& p, int tokens, int t, Part& r) {
+    r.u0 = t - t % p.tt;
+    r.u1 = min(tokens, r.u0 + p.tt);
+    r.b = seq_of(p.seq, t);
+    r.t0 = t;
+    r.t1 = max(t + 1, min(r.u1, seq_end(p.seq, r.b)));
+    int most = 0;
+    for (int i = r.t0; i < r.t1; ++i) most = max(most, seq_length(p.seq, i));
+    r.tiles = (min(most, p.n) + kKeys - 1) / kKeys;
+    r.accs = (r.t1 - r.t0 + p.gtok - 1) / p.gtok;
+}
+
+// A CTA's run lo .. hi - 1 of the list, from the part at token t, the list's entry `at`, on.
+struct Start {
+    long long lo, hi, at;
+    int t, pad;
+};
+// Its parts, in order; every thread that walks sees the same ones.
+struct Walk {
+    Start s;
+    int tokens;
+    MOE_DEV Walk(const Start& st, int tokens) : s(st), tokens(tokens) {}
     MOE_DEV bool part(const Params& p, Part& r) {
-        if (next >= u1) return false;
-        r.t0 = next;
-        r.b = seq_of(p.seq, next);
-        r.t1 = max(next + 1, min(u1, seq_end(p.seq, r.b)));
-        next = r.t1;
-        int most = 0;
-        for (int t = r.t0; t < r.t1; ++t) most = max(most, seq_length(p.seq, t));
-        r.c0 = c0;
-        r.c1 = max(c0, min(c1, (min(most, p.n) + kKeys - 1) / kKeys));
-        return true;
+        while (s.t < tokens && s.at < s.hi) {
+            part_at(p, tokens, s.t, r);
+            // a tile is the run's that holds its first accumulator
+            const auto from = [&](long long x) {
+                const long long d = x - s.at;
+                return d <= 0 ? 0 : d >= (long long)r.tiles * r.accs
+                           ? r.tiles : (int)((unsigned)(d + r.accs - 1) / (unsigned)r.accs);
+            };
+            r.c0 = from(s.lo);
+            r.c1 = from(s.hi);
+            s.at += (long long)r.tiles * r.accs;
+            s.t = r.t1;
+            if (r.c0 < r.c1) return true;
+        }
+        return false;
     }
 };
 
-// The key tiles of a CTA's units, in order.
+// The key tiles of a run, in order.
 struct Tiles {
-    long long u;
-    int tokens, c;
-    bool more;
-    Unit un;
+    Walk w;
     Part r;
-    MOE_DEV Tiles(const Params& p, int tokens) : u(blockIdx.x), tokens(tokens), un(p, blockIdx.x, tokens) {
-        r.c0 = r.c1 = 0;
-        c = 0;
-        more = u < p.units;
-        step(p);
-    }
-    MOE_DEV void step(const Params& p) {  // to a tile, or to the end
-        while (more && c >= r.c1) {
-            if (un.part(p, r)) {
-                c = r.c0;
-            } else {
-                u += gridDim.x;
-                more = u < p.units;
-                if (more) un = Unit(p, u, tokens);
-            }
-        }
+    int c;
+    bool more;
+    MOE_DEV Tiles(const Params& p, const Start& st, int tokens) : w(st, tokens) {
+        more = w.part(p, r);
+        c = more ? r.c0 : 0;
     }
     MOE_DEV void next(const Params& p) {
-        ++c;
-        step(p);
+        if (++c < r.c1) return;
+        more = w.part(p, r);
+        c = r.c0;
     }
 };
 
@@ -198,6 +204,19 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // entries of the list of this thread's groups (asked for before the set-up waits for anything)
+    const int tokens = seq_tokens(p.seq);
+    const int groups = (tokens + p.tt - 1) / p.tt, per = (groups + kThreads - 1) / kThreads;
+    const int a = min((long long)tokens, (long long)threadIdx.x * per * p.tt);
+    const int z = min((long long)tokens, (long long)a + (long long)per * p.tt);
+    long long mine = 0;
+    {
+        Part r;
+        for (int t = a; t < z; t = r.t1) {
+            part_at(p, tokens, t, r);
+            mine += (long long)r.tiles * r.accs;
+        }
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -215,12 +234,58 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         fence_mbar_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
-    tc_fence_before();
+    // this CTA's run: a prefix sum over the groups, through what will hold the queries
+    Start* start = reinterpret_cast<Start*>(smem + 256);
+    {
+        long long* scan = reinterpret_cast<long long*>(smem);
+        long long incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) scan[warp] = incl;
+        if (threadIdx.x == 0) start->lo = start->hi = start->at = 0, start->t = tokens;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (__any_sync(0xFFFFFFFFu, mine > 0)) {
+            long long upto = lane < kThreads / 32 ? scan[lane] : 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const long long total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+            const long long before = (warp ? __shfl_sync(0xFFFFFFFFu, upto, max(warp, 1) - 1) : 0) + incl - mine;
+            long long lo, hi;
+            if (total < (1 << 22)) {  // (64-bit divisions take a microsecond)
+                lo = (unsigned)total * blockIdx.x / gridDim.x;
+                hi = (unsigned)total * (blockIdx.x + 1) / gridDim.x;
+            } else {
+                lo = total * blockIdx.x / gridDim.x;
+                hi = total * (blockIdx.x + 1) / gridDim.x;
+            }
+            if (lo < hi && before <= lo && lo < before + mine) {
+                long long at = before;
+                Part r;
+                for (int t = a; t < z; t = r.t1) {
+                    part_at(p, tokens, t, r);
+                    const long long n = (long long)r.tiles * r.accs;
+                    if (at <= lo && lo < at + n) {
+                        start->lo = lo;
+                        start->hi = hi;
+                        start->at = at;
+                        start->t = t;
+                    }
+                    at += n;
+                }
+            }
+        }
+    }
     __syncthreads();
-    tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int tokens = seq_tokens(p.seq);
-    const int gtok = kAccCols / p.Hp;  // tokens of an accumulator
+    const Start st = *start;
+    __syncthreads();  // (where it was, queries come)
+    const int gtok = p.gtok;
     bool ok = true;
     const auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort))) return true;
@@ -234,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         constexpr int kRows = 32 / kPer;          // rows that a warp copies at once
         const int piece = lane % kPer, sub = lane / kPer;
         const uint32_t dst0 = (piece / 8) * (kKeys * 128) + sub * 128;
-        Tiles tile(p, tokens);
+        Tiles tile(p, st, tokens);
         uint32_t it = 0;
         for (; (int)it < warp - kEpiWarps && tile.more; ++it) tile.next(p);
         int id[4], off[4];                        // page and row in it of the keys 32 k + lane
@@ -259,11 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                 if (F8) ks[k] = row[k] >= 0 ? __ldg(p.ks + row[k]) : 0.0f;
             }
             if (!wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u)) break;
-            const uint32_t st = smem_u32(smem + C::kStageOff + s * C::kStageBytes) + dst0;
+            const uint32_t to = smem_u32(smem + C::kStageOff + s * C::kStageBytes) + dst0;
 #pragma unroll
             for (int i = 0; i < kKeys / kRows; ++i) {
                 const int at = __shfl_sync(0xFFFFFFFFu, row[i * kRows / 32], (i * kRows + sub) & 31);
-                copy16(st + i * kRows * 128 + (((piece & 7) ^ ((i * kRows + sub) & 7)) << 4),
+                copy16(to + i * kRows * 128 + (((piece & 7) ^ ((i * kRows + sub) & 7)) << 4),
                        p.k + (long long)max(at, 0) * C::kRowBytes + piece * 16, at < 0 ? 0u : 16u);
             }
             copy_commit();
@@ -287,42 +352,48 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     } else if (warp >= kQueryWarp) {
         // ============================ queries and weights ============================
         const int tid = (int)threadIdx.x - 32 * kQueryWarp;
-        uint32_t n = 0;
-        for (long long u = blockIdx.x; u < p.units; u += gridDim.x, ++n) {
-            Unit un(p, u, tokens);
+        Walk w(st, tokens);
+        Part r;
+        bool more = w.part(p, r);
+        for (uint32_t n = 0; more; ++n) {
+            const int u0 = r.u0, u1 = r.u1;
             if (!wait(qempty, (n & 1u) ^ 1u)) break;
             const uint32_t base = smem_u32(smem);
             constexpr int kPer = C::kRowBytes / 16;
-            const int rows = max(0, un.u1 - un.u0) * p.Hp;
+            const int rows = (u1 - u0) * p.Hp;
             const int piece = tid % kPer;
 #pragma unroll 8
             for (int rr = tid / kPer; rr < rows; rr += 32 * kQueryWarps / kPer) {
                 const int t = rr / p.Hp, h = rr % p.Hp;
-                const long long at = ((long long)(un.u0 + t) * p.H + (h < p.H ? h : 0)) * C::kRowBytes;
+                const long long at = ((long long)(u0 + t) * p.H + (h < p.H ? h : 0)) * C::kRowBytes;
                 copy16(base + (piece / 8) * (C::kCols * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4),
                        p.q + at + piece * 16, h < p.H ? 16u : 0u);
             }
             copy_commit();
             for (int i = tid; i < rows; i += 32 * kQueryWarps) {
                 const int t = i / p.Hp, h = i % p.Hp;
-                wts[i] = h < p.H ? __ldg(p.w + (long long)(un.u0 + t) * p.H + h) : 0.0f;
+                wts[i] = h < p.H ? __ldg(p.w + (long long)(u0 + t) * p.H + h) : 0.0f;
             }
-            for (int t = tid; t < un.u1 - un.u0; t += 32 * kQueryWarps) lens[t] = seq_length(p.seq, un.u0 + t);
+            for (int t = tid; t < u1 - u0; t += 32 * kQueryWarps) lens[t] = seq_length(p.seq, u0 + t);
             copy_wait<0>();
             fence_async_shared();
             mbar_arrive(qfull);
+            do more = w.part(p, r);
+            while (more && r.u0 == u0);
         }
     } else if (warp >= kMmaWarp) {
         // ================================ UMMA issuers ================================
         const uint32_t mine = warp - kMmaWarp;  // accumulators of this parity
-        uint32_t it = 0, acc = 0, n = 0;
+        uint32_t it = 0, acc = 0;
         const uint64_t dq = sdesc_k128(smem_u32(smem)), dk = sdesc_k128(smem_u32(smem + C::kStageOff));
-        for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++n) {
-            Unit un(p, u, tokens);
+        Walk w(st, tokens);
+        Part r;
+        bool more = w.part(p, r);
+        for (uint32_t n = 0; more && ok; ++n) {
+            const int u0 = r.u0;
             if (!wait(qfull, n & 1u)) break;
-            Part r;
-            while (ok && un.part(p, r)) {
-                const int accs = (r.t1 - r.t0 + gtok - 1) / gtok;  // of a tile
+            do {
+                const int accs = r.accs;
                 for (int c = r.c0; c < r.c1 && ok; ++c, ++it, acc += accs) {
                     const uint32_t s = it % C::kStages;
                     int k = (int)((mine - acc) & (kMmaWarps - 1));
@@ -337,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                         tc_fence_after();
                         const int t = r.t0 + k * gtok, cols = min(gtok, r.t1 - t) * p.Hp;
                         const uint32_t idesc = C::kIdesc0 | ((uint32_t)(cols >> 3) << 17);
-                        const uint64_t db = dq + (uint64_t)((t - un.u0) * p.Hp * 8);
+                        const uint64_t db = dq + (uint64_t)((t - u0) * p.Hp * 8);
                         if (elect_lane()) {
 #pragma unroll
                             for (int blk = 0; blk < C::kBlocks; ++blk)
@@ -355,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                     if (ok && elect_lane()) umma_commit(&empty[s]);
                     __syncwarp();
                 }
-            }
+                more = w.part(p, r);
+            } while (more && ok && r.u0 == u0);
             if (ok && elect_lane()) umma_commit(qempty);
             __syncwarp();
         }
@@ -367,13 +439,27 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         const int quarter = warp & 3;
         const uint32_t mine = warp >> 2;  // its accumulator
         const uint32_t ta0 = tmem + ((uint32_t)(quarter * 32) << 16) + mine * kAccCols;
-        uint32_t it = 0, acc = 0, n = 0;
-        for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++n) {
-            Unit un(p, u, tokens);
-            if (!wait(qfull, n & 1u)) break;  // (the weights and lengths)
+        // what no token of a part can see, 4096 positions per warp
+        const int runs = (p.n + 4095) / 4096;
+        for (long long f = (long long)blockIdx.x * kEpiWarps + warp; f < (long long)tokens * runs;
+             f += (long long)gridDim.x * kEpiWarps) {
+            const int t = (int)(f / runs), b = seq_of(p.seq, t), u0 = t - t % p.tt;
+            const int t0 = p.seq.cu ? max(u0, p.seq.cu[b]) : t;
             Part r;
-            while (ok && un.part(p, r)) {
-                const int accs = (r.t1 - r.t0 + gtok - 1) / gtok;  // of a tile
+            part_at(p, tokens, t0, r);
+            const int j0 = max((int)(f % runs) * 4096, r.tiles * kKeys), j1 = min(p.n, (int)(f % runs) * 4096 + 4096);
+            for (int j = j0 + lane; j < j1; j += 32)
+                p.out[(long long)t * p.ld + j] = -__int_as_float(0x7F800000);
+        }
+        uint32_t it = 0, acc = 0;
+        Walk walk(st, tokens);
+        Part r;
+        bool more = walk.part(p, r);
+        for (uint32_t n = 0; more && ok; ++n) {
+            const int u0 = r.u0;
+            if (!wait(qfull, n & 1u)) break;  // (the weights and lengths)
+            do {
+                const int accs = r.accs;
                 // of the accumulator `was` of a tile (always the same one, where a tile has kAccs)
                 int was = -1, cnt = 0, pos = r.c0 * kKeys + quarter * 32 + lane;
                 const float* w0 = wts;
@@ -389,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                             was = k;
                             const int t = r.t0 + k * gtok;
                             cnt = min(gtok, r.t1 - t);
-                            w0 = wts + (t - un.u0) * p.Hp;
-                            len = lens + (t - un.u0);
+                            w0 = wts + (t - u0) * p.Hp;
+                            len = lens + (t - u0);
                             out0 = p.out + (long long)t * p.ld;
                         }
                         if (!told) {
@@ -430,13 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                         if (lane == 0) mbar_arrive(&aempty[mine]);
                     }
                 }
-                if (!ok) break;
-                // what no token of the part may see
-                const int e0 = max(r.c1, un.c0) * kKeys, e1 = min(p.n, un.c1 * kKeys);
-                for (int t = r.t0; t < r.t1; ++t)
-                    for (int j = e0 + (int)threadIdx.x; j < e1; j += 32 * kEpiWarps)
-                        p.out[(long long)t * p.ld + j] = -__int_as_float(0x7F800000);
-            }
+                more = walk.part(p, r);
+            } while (more && ok && r.u0 == u0);
             __syncwarp();
             if (lane == 0) mbar_arrive(qempty);
         }
@@ -472,31 +553,14 @@ cudaError_t run(const ScoresArgs& a, cudaStream_t s) {
     p.n = a.n;
     p.out = a.out;
     p.ld = a.ld;
-    p.tiles = (a.n + kKeys - 1) / kKeys;
-    // tokens of a unit: what a sequence has on average, as far as the columns go
+    p.gtok = kAccCols / p.Hp;
+    // tokens of a group: what a sequence has on average, as far as the columns go
     const int avg = a.cu ? (int)((a.T + a.B - 1) / a.B) : 1;
     p.tt = C::kCols / p.Hp;
     if (avg < p.tt) p.tt = avg;
-    const long long groups = (a.T + p.tt - 1) / p.tt;
-    // key tiles of a unit: the number of rounds of units times their clocks, at the least (queries
-    // loaded, then 280 clocks per accumulator and tile, or what 128 keys take from HBM)
-    const int accs = (p.tt + kAccCols / p.Hp - 1) / (kAccCols / p.Hp);
-    const long long tile = accs * 280 > 3 * C::kRowBytes * 2 ? accs * 280 : 3 * C::kRowBytes * 2;
-    const long long query = p.tt * p.Hp > kAccCols ? 3000 + p.tt * p.Hp * C::kRowBytes / 32 : 300;
-    long long best = -1;
-    for (long long cuts = 1; cuts <= p.tiles; cuts += 1 + cuts / 8) {
-        const long long kc = (p.tiles + cuts - 1) / cuts;
-        const long long units = groups * ((p.tiles + kc - 1) / kc);
-        const long long t = (units + num_sms() - 1) / num_sms() * (query + kc * tile);
-        // (as long, and more units: sequences of different lengths even out)
-        if (best < 0 || t <= best) {
-            best = t;
-            p.kc = (int)kc;
-        }
-    }
-    p.units = groups * ((p.tiles + p.kc - 1) / p.kc);
-    long long grid = num_sms();
-    if (p.units < grid) grid = p.units;
+    // no more CTAs than entries of the list where every token sees all n positions
+    const long long most = (a.T + p.tt - 1) / p.tt * ((a.n + kKeys - 1) / kKeys) * ((p.tt + p.gtok - 1) / p.gtok);
+    const long long grid = most < num_sms() ? most : num_sms();
     return launch_kernel(scores_kernel<F8>, dim3((unsigned)grid), dim3(kThreads), (size_t)C::kSmemBytes,
                          s, p);
 }
