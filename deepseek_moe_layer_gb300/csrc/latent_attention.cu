@@ -155,6 +155,7 @@ struct Walk {
         if (left <= 0 || segments <= 0) return false;
         --segments;
         if (t >= 0) {  // (the first segment is at hand)
+            if (t >= p.seq.T) return false;  // (ends of sequences that do not ascend)
             b = s.b;
             if (!p.seq.cu) b = t;
             else while (b < p.seq.B - 1 && t >= seq_end(p.seq, b)) ++b;
