@@ -18,6 +18,9 @@
 // tokens can see, cut into equal runs, one per CTA (units of as many tiles, some of them out of sight:
 // 64 sequences of 8192 to 32768 positions 59 us, 42 so).
 //
+// What bounds it is the epilogue's issue slots and latencies: an accumulator takes its four warps 2500
+// clocks and 1000 more until the next one is full (1510 TFLOP/s at 4096 x 16384, 60% of issue slots).
+//
 // Warp roles (768 threads, one CTA per SM): warps 0..15 epilogue (warp % 4 =
 // TMEM lane quarter, warp / 4 = accumulator), 16..19 key copies (16-byte asynchronous copies, so that
 // pages of any size and any order do; rows without a page or behind the end are zeros; a warp takes

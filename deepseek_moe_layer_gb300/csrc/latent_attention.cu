@@ -7,16 +7,22 @@
 // One pass over the positions with the softmax's running maximum m and sum l per (token, head) row,
 // both fp32 and in base 2.  The maximum is a reference only: it moves (and the sums are
 // rescaled) when a score passes it by more than 8, so p <= 2^8 and the rescaling of 512 columns of
-// TMEM is rare.  p is rounded to bf16 for the second product (2^-9 of each term, the inputs' own
-// precision); l sums the fp32 values.
+// TMEM is rare.  p is rounded to bf16 for the second product (at most 2^-8 of each term, the inputs'
+// own precision); l sums the fp32 values.
 //
 // 128 rows x 512 fp32 columns of o are all of an SM's TMEM, so a CTA pair shares them: each CTA
 // has 64 rows, and cta_group::2 UMMAs with M = 128 run both halves at the full rate (a CTA's 64 rows
-// lie in lanes 0..63 for the first half of N and in lanes 64..127 for the second).  A tile is 64
-// positions.  s = q c^T (N = 64, K = 576): each CTA holds 32 of the positions as the K-major B
-// operand.  o += p c (N = 512 as two UMMAs of 256, K = 64): each CTA holds half of the columns of
-// all 64 positions, the same swizzled rows read as an MN-major B operand.  So a pair loads
-// 139 KB per tile where 74 KB are unique: the rest comes from L2.
+// lie in lanes 0..63 for the first half of N and in lanes 64..127 for the second).  A tile is 128
+// positions.  s = q c^T (N = 128, K = 576): each CTA holds 64 of the positions as the K-major B
+// operand.  o += p c (N = 512 as two UMMAs of 256, K = 128): each CTA holds half of the columns of
+// all 128 positions, the same swizzled rows read as an MN-major B operand.  (N = 64 takes as long as
+// N = 128, 36 clocks, so tiles of 64 positions spend twice the time on s.)
+//
+// A pair loads 278 KB per tile where 147 KB are unique: the rest comes from L2.  q, one tile of keys,
+// its values and p fill shared memory, so every operand block has one place, and what bounds a
+// long call is its way round: freed by its UMMAs, copied (1900 .. 2100 clocks under load), waited for,
+// used: 3400 clocks a tile, of which the UMMAs take 2340 (measured: 2048 tokens x 2048 selected
+// 880 us, 1327 TFLOP/s; 64 sequences of up to 16384 positions 167 us, 4.6 TB/s).
 //
 // Work is one list of tiles over all segments (up to 128 / H consecutive tokens of a sequence;
 // one token with a selection), cut into equal runs, one per pair, so that sequences of any
@@ -28,9 +34,9 @@
 // Warp roles (1024 threads): warps 0..7 softmax, rescaling and epilogue (a row's 128 positions are
 // four threads': TMEM lane half x half of its columns), 8 and 9 issue the two products' UMMAs (of the
 // pair's even CTA; one warp for both waits for barriers as long as the tensor cores work), 10
-// finds the rows of the tiles ahead, 11 and 29..31 load the queries, 12..20 copy the K-major rows, a block of 64 columns
-// each, 21..28 the MN-major columns, 16 positions each (16-byte asynchronous copies, so pages of any
-// size and selected rows are alike; absent rows are zeros).  A copying warp has one place in shared
+// finds the rows of the tiles ahead, 11 and 29..31 load the queries, 12..20 copy the K-major rows, a
+// block of 64 columns each, 21..28 the MN-major columns, 16 positions each (16-byte asynchronous
+// copies, so pages of any size and selected rows are alike; absent rows are zeros).  A copying warp has one place in shared
 // memory: it waits until that is free, copies, waits for the data and announces it.  p goes
 // through two blocks of 64 positions that are freed and filled apart, so that the second product of
 // a tile follows on the last one's.  Every wait is bounded.
@@ -89,7 +95,7 @@ constexpr float kLag = 8.0f;                    // how far a score may pass the 
 constexpr int kMaxPairs = 76;
 constexpr int kMinTiles = 1;                    // tiles of a pair at least
 // What cutting costs a call, in tiles: partial sums written (2 us) and joined (8 us).  64 segments of
-// 16 tiles on 76 pairs: 62 us cut into runs of 13 or 14 tiles, XX us whole.
+// 16 tiles on 76 pairs: 62 us cut into runs of 13 or 14 tiles, 47 us whole.
 constexpr int kCutTiles = 6;
 // A piece's partial sums: o as the epilogue's warps hold it, in blocks of 32 rows x 16 columns
 // ([CTA][warp][8]), a block as [4][32 rows][4 columns], so that stores and the join's loads are whole
@@ -851,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
 // slot of some pair, the others the first slots of the pairs behind it.  A lane has a row of a block.
 // SPLIT 1: a warp takes a block and all its pieces, in their order.  SPLIT 8: eight warps share the
 // pieces of one block (warp w: w, w + 8, ..) and join their sums in the order of the warps; for
-// the few tokens whose pieces are many (one token of 4096 positions: 30 us with SPLIT 1, 20 with 8).
+// the few tokens whose pieces are many (one token of 4096 positions: 30 us with SPLIT 1, 19 with 8).
 constexpr int kJoinWarps = 4;
 constexpr int kJoinFew = 8;  // tokens up to which SPLIT is 8
 template <int SPLIT>

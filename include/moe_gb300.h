@@ -25,6 +25,8 @@
  *     gate's contract: outputs unchanged on failure).  MOE_ERR_CUDA means a launch failed;
  *     outputs are then undefined.  moe_last_error() returns a thread-local message naming
  *     the failed check.
+ *   - The operators of sparse attention (moe_cache_append, moe_indexer_scores, moe_indexer_topk,
+ *     moe_latent_attention) stand beside the layer: what they read and fill are paged caches.
  *   - Device-side waits are bounded: a kernel whose wait exceeds its limit stops, leaves
  *     its outputs undefined and records MOE_ERR_TIMEOUT in a per-device status word read
  *     by moe_device_status().
