@@ -11,8 +11,8 @@
 // sequence's tokens only.  Columns run in accumulators of up to 128 (whole tokens), four in
 // TMEM with four warps each, so that the epilogue (a maximum and half a packed multiply-add per
 // product) runs beside the UMMAs of the accumulators ahead and four of its warps share a scheduler
-// (4096 x 16384 in 643 us; before runs 770, 1288 with two and 32 columns loaded ahead, 1016 with four and 16 ahead,
-// 955 with eight accumulators of 64 columns).
+// (4096 x 16384 in 770 us; 1288 with two and 32 columns loaded ahead, 1016 with four and 16 ahead,
+// 955 with eight accumulators of 64 columns; 637 with the runs below).
 //
 // Work is one list of (tile, accumulator) over all groups and their sequences, as many tiles as the
 // tokens can see, cut into equal runs, one per CTA (units of as many tiles, some of them out of sight:
@@ -21,13 +21,12 @@
 // What bounds it is the epilogue's issue slots and latencies: an accumulator takes its four warps 2500
 // clocks and 1000 more until the next one is full (1510 TFLOP/s at 4096 x 16384, 60% of issue slots).
 //
-// Warp roles (768 threads, one CTA per SM): warps 0..15 epilogue (warp % 4 =
-// TMEM lane quarter, warp / 4 = accumulator), 16..19 key copies (16-byte asynchronous copies, so that
-// pages of any size and any order do; rows without a page or behind the end are zeros; a warp takes
-// every fourth tile, so that four are in flight, and looks its next one's pages up meanwhile), 20 and 21 issue the UMMAs of
-// every other accumulator (an issuer's waits and commits take as long as the UMMAs), 22 and 23
-// queries and weights.  Every
-// wait is bounded.
+// Warp roles (768 threads, one CTA per SM): warps 0..15 epilogue (warp % 4 = TMEM lane quarter, warp / 4 =
+// accumulator), 16..19 key copies (16-byte asynchronous copies, so that pages of any size and any order
+// do; rows without a page or behind the end are zeros; a warp takes every fourth tile, so that
+// four are in flight, and looks its next one's pages up meanwhile), 20 and 21 issue the UMMAs of every
+// other accumulator (an issuer's waits and commits take as long as the UMMAs), 22 and 23 queries and
+// weights.  Every wait is bounded.
 #include <mutex>
 
 #include "launch.h"

@@ -18,11 +18,13 @@
 // all 128 positions, the same swizzled rows read as an MN-major B operand.  (N = 64 takes as long as
 // N = 128, 36 clocks, so tiles of 64 positions spend twice the time on s.)
 //
-// A pair loads 278 KB per tile where 147 KB are unique: the rest comes from L2.  q, one tile of keys,
-// its values and p fill shared memory, so every operand block has one place, and what bounds a
-// long call is its way round: freed by its UMMAs, copied (1900 .. 2100 clocks under load), waited for,
-// used: 3400 clocks a tile, of which the UMMAs take 2340 (measured: 2048 tokens x 2048 selected
-// 880 us, 1327 TFLOP/s; 64 sequences of up to 16384 positions 167 us, 4.6 TB/s).
+// A pair loads 278 KB per tile where 147 KB are unique, the rest a second time from L2, and that is what
+// bounds a long call: 14.5 TB/s out of L2, where copies alone reach 15.5 (2048 tokens x 2048
+// selected 880 us, 1327 TFLOP/s; 64 sequences of up to 16384 positions 167 us, 4.6 TB/s of HBM).  q, one
+// tile of keys, its values and p fill shared memory, so every operand block has one place and goes
+// round once a tile: freed by its UMMAs, copied (1900 .. 2100 clocks under that load), waited for,
+// used: 3400 clocks a tile, of which the UMMAs take 2340.  Values copied out of the pair's keys instead
+// would have to wait for the last tile's second product and hold the keys' places meanwhile.
 //
 // Work is one list of tiles over all segments (up to 128 / H consecutive tokens of a sequence;
 // one token with a selection), cut into equal runs, one per pair, so that sequences of any
