@@ -364,17 +364,27 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
             constexpr int kPer = C::kRowBytes / 16;
             const int rows = (u1 - u0) * p.Hp;
             const int piece = tid % kPer;
+            const uint32_t dst = base + (piece / 8) * (C::kCols * 128);
+            const uint8_t* q = p.q + (long long)u0 * p.H * C::kRowBytes + piece * 16;
+            const float* w0 = p.w + (long long)u0 * p.H;
+            if (p.H == p.Hp) {  // (rows as they lie)
 #pragma unroll 8
-            for (int rr = tid / kPer; rr < rows; rr += 32 * kQueryWarps / kPer) {
-                const int t = rr / p.Hp, h = rr % p.Hp;
-                const long long at = ((long long)(u0 + t) * p.H + (h < p.H ? h : 0)) * C::kRowBytes;
-                copy16(base + (piece / 8) * (C::kCols * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4),
-                       p.q + at + piece * 16, h < p.H ? 16u : 0u);
-            }
-            copy_commit();
-            for (int i = tid; i < rows; i += 32 * kQueryWarps) {
-                const int t = i / p.Hp, h = i % p.Hp;
-                wts[i] = h < p.H ? __ldg(p.w + (long long)(u0 + t) * p.H + h) : 0.0f;
+                for (int rr = tid / kPer; rr < rows; rr += 32 * kQueryWarps / kPer)
+                    copy16(dst + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4), q + rr * C::kRowBytes, 16u);
+                copy_commit();
+                for (int i = tid; i < rows; i += 32 * kQueryWarps) wts[i] = __ldg(w0 + i);
+            } else {
+#pragma unroll 4
+                for (int rr = tid / kPer; rr < rows; rr += 32 * kQueryWarps / kPer) {
+                    const int t = rr / p.Hp, h = rr % p.Hp;
+                    copy16(dst + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4),
+                           q + (t * p.H + (h < p.H ? h : 0)) * C::kRowBytes, h < p.H ? 16u : 0u);
+                }
+                copy_commit();
+                for (int i = tid; i < rows; i += 32 * kQueryWarps) {
+                    const int t = i / p.Hp, h = i % p.Hp;
+                    wts[i] = h < p.H ? __ldg(w0 + t * p.H + h) : 0.0f;
+                }
             }
             for (int t = tid; t < u1 - u0; t += 32 * kQueryWarps) lens[t] = seq_length(p.seq, u0 + t);
             copy_wait<0>();
@@ -382,6 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
             mbar_arrive(qfull);
             do more = w.part(p, r);
             while (more && r.u0 == u0);
+            // the next group's on their way to L2
+            if (more)
+                for (int i = tid; i < (r.u1 - r.u0) * p.H * (C::kRowBytes / 128); i += 32 * kQueryWarps)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (long long)r.u0 * p.H * C::kRowBytes +
+                                                                 i * 128)
+                                 : "memory");
         }
     } else if (warp >= kMmaWarp) {
         // ================================ UMMA issuers ================================
