@@ -186,7 +186,9 @@ MOE_DEV void weigh16(const uint32_t* v, const float* w, float2& s0, float2& s1) 
     }
 }
 
-template <bool F8>
+// HP: the columns of a token, for loops of known length in the epilogue, or 0 for any number of them
+// (4096 x 16384 with 64 heads: 615 us with 0, 544 with 64; 3 ragged prompts with 32: 47 and 44).
+template <bool F8, int HP>
 __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     using C = Cfg<F8>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -508,26 +510,46 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                         uint32_t ta = ta0;
                         const float* w = w0;
                         float* out = out0 + pos;
-                        for (int i = 0; i < cnt; ++i, out += p.ld) {
-                            float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-                            int h = p.Hp;
-                            for (; h >= 32; h -= 32, ta += 32, w += 32) {
-                                uint32_t v[32];
-                                tmem_ld32(ta, v);
-                                tmem_ready(v);
-                                weigh16(v, w, s0, s1);
-                                weigh16(v + 16, w + 16, s0, s1);
-                            }
-                            if (h) {
-                                uint32_t v[16];
-                                tmem_ld16(ta, v);
-                                tmem_ready(v);
-                                weigh16(v, w, s0, s1);
-                                ta += 16;
-                                w += 16;
-                            }
+                        const auto put = [&](int i, float2 s0, float2 s1) {
                             const float sum = (s0.x + s0.y) + (s1.x + s1.y);
                             if (pos < p.n) *out = hidden < len[i] ? sum * ks : -__int_as_float(0x7F800000);
+                        };
+                        if constexpr (HP != 0) {
+#pragma unroll
+                            for (int i = 0; i < kAccCols / HP; ++i, out += p.ld) {
+                                if (i >= cnt) break;
+                                float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+#pragma unroll
+                                for (int h = i * HP; h < i * HP + HP; h += 32) {
+                                    uint32_t v[32];
+                                    tmem_ld32(ta + (uint32_t)h, v);
+                                    tmem_ready(v);
+                                    weigh16(v, w + h, s0, s1);
+                                    weigh16(v + 16, w + h + 16, s0, s1);
+                                }
+                                put(i, s0, s1);
+                            }
+                        } else {
+                            for (int i = 0; i < cnt; ++i, out += p.ld) {
+                                float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+                                int h = p.Hp;
+                                for (; h >= 32; h -= 32, ta += 32, w += 32) {
+                                    uint32_t v[32];
+                                    tmem_ld32(ta, v);
+                                    tmem_ready(v);
+                                    weigh16(v, w, s0, s1);
+                                    weigh16(v + 16, w + 16, s0, s1);
+                                }
+                                if (h) {
+                                    uint32_t v[16];
+                                    tmem_ld16(ta, v);
+                                    tmem_ready(v);
+                                    weigh16(v, w, s0, s1);
+                                    ta += 16;
+                                    w += 16;
+                                }
+                                put(i, s0, s1);
+                            }
                         }
                         tc_fence_before();
                         __syncwarp();
@@ -549,12 +571,12 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     }
 }
 
-template <bool F8>
+template <bool F8, int HP>
 cudaError_t run(const ScoresArgs& a, cudaStream_t s) {
     using C = Cfg<F8>;
     static DeviceOnce once;
     const cudaError_t e = once.run([] {
-        return cudaFuncSetAttribute(scores_kernel<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(scores_kernel<F8, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     C::kSmemBytes);
     });
     if (e != cudaSuccess) return e;
@@ -579,14 +601,17 @@ cudaError_t run(const ScoresArgs& a, cudaStream_t s) {
     // no more CTAs than entries of the list where every token sees all n positions
     const long long most = (a.T + p.tt - 1) / p.tt * ((a.n + kKeys - 1) / kKeys) * ((p.tt + p.gtok - 1) / p.gtok);
     const long long grid = most < num_sms() ? most : num_sms();
-    return launch_kernel(scores_kernel<F8>, dim3((unsigned)grid), dim3(kThreads), (size_t)C::kSmemBytes,
+    return launch_kernel(scores_kernel<F8, HP>, dim3((unsigned)grid), dim3(kThreads), (size_t)C::kSmemBytes,
                          s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
-    return a.key_scales ? run<true>(a, s) : run<false>(a, s);
+    const int columns = (a.H + 15) / 16 * 16;
+    if (a.key_scales)
+        return columns == 64 ? run<true, 64>(a, s) : columns == 32 ? run<true, 32>(a, s) : run<true, 0>(a, s);
+    return columns == 64 ? run<false, 64>(a, s) : columns == 32 ? run<false, 32>(a, s) : run<false, 0>(a, s);
 }
 
 cudaError_t read_scores_status(unsigned int* out, int clear, cudaStream_t s) {
