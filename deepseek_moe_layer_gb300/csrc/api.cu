@@ -1083,6 +1083,14 @@ int moe_cache_append(const moe_append_args_t* args, moe_stream_t stream) {
         MOE_CHECK(a.q_token % 8 == 0 && a.q_head % 8 == 0 && a.q_out_token % 8 == 0 &&
                       a.q_out_head % 8 == 0,
                   "strides of q and q_out must be multiples of 8");
+        // the axis of the smaller step inside a step of the other one, and no two rows on each other
+        // (in 128 bits: strides are any number)
+        const auto step = [](int64_t v) { return v < 0 ? -(__int128)v : (__int128)v; };
+        const __int128 st = step(a.q_out_token), sh = step(a.q_out_head), R = a.rope_cols;
+        MOE_CHECK((a.T <= 1 || st >= (a.H > 1 && sh <= st ? sh * (a.H - 1) + R : R)) &&
+                      (a.H <= 1 || sh >= (a.T > 1 && st < sh ? st * (a.T - 1) + R : R)),
+                  "rows of q_out overlap: strides %lld and %lld for %lld tokens, %d heads, %d columns",
+                  (long long)a.q_out_token, (long long)a.q_out_head, (long long)a.T, a.H, a.rope_cols);
     }
     MOE_CHECK(a.T == 0 || (a.x && a.slots && a.cache && (!a.norm_cols || a.norm_weight) &&
                            (!a.rope_cols || (a.positions && a.inv_freq)) && (!a.q || a.q_out)),

@@ -52,6 +52,19 @@ def test_append_refusals(kw, msg):
     assert rc == binding.MOE_ERR_INVALID and msg in err, err
 
 
+@pytest.mark.parametrize("T,H,token,head,fits", [
+    (4, 8, 512, 64, True), (4, 8, 8 * 576, 576, True), (4, 8, 64, 256, True), (1, 8, 0, 64, True),
+    (4, 1, 64, 0, True), (1, 1, 0, 0, True), (4, 8, -512, -64, True),
+    (4, 8, 0, 64, False), (4, 8, 512, 0, False), (4, 8, 504, 64, False), (4, 8, 512, 56, False),
+    (4, 8, 64, 248, False), (4, 8, 512, 512, False), (4, 1, 56, 0, False), (1, 8, 0, 56, False),
+    (4, 8, 1 << 62, (1 << 62) - 8, False), (4, 8, -(1 << 63), 64, True),
+])
+def test_append_query_rows_do_not_lie_on_each_other(T, H, token, head, fits):
+    # (a call whose rows fit goes on to the next check: slots that are misaligned)
+    rc, err = _append(T=T, H=H, q_out_token=token, q_out_head=head, slots=FAKE + 4)
+    assert rc == binding.MOE_ERR_INVALID and ("aligned to" if fits else "overlap") in err, err
+
+
 def test_append_nothing_to_do():
     assert _append(T=0, x=None, slots=None, q=None)[0] == binding.MOE_OK
     rc, err = _rc(binding.lib().moe_cache_append(None, None))
