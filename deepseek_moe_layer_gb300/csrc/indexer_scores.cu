@@ -186,7 +186,14 @@ MOE_DEV void weigh16(const uint32_t* v, const float* w, float2& s0, float2& s1) 
     }
 }
 
-// HP: the columns of a token, for loops of known length in the epilogue, or 0 for any number of them
+// The products of heads that are not there: 0, where an infinite key makes them NaN.
+MOE_DEV void clear_last(uint32_t* v, int n) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (e >= 16 - n) v[e] = 0u;
+}
+
+// HP: the heads, for loops of known length in the epilogue, or 0 for any number of them
 // (4096 x 16384 with 64 heads: 615 us with 0, 544 with 64; 3 ragged prompts with 32: 47 and 44).
 template <bool F8, int HP>
 __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
@@ -460,15 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         const uint32_t mine = warp >> 2;  // its accumulator
         const uint32_t ta0 = tmem + ((uint32_t)(quarter * 32) << 16) + mine * kAccCols;
         // what no token of a part can see, 4096 positions per warp
-        const int runs = (p.n + 4095) / 4096;
+        const int runs = (int)(((long long)p.n + 4095) / 4096);
         for (long long f = (long long)blockIdx.x * kEpiWarps + warp; f < (long long)tokens * runs;
              f += (long long)gridDim.x * kEpiWarps) {
             const int t = (int)(f / runs), b = seq_of(p.seq, t), u0 = t - t % p.tt;
-            const int t0 = p.seq.cu ? max(u0, p.seq.cu[b]) : t;
+            const int t0 = p.seq.cu ? min(t, max(u0, p.seq.cu[b])) : t;
             Part r;
             part_at(p, tokens, t0, r);
-            const int j0 = max((int)(f % runs) * 4096, r.tiles * kKeys), j1 = min(p.n, (int)(f % runs) * 4096 + 4096);
-            for (int j = j0 + lane; j < j1; j += 32)
+            const int at = (int)(f % runs) * 4096, j1 = at + min(p.n - at, 4096);
+            for (int j = max(at, r.tiles * kKeys) + lane; j < j1; j += 32)
                 p.out[(long long)t * p.ld + j] = -__int_as_float(0x7F800000);
         }
         uint32_t it = 0, acc = 0;
@@ -530,6 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                                 put(i, s0, s1);
                             }
                         } else {
+                            const int absent = p.Hp - p.H;  // of a token's last 16 columns
                             for (int i = 0; i < cnt; ++i, out += p.ld) {
                                 float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
                                 int h = p.Hp;
@@ -537,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                                     uint32_t v[32];
                                     tmem_ld32(ta, v);
                                     tmem_ready(v);
+                                    if (h == 32 && absent) clear_last(v + 16, absent);
                                     weigh16(v, w, s0, s1);
                                     weigh16(v + 16, w + 16, s0, s1);
                                 }
@@ -544,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
                                     uint32_t v[16];
                                     tmem_ld16(ta, v);
                                     tmem_ready(v);
+                                    if (absent) clear_last(v, absent);
                                     weigh16(v, w, s0, s1);
                                     ta += 16;
                                     w += 16;
@@ -608,10 +618,9 @@ cudaError_t run(const ScoresArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
-    const int columns = (a.H + 15) / 16 * 16;
     if (a.key_scales)
-        return columns == 64 ? run<true, 64>(a, s) : columns == 32 ? run<true, 32>(a, s) : run<true, 0>(a, s);
-    return columns == 64 ? run<false, 64>(a, s) : columns == 32 ? run<false, 32>(a, s) : run<false, 0>(a, s);
+        return a.H == 64 ? run<true, 64>(a, s) : a.H == 32 ? run<true, 32>(a, s) : run<true, 0>(a, s);
+    return a.H == 64 ? run<false, 64>(a, s) : a.H == 32 ? run<false, 32>(a, s) : run<false, 0>(a, s);
 }
 
 cudaError_t read_scores_status(unsigned int* out, int clear, cudaStream_t s) {

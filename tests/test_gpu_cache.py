@@ -332,6 +332,48 @@ def test_scores_not_finite():
     assert bool(binding.indexer_scores(q, w, bt.cache, bt.table, bt.lengths, 200).isnan().all())
 
 
+@pytest.mark.parametrize("H", [5, 20, 33, 50, 64])
+def test_scores_infinite_key(H):
+    # the products of all heads are infinite: +inf where a head's is and its weight is not 0, 0 where
+    # all are -inf; what pads the heads to a multiple of 16 must not be in it
+    g = gen(7)
+    bt = Batch([200], [1], 64, 128, g)
+    q, w = randn(1, H, 128, g=g, dtype=BF), torch.rand(1, H, generator=g, device=DEV) + 0.5
+    q[0, :, 3] = 1.0
+    for value, want in ((INF, INF), (-INF, 0.0)):
+        bt.rows[bt.slots[0][7], 3] = value
+        out = binding.indexer_scores(q, w, bt.cache, bt.table, bt.lengths, 200)
+        assert float(out[0, 7]) == want and int(out.isfinite().sum()) == 200 - (want == INF)
+
+
+def test_scores_longest_row():
+    # 2^31 - 512 positions, of which 130 are there
+    g = gen(8)
+    bt = Batch([130], [1], 64, 128, g)
+    n = 2 ** 31 - 512
+    q, w = randn(1, 64, 128, g=g, dtype=BF), randn(1, 64, g=g)
+    out = binding.indexer_scores(q, w, bt.cache, bt.table, bt.lengths, n, out=torch.zeros(1, n, device=DEV))
+    scores_check(out[:, :5000], bt, q, w, None, 5000)
+    assert all(bool((part == -INF).all()) for part in out[0, 130:].split(1 << 28))
+
+
+def test_ends_of_sequences_that_do_not_ascend():
+    # no results to speak of, but calls that end and rows behind the last end as they were
+    g = gen(9)
+    bt = Batch([300, 200, 90], [3, 2, 4], 16, 576, g)
+    keys = bt.cache[..., :128].contiguous()
+    q, qi, w = (randn(9, 16, n, g=g, dtype=BF) for n in (576, 128, 1))
+    for cu in ([5, 9, 2, 7], [1000000, -5, 1000000, 7], [-9, 2, 2 ** 31 - 1, 3], [7, 7, 7, 7], [4, 3, 2, -1]):
+        kept = max(0, min(9, cu[3]))
+        o = torch.full((9, 16, 512), 5.0, dtype=BF, device=DEV)
+        binding.latent_attention(q, bt.cache, bt.table, bt.lengths, 0.1, cu_tokens=ints(cu), out=o)
+        s = torch.full((9, 300), 5.0, device=DEV)
+        binding.indexer_scores(qi, w[..., 0].float().contiguous(), keys, bt.table, bt.lengths, 300,
+                               cu_tokens=ints(cu), out=s)
+        assert bool((s[kept:] == 5.0).all()) and (kept > 0 or bool((o == 5.0).all()))
+        binding.device_status()
+
+
 # ---- attention ----------------------------------------------------------------------------------
 
 def attention_check(out, lse, bt, q, scale, inds=None):
