@@ -554,6 +554,27 @@ def test_attention_not_finite_scores():
     close(out[0], mean.mean(0).expand(128, 512), (2.0 ** -8 + 300 * U) * 2 * mean.abs().mean(0))
 
 
+@pytest.mark.parametrize("shape", ["even", "one long", "many short", "drafts"])
+@pytest.mark.parametrize("count", [75, 76, 77, 151, 152, 153, 305])
+def test_runs_of_the_list_of_tiles(count, shape):
+    # as many sequences as there are CTA pairs or CTAs, one fewer and one more: runs that begin and end
+    # at, before and behind the borders of sequences
+    g = gen(count)
+    lens = {"even": [256] * count, "one long": [9000] + [130] * (count - 1), "drafts": [300] * count,
+            "many short": [(37 * i) % 129 for i in range(count)]}[shape]
+    new = [1 + i % 3 if shape == "drafts" else 1 for i in range(count)]
+    bt = Batch(lens, new, 32, 576, g)
+    q, qi, w = randn(bt.T, 20, 576, g=g, dtype=BF), randn(bt.T, 32, 128, g=g, dtype=BF), randn(bt.T, 32, g=g)
+    out, lse = binding.latent_attention(q, bt.cache, bt.table, bt.lengths, 0.1, cu_tokens=bt.cu_or_none(), want_lse=True)
+    attention_check(out, lse, bt, q, 0.1)
+    keys = bt.cache[..., :128].contiguous()
+    n = max(lens)
+    s = binding.indexer_scores(qi, w, keys, bt.table, bt.lengths, n, cu_tokens=bt.cu_or_none())
+    bt.rows = keys.view(-1, 128)
+    scores_check(s, bt, qi, w, None, n)
+    binding.device_status()
+
+
 # ---- a cache behind 32-bit offsets, graphs, streams, failed launches ------------------------------
 
 def test_rows_behind_32_bit_offsets():
