@@ -12,14 +12,17 @@
 // TMEM with four warps each, so that the epilogue (a maximum and half a packed multiply-add per
 // product) runs beside the UMMAs of the accumulators ahead and four of its warps share a scheduler
 // (4096 x 16384 in 770 us; 1288 with two and 32 columns loaded ahead, 1016 with four and 16 ahead,
-// 955 with eight accumulators of 64 columns; 637 with the runs below).
+// 955 with eight accumulators of 64 columns; 637 with the runs below, 548 now).
 //
 // Work is one list of (tile, accumulator) over all groups and their sequences, as many tiles as the
 // tokens can see, cut into equal runs, one per CTA (units of as many tiles, some of them out of sight:
 // 64 sequences of 8192 to 32768 positions 59 us, 42 so).
 //
-// What bounds it is the epilogue's issue slots and latencies: an accumulator takes its four warps 2500
-// clocks and 1000 more until the next one is full (1510 TFLOP/s at 4096 x 16384, 60% of issue slots).
+// What bounds long prompts is the epilogue's instructions: 59% of issue slots and 55% of the pipe that
+// takes the maxima at half rate, the tensor cores 35% (4096 x 16384 with 64 heads, e4m3: 548 us, 1755
+// TFLOP/s).  Columns loaded ahead with more registers for it (563), an issuer per accumulator (563), an
+// accumulator handed back before its last columns are weighed (543, but 64 sequences 41 -> 44) gain
+// nothing.  64 sequences of up to 32768 positions: 41 us, of which 8 are start and end; HBM at 5.5 TB/s.
 //
 // Warp roles (768 threads, one CTA per SM): warps 0..15 epilogue (warp % 4 = TMEM lane quarter, warp / 4 =
 // accumulator), 16..19 key copies (16-byte asynchronous copies, so that pages of any size and any order
