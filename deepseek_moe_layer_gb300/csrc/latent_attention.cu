@@ -31,7 +31,7 @@
 // lengths fill the device; a segment cut apart leaves partial sums (m, l, o in fp32) that a second
 // kernel joins in the order of the pairs: equal calls give equal bits.  Where whole segments give
 // a longest run that is no longer than an equal one and the cost of cutting (kCutTiles), runs are
-// whole segments.
+// whole segments; where there are two pairs or more for each, pieces of one segment each (kTries).
 //
 // Warp roles (1024 threads): warps 0..7 softmax, rescaling and epilogue (a row's 128 positions are
 // four threads': TMEM lane half x half of its columns), 8 and 9 issue the two products' UMMAs (of the
@@ -99,6 +99,11 @@ constexpr int kMinTiles = 1;                    // tiles of a pair at least
 // What cutting costs a call, in tiles: partial sums written (2 us) and joined (8 us).  64 segments of
 // 16 tiles on 76 pairs: 62 us cut into runs of 13 or 14 tiles, 47 us whole.
 constexpr int kCutTiles = 6;
+// What a run pays for holding the border of two segments, in tiles: a piece's partial sums written, the next
+// one's queries and first rows (17 sequences of up to 3001 positions: runs of 4 tiles take 37000 clocks within
+// a segment, 54000 across a border).  So pieces of one segment each, up to so many tiles longer than an equal
+// run, go before runs across borders where the pairs suffice for them: 38 us without, 34 with.
+constexpr int kTries = 4;
 // A piece's partial sums: o as the epilogue's warps hold it, in blocks of 32 rows x 16 columns
 // ([CTA][warp][8]), a block as [4][32 rows][4 columns], so that stores and the join's loads are whole
 // lines; then m and l of the 128 rows.
@@ -132,13 +137,17 @@ MOE_DEV void record_timeout(volatile int* abort) {
 struct Seg {
     int t, n, b, see, len, tiles;
 };
-MOE_DEV Seg segment(const Params& p, const Sequences& q, int t, int b) {
+// `near`: the lengths of tokens from 0 on in shared memory, or nullptr.
+MOE_DEV Seg segment(const Params& p, const Sequences& q, int t, int b, const volatile int32_t* near = nullptr) {
     Seg s;
     s.t = t;
     s.b = b;
     s.n = max(1, min(p.tt, seq_end(q, b) - t));
     s.see = 0;
-    for (int i = 0; i < s.n; ++i) s.see = max(s.see, seq_length(q, t + i));
+    if (near)
+        for (int i = 0; i < s.n; ++i) s.see = max(s.see, min(q.most, near[t + i]));
+    else
+        for (int i = 0; i < s.n; ++i) s.see = max(s.see, seq_length(q, t + i));
     s.len = p.inds ? min(s.see, p.k) : s.see;
     s.tiles = max(1, (s.len + kTile - 1) / kTile);
     return s;
@@ -239,17 +248,20 @@ MOE_DEV uint32_t finite2(uint32_t v) {
 
 // Tiles of the tokens a .. z - 1 (of those that begin a segment).
 template <class F>
-MOE_DEV void for_segments(const Params& p, const Sequences& q, int a, int z, F&& f) {
+MOE_DEV void for_segments(const Params& p, const Sequences& q, const volatile int32_t* near, int a, int z, F&& f) {
     if (a >= z) return;
     int b = seq_of(q, a);
     for (int t = a; t < z; ++t) {
         if (!q.cu) b = t;
         else while (b < q.B - 1 && t >= seq_end(q, b)) ++b;
         const int first = q.cu ? q.cu[b] : t;
-        if ((t - first) % p.tt == 0) f(segment(p, q, t, b));
+        if ((t - first) % p.tt == 0) f(segment(p, q, t, b, near));
     }
 }
 
+// FEW: there may be at most half as many segments as pairs (the code of their pieces alone costs the other
+// calls 0.6 us of set-up: one token of 4096 positions 18.6 us without, 19.2 with).
+template <bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
@@ -271,12 +283,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
 
     // ---- set-up ----
     // tiles, segments (from bit 40 on) and the longest segment of this thread's tokens; the sequences'
-    // ends are searched in shared memory, where the rows of the first tiles will be
+    // ends and the tokens' lengths are looked at in shared memory, where the first rows will be
     Sequences seq = p.seq;
+    const volatile int32_t* near = nullptr;
     if (seq.cu && seq.B < 4 * kVBlock / 4) {
         int32_t* ends = reinterpret_cast<int32_t*>(smem + kVOff);
+        const bool hold = FEW && seq.T <= kThreads;
+        const int length = hold && (int)threadIdx.x < seq.T ? __ldg(p.seq.lengths + threadIdx.x) : 0;
         for (int i = threadIdx.x; i <= seq.B; i += kThreads) ends[i] = __ldg(p.seq.cu + i);
         seq.cu = ends;
+        if (hold) {
+            int32_t* lengths = reinterpret_cast<int32_t*>(smem + kKOff);
+            lengths[threadIdx.x] = length;
+            near = lengths;
+        }
         __syncthreads();
     }
     const int tokens = seq_tokens(seq);
@@ -284,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
     const int a = min(tokens, (int)threadIdx.x * per), z = min(tokens, a + per);
     unsigned long long mine = 0;
     int longest = 0;
-    for_segments(p, seq, a, z, [&](const Seg& s) {
+    for_segments(p, seq, near, a, z, [&](const Seg& s) {
         mine += (unsigned)s.tiles + (1ull << 40);
         longest = max(longest, s.tiles);
     });
@@ -357,6 +377,50 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             const unsigned longest_run = small ? (segs + pairs - 1) / pairs * top : 0xFFFFFFFFu;
             const bool whole = small && longest_run <= fair + kCutTiles &&
                                (segs <= pairs || (long long)top * segs == total);
+            // pieces of one segment each, of up to fair + 1 .. fair + kTries tiles: how many each would give
+            // (in 16 bits), and the shortest that the pairs suffice for
+            int most = 0;
+            if (FEW && !whole && segs > 1 && 2 * segs <= pairs && tokens <= kThreads && total < (1 << 16)) {
+                int shift = 0;
+                unsigned long long before2 = 0, pieces = 0;
+                const unsigned tiles = (unsigned)(mine & kTiles);
+                if (mine) {  // (a thread has one token)
+#pragma unroll
+                    for (int c = 0; c < kTries; ++c)
+                        pieces += (unsigned long long)((tiles + fair + c) / (fair + 1 + c)) << (16 * c);
+                }
+                unsigned long long incl2 = pieces;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned long long v = __shfl_up_sync(0xFFFFFFFFu, incl2, o);
+                    if (lane >= o) incl2 += v;
+                }
+                unsigned long long all2 = __shfl_sync(0xFFFFFFFFu, incl2, 31);
+                const int warps = (tokens + 31) / 32;  // that have tokens
+                if (warps > 1) {
+                    unsigned long long* scan2 = reinterpret_cast<unsigned long long*>(smem + kXchOff + 256);
+                    if (lane == 31) scan2[warp] = incl2;
+                    asm volatile("bar.sync 2, %0;" ::"r"(32 * warps) : "memory");
+                    all2 = 0;
+                    for (int i = 0; i < warps; ++i) {
+                        if (i < warp) before2 += scan2[i];
+                        all2 += scan2[i];
+                    }
+                }
+                before2 += incl2 - pieces;
+#pragma unroll
+                for (int c = kTries - 1; c >= 0; --c)
+                    if (((all2 >> (16 * c)) & 0xFFFFu) <= pairs) {
+                        most = (int)fair + 1 + c;
+                        shift = 16 * c;
+                    }
+                const int i = pair - (int)((before2 >> shift) & 0xFFFFu), n = (int)((pieces >> shift) & 0xFFFFu);
+                if (most && mine && i >= 0 && i < n) {
+                    for_segments(p, seq, near, a, z, [&](const Seg& s) { sched->s = s; });
+                    sched->tile = (int)tiles * i / n;
+                    sched->segments = 1;
+                    sched->left = (int)tiles * (i + 1) / n - (int)tiles * i / n;
+                }
+            }
             long long lo = 0, hi = 0, mine0, mine1;
             if (whole) {
                 if ((unsigned)pair < whole_runs) {
@@ -379,9 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                 mine0 = (long long)(before & kTiles);
                 mine1 = (long long)((before + mine) & kTiles);
             }
-            if (lo < hi && mine0 <= lo && lo < mine1) {
+            if (!most && lo < hi && mine0 <= lo && lo < mine1) {
                 long long at = mine0;
-                for_segments(p, seq, a, z, [&](const Seg& s) {
+                for_segments(p, seq, near, a, z, [&](const Seg& s) {
                     const int n = whole ? 1 : s.tiles;
                     if (at <= lo && lo < at + n) {
                         sched->s = s;
@@ -996,8 +1060,10 @@ cudaError_t attention_plan(AttentionArgs& a) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= DeviceOnce::kMaxDevices) return cudaErrorInvalidDevice;
     e = once.run([&] {
-        cudaError_t err = cudaFuncSetAttribute(
-            attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        cudaError_t err = cudaSuccess;
+        for (auto kernel : {attention_kernel<false>, attention_kernel<true>})
+            if (err == cudaSuccess)
+                err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (err != cudaSuccess) return err;
         // as many pairs as the device can hold at once (an SM left over in a GPC takes none)
         cudaLaunchConfig_t cfg = {};
@@ -1011,7 +1077,7 @@ cudaError_t attention_plan(AttentionArgs& a) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        err = cudaOccupancyMaxActiveClusters(&n, attention_kernel, &cfg);
+        err = cudaOccupancyMaxActiveClusters(&n, attention_kernel<true>, &cfg);
         if (err == cudaSuccess) resident[dev] = n > 0 ? n : 1;
         return err;
     });
@@ -1033,7 +1099,10 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_kernel, params_of(a, a.pairs));
+    // (of several tokens a segment may hold some, so there may be as few segments as sequences)
+    const bool few = a.T > 1 && 2 * (a.inds || !a.cu ? a.T : (long long)a.B) <= a.pairs;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, few ? attention_kernel<true> : attention_kernel<false>,
+                                             params_of(a, a.pairs));
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -554,6 +554,24 @@ def test_attention_not_finite_scores():
     close(out[0], mean.mean(0).expand(128, 512), (2.0 ** -8 + 300 * U) * 2 * mean.abs().mean(0))
 
 
+@pytest.mark.parametrize("lens,new,H", [
+    ([3001, 2000, 2700, 1500, 1, 2999, 900, 2222, 128, 129, 1777, 2048, 2600, 3000, 640, 2500, 1999], [4] * 17, 16),
+    ([5000, 5000], [1, 1], 128), ([9000, 100, 3000], [1, 2, 9], 32), ([2560] * 30, [1] * 30, 128),
+    ([1280 + 128 * i for i in range(20)], [1] * 20, 64), ([640] * 50 + [4000], [1] * 51, 128),
+    ([0, 8000, 0, 7000, 0], [1, 1, 1, 1, 1], 100),
+])
+def test_attention_of_a_few_long_sequences(lens, new, H):
+    # segments of several tiles, fewer than CTA pairs: pieces of one segment each, or runs across them
+    g = gen(sum(lens))
+    bt = Batch(lens, new, 64, 576, g)
+    q = randn(bt.T, H, 576, g=g, dtype=BF)
+    out, lse = binding.latent_attention(q, bt.cache, bt.table, bt.lengths, 0.1, cu_tokens=bt.cu_or_none(), want_lse=True)
+    attention_check(out, lse, bt, q, 0.1)
+    again = binding.latent_attention(q, bt.cache, bt.table, bt.lengths, 0.1, cu_tokens=bt.cu_or_none())
+    assert torch.equal(again, out)
+    binding.device_status()
+
+
 @pytest.mark.parametrize("shape", ["even", "one long", "many short", "drafts"])
 @pytest.mark.parametrize("count", [75, 76, 77, 151, 152, 153, 305])
 def test_runs_of_the_list_of_tiles(count, shape):
