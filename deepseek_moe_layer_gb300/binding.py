@@ -470,6 +470,12 @@ def _fits(t, dtype, shape, dev):
             and t.get_device() == dev and t.is_contiguous())
 
 
+def _address(t):
+    """The address of a tensor that may be left out: None without one.  Never 0 for one that is there:
+    the library takes NULL for "not given", and torch gives 0 as an empty tensor's address."""
+    return None if t is None else t.data_ptr() or 256
+
+
 def _need_vector(t, dtype, name, n, device):
     _need(t, dtype, name, device)
     if t.shape != (n,):
@@ -589,7 +595,6 @@ def indexer_scores(q, weights, keys, block_table, lengths, n, key_scales=None, c
         _need(key_scales, torch.float32, "key_scales", device)
         if key_scales.shape not in (keys.shape[:2], (*keys.shape[:2], 1)):
             raise ValueError(f"key_scales must be {(*keys.shape[:2], 1)}, not {tuple(key_scales.shape)}")
-        key_scales = key_scales.data_ptr()
     n = int(n)
     if out is None:
         out = _empty((T, n), torch.float32, device, stream)
@@ -601,7 +606,7 @@ def indexer_scores(q, weights, keys, block_table, lengths, n, key_scales=None, c
             raise ValueError(f"out must be [{T}, {n}] on {device} with unit stride along its rows")
         ld = out.stride(0) if T > 1 else n
     _check((_lib or lib()).moe_indexer_scores(
-        q.data_ptr(), weights.data_ptr(), T, H, ctypes.byref(c), key_scales,
+        q.data_ptr(), weights.data_ptr(), T, H, ctypes.byref(c), _address(key_scales),
         None if cu_tokens is None else cu_tokens.data_ptr(), lengths.data_ptr(), n, out.data_ptr(),
         ld, _raw_stream(q, stream)))
     return out

@@ -301,7 +301,8 @@ typedef struct {
  *   -inf for the other j < n and for positions whose page is not there.
  *   q [T, H, 128] and the cache's rows [128] bf16, products and sums in fp32; or, with key_scales
  *   (fp32, one per cache row) both e4m3, s_j the key's scale (1 without; a query's own scale goes into
- *   its weights).  weights fp32 [T, H], of any sign.  1 <= H <= 128.  out fp32 [T, ld], n positions
+ *   its weights).  key_scales alone says which: of an e4m3 cache without pages it is not read, but must
+ *   not be NULL either.  weights fp32 [T, H], of any sign.  1 <= H <= 128.  out fp32 [T, ld], n positions
  *   per row (ld >= n, in elements); what lies between n and ld is left as it was.
  * Errors: MOE_ERR_INVALID for NULL pointers, H outside [1, 128], n outside [0, 2^31 - 512], ld < n,
  * a cache with page < 1, 2^31 rows or more, or more than 2^31 - 512 positions per sequence,

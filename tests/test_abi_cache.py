@@ -245,3 +245,35 @@ def _call_attention(**kw):
 def test_binding_attention(kw, exc, msg):
     with pytest.raises(exc, match=msg):
         _call_attention(**kw)
+
+
+# ---- what the binding hands to the library --------------------------------------------------------
+
+class _Recorder:
+    """Stands in for the library: keeps each call's arguments and answers MOE_OK."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 1 << 20 if name.endswith("_bytes") else 0
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    r = _Recorder()
+    monkeypatch.setattr(binding, "_lib", r)
+    monkeypatch.setattr(binding, "_raw_stream", lambda t, stream: 0)
+    return r.calls
+
+
+def test_scores_of_an_empty_8_bit_cache_stay_8_bit(calls):
+    # an empty tensor's address is 0, and without key_scales the library takes q for bf16: twice its bytes
+    _call_scores(q=z(3, 64, 128, dtype=F8), keys=z(0, 64, 128, dtype=F8), key_scales=z(0, 64, 1, dtype=F32))
+    _call_scores(q=z(3, 64, 128, dtype=F8), keys=z(4, 64, 128, dtype=F8), key_scales=z(4, 64, dtype=F32))
+    _call_scores()
+    scales = [args[5] for name, args in calls]
+    assert scales[0] and scales[1] and scales[2] is None

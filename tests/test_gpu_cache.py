@@ -321,6 +321,19 @@ def test_scores_rows_behind_the_last_sequence_and_pages_that_are_not_there():
         assert torch.equal(got[:3, keep], out[:3, keep]) and torch.equal(got[3:5], out[3:5])
 
 
+@pytest.mark.parametrize("f8", [False, True])
+def test_scores_of_a_cache_without_pages(f8):
+    g = gen(21)
+    dtype = F8 if f8 else BF
+    q, w = randn(3, 64, 128, g=g).to(dtype), randn(3, 64, g=g)
+    keys = torch.empty(0, 16, 128, dtype=dtype, device=DEV)
+    ks = torch.empty(0, 16, 1, device=DEV) if f8 else None
+    out = binding.indexer_scores(q, w, keys, torch.zeros(3, 20, dtype=I32, device=DEV), ints([300, 1, 77]), 310,
+                                 key_scales=ks)
+    assert bool((out == -INF).all())
+    binding.device_status()
+
+
 def test_scores_not_finite():
     g = gen(6)
     bt = Batch([200], [1], 64, 128, g)
