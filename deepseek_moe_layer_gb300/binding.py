@@ -505,6 +505,8 @@ def cache_append(x, slots, cache, scales=None, norm_weight=None, norm_bias=None,
     pages, page, _ = cache.shape
     _need(cache, torch.bfloat16 if scales is None else torch.float8_e4m3fn, "cache", x.device)
     if scales is not None:
+        if W % 128:
+            raise ValueError(f"rows of an e4m3 cache must have a multiple of 128 columns, not {W}")
         _need_out(scales, torch.float32, "scales", (pages, page, W // 128), x.device)
     n = R = at = 0
     weight = bias = pos = freq = None
@@ -548,7 +550,7 @@ def cache_append(x, slots, cache, scales=None, norm_weight=None, norm_bias=None,
     elif q_out is not None:
         raise ValueError("q_out given without q")
     a = AppendArgs(x.data_ptr(), T, x.stride(0) if T > 1 else W, W, slots.data_ptr(),
-                   cache.data_ptr(), None if scales is None else scales.data_ptr(), pages * page,
+                   cache.data_ptr(), _address(scales), pages * page,
                    weight, bias, n, eps, pos, freq, R, at, int(bool(interleaved)), src, dst, H, *st)
     _check((_lib or lib()).moe_cache_append(ctypes.byref(a), _raw_stream(x, stream)))
     return cache if q is None else (cache, q_out)

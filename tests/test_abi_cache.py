@@ -277,3 +277,18 @@ def test_scores_of_an_empty_8_bit_cache_stay_8_bit(calls):
     _call_scores()
     scales = [args[5] for name, args in calls]
     assert scales[0] and scales[1] and scales[2] is None
+
+
+@pytest.mark.parametrize("W", [8, 64, 120, 192, 576])
+def test_append_8_bit_rows_are_whole_blocks(calls, W):
+    # (below 128 columns the scales are an empty tensor, whose address is 0: a cache of bf16 rows to the library)
+    with pytest.raises(ValueError, match="multiple of 128"):
+        binding.cache_append(z(3, W), z(3, dtype=I64), z(2, 64, W, dtype=F8), scales=z(2, 64, W // 128, dtype=F32))
+    assert not calls
+
+
+@pytest.mark.parametrize("pages,f8", [(0, True), (2, True), (2, False)])
+def test_append_says_which_type_its_cache_has(calls, pages, f8):
+    binding.cache_append(z(3, 256), z(3, dtype=I64), z(pages, 64, 256, dtype=F8 if f8 else BF),
+                         scales=z(pages, 64, 2, dtype=F32) if f8 else None)
+    assert (calls[0][1][0]._obj.scales is not None) == f8
