@@ -1092,7 +1092,7 @@ int moe_cache_append(const moe_append_args_t* args, moe_stream_t stream) {
                   "rows of q_out overlap: strides %lld and %lld for %lld tokens, %d heads, %d columns",
                   (long long)a.q_out_token, (long long)a.q_out_head, (long long)a.T, a.H, a.rope_cols);
     }
-    MOE_CHECK(a.T == 0 || (a.x && a.slots && a.cache && (!a.norm_cols || a.norm_weight) &&
+    MOE_CHECK(a.T == 0 || (a.x && a.slots && (a.cache || a.rows == 0) && (!a.norm_cols || a.norm_weight) &&
                            (!a.rope_cols || (a.positions && a.inv_freq)) && (!a.q || a.q_out)),
               "NULL pointer argument");
     MOE_CHECK(aligned(a.x, 16) && aligned(a.cache, 16) && aligned(a.q, 16) && aligned(a.q_out, 16),

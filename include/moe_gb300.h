@@ -249,8 +249,9 @@ int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t ld
  *   elements, multiples of 8), rotated in the same way into q_out (strides q_out_token,
  *   q_out_head, by which no two rows may lie on each other); q_out may be q itself, with q's strides,
  *   and must not overlap it otherwise.  Tokens without a slot are rotated too.
- * Errors: MOE_ERR_INVALID for NULL pointers, T outside [0, 2^31), sizes and strides against the
- * rules above, H outside [1, 1024], x, cache, q or q_out not 16-byte aligned.  T == 0 is a no-op.
+ * Errors: MOE_ERR_INVALID for NULL pointers (of a cache with rows == 0 it may be one), T outside
+ * [0, 2^31), sizes and strides against the rules above, H outside [1, 1024], x, cache, q or q_out not
+ * 16-byte aligned.  T == 0 is a no-op.
  */
 typedef struct {
     const void* x;

@@ -71,6 +71,14 @@ def test_append_nothing_to_do():
     assert rc == binding.MOE_ERR_INVALID and "args" in err
 
 
+@pytest.mark.parametrize("f8", [False, True])
+def test_append_to_a_cache_without_rows(f8):
+    # its rows' address is NULL, as an empty tensor's is (the call goes on to the next check)
+    kw = dict(W=512, ldx=512, rope_at=448, scales=FAKE) if f8 else {}
+    rc, err = _append(cache=None, rows=0, slots=FAKE + 4, **kw)
+    assert rc == binding.MOE_ERR_INVALID and "aligned to" in err, err
+
+
 def _cache(**kw):
     f = dict(rows=FAKE, pages=16, page=64, table=FAKE, sequences=4, width=8)
     f.update(kw)

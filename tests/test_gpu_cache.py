@@ -207,6 +207,19 @@ def test_append_no_tokens():
     assert r is cache and bool((cache == 1).all())
 
 
+@pytest.mark.parametrize("f8", [False, True])
+def test_append_to_a_cache_without_pages(f8):
+    g = gen(22)
+    x, q, slots = randn(5, 128, g=g, dtype=BF), randn(5, 3, 64, g=g, dtype=BF), torch.arange(-1, 4, device=DEV)
+    freq, pos = torch.rand(32, generator=g, device=DEV), ints([0, 1, 70, 5000, 100000])
+    empty = torch.empty(0, 16, 128, dtype=F8 if f8 else BF, device=DEV)
+    scales = torch.empty(0, 16, 1, device=DEV) if f8 else None
+    cache, out = binding.cache_append(x, slots, empty, scales=scales, positions=pos, inv_freq=freq, q=q)
+    assert cache is empty
+    ref, pair = rotate64(q.double(), pos, freq, True)
+    close(out, ref, 2.0 ** -8 * ref.abs() + (2 * math.pi * 2.0 ** -25 + 8 * U) * pair, "q")
+
+
 # ---- a paged cache ------------------------------------------------------------------------------
 
 class Batch:
