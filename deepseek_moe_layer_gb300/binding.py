@@ -633,7 +633,7 @@ def latent_attention(q, cache, block_table, lengths, scale, inds=None, cu_tokens
         if inds.dim() != 2 or inds.shape[0] != T:
             raise ValueError(f"inds must be [{T}, k], not {tuple(inds.shape)}")
         _need(inds, torch.int32, "inds", device)
-        k, chosen = inds.shape[1], inds.data_ptr()
+        k, chosen = inds.shape[1], _address(inds) if T else None
     if out is None:
         out = _empty((T, H, 512), torch.bfloat16, device, stream)
     else:

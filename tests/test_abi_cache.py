@@ -206,6 +206,18 @@ def test_binding_append(kw, exc, msg):
         _call_append(**kw)
 
 
+def test_attention_over_no_selection(monkeypatch):
+    # [T, 0] entries select nothing, which the library refuses; its address is 0, which means all positions
+    monkeypatch.setattr(binding, "_raw_stream", lambda t, stream: 0)
+    for T, ws in ((3, None), (90, None), (3, torch.zeros(1 << 26, dtype=torch.uint8))):
+        with pytest.raises(binding.MoeError, match="k = 0"):
+            binding.latent_attention(z(T, 16, 576), z(4, 64, 576), z(T, 2, dtype=I32), z(T, dtype=I32), 0.1,
+                                     inds=z(T, 0, dtype=I32), ws=ws)
+    for k in (0, 5):  # no tokens: nothing to do
+        assert binding.latent_attention(z(0, 16, 576), z(4, 64, 576), z(0, 2, dtype=I32), z(0, dtype=I32), 0.1,
+                                        inds=z(0, k, dtype=I32), ws=z(0, dtype=torch.uint8)).shape == (0, 16, 512)
+
+
 def _call_scores(**kw):
     a = dict(q=z(3, 64, 128), weights=z(3, 64, dtype=F32), keys=z(4, 64, 128),
              block_table=z(3, 2, dtype=I32), lengths=z(3, dtype=I32), n=100)
@@ -300,3 +312,11 @@ def test_append_says_which_type_its_cache_has(calls, pages, f8):
     binding.cache_append(z(3, 256), z(3, dtype=I64), z(pages, 64, 256, dtype=F8 if f8 else BF),
                          scales=z(pages, 64, 2, dtype=F32) if f8 else None)
     assert (calls[0][1][0]._obj.scales is not None) == f8
+
+
+@pytest.mark.parametrize("T,k", [(3, 0), (90, 0), (3, 5), (3, None)])
+def test_attention_says_whether_positions_are_selected(calls, T, k):
+    binding.latent_attention(z(T, 16, 576), z(4, 64, 576), z(T, 2, dtype=I32), z(T, dtype=I32), 0.1,
+                             inds=None if k is None else z(T, k, dtype=I32))
+    chosen, n = calls[-1][1][9:11]
+    assert bool(chosen) == (k is not None) and n == (k or 0)
