@@ -476,6 +476,12 @@ def _address(t):
     return None if t is None else t.data_ptr() or 256
 
 
+def _need_32_bits(*sizes):
+    """ctypes cuts what does not fit an int32_t argument down to its lowest 32 bits, silently."""
+    if not -0x80000000 <= min(sizes) <= max(sizes) <= 0x7FFFFFFF:
+        raise ValueError(f"sizes {sizes} do not fit 32 bits")
+
+
 def _need_vector(t, dtype, name, n, device):
     _need(t, dtype, name, device)
     if t.shape != (n,):
@@ -549,6 +555,7 @@ def cache_append(x, slots, cache, scales=None, norm_weight=None, norm_bias=None,
         st = (q0 if T > 1 else 0, q1 if H > 1 else 0, o0 if T > 1 else 0, o1 if H > 1 else 0)
     elif q_out is not None:
         raise ValueError("q_out given without q")
+    _need_32_bits(W, n, R, at, H)
     a = AppendArgs(x.data_ptr(), T, x.stride(0) if T > 1 else W, W, slots.data_ptr(),
                    cache.data_ptr(), _address(scales), pages * page,
                    weight, bias, n, eps, pos, freq, R, at, int(bool(interleaved)), src, dst, H, *st)
@@ -573,6 +580,7 @@ def _paged_cache(rows, dtype, name, width, table, lengths, cu_tokens, T, device,
         _need_vector(cu_tokens, torch.int32, "cu_tokens", B + 1, device)
     elif B != T:
         raise ValueError(f"block_table has {B} rows for {T} tokens, and cu_tokens is None")
+    _need_32_bits(page, B, wide)
     return PagedCache(rows.data_ptr(), pages, page, table.data_ptr(), B, wide)
 
 
@@ -598,6 +606,7 @@ def indexer_scores(q, weights, keys, block_table, lengths, n, key_scales=None, c
         if key_scales.shape not in (keys.shape[:2], (*keys.shape[:2], 1)):
             raise ValueError(f"key_scales must be {(*keys.shape[:2], 1)}, not {tuple(key_scales.shape)}")
     n = int(n)
+    _need_32_bits(n, H)
     if out is None:
         out = _empty((T, n), torch.float32, device, stream)
         ld = n
@@ -632,8 +641,10 @@ def latent_attention(q, cache, block_table, lengths, scale, inds=None, cu_tokens
     if inds is not None:
         if inds.dim() != 2 or inds.shape[0] != T:
             raise ValueError(f"inds must be [{T}, k], not {tuple(inds.shape)}")
-        _need(inds, torch.int32, "inds", device)
         k, chosen = inds.shape[1], _address(inds) if T else None
+    _need_32_bits(k, H)
+    if inds is not None:
+        _need(inds, torch.int32, "inds", device)
     if out is None:
         out = _empty((T, H, 512), torch.bfloat16, device, stream)
     else:

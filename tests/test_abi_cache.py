@@ -320,3 +320,41 @@ def test_attention_says_whether_positions_are_selected(calls, T, k):
                              inds=None if k is None else z(T, k, dtype=I32))
     chosen, n = calls[-1][1][9:11]
     assert bool(chosen) == (k is not None) and n == (k or 0)
+
+
+def _meta(*shape, dtype=BF):
+    return torch.empty(*shape, dtype=dtype, device="meta")
+
+
+BIG = 1 << 32  # a multiple of it vanishes in 32 bits
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=BIG + 100, out=_meta(3, BIG + 100, dtype=F32)), dict(block_table=_meta(3, BIG + 2, dtype=I32)),
+    dict(keys=_meta(0, BIG + 64, 128)),
+])
+def test_scores_sizes_beyond_32_bits(calls, kw):
+    with pytest.raises(ValueError, match="32 bits"):
+        _call_scores(**kw)
+    assert not calls
+
+
+@pytest.mark.parametrize("kw", [
+    dict(inds=_meta(3, BIG + 5, dtype=I32)), dict(block_table=_meta(3, BIG + 2, dtype=I32)),
+    dict(q=_meta(3, 1, 576).expand(3, BIG + 16, 576)), dict(cache=_meta(0, BIG + 64, 576)),
+])
+def test_attention_sizes_beyond_32_bits(calls, kw):
+    with pytest.raises(ValueError, match="32 bits"):
+        _call_attention(**kw)
+    assert not calls
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rope_at=BIG + 512), dict(rope_at=512 - BIG), dict(x=_meta(3, BIG + 576), cache=_meta(2, 64, BIG + 576)),
+    dict(norm_weight=_meta(BIG + 512, dtype=F32)),
+    dict(q=_meta(3, 1, 64).expand(3, BIG + 8, 64), q_out=_meta(3, 1, 64).expand(3, BIG + 8, 64)),
+])
+def test_append_sizes_beyond_32_bits(calls, kw):
+    with pytest.raises(ValueError, match="32 bits"):
+        _call_append(**kw)
+    assert not calls
