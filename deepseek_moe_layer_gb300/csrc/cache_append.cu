@@ -4,16 +4,17 @@
 // bias the layer norm: (x - mean) / std * w + b), the R columns from r0 on turned pair by pair by
 // the angle positions[t] * inv_freq[i], then rounded once, to bf16 or to e4m3 codes with one
 // power-of-two scale per 128 columns, into row slots[t] of the cache.  Sums and values in fp32.  The
-// angle is formed in turns from exact fp32 products (turn_of): at position 10^6 a rounded one is
-// off by 0.03 radians, and the device's 64-bit rate is a hundredth of its 32-bit one (4001 index
-// keys: 18 us with angles in 64 bits, 7.6 so).
+// angle is formed in turns from whole numbers (turn_of): at position 10^6 an fp32 product is off by
+// 0.03 radians, and the device's 64-bit floating-point rate is a hundredth of its 32-bit one (4001 index
+// keys: 18 us with angles in fp64, 7.7 so).
 //
-// The bound is HBM (8192 rows of 576 columns with 128 heads' rotations move 287 MB) or, for a few
-// tokens, the launch.  A row is a warp's, 8 columns per lane and step, its sums five shuffles; queries
+// The bound of a prompt's rows is memory (8192 rows of 576 columns with 128 heads' rotations move 287 MB),
+// of a few tokens the launch.  A row is a warp's, 8 columns per lane and step, its sums five shuffles; queries
 // go through blocks of their own, which make their tokens' cosines and sines once in shared memory
-// while the first columns are on their way.  Measured: 287 MB in 65 us (4.4 TB/s: pieces of 128 bytes,
-// two of three lines skipped on one side, eight of nine on the other), one token in 4.2 us; with 2
-// or 8 pieces in flight per thread instead of 4 68 and 88 us, with 3, 5 or 6 blocks per SM 68 .. 71.
+// while the first columns are on their way.  Measured: 287 MB in 65 us (4.4 TB/s), one token in 3.6 us;
+// with 2 or 8 pieces in flight per thread instead of 4 68 and 88 us, with 3, 5 or 6 blocks per SM 68 .. 71.
+// The lanes that hold rotated columns compute their angles one after the other (8 of 32 lanes, 4 or 8
+// angles each, where a row has 64 rotated columns), which short rows in large numbers show.
 #include "launch.h"
 #include "scaled.cuh"
 
@@ -26,20 +27,22 @@ constexpr int kMaxChunks = 4;      // of 8 columns per lane: rows up to 1024 col
 constexpr int kMaxAngles = 2048;   // of a query block: tokens * R / 2
 constexpr int kQueryUnits = 4;     // 16-byte columns (or pairs of them) in flight per thread
 
-// cos and sin of the angle pos * f.  f / (2 pi) is g1 + g2 (g1 rounded, its rounding error and the
-// constant's own in g2), pos the sum of hi, a multiple of 4096, and lo; the products hi g1 and
-// lo g1 and what their rounding leaves are exact, and so is every difference to the nearest
-// whole number.  Off by less than 2^-25 turns to position 2^26, 2^-20 to 2^31 (f <= 1).
+// cos and sin of the angle pos * f.  In turns it is pos * g with g = f / (2 pi), of which only what
+// lies behind the point counts: g is held in units of 2^-64 turns (rounded down, off by less than two for
+// f <= 2), and its product with pos modulo 2^64 is exact.  So the angle is off by less than 2^-25 turns at
+// every position for f <= 64: 2^-26 from its rounding to fp32, the rest from g.  (Sums of
+// fp32 products with their errors: 2^-22.7 turns at 2^26, 2^-18 at 2^31.)
 MOE_DEV void turn_of(int pos, float f, float& c, float& s) {
-    constexpr float kInv1 = 0x1.45f306p-3f, kInv2 = 0x1.b93910p-28f;  // 1 / (2 pi)
-    const float g1 = f * kInv1, g2 = fmaf(f, kInv2, fmaf(f, kInv1, -g1));
-    const float hi = (float)(pos & ~0xFFF), lo = (float)(pos & 0xFFF);
-    const float h = hi * g1, l = lo * g1;
-    const float eh = fmaf(hi, g1, -h), el = fmaf(lo, g1, -l);
-    float t = (eh - rintf(eh)) + el + (hi + lo) * g2;
-    t = (h - rintf(h)) + (l - rintf(l)) + (t - rintf(t));
-    t -= rintf(t);
-    sincospif(2.0f * t, &s, &c);
+    constexpr uint64_t kTurn = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
+    const uint32_t bits = __float_as_uint(f), m = (bits | 0x800000u) << 8;
+    const int e = (int)(bits >> 23 & 255u) - 126;      // |f| = m 2^(e - 32)
+    uint64_t g = (uint64_t)(uint32_t)(kTurn >> 32) * m + __umulhi((uint32_t)kTurn, m);
+    g = e > 0 ? g << min(e, 63) : g >> min(-e, 63);
+    const uint64_t a = (uint64_t)(long long)pos * g;
+    float t = fmaf((float)(uint32_t)a, 0x1p-63f, (float)(int)(a >> 32) * 0x1p-31f);  // half turns
+    if (e == 129) t = f - f;                           // no finite frequency
+    sincospif(t, &s, &c);
+    if ((int)bits < 0) s = -s;
 }
 
 MOE_DEV void unpack8(const uint4& q, float (&v)[8]) {

@@ -182,6 +182,70 @@ def test_append_far_positions(first):
     close(q, ref, 2.0 ** -8 * ref.abs() + (2 * math.pi * turn + 8 * U) * pair, "q in place")
 
 
+def turns64(pos, freq):
+    """pos * f / (2 pi) behind the point, from whole numbers: float64 [positions, frequencies]."""
+    bits = 320
+
+    def arctan_of_inverse(n):
+        term = total = (1 << bits) // n
+        k = 1
+        while term:
+            term //= -n * n
+            k += 2
+            total += term // k
+        return total
+
+    two_pi = 8 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239))  # Machin's formula, in units of 2^-320
+    out = []
+    for p in pos:
+        for f in freq:
+            m, d = f.as_integer_ratio()  # d a power of two
+            out.append((p * m << 2 * bits) // (d * two_pi) % (1 << bits) / (1 << bits))
+    return torch.tensor(out, dtype=torch.float64).reshape(len(pos), len(freq))
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("first,top", [(112736, 1.0), ((1 << 20) - 7, 1.0), (65710802, 1.0), ((1 << 26) - 40, 1.0),
+                                       ((1 << 31) - 16, 1.0), (-(1 << 31), 1.0), ((1 << 31) - 16, 63.0)])
+def test_append_angles(first, top, interleaved):
+    """The angle itself: of every pair (u, v), u = 1 .. 2 and v are chosen so that u cos a - v sin a is almost 0,
+    where the rounding to bf16 hides nothing.  Off by 2^-25 turns, and by 2 units of cos and sin and two
+    roundings of the products: (2^-23 + 2 2^-24) of the pair."""
+    T, R = 16, 64
+    g = torch.Generator().manual_seed(first % 1000)
+    freq = (torch.rand(R // 2, generator=g) ** 2 * top).float()
+    freq[0], freq[1], freq[2] = 1.0, 0.7498942, 0.0013335214
+    pos = [first + t for t in range(T)]
+    a = turns64(pos, [float(f) for f in freq]) * 2 * math.pi
+    c, s = torch.cos(a), torch.sin(a)
+    u = 1 + torch.arange(128, dtype=torch.float64) / 128
+    u = u.expand(T, R // 2, 128)
+    v = (u * (c / s)[..., None]).clamp(-1e4, 1e4).to(BF).double()
+    left = (u * c[..., None] - v * s[..., None]).abs() / (u + v.abs())
+    best = left.argmin(-1, keepdim=True)
+    u, v = u.gather(-1, best)[..., 0], v.gather(-1, best)[..., 0]
+    join = (lambda p, q: torch.stack((p, q), -1).flatten(-2)) if interleaved else (lambda p, q: torch.cat((p, q), -1))
+    x = join(u, v).to(DEV, BF)
+    ref = join(u * c - v * s, v * c + u * s).to(DEV)
+    pair = join(u + v.abs(), u + v.abs()).to(DEV)
+    cache = torch.zeros(1, T, R, dtype=BF, device=DEV)
+    _, q = binding.cache_append(x, torch.arange(T, device=DEV), cache, positions=ints(pos), inv_freq=freq.to(DEV),
+                                interleaved=interleaved, q=x[:, None])
+    tol = 2.0 ** -8 * ref.abs() + (2 * math.pi * 2.0 ** -25 + 2.0 ** -22) * pair
+    close(cache[0], ref, tol, "rows")
+    close(q[:, 0], ref, tol, "q")
+
+
+def test_append_frequencies_without_a_value():
+    x = torch.ones(4, 16, dtype=BF, device=DEV)
+    freq = torch.tensor([0.0, INF, -INF, float("nan"), -0.5, 1e-40, 0.5, 1e-12], device=DEV)
+    cache = torch.zeros(1, 4, 16, dtype=BF, device=DEV)
+    binding.cache_append(x, torch.arange(4, device=DEV), cache, positions=ints([0, 1, 3, 1000]), inv_freq=freq)
+    y = cache[0].view(4, 8, 2)
+    assert bool(y[:, 1:4].isnan().all()) and bool((y[:, [0, 5, 7]] == 1.0).all())
+    assert torch.equal(y[:, 4], y[:, 6].flip(-1)) and not torch.equal(y[1:, 4], y[1:, 6])
+
+
 def test_append_not_finite():
     x = torch.ones(4, 128, dtype=BF, device=DEV)
     x[0, 5], x[1, 5], x[2, 5] = float("nan"), INF, -INF
