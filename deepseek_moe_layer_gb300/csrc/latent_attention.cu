@@ -222,6 +222,11 @@ MOE_DEV float exp2_of(float x) {
     return y;
 }
 
+// What the sums are multiplied by: 1 / l, 0 without any position, NaN where all scores are -inf.
+MOE_DEV float over(float l, float m) {
+    return l == 0.0f ? 0.0f : m == -kInf ? __int_as_float(0x7FFFFFFF) : 1.0f / l;
+}
+
 // Barrier of the softmax threads: whether v holds for one of them.
 MOE_DEV bool soft_any(bool v) {
     uint32_t r;
@@ -752,6 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             const int tok = w.s.t + gr / p.H, head = gr % p.H;
             const int see = !live ? 0 : p.inds ? w.s.len : seq_length(p.seq, tok);
             float m = -kInf, l = 0.0f;
+            uint32_t seen = 0;  // whether there was any position
             for (int i = w.i0; i < w.i1; ++i, ++g) {
                 const uint32_t b = g & 1u;
                 // (a warp whose wait gave up keeps to the softmax barriers until all know)
@@ -771,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                 if (lane == 0 && ok) arrive_even(&sfree[b]);
                 const uint32_t bits = mask[(g & 3u) * 4 + 2 * half + set] &
                                       low_bits(see - i * kTile - half * 64 - set * 32);
+                seen |= bits;
                 if (!__all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
@@ -830,6 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
                 if (lane == 0 && ok) arrive_even(&pfull[half]);
             }
             ok = ok && wait_all(pvdone, (g - 1) & 1u, abort);
+            // scores that are all -inf are told from no positions by their sum, 0 otherwise
+            if (m == -kInf && seen) l += 1.0f;
             xch[L] = l;
             if (soft_any(!ok)) { ok = false; break; }
             l = of_row(l, [](float u, float v) { return u + v; });
@@ -837,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const Params p) 
             const bool whole = w.begins() && w.ends();
             const int slot = 2 * pair + (w.begins() ? 1 : 0);
             float* part = p.part + (long long)slot * kPartFloats;
-            const float f = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            const float f = whole ? over(l, m) : 1.0f;
             if (live && half == 0 && set == 0) {
                 if (whole) {
                     if (p.lse)
@@ -971,7 +980,7 @@ __global__ void __launch_bounds__(SPLIT == 1 ? 32 * kJoinWarps : 32 * SPLIT) joi
         const float mi = a[kRows * kLatent + row], li = a[kRows * kLatent + kRows + row];
         const float4* o = reinterpret_cast<const float4*>(a + blk * kBlockFloats) + lane;
         const float to = fmaxf(m, mi);
-        const float f = mi == -kInf ? 0.0f : mi == to ? 1.0f : exp2_of(mi - to);
+        const float f = mi == to ? 1.0f : exp2_of(mi - to);
         const float g = m == to ? 1.0f : exp2_of(m - to);
         m = to;
         l = fmaf(f, li, l * g);
@@ -997,14 +1006,14 @@ __global__ void __launch_bounds__(SPLIT == 1 ? 32 * kJoinWarps : 32 * SPLIT) joi
         for (int c = 0; c < 16; ++c) acc[c] = 0.0f;
         for (int k = 0; k < SPLIT; ++k) {
             const float mi = held[k][16][lane];
-            const float f = mi == -kInf ? 0.0f : mi == m ? 1.0f : exp2_of(mi - m);
+            const float f = mi == m ? 1.0f : exp2_of(mi - m);
             l = fmaf(f, held[k][17][lane], l);
 #pragma unroll
             for (int c = 0; c < 16; ++c) acc[c] = fmaf(f, held[k][c][lane], acc[c]);
         }
     }
     if (row >= first.z * p.H) return;
-    const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    const float f = over(l, m);
     const long long o = (long long)first.y * p.H + row;
     uint32_t r[8];
 #pragma unroll

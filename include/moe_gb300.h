@@ -327,7 +327,8 @@ int moe_indexer_scores(const void* q, const float* weights, int64_t T, int32_t H
  *   q bf16 [T, H, 576], token and head strides q_token and q_head (in elements, multiples of 8);
  *   1 <= H <= 128.  Scores, softmax and sums in fp32; p is rounded to bf16 for its product.
  *   Out: out bf16 [T, H, 512]; lse fp32 [T, H] or NULL: log of the sum of exp of the scaled scores.
- *   A token without any position gives out 0 and lse -inf.
+ *   A token without any position gives out 0 and lse -inf, one whose scores are all -inf out NaN and
+ *   lse -inf.
  *   ws: at least moe_latent_attention_workspace_bytes(T, k or width * page) bytes, 256-byte
  *   aligned, in use until the call's work is done (calls that overlap need one each).
  * Errors: MOE_ERR_INVALID for NULL pointers, H outside [1, 128], k < 1 with inds, strides that are no

@@ -644,6 +644,47 @@ def test_attention_not_finite_scores():
     close(out[0], mean.mean(0).expand(128, 512), (2.0 ** -8 + 300 * U) * 2 * mean.abs().mean(0))
 
 
+@pytest.mark.parametrize("lens", [[100, 5], [4096], [2000] * 12, [3000] * 2, [1, 128, 129]])
+@pytest.mark.parametrize("k", [0, 300])
+def test_attention_scores_of_minus_infinity(lens, k):
+    """Scores that are all -inf have no softmax: NaN, in one piece and in many, told from no positions (0).  With
+    one finite score among them, wherever it lies, the output is that row."""
+    g = gen(23)
+    bt = Batch(lens, [1] * len(lens), 64, 576, g)
+    q = randn(bt.T, 20, 576, g=g, dtype=BF)
+    q[:, :, 540] = -1.0
+    q[:, 5, 540] = 0.0  # 0 * inf
+    inds = select(bt, k, g) if k else None
+    rows = bt.rows.clone()
+    for s in bt.slots:
+        rows[s, 540] = INF
+
+    def run(lengths=bt.lengths):
+        return binding.latent_attention(q, rows.view(bt.cache.shape), bt.table, lengths, 0.1, inds=inds, want_lse=True)
+
+    out, lse = run()
+    assert bool(out.isnan().all())
+    lse[:, 5] = -INF  # (NaN there)
+    assert bool((lse == -INF).all())
+    out, lse = run(torch.zeros_like(bt.lengths))
+    assert bool((out == 0).all()) and bool((lse == -INF).all())
+    heads = [h for h in range(20) if h != 5]
+    for where in (0.0, 0.4, 0.99):
+        at = [int(where * len(s)) if inds is None else int(inds[t][int(where * min(k, len(s)))])
+              for t, s in enumerate(bt.slots)]
+        for s, j in zip(bt.slots, at):
+            rows[s[j], 540] = 1.0
+        out, lse = run()
+        c = torch.stack([rows[s[j]] for s, j in zip(bt.slots, at)])
+        assert torch.equal(out[:, heads], c[:, None, :512].expand(-1, 19, -1))
+        z = (q.double() * c[:, None].double()).sum(-1) * 0.1
+        mag = (q.double() * c[:, None].double()).abs().sum(-1) * 0.1
+        close(lse[:, heads], z[:, heads], ((576 * 2.0 ** -23 + 4 * U) * mag + 40 * U * (z.abs() + 8))[:, heads], "lse")
+        for s, j in zip(bt.slots, at):
+            rows[s[j], 540] = INF
+    binding.device_status()
+
+
 @pytest.mark.parametrize("lens,new,H", [
     ([3001, 2000, 2700, 1500, 1, 2999, 900, 2222, 128, 129, 1777, 2048, 2600, 3000, 640, 2500, 1999], [4] * 17, 16),
     ([5000, 5000], [1, 1], 128), ([9000, 100, 3000], [1, 2, 9], 32), ([2560] * 30, [1] * 30, 128),
