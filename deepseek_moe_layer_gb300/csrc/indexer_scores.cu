@@ -34,6 +34,7 @@
 
 #include "launch.h"
 #include "paged.cuh"
+#include "score_list.h"
 
 namespace moe {
 
@@ -611,8 +612,8 @@ cudaError_t run(const ScoresArgs& a, cudaStream_t s) {
     const int avg = a.cu ? (int)((a.T + a.B - 1) / a.B) : 1;
     p.tt = C::kCols / p.Hp;
     if (avg < p.tt) p.tt = avg;
-    // no more CTAs than entries of the list where every token sees all n positions
-    const long long most = (a.T + p.tt - 1) / p.tt * ((a.n + kKeys - 1) / kKeys) * ((p.tt + p.gtok - 1) / p.gtok);
+    // no more CTAs than the list can have entries
+    const long long most = score_list_bound(a.T, a.cu ? a.B : 0, p.tt, p.gtok, a.n, kKeys);
     const long long grid = most < num_sms() ? most : num_sms();
     return launch_kernel(scores_kernel<F8, HP>, dim3((unsigned)grid), dim3(kThreads), (size_t)C::kSmemBytes,
                          s, p);

@@ -2,6 +2,9 @@
 moe_cache_append, moe_indexer_scores and moe_latent_attention runs on the host before any CUDA call,
 and the binding refuses tensors that do not fit before it reaches the library."""
 import ctypes
+import os
+import random
+import subprocess
 
 import pytest
 import torch
@@ -119,6 +122,43 @@ def test_scores_cache_refusals(cache, msg):
 def test_scores_refusals(kw, msg):
     rc, err = _scores(**kw)
     assert rc == binding.MOE_ERR_INVALID and msg in err, err
+
+
+@pytest.fixture(scope="module")
+def list_bound(tmp_path_factory):
+    d = tmp_path_factory.mktemp("list")
+    header = os.path.join(os.path.dirname(binding.__file__), "csrc", "score_list.h")
+    (d / "b.cc").write_text(f'#include "{header}"\nextern "C" long long bound(long long T, long long B, int tt, int gtok, '
+                            "long long n, int keys) { return moe::score_list_bound(T, B, tt, gtok, n, keys); }\n")
+    subprocess.run(["g++", "-shared", "-fPIC", "-o", str(d / "b.so"), str(d / "b.cc")], check=True)
+    f = ctypes.CDLL(str(d / "b.so")).bound
+    f.argtypes = [ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_longlong, ctypes.c_int]
+    f.restype = ctypes.c_longlong
+    return f
+
+
+def _entries(new, tt, gtok, n):
+    """The list's entries where every token sees all n positions: groups of tt tokens, cut at sequences' ends."""
+    owner = [b for b, t in enumerate(new) for _ in range(t)]
+    total = 0
+    for u in range(0, len(owner), tt):
+        group = owner[u:u + tt]
+        total += sum(-(-group.count(b) // gtok) for b in set(group)) * -(-n // 128)
+    return total
+
+
+def test_scores_list_is_no_longer_than_its_bound(list_bound):
+    # (CTAs that the grid lacks leave the device idle: 1, 2 and 1 tokens of three sequences are four parts)
+    assert _entries([1, 2, 1], 2, 2, 4096) == list_bound(4, 3, 2, 2, 4096, 128) == 128
+    r = random.Random(1)
+    for _ in range(2000):
+        new = [r.choice((0, 1, 1, 2, 5, r.randint(0, 70))) for _ in range(r.randint(1, 12))]
+        T, tt, gtok, n = sum(new), r.randint(1, 32), r.choice((1, 2, 4, 8)), r.randint(1, 3000)
+        if T:
+            assert _entries(new, tt, gtok, n) <= list_bound(T, len(new), tt, gtok, n, 128), (new, tt, gtok, n)
+            assert _entries([1] * T, 1, gtok, n) == list_bound(T, 0, 1, gtok, n, 128)
+            assert _entries([T], tt, gtok, n) <= list_bound(T, 1, tt, gtok, n, 128) < \
+                _entries([T], tt, gtok, n) + -(-n // 128) * -(-tt // gtok)
 
 
 def test_scores_nothing_to_do():
