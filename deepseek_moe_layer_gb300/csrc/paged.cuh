@@ -1,5 +1,5 @@
-// paged.cuh -- device helpers of the operators over a paged cache: where a sequence's position
-// lies, which sequence a token belongs to, asynchronous 16-byte copies.
+// paged.cuh -- device helpers of the operators over a paged cache: which sequence a token belongs to,
+// asynchronous 16-byte copies, waits, the issue of UMMAs.
 #pragma once
 
 #include "common.cuh"
@@ -13,15 +13,6 @@ struct Paged {
     int width, page;
     long long pages;
 };
-
-// Row of the cache that holds position pos of sequence b, -1 for a page outside the cache.
-MOE_DEV long long paged_row(const Paged& c, int b, int pos) {
-    const unsigned at = (unsigned)pos / (unsigned)c.page;
-    const int id = __ldg(c.table + (long long)b * c.width + at);
-    return (unsigned)id < (unsigned long long)c.pages
-               ? (long long)id * c.page + ((unsigned)pos - at * (unsigned)c.page)
-               : -1;
-}
 
 // Sequences of tokens: sequence b's are cu[b] .. cu[b + 1] - 1, or token b alone without cu.  (cu may
 // be a copy in shared memory.)
