@@ -471,15 +471,14 @@ def _fits(t, dtype, shape, dev):
 
 
 def _address(t):
-    """The address of a tensor that may be left out: None without one.  Never 0 for one that is there:
-    the library takes NULL for "not given", and torch gives 0 as an empty tensor's address."""
-    return None if t is None else t.data_ptr() or 256
+    """The address of a tensor that a caller may leave out, never 0: the library takes NULL for "not
+    given", and torch gives 0 as an empty tensor's address."""
+    return t.data_ptr() or 256
 
 
-def _need_32_bits(*sizes):
-    """ctypes cuts what does not fit an int32_t argument down to its lowest 32 bits, silently."""
-    if not -0x80000000 <= min(sizes) <= max(sizes) <= 0x7FFFFFFF:
-        raise ValueError(f"sizes {sizes} do not fit 32 bits")
+def _too_large(*sizes):
+    """Of sizes that do not fit an int32_t: ctypes cuts those down to their lowest 32 bits, silently."""
+    return ValueError(f"sizes {sizes} do not fit 32 bits")
 
 
 def _need_vector(t, dtype, name, n, device):
@@ -555,9 +554,10 @@ def cache_append(x, slots, cache, scales=None, norm_weight=None, norm_bias=None,
         st = (q0 if T > 1 else 0, q1 if H > 1 else 0, o0 if T > 1 else 0, o1 if H > 1 else 0)
     elif q_out is not None:
         raise ValueError("q_out given without q")
-    _need_32_bits(W, n, R, at, H)
+    if (W | n | R | H | (at if at >= 0 else ~at)) >> 31:
+        raise _too_large(W, n, R, H, at)
     a = AppendArgs(x.data_ptr(), T, x.stride(0) if T > 1 else W, W, slots.data_ptr(),
-                   cache.data_ptr(), _address(scales), pages * page,
+                   cache.data_ptr(), None if scales is None else _address(scales), pages * page,
                    weight, bias, n, eps, pos, freq, R, at, int(bool(interleaved)), src, dst, H, *st)
     _check((_lib or lib()).moe_cache_append(ctypes.byref(a), _raw_stream(x, stream)))
     return cache if q is None else (cache, q_out)
@@ -580,7 +580,8 @@ def _paged_cache(rows, dtype, name, width, table, lengths, cu_tokens, T, device,
         _need_vector(cu_tokens, torch.int32, "cu_tokens", B + 1, device)
     elif B != T:
         raise ValueError(f"block_table has {B} rows for {T} tokens, and cu_tokens is None")
-    _need_32_bits(page, B, wide)
+    if (page | B | wide) >> 31:
+        raise _too_large(page, B, wide)
     return PagedCache(rows.data_ptr(), pages, page, table.data_ptr(), B, wide)
 
 
@@ -606,7 +607,8 @@ def indexer_scores(q, weights, keys, block_table, lengths, n, key_scales=None, c
         if key_scales.shape not in (keys.shape[:2], (*keys.shape[:2], 1)):
             raise ValueError(f"key_scales must be {(*keys.shape[:2], 1)}, not {tuple(key_scales.shape)}")
     n = int(n)
-    _need_32_bits(n, H)
+    if (n | H) >> 31:
+        raise _too_large(n, H)
     if out is None:
         out = _empty((T, n), torch.float32, device, stream)
         ld = n
@@ -617,7 +619,8 @@ def indexer_scores(q, weights, keys, block_table, lengths, n, key_scales=None, c
             raise ValueError(f"out must be [{T}, {n}] on {device} with unit stride along its rows")
         ld = out.stride(0) if T > 1 else n
     _check((_lib or lib()).moe_indexer_scores(
-        q.data_ptr(), weights.data_ptr(), T, H, ctypes.byref(c), _address(key_scales),
+        q.data_ptr(), weights.data_ptr(), T, H, ctypes.byref(c),
+        None if key_scales is None else _address(key_scales),
         None if cu_tokens is None else cu_tokens.data_ptr(), lengths.data_ptr(), n, out.data_ptr(),
         ld, _raw_stream(q, stream)))
     return out
@@ -642,7 +645,8 @@ def latent_attention(q, cache, block_table, lengths, scale, inds=None, cu_tokens
         if inds.dim() != 2 or inds.shape[0] != T:
             raise ValueError(f"inds must be [{T}, k], not {tuple(inds.shape)}")
         k, chosen = inds.shape[1], _address(inds) if T else None
-    _need_32_bits(k, H)
+    if (k | H) >> 31:
+        raise _too_large(k, H)
     if inds is not None:
         _need(inds, torch.int32, "inds", device)
     if out is None:
