@@ -724,6 +724,25 @@ def test_runs_of_the_list_of_tiles(count, shape):
     binding.device_status()
 
 
+@pytest.mark.parametrize("H,before,prompt,behind", [(128, 40, 150, 41), (16, 3, 260, 90), (64, 0, 130, 130), (20, 130, 33, 0)])
+def test_one_prompt_beside_decoding_sequences(H, before, prompt, behind):
+    # one sequence with many new tokens among sequences with one each: groups and segments of every kind
+    g = gen(24 + H)
+    lens = [(97 * i) % 700 + 1 for i in range(before)] + [prompt + 200] + [(61 * i) % 900 + 1 for i in range(behind)]
+    bt = Batch(lens, [1] * before + [prompt] + [1] * behind, 32, 576, g)
+    q, qi, w = randn(bt.T, H, 576, g=g, dtype=BF), randn(bt.T, H, 128, g=g, dtype=BF), randn(bt.T, H, g=g)
+    out, lse = binding.latent_attention(q, bt.cache, bt.table, bt.lengths, 0.1, cu_tokens=bt.cu, want_lse=True)
+    attention_check(out, lse, bt, q, 0.1)
+    inds = select(bt, 130, g)
+    attention_check(binding.latent_attention(q, bt.cache, bt.table, bt.lengths, 0.1, inds=inds, cu_tokens=bt.cu), None,
+                    bt, q, 0.1, inds)
+    keys = bt.cache[..., :128].contiguous()
+    s = binding.indexer_scores(qi, w, keys, bt.table, bt.lengths, max(lens), cu_tokens=bt.cu)
+    bt.rows = keys.view(-1, 128)
+    scores_check(s, bt, qi, w, None, max(lens))
+    binding.device_status()
+
+
 # ---- a cache behind 32-bit offsets, graphs, streams, failed launches ------------------------------
 
 def test_rows_behind_32_bit_offsets():
