@@ -198,7 +198,8 @@ MOE_DEV void clear_last(uint32_t* v, int n) {
 }
 
 // HP: the heads, for loops of known length in the epilogue, or 0 for any number of them
-// (4096 x 16384 with 64 heads: 615 us with 0, 544 with 64; 3 ragged prompts with 32: 47 and 44).
+// (4096 x 16384 with 64 heads: 615 us with 0, 548 with 64; 3 ragged prompts with 32: 47 and 44).
+// 16 and 128 also divide an accumulator; they were not measured and take the loop of any length.
 template <bool F8, int HP>
 __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     using C = Cfg<F8>;

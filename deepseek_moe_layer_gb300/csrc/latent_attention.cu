@@ -18,12 +18,12 @@
 // all 128 positions, the same swizzled rows read as an MN-major B operand.  (N = 64 takes as long as
 // N = 128, 36 clocks, so tiles of 64 positions spend twice the time on s.)
 //
-// A pair loads 278 KB per tile where 147 KB are unique, the rest a second time from L2, and that is what
-// bounds a long call: 14.5 TB/s out of L2, where copies alone reach 15.5 (2048 tokens x 2048
-// selected 880 us, 1327 TFLOP/s; 64 sequences of up to 16384 positions 167 us, 4.6 TB/s of HBM).  q, one
-// tile of keys, its values and p fill shared memory, so every operand block has one place and goes
-// round once a tile: freed by its UMMAs, copied (1900 .. 2100 clocks under that load), waited for,
-// used: 3400 clocks a tile, of which the UMMAs take 2340.  Values copied out of the pair's keys instead
+// q, one tile of keys, its values and p fill shared memory, so every operand block has one place and goes
+// round once a tile: freed by its UMMAs, copied (1900 .. 2100 clocks), waited for, used.  That bounds a
+// long call: 3400 clocks a tile, where the UMMAs take 2340 and the copies, at the 15.5 TB/s that they reach
+// alone, 2500 (a pair loads 278 KB per tile where 147 KB are unique, the rest a second time from L2): 2048
+// tokens x 2048 selected 871 us, 10.5 TB/s copied, 1340 TFLOP/s (955 us after some seconds, under the power
+// cap); 64 sequences of up to 16384 positions 164 us (185), 8.8 TB/s copied, 4.6 of them from HBM.  Values copied out of the pair's keys instead
 // would have to wait for the last tile's second product and hold the keys' places meanwhile.
 //
 // Work is one list of tiles over all segments (up to 128 / H consecutive tokens of a sequence;

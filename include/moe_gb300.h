@@ -243,7 +243,8 @@ int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t ld
  *   Out: row slots[t] of the cache [rows, W] (row = page id * rows per page + row in the page; a
  *   slot outside [0, rows) is not written, -1 for tokens without a place), rounded once: bf16, or
  *   with scales != NULL e4m3 codes and fp32 scales [rows, W / 128] as of moe_quantize_blocks (W a
- *   multiple of 128).  The slots inside [0, rows) must differ from each other: of two tokens with
+ *   multiple of 128).  Sums are fp32: magnitudes from 2^58 on overflow a normalised row's.  The codes are
+ *   those of y itself, not of y turned by a Hadamard matrix, as some indexers store them.  The slots inside [0, rows) must differ from each other: of two tokens with
  *   one slot any part of either may stay.  The cache and x must not overlap.
  *   q != NULL: queries bf16 [T, H, rope_cols], token and head strides q_token and q_head (in
  *   elements, multiples of 8), rotated in the same way into q_out (strides q_out_token,
@@ -328,7 +329,8 @@ int moe_indexer_scores(const void* q, const float* weights, int64_t T, int32_t H
  *   1 <= H <= 128.  Scores, softmax and sums in fp32; p is rounded to bf16 for its product.
  *   Out: out bf16 [T, H, 512]; lse fp32 [T, H] or NULL: log of the sum of exp of the scaled scores.
  *   A token without any position gives out 0 and lse -inf, one whose scores are all -inf out NaN and
- *   lse -inf.
+ *   lse -inf.  (Of a position whose score alone is -inf, an infinity among its 512 columns may make
+ *   NaN of that column or count as nothing.)
  *   ws: at least moe_latent_attention_workspace_bytes(T, k or width * page) bytes, 256-byte
  *   aligned, in use until the call's work is done (calls that overlap need one each).
  * Errors: MOE_ERR_INVALID for NULL pointers, H outside [1, 128], k < 1 with inds, strides that are no
