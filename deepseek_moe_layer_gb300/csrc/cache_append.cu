@@ -29,8 +29,8 @@ constexpr int kQueryUnits = 4;     // 16-byte columns (or pairs of them) in flig
 
 // cos and sin of the angle pos * f.  In turns it is pos * g with g = f / (2 pi), of which only what
 // lies behind the point counts: g is held in units of 2^-64 turns (rounded down, off by less than two for
-// f <= 2), and its product with pos modulo 2^64 is exact.  So the angle is off by less than 2^-25 turns at
-// every position for f <= 64: 2^-26 from its rounding to fp32, the rest from g.  (Sums of
+// f < 1 and twice as much with every doubling), and its product with pos modulo 2^64 is exact.  So the angle is
+// off by less than 2^-25 turns at every position for f < 64: 2^-26 from its rounding to fp32, the rest from g.  (Sums of
 // fp32 products with their errors: 2^-22.7 turns at 2^26, 2^-18 at 2^31.)
 MOE_DEV void turn_of(int pos, float f, float& c, float& s) {
     constexpr uint64_t kTurn = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
