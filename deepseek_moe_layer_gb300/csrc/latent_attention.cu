@@ -23,8 +23,9 @@
 // long call: 3400 clocks a tile, where the UMMAs take 2340 and the copies, at the 15.5 TB/s that they reach
 // alone, 2500 (a pair loads 278 KB per tile where 147 KB are unique, the rest a second time from L2): 2048
 // tokens x 2048 selected 871 us, 10.5 TB/s copied, 1340 TFLOP/s (955 us after some seconds, under the power
-// cap); 64 sequences of up to 16384 positions 164 us (185), 8.8 TB/s copied, 4.6 of them from HBM.  Values copied out of the pair's keys instead
-// would have to wait for the last tile's second product and hold the keys' places meanwhile.
+// cap); 64 sequences of up to 16384 positions 164 us (185), 8.8 TB/s copied, 4.6 of them from HBM.  Values
+// copied out of the pair's keys instead would have to wait for the last tile's second product and hold the
+// keys' places meanwhile.
 //
 // Work is one list of tiles over all segments (up to 128 / H consecutive tokens of a sequence;
 // one token with a selection), cut into equal runs, one per pair, so that sequences of any

@@ -244,8 +244,9 @@ int moe_matmul_blocks(const void* a, const float* a_scale, int64_t M, int64_t ld
  *   slot outside [0, rows) is not written, -1 for tokens without a place), rounded once: bf16, or
  *   with scales != NULL e4m3 codes and fp32 scales [rows, W / 128] as of moe_quantize_blocks (W a
  *   multiple of 128).  Sums are fp32: magnitudes from 2^58 on overflow a normalised row's.  The codes are
- *   those of y itself, not of y turned by a Hadamard matrix, as some indexers store them.  The slots inside [0, rows) must differ from each other: of two tokens with
- *   one slot any part of either may stay.  The cache and x must not overlap.
+ *   those of y itself, not of y turned by a Hadamard matrix, as some indexers store them.  The slots
+ *   inside [0, rows) must differ from each other: of two tokens with one slot any part of either may
+ *   stay.  The cache and x must not overlap.
  *   q != NULL: queries bf16 [T, H, rope_cols], token and head strides q_token and q_head (in
  *   elements, multiples of 8), rotated in the same way into q_out (strides q_out_token,
  *   q_out_head, by which no two rows may lie on each other); q_out may be q itself, with q's strides,
